@@ -387,6 +387,137 @@ moe_status_t moe_route_topk_noalloc(const void* hidden, int32_t T, const void* r
                                     int32_t num_experts, int32_t hidden_size, int32_t top_k, int32_t norm_topk,
                                     int32_t* ids, float* weights, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The attention half of a decoder layer (no counterpart on the pages: they
+ * describe the expert FFN, and a program that runs the model needs attention
+ * beside it). Keys and values of earlier tokens are held in 4 bits in a paged
+ * cache; a prompt's own attention runs on its bf16 keys and values.
+ *
+ * A paged key/value cache (moe_kv_t) holds, per layer, num_pages pages of
+ * page_tokens tokens. Keys and values are Q4_0 blocks of 32 consecutive head
+ * dimensions, w = d * (q - 8), 18 bytes per block as in MOE_FMT_Q4_0. A block
+ * is made from bf16 values so: m is the value of largest magnitude (the
+ * positive one of an exact tie), d = m / -8 rounded to fp16 and held within
+ * +-65504, q = clamp(rint(b / d) + 8, 0, 15) (8 where d = 0). A block with an
+ * infinity or NaN reads back as NaN throughout.
+ *
+ * Sequences are packed: the new tokens of sequence b are rows cu_tokens[b] ..
+ * cu_tokens[b + 1] - 1 of every per-token tensor, and kv_lens[b] counts the
+ * tokens it holds in the cache with those included, so row i sits at position
+ * kv_lens[b] - (cu_tokens[b + 1] - i). A sequence may have no new token.
+ * Position p lives in page block_table[b][p / page_tokens]. Rows at or past
+ * cu_tokens[num_seqs] belong to no sequence and are left alone. These arrays
+ * are read on the device when the kernels run, never on the host, so a CUDA
+ * graph of the calls can be replayed with other contents.
+ *
+ * What the arrays hold is checked by the kernels: a position or page outside
+ * the table, the pool or the rotation table is not read or written, the rows
+ * concerned come out as NaN, and moe_kv_status reports it.
+ *
+ * Errors of these entry points leave their message with moe_last_error(NULL).
+ * Calls on one handle must not overlap (one stream, or ordered streams).
+ */
+typedef struct moe_kv moe_kv_t;
+
+typedef struct {
+    int32_t num_layers;   /* >= 1 */
+    int32_t num_pages;    /* pages per layer, >= 1 */
+    int32_t page_tokens;  /* a multiple of 16 in 16..1024 (default 64) */
+    int32_t q_heads;      /* a multiple of kv_heads; q_heads / kv_heads <= 128 */
+    int32_t kv_heads;     /* >= 1 */
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t device;
+} moe_kv_config_t;
+
+/* The packed sequences of a call; all pointers device. */
+typedef struct {
+    int32_t num_seqs;            /* >= 1 */
+    int32_t table_stride;        /* int32 entries between the block table's rows, >= 1: the pages a sequence can have */
+    const int32_t* cu_tokens;    /* [num_seqs + 1], first entry 0, not decreasing */
+    const int32_t* kv_lens;      /* [num_seqs] */
+    const int32_t* block_table;  /* [num_seqs x table_stride] page numbers, the same in every layer */
+} moe_kv_batch_t;
+
+typedef struct {
+    uint64_t page_bytes;            /* one page of one layer, keys and values */
+    uint64_t pool_device_bytes;     /* all layers */
+    uint64_t scratch_device_bytes;
+} moe_kv_info_t;
+
+void moe_kv_config_default(moe_kv_config_t* cfg);
+
+/* Allocates the pool (zeroed) and the scratch. MOE_ERR_INVALID for a bad
+ * configuration, MOE_ERR_OOM if an allocation fails. */
+moe_status_t moe_kv_create(const moe_kv_config_t* cfg, moe_kv_t** out);
+
+/* Rotates and stores T new tokens of a layer, and rotates their queries.
+ *   q, k, v : device bf16 rows [T] of q_heads / kv_heads / kv_heads heads x
+ *             head_dim, rows q_stride / k_stride / v_stride elements apart
+ *             (parts of one fused projection are fine); 16-byte aligned, the
+ *             strides multiples of 8. q may be NULL (keys and values only).
+ *   rope    : device fp32 [rope_rows x head_dim], row p the cosines of
+ *             position p for pairs 0 .. head_dim/2 - 1, then the sines; or
+ *             NULL for no rotation. Pair j is (x[j], x[j + head_dim/2]),
+ *             rotated in fp32 and rounded to bf16; the cache holds the blocks
+ *             of the rounded keys.
+ *   q_out   : device bf16 [T x q_heads x head_dim], the rotated queries (may
+ *             be q itself where q is dense); needed with q.
+ *   k_out   : device bf16 [T x kv_heads x head_dim], the rotated keys, or NULL.
+ * Asynchronous on `stream`. MOE_ERR_INVALID for bad arguments (nothing is
+ * enqueued); T = 0 does nothing. */
+moe_status_t moe_kv_append(moe_kv_t* h, int32_t layer, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, int32_t T,
+                           const moe_kv_batch_t* batch, const float* rope, int32_t rope_rows, void* q_out,
+                           void* k_out, void* stream);
+
+/* Attention of the T newest tokens over the cache: row i of sequence b sees
+ * the positions 0 .. its own, out = softmax(scale q k^T) v with the values
+ * the cache holds; query head h reads key/value head h / (q_heads /
+ * kv_heads). A row that sees no position is zero.
+ *   q   : device bf16 rows [T] x q_heads x head_dim (rotated), q_stride apart
+ *   out : device bf16 [T x q_heads x head_dim]
+ * Made for one or a few new tokens per sequence; any number is right.
+ * Asynchronous on `stream`. */
+moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_stride, int32_t T,
+                           const moe_kv_batch_t* batch, float scale, void* out, void* stream);
+
+/* Reads the keys and values of the batch's T rows back as bf16 (the held
+ * values rounded once): k_out, v_out device bf16 [T x kv_heads x head_dim].
+ * With cu_tokens the running sums of kv_lens that is every held token, packed
+ * as moe_attn_prompt takes them. Asynchronous on `stream`. */
+moe_status_t moe_kv_read(moe_kv_t* h, int32_t layer, int32_t T, const moe_kv_batch_t* batch, void* k_out,
+                         void* v_out, void* stream);
+
+/* Causal attention over packed sequences of bf16 keys and values: row i of
+ * the lq queries of sequence b (rows cu_q[b] .. cu_q[b + 1] - 1) sees the keys
+ * 0 .. lk - lq + i of its lk keys (rows cu_k[b] ..), so with cu_k = cu_q whole
+ * prompts, and with more keys than queries a prompt's later chunk over its
+ * context. Rows that see no key are zero; keys and values a row does not see
+ * do not touch it, whatever they hold.
+ *   q, k, v : device bf16 rows [Tq], [Tk], [Tk]; strides and alignment as in
+ *             moe_kv_append
+ *   cu_q, cu_k : device int32 [num_seqs + 1], first entry 0, not decreasing,
+ *             last ones at most Tq and Tk
+ *   head_dim 64 or 128; q_heads a multiple of kv_heads, at most 128 times it
+ *   out     : device bf16 [Tq x q_heads x head_dim]
+ * Runs on the current device, asynchronous on `stream`. MOE_ERR_INVALID for
+ * bad arguments. Allocates nothing. */
+moe_status_t moe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, int32_t Tq, int32_t Tk, int32_t num_seqs, const int32_t* cu_q,
+                             const int32_t* cu_k, int32_t q_heads, int32_t kv_heads, int32_t head_dim, float scale,
+                             void* out, void* stream);
+
+/* Sizes of the handle (host only, no sync). */
+moe_status_t moe_kv_info(const moe_kv_t* h, moe_kv_info_t* out);
+
+/* Synchronises and reports (then forgets) what the handle's kernels found:
+ * MOE_ERR_INVALID if a call met a position or page out of range,
+ * MOE_ERR_TIMEOUT if a bounded wait gave up, MOE_ERR_CUDA for a CUDA error. */
+moe_status_t moe_kv_status(moe_kv_t* h);
+
+/* Synchronises and frees everything the handle owns. NULL is accepted. */
+moe_status_t moe_kv_destroy(moe_kv_t* h);
+
 /* Synchronises, empties every slot, restores the initial LRU order and clears
  * the counters and trace. Expert data stays loaded. */
 moe_status_t moe_cache_reset(moe_cache_t* h);
@@ -394,8 +525,9 @@ moe_status_t moe_cache_reset(moe_cache_t* h);
 /* Synchronises and frees everything the handle owns. NULL is accepted. */
 moe_status_t moe_cache_destroy(moe_cache_t* h);
 
-/* Last error message of the handle (or of the calling thread's last failed
- * create when h is NULL). Never NULL; valid until the next call on h. */
+/* Last error message of the handle (when h is NULL, of the calling thread's
+ * last failed create, moe_kv_* or moe_attn_* call). Never NULL; valid until
+ * the next call on h. */
 const char* moe_last_error(const moe_cache_t* h);
 
 /* MOE_ABI_VERSION of the loaded library. */

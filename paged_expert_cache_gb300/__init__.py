@@ -26,7 +26,7 @@ PREFILL_MODES = {"read_only": 0, "page_in": 1}
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID", 2: "MOE_ERR_CAPACITY", 3: "MOE_ERR_CUDA", 4: "MOE_ERR_OOM",
                 5: "MOE_ERR_STATE", 6: "MOE_ERR_TIMEOUT"}
 
-i32, u64, dbl, vp = ctypes.c_int32, ctypes.c_uint64, ctypes.c_double, ctypes.c_void_p
+i32, i64, u64, dbl, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_double, ctypes.c_void_p
 
 
 class MoeConfig(ctypes.Structure):
@@ -51,6 +51,19 @@ class MoeInfo(ctypes.Structure):
     _fields_ = [("num_pools", i32), ("slots_per_pool", i32), ("slot_bytes", u64), ("slot_stride", u64),
                 ("record_bytes", u64), ("pool_device_bytes", u64), ("store_host_bytes", u64),
                 ("scratch_device_bytes", u64), ("fused_decode_calls", u64), ("split_decode_calls", u64)]
+
+
+class KvConfig(ctypes.Structure):
+    _fields_ = [("num_layers", i32), ("num_pages", i32), ("page_tokens", i32), ("q_heads", i32), ("kv_heads", i32),
+                ("head_dim", i32), ("device", i32)]
+
+
+class KvBatchArgs(ctypes.Structure):
+    _fields_ = [("num_seqs", i32), ("table_stride", i32), ("cu_tokens", vp), ("kv_lens", vp), ("block_table", vp)]
+
+
+class KvInfo(ctypes.Structure):
+    _fields_ = [("page_bytes", u64), ("pool_device_bytes", u64), ("scratch_device_bytes", u64)]
 
 
 NUM_STAGES = 7
@@ -96,6 +109,16 @@ def load():
         "moe_route_topk_noalloc": (i32, [vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp]),
         "moe_cache_set_router": (i32, [vp, i32, vp, vp]),
         "moe_cache_pool_slots": (i32, [vp, vp]),
+        "moe_kv_config_default": (None, [P(KvConfig)]),
+        "moe_kv_create": (i32, [P(KvConfig), P(vp)]),
+        "moe_kv_append": (i32, [vp, i32, vp, i64, vp, i64, vp, i64, i32, vp, vp, i32, vp, vp, vp]),
+        "moe_kv_attend": (i32, [vp, i32, vp, i64, i32, vp, ctypes.c_float, vp, vp]),
+        "moe_kv_read": (i32, [vp, i32, i32, vp, vp, vp, vp]),
+        "moe_kv_info": (i32, [vp, P(KvInfo)]),
+        "moe_kv_status": (i32, [vp]),
+        "moe_kv_destroy": (i32, [vp]),
+        "moe_attn_prompt": (i32, [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, i32, i32, ctypes.c_float, vp,
+                                  vp]),
         "moe_cache_reset": (i32, [vp]),
         "moe_cache_destroy": (i32, [vp]),
     }
@@ -360,3 +383,199 @@ class MoECache:
 
     def reset(self):
         _check(load().moe_cache_reset(self.h), self.h)
+
+
+# ---------------------------------------------------------------------------
+# The attention half of a decoder layer: a paged key/value cache in Q4_0
+# blocks, attention over it, and attention of whole prompts.
+# ---------------------------------------------------------------------------
+def _rows(name, t, heads, dim, rows=None):
+    """Checks t as bf16 rows [T, heads, dim] (or [T, heads * dim]) on the
+    current CUDA device, dense within a row; returns its row stride."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        _refuse(f"{name} must be a torch tensor")
+    shape = t.shape
+    if not (len(shape) == 3 and shape[1] == heads and shape[2] == dim or len(shape) == 2 and shape[1] == heads * dim):
+        _refuse(f"{name} must be [T, {heads}, {dim}], got {tuple(shape)}")
+    if rows is not None and shape[0] != rows:
+        _refuse(f"{name} has {shape[0]} rows, not {rows}")
+    if t.dtype is not torch.bfloat16:
+        _refuse(f"{name} must be bfloat16")
+    st = t.stride()
+    if st[-1] != 1 or len(shape) == 3 and heads > 1 and st[1] != dim:
+        _refuse(f"the heads and dims of a row of {name} must be contiguous")
+    _on_device(name, t)
+    return st[0] if shape[0] > 1 else max(st[0], heads * dim)
+
+
+def _dense(name, t, heads, dim, rows):
+    if _rows(name, t, heads, dim, rows) != heads * dim:
+        _refuse(f"{name} must be contiguous")
+
+
+def _on_device(name, t):
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        _refuse(f"{name} must be on the current CUDA device")
+
+
+def _indexes(name, t, shape=None, dims=1):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != dims or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous int32 tensor of {dims} dimension(s)")
+    if shape is not None and tuple(t.shape) != shape:
+        _refuse(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    _on_device(name, t)
+
+
+def _batch(batch):
+    if not isinstance(batch, KVBatch):
+        _refuse("batch must be a KVBatch")
+    return batch._ref
+
+
+def _stream(stream):
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream().cuda_stream or None
+    return (stream if isinstance(stream, int) else stream.cuda_stream) or None
+
+
+def make_kv_config(L, pages, q_heads, kv_heads, head_dim, page_tokens=64, device=0):
+    c = KvConfig()
+    load().moe_kv_config_default(ctypes.byref(c))
+    c.num_layers, c.num_pages, c.page_tokens = L, pages, page_tokens
+    c.q_heads, c.kv_heads, c.head_dim, c.device = q_heads, kv_heads, head_dim, device
+    return c
+
+
+class KVBatch:
+    """moe_kv_batch_t: the packed sequences of a call. cu_tokens int32
+    [B + 1], kv_lens int32 [B], block_table int32 [B, pages a sequence can
+    have], all on the device and kept by the object; the tensors may be
+    rewritten between calls (the kernels read them)."""
+
+    def __init__(self, cu_tokens, kv_lens, block_table):
+        _indexes("kv_lens", kv_lens)
+        B = kv_lens.shape[0]
+        if B < 1:
+            _refuse("a batch needs at least one sequence")
+        _indexes("cu_tokens", cu_tokens, (B + 1,))
+        _indexes("block_table", block_table, dims=2)
+        if block_table.shape[0] != B or block_table.shape[1] < 1:
+            _refuse(f"block_table must have {B} rows of at least one page")
+        self.cu_tokens, self.kv_lens, self.block_table = cu_tokens, kv_lens, block_table
+        self.args = KvBatchArgs(B, block_table.shape[1], cu_tokens.data_ptr(), kv_lens.data_ptr(),
+                                block_table.data_ptr())
+        self._ref = ctypes.addressof(self.args)
+
+
+class KVCache:
+    """One handle of the C library (moe_kv_t*): keys and values of every layer
+    in pages of Q4_0 blocks. Calls run on torch's current stream unless one is
+    given."""
+
+    def __init__(self, cfg):
+        L = load()
+        self.cfg = cfg
+        self.h = None
+        h = vp()
+        _check(L.moe_kv_create(ctypes.byref(cfg), ctypes.byref(h)))
+        self.h = h.value
+
+    def close(self):
+        if getattr(self, "h", None):
+            load().moe_kv_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def append(self, layer, q, k, v, batch, rope=None, q_out=None, k_out=None, stream=None):
+        """moe_kv_append: k, v bf16 [T, kv_heads, head_dim] (views into a fused
+        projection are fine) rotated by the rows of rope (fp32 [positions,
+        head_dim], cosines then sines; None: no rotation) and stored; q bf16
+        [T, q_heads, head_dim] rotated into q_out (None: keys and values only).
+        Returns q_out."""
+        c = self.cfg
+        T = k.shape[0]
+        ks = _rows("k", k, c.kv_heads, c.head_dim)
+        vs = _rows("v", v, c.kv_heads, c.head_dim, T)
+        qs = 0
+        if q is not None:
+            qs = _rows("q", q, c.q_heads, c.head_dim, T)
+            if q_out is None:
+                _refuse("q needs q_out")
+            _dense("q_out", q_out, c.q_heads, c.head_dim, T)
+        if k_out is not None:
+            _dense("k_out", k_out, c.kv_heads, c.head_dim, T)
+        if rope is not None:
+            import torch
+            if rope.dtype is not torch.float32 or rope.dim() != 2 or rope.shape[1] != c.head_dim \
+                    or not rope.is_contiguous() or not rope.shape[0]:
+                _refuse(f"rope must be contiguous float32 [positions, {c.head_dim}]")
+            _on_device("rope", rope)
+        _check(load().moe_kv_append(self.h, layer, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, _batch(batch),
+                                    _ptr(rope), 0 if rope is None else rope.shape[0],
+                                    None if q is None else q_out.data_ptr(), _ptr(k_out), _stream(stream)))
+        return q_out
+
+    def attend(self, layer, q, batch, out, scale=None, stream=None):
+        """moe_kv_attend: attention of the newest tokens, q bf16 [T, q_heads,
+        head_dim] (rotated), into out. scale None: head_dim ** -0.5."""
+        c = self.cfg
+        qs = _rows("q", q, c.q_heads, c.head_dim)
+        T = q.shape[0]
+        _dense("out", out, c.q_heads, c.head_dim, T)
+        _check(load().moe_kv_attend(self.h, layer, q.data_ptr(), qs, T, _batch(batch),
+                                    c.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), _stream(stream)))
+        return out
+
+    def read(self, layer, batch, k_out, v_out, stream=None):
+        """moe_kv_read: the batch's rows of the cache as bf16 into k_out, v_out
+        [T, kv_heads, head_dim]."""
+        c = self.cfg
+        T = k_out.shape[0]
+        _dense("k_out", k_out, c.kv_heads, c.head_dim, T)
+        _dense("v_out", v_out, c.kv_heads, c.head_dim, T)
+        _check(load().moe_kv_read(self.h, layer, T, _batch(batch), k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
+        return k_out, v_out
+
+    def info(self):
+        s = KvInfo()
+        _check(load().moe_kv_info(self.h, ctypes.byref(s)))
+        return {f: getattr(s, f) for f, _ in KvInfo._fields_}
+
+    def status(self):
+        """moe_kv_status: synchronises; raises what the kernels found."""
+        _check(load().moe_kv_status(self.h))
+
+
+def attention_prompt(q, k, v, out, cu_q, cu_k=None, scale=None, stream=None):
+    """moe_attn_prompt: causal attention of packed prompts, q bf16 [Tq, q_heads,
+    D], k and v bf16 [Tk, kv_heads, D], out [Tq, q_heads, D]; cu_q, cu_k int32
+    [B + 1] (cu_k None: cu_q). scale None: D ** -0.5. Returns out."""
+    import torch
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            _refuse(f"{name} must be a torch tensor [T, heads, head_dim]")
+    Tq, hq, dim = q.shape
+    Tk, hkv = k.shape[:2]
+    qs = _rows("q", q, hq, dim)
+    ks = _rows("k", k, hkv, dim)
+    vs = _rows("v", v, hkv, dim, Tk)
+    _dense("out", out, hq, dim, Tq)
+    _indexes("cu_q", cu_q)
+    B = cu_q.shape[0] - 1
+    if cu_k is None:
+        cu_k = cu_q
+    else:
+        _indexes("cu_k", cu_k, (B + 1,))
+    _check(load().moe_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, Tq, Tk, B, cu_q.data_ptr(),
+                                  cu_k.data_ptr(), hq, hkv, dim, dim ** -0.5 if scale is None else scale,
+                                  out.data_ptr(), _stream(stream)))
+    return out

@@ -179,6 +179,14 @@ bool valid_fmt(int f) { return f >= MOE_FMT_BF16 && f <= MOE_FMT_NVFP4; }
 
 }  // namespace
 
+// The message moe_last_error(NULL) returns, for entry points outside this file.
+void moe::set_last_error(const char* msg) noexcept {
+    try {
+        g_create_error = msg;
+    } catch (...) {
+    }
+}
+
 extern "C" {
 
 void moe_config_default(moe_config_t* cfg) {

@@ -416,6 +416,9 @@ constexpr int kSpecMaxTokens = 2;  // decode calls with at most this many tokens
 void launch_spec_route(const CacheDev& c, const SpecArgs& a, cudaStream_t st);
 void launch_spec_copy(const CacheDev& c, int half, cudaStream_t st);
 
+// Sets the calling thread's message for moe_last_error(NULL) (api.cu).
+void set_last_error(const char* msg) noexcept;
+
 // Host-side repack of canonical records into the slot layout (repack.cpp).
 void repack_record(int fmt, int H, int I, const uint8_t* canonical, uint8_t* slot, float* gscales3);
 

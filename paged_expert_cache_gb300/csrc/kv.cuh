@@ -1,0 +1,79 @@
+// kv.cuh -- the paged key/value cache in Q4_0 blocks: its layout, and the
+// device helpers that its kernels share.
+//
+// Layout. A page of one layer is [kv_heads][page_tokens / 16] cells; a cell
+// holds 16 tokens of one head, in the order in which the lanes of a warp hold
+// the operands of mma.sync.m16n8k16, so that attention loads it with 16-byte
+// reads and no shuffles. With G = head_dim / 32 blocks per token, lane l,
+// g = l / 4 and i = l % 4, a cell is
+//   K codes   words [16 tokens][4 i][G]    word (t, i, b): dims 32b + 8i + 2j (bits 4j) and + 1 (bits 16 + 4j)
+//   K scales  fp16x2 [2 halves][4 i][G]    tokens 8 half + 2i, + 1
+//   V codes   words [2 halves][8 g][4 i][G]  dims 32b + g + 8j of tokens 8 half + 2i (bits 4j) and + 1 (bits 16 + 4j)
+//   V scales  as K scales
+// 576 G bytes, 18 per block. Every token owns whole 16-bit units, so tokens
+// are written without reading their neighbours.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kCellTokens = 16;
+
+template <int D>
+struct Cell {
+    static constexpr int G = D / 32;
+    static constexpr int kCodes = 256 * G, kScales = 32 * G;
+    static constexpr int kKs = kCodes, kV = kCodes + kScales, kVs = kV + kCodes, kBytes = kVs + kScales;
+    // byte offsets for token t of the cell
+    __device__ static int k_word(int t, int i, int b) { return (t * 4 + i) * G * 4 + b * 4; }
+    __device__ static int v_half(int t, int g, int b) {
+        return (((t >> 3) * 32 + g * 4 + ((t & 7) >> 1)) * G + b) * 4 + (t & 1) * 2;
+    }
+    __device__ static int scale(int t, int b) { return (((t >> 3) * 4 + ((t & 7) >> 1)) * G + b) * 4 + (t & 1) * 2; }
+};
+
+// What the kernels need of a handle and a batch, by value.
+struct KvDev {
+    uint8_t* pool;        // this layer's pages
+    unsigned* err;        // sticky bits: 1 a position or page out of range, 2 a wait gave up
+    uint64_t page_bytes;
+    int num_pages, page_tokens, hq, hkv;
+};
+struct KvBatch {
+    const int *cu, *kv_lens, *table;
+    int B, table_stride;
+};
+
+// The cell of position `pos` for head `head`, or null where the table or the
+// pool has no such page.
+template <int D>
+__device__ __forceinline__ uint8_t* kv_cell(const KvDev& c, const KvBatch& b, int seq, int pos, int head) {
+    if (pos < 0) return nullptr;
+    const int pg = pos / c.page_tokens;
+    if (pg >= b.table_stride) return nullptr;
+    const int page = __ldg(b.table + (size_t)seq * b.table_stride + pg);
+    if ((unsigned)page >= (unsigned)c.num_pages) return nullptr;
+    const int cells = c.page_tokens / kCellTokens, in = (pos - pg * c.page_tokens) / kCellTokens;
+    return c.pool + (size_t)page * c.page_bytes + (size_t)(head * cells + in) * Cell<D>::kBytes;
+}
+
+// The sequence of packed row t: the last b with cu[b] <= t, or -1 where t is
+// at or past cu[B]. cu may be in shared memory.
+__device__ __forceinline__ int seq_of_row(const int* cu, int B, int t) {
+    if (t >= cu[B]) return -1;
+    int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Device scratch of the attention kernel on `device`, zeroed once.
+uint64_t attend_scratch_bytes(int device);
+void launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
+                   uint16_t* out, void* scratch, cudaStream_t st);
+
+}  // namespace moe
