@@ -1,91 +1,701 @@
 // kv_attend.cu -- attention of the newest tokens over the paged Q4_0 cache.
 //
-// out = sum_p softmax_p(scale q . k_p) v_p over the positions p a row sees.
+// A row is one query head of one new token; out = sum_p softmax_p(scale q .
+// k_p) v_p over the positions p it sees. The rows that share a key/value head
+// (its group of query heads, times the sequence's new tokens) are taken 8 or
+// 16 at a time against the cache, so each block is read from HBM once for a
+// decode step. The bytes of the cache are the floor: 18 per 32 values, keys
+// and values once.
+//
+// Work. The sequences' contexts are cut into units of kWarps cells (a cell is
+// 16 tokens of one head); units are numbered over (sequence, head, row tile)
+// and every CTA takes an equal run of them, whatever the lengths are: the
+// lengths are read on the device, and a long sequence is spread over the whole
+// GPU. A run's pieces that cover an item only in part leave a partial sum
+// (maximum, sum, unnormalised output); the CTA that arrives last at the item
+// adds them in order, so the result does not depend on who is last.
+//
+// A warp owns every kWarps-th cell of the run: it asks for its cells kStages
+// ahead with bulk copies into a ring of its own, and never waits for another
+// warp before the end of an item. A cell is 2304 bytes at head_dim 128.
+//
+// Arithmetic. A 4-bit code q masked out of its word is the fp16 subnormal q *
+// 2^-24 (or q * 2^-20 for the upper nibble of a byte), which the tensor cores
+// multiply exactly, so codes become operands with one AND.
+//  scores: A = q (fp16 after the exact power-of-two prescale of its row), B =
+//    key codes without their - 8: a block's sum starts at -8 sum(q) instead
+//    (the sums are then within 8e-7 of a random row's score, measured), and is
+//    multiplied by the block's scale in fp32.
+//  values: A = value codes (transposed), here with the - 8 subtracted (exact in
+//    fp16), since a sum that only cancels would leave a rounding of 8 d p where
+//    the values met are zero; B = p * d for each block, rounded to fp16 twice
+//    (p, then the product: 2^-11 each, an eighth of the output's own rounding
+//    each); d is first brought near 1 by a power of two that follows the
+//    largest scale met, so fp16's range is no limit.
+// Softmax statistics, sums and outputs are fp32. A row's running maximum is
+// raised only when a score exceeds it by 2^kLazy, the outputs being rescaled
+// then.
 #include "kv.cuh"
 
 namespace moe {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int kAttThreads = 32 * kWarps;
+constexpr int kStages = 4;
+// fp16's range for the product p * d: a row's largest weight is 2^kOffset when
+// its maximum is set and may grow by 2^kLazy; the value blocks' scales are
+// multiplied by at most 2^kSigmaMax, to below 2^kTop when a new largest one is
+// met, and may grow by 2^kHeadroom. So a product is below 2^15, and weights down
+// to 2^-31 of the largest still count.
+constexpr float kLazy = 4.0f, kOffset = 11.0f;
+constexpr int kSigmaMax = 15, kTop = -4, kHeadroom = 4;
+constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
+constexpr float kLog2e = 1.4426950408889634f;
 
-// One warp per (row, query head): 32 positions at a time, a lane each for the
-// scores, then a lane per D / 32 dims for the values; running maximum and sum
-// in fp32.
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) k_attend(KvDev c, KvBatch b, const uint16_t* __restrict__ q, int64_t qs,
-                                                        int T, float scale, uint16_t* __restrict__ out) {
-    constexpr int G = D / 32;
+struct AttendArgs {
+    const uint16_t* q;
+    int64_t qs;
+    int T;
+    float scale;
+    uint16_t* out;
+    float* partial;       // [grid][2] records: first and last piece of each CTA
+    unsigned* arrived;    // [grid] pieces arrived at the item that starts in a CTA and ends elsewhere
+};
+
+// (q - 8) 2^-24 of the codes at bits 0-3 and 16-19, (q - 8) 2^-20 of those at 4-7 and 20-23, as fp16 pairs.
+__device__ __forceinline__ uint32_t centred_lo(uint32_t w) {
+    return h2_as_u32(__hadd2(u32_as_h2(w & 0x000f000fu), u32_as_h2(0x80088008u)));
+}
+__device__ __forceinline__ uint32_t centred_hi(uint32_t w) {
+    return h2_as_u32(__hadd2(u32_as_h2(w & 0x00f000f0u), u32_as_h2(0x80808080u)));
+}
+
+// What a sequence asks for. cells: of its context (one more than the table
+// has where the length is past it, so that the missing page is met).
+struct SeqWork {
+    int n, kv, cells, units, tiles;
+    long long work;
+};
+template <int NT>
+__device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, int T, int seq) {
+    SeqWork s;
+    const int t0 = min(max(__ldg(b.cu + seq), 0), T), t1 = min(max(__ldg(b.cu + seq + 1), 0), T);
+    s.n = max(t1 - t0, 0);
+    s.kv = __ldg(b.kv_lens + seq);
+    const long long cap = (long long)b.table_stride * c.page_tokens + 1;
+    s.cells = (int)((min((long long)max(s.kv, 0), cap) + kCellTokens - 1) / kCellTokens);
+    s.units = max(1, (s.cells + kWarps - 1) / kWarps);
+    s.tiles = (int)(((long long)s.n * (c.hq / c.hkv) + 8 * NT - 1) / (8 * NT));
+    s.work = (long long)s.units * c.hkv * s.tiles;
+    return s;
+}
+
+// A piece of an item: units [u0, u1) of (sequence, head, row tile).
+struct Piece {
+    int seq, head, tile, u0, u1;
+    SeqWork s;
+    long long x, prefix;  // number of its first unit, and of its sequence's first
+};
+
+// The piece that starts at unit x (x in seq's range), cut at `hi`.
+__device__ __forceinline__ void piece_at(Piece& p, long long x, long long hi) {
+    const long long off = x - p.prefix;
+    const long long item = off / p.s.units;
+    p.u0 = (int)(off - item * p.s.units);
+    p.u1 = (int)min((long long)p.s.units, p.u0 + (hi - x));
+    p.head = (int)(item / p.s.tiles);
+    p.tile = (int)(item - (long long)p.head * p.s.tiles);
+    p.x = x;
+}
+// Steps to the next piece; false at `hi`. Whole warps.
+template <int NT>
+__device__ __forceinline__ bool next_piece(Piece& p, long long hi, const KvDev& c, const KvBatch& b, int T, int lane) {
+    const long long x = p.x + (p.u1 - p.u0);
+    if (x >= hi) return false;
+    if (x >= p.prefix + p.s.work) {
+        p.prefix += p.s.work;
+        int s = p.seq + 1;
+        for (;; s += 32) {  // the next sequence with new tokens: there is one, since x < hi
+            const int e = min(s + lane, b.B - 1);
+            const bool has = s + lane < b.B && min(max(__ldg(b.cu + e + 1), 0), T) > min(max(__ldg(b.cu + e), 0), T);
+            const unsigned any = __ballot_sync(0xffffffffu, has);
+            if (any) { s += __ffs(any) - 1; break; }
+            if (s + 32 >= b.B) return false;
+        }
+        p.seq = s;
+        p.s = seq_work<NT>(c, b, T, s);
+    }
+    piece_at(p, x, hi);
+    return true;
+}
+
+// Cells of the piece that fall to warp w: (u0 + k) * kWarps + w, k below this.
+__device__ __forceinline__ int warp_cells(const Piece& p, int w) {
+    const int last = (p.s.cells - w + kWarps - 1) / kWarps;  // units in which the warp has a cell (cells >= 0)
+    return max(0, min(p.u1, last) - p.u0);
+}
+
+template <int D, int NT>
+struct AttSmem {
+    static constexpr int kRows = 8 * NT, kPad = D + 4;
+    alignas(128) uint8_t ring[kWarps][kStages][Cell<D>::kBytes];
+    float tree[kWarps / 2][kRows][kPad];
+    float m[kWarps][kRows], l[kWarps][kRows];
+    float mrow[kRows], lrow[kRows];
+    alignas(8) unsigned long long bar[kWarps][kStages];
+    long long wsum[kWarps];
+    Piece cur[kWarps], ask[kWarps];  // a warp's piece at work and the one it asks for: rarely read, so not in registers
+    long long prefix;
+    int seq, last;
+};
+
+constexpr int kPartFloats(int D) { return 16 * D + 32; }  // output rows, maxima, sums
+
+__device__ __forceinline__ void abar_init(uint32_t bar) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool abar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok;
+}
+__device__ __noinline__ bool abar_wait_long(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = globaltimer_ns();
+    for (unsigned it = 0; it < (1u << 26); ++it) {
+        if (abar_try(bar, parity)) return true;
+        if (globaltimer_ns() - t0 > kWaitNs) break;
+    }
+    return false;
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return h2_as_u32(__floats2half2_rn(lo, hi)); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a) {
+    constexpr int G = D / 32, kRows = 8 * NT;
     using C = Cell<D>;
-    __shared__ float q_s[kWarps][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x, h = blockIdx.y * kWarps + warp;
-    const int seq = seq_of_row(b.cu, b.B, t);
-    if (seq < 0 || h >= c.hq) return;
-    for (int d = lane; d < D; d += 32)
-        q_s[warp][d] = scale * __uint_as_float((uint32_t)q[(size_t)t * qs + (size_t)h * D + d] << 16);
-    __syncwarp();
-    const int seen = __ldg(b.kv_lens + seq) - (__ldg(b.cu + seq + 1) - t) + 1;
-    const int head = h / (c.hq / c.hkv);
-    float m = -INFINITY, l = 0.f, o[G] = {};
-    bool bad = false;
-    for (int p0 = 0; p0 < seen; p0 += 32) {
-        const int p = p0 + lane, tc = p & (kCellTokens - 1);
-        const uint8_t* cell = p < seen ? kv_cell<D>(c, b, seq, p, head) : nullptr;
-        bad |= p < seen && !cell;
-        float s = -INFINITY;
-        if (cell) {
-            s = 0.f;
+    extern __shared__ uint8_t raw[];
+    AttSmem<D, NT>& sm = *reinterpret_cast<AttSmem<D, NT>*>(raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, i = lane & 3;
+    const int group = c.hq / c.hkv;
+
+    // --- this CTA's run of units [lo, hi), and the sequence that lo falls in
+    if (lane < kStages) abar_init(smem_addr(&sm.bar[warp][lane]));
+    long long total = 0;
+    auto block_scan = [&](long long w, long long& incl, long long& sum) {
+        incl = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        if (lane == 31) sm.wsum[warp] = incl;
+        __syncthreads();
+        sum = 0;
+        long long before = 0;
+#pragma unroll
+        for (int w2 = 0; w2 < kWarps; ++w2) {
+            if (w2 == warp) before = sum;
+            sum += sm.wsum[w2];
+        }
+        incl += before;
+        __syncthreads();
+    };
+    if (b.B > kAttThreads) {
+        long long mine = 0;
+        for (int s = tid; s < b.B; s += kAttThreads) mine += seq_work<NT>(c, b, a.T, s).work;
+        long long incl;
+        block_scan(mine, incl, total);
+    }
+    long long lo = 0, hi = 0, base = 0;
+    long long ctas = 0;
+    for (int s0 = 0; s0 < b.B; s0 += kAttThreads) {
+        const int s = s0 + tid;
+        const long long w = s < b.B ? seq_work<NT>(c, b, a.T, s).work : 0;
+        long long incl, sum;
+        block_scan(w, incl, sum);
+        if (s0 == 0) {
+            if (b.B <= kAttThreads) total = sum;
+            ctas = min(total, (long long)gridDim.x);
+            if (blockIdx.x >= ctas) return;
+            lo = (long long)blockIdx.x * total / ctas;
+            hi = (long long)(blockIdx.x + 1) * total / ctas;
+        }
+        incl += base;
+        if (incl - w <= lo && lo < incl) {
+            sm.seq = s;
+            sm.prefix = incl - w;
+        }
+        base += sum;
+        if (base > lo) break;
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    __syncthreads();
+
+    // --- the warp's ring: `ask` is the piece being asked for, `p` the one at work
+    auto keep_piece = [&](Piece& to, const Piece& from) {
+        __syncwarp();
+        if (lane == 0) to = from;
+        __syncwarp();
+    };
+    int ask_n, ask_k = 0;
+    {
+        Piece p;
+        p.seq = sm.seq;
+        p.prefix = sm.prefix;
+        p.s = seq_work<NT>(c, b, a.T, p.seq);
+        piece_at(p, lo, hi);
+        ask_n = warp_cells(p, warp);
+        keep_piece(sm.cur[warp], p);
+        keep_piece(sm.ask[warp], p);
+    }
+    // steps a kept piece on; false (and the piece as it was) at the end of the run
+    auto step = [&](Piece& at) {
+        Piece p = at;
+        const bool there = next_piece<NT>(p, hi, c, b, a.T, lane);
+        if (there) keep_piece(at, p);
+        return there;
+    };
+    unsigned issued = 0, used = 0;
+    bool more = true, dead = false;
+    const uint8_t* addr = nullptr;
+    auto issue = [&]() {  // asks for the warp's next cell, if there is one
+        while (more && ask_k == ask_n) {
+            more = step(sm.ask[warp]);
+            ask_n = more ? warp_cells(sm.ask[warp], warp) : 0;
+            ask_k = 0;
+        }
+        if (!more) return;
+        if ((ask_k & 31) == 0) {
+            const int k = ask_k + lane;
+            const Piece& q = sm.ask[warp];
+            addr = k < ask_n ? kv_cell<D>(c, b, q.seq, ((q.u0 + k) * kWarps + warp) * kCellTokens, q.head) : nullptr;
+        }
+        if (lane == (ask_k & 31)) {
+            const int slot = issued % kStages;
+            const uint32_t bar = smem_addr(&sm.bar[warp][slot]);
+            if (addr) {
+                asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n" ::"r"(bar),
+                             "r"((uint32_t)C::kBytes)
+                             : "memory");
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                        smem_addr(sm.ring[warp][slot])),
+                    "l"(addr), "r"((uint32_t)C::kBytes), "r"(bar)
+                    : "memory");
+            } else {  // no such page: its values are NaN
+                atomicOr(c.err, 1u);
+                uint4* s = reinterpret_cast<uint4*>(sm.ring[warp][slot]);
+                for (int e = 0; e < C::kBytes / 16; ++e) s[e] = make_uint4(0, 0, 0, 0);
+                for (int e = C::kVs / 16; e < C::kBytes / 16; ++e) s[e] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.shared::cta.b64 st, [%0];\n}\n" ::"r"(bar) : "memory");
+            }
+        }
+        ++issued;
+        ++ask_k;
+    };
+#pragma unroll 1
+    for (int k = 0; k < kStages; ++k) issue();
+
+    for (bool any = true; any; any = step(sm.cur[warp])) {
+        const Piece& p = sm.cur[warp];
+        // --- rows of the piece: row r of the tile is query row tile * kRows + r of the head's n * group
+        const int t0 = min(max(__ldg(b.cu + p.seq), 0), a.T);
+        const int rows = (int)min((long long)kRows, (long long)p.s.n * group - (long long)p.tile * kRows);
+        uint32_t qa[G][2][2 * NT];  // A registers: k-step s, (a0, a2) of row g, then of row g + 8
+        float corr[G][NT], rf[NT];
+        int lim[NT];
+        int min_lim = 0x7fffffff;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = g + 8 * nt;
+            const long long row = (long long)p.tile * kRows + (r < rows ? r : 0);
+            const int tok = (int)(row / group), head = p.head * group + (int)(row - (long long)tok * group);
+            lim[nt] = p.s.kv - p.s.n + tok + 1;
+            min_lim = min(min_lim, lim[nt]);
+            uint4 u[G];
+            const uint16_t* src = a.q + (size_t)(t0 + tok) * a.qs + (size_t)head * D + 8 * i;
+            unsigned mx = 0;
+#pragma unroll
             for (int bl = 0; bl < G; ++bl) {
-                float a = 0.f;
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(cell + C::k_word(tc, i, bl));
-                    for (int j = 0; j < 4; ++j) {
-                        const float* qq = &q_s[warp][32 * bl + 8 * i + 2 * j];
-                        a += qq[0] * ((float)((w >> (4 * j)) & 15u) - 8.f) + qq[1] * ((float)((w >> (16 + 4 * j)) & 15u) - 8.f);
+                u[bl] = __ldg(reinterpret_cast<const uint4*>(src + 32 * bl));
+                mx = max(max(mx, bf16x2_absmax(u[bl].x)), max(bf16x2_absmax(u[bl].y), max(bf16x2_absmax(u[bl].z), bf16x2_absmax(u[bl].w))));
+            }
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const int sh = token_shift(mx);
+            const float f = pow2f(-sh);
+#pragma unroll
+            for (int bl = 0; bl < G; ++bl) {
+                const uint32_t w[4] = {u[bl].x, u[bl].y, u[bl].z, u[bl].w};
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x0 = __uint_as_float(w[j] << 16) * f, x1 = __uint_as_float(w[j] & 0xffff0000u) * f;
+                    const float k = (j & 1) ? 0.0625f : 1.0f;  // the upper nibbles' codes are 16 times larger
+                    const uint32_t h = pack_h2(x0 * k, x1 * k);
+                    const float2 back = __half22float2(u32_as_h2(h));
+                    sum += (back.x + back.y) * ((j & 1) ? 16.0f : 1.0f);
+                    qa[bl][j >> 1][2 * nt + (j & 1)] = h;
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                corr[bl][nt] = sum * (-8.0f / 16777216.0f);
+            }
+            rf[nt] = a.scale * kLog2e * 16777216.0f * pow2f(sh);
+        }
+        min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 4));
+        min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 8));
+        min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 16));
+
+        float o[G][2][NT][4] = {};   // c0, c1: dim 32 bl + 16 mu + g of rows 2i, 2i + 1; c2, c3: dim + 8, times 16
+        float m[NT], l[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) { m[nt] = -INFINITY; l[nt] = 0.f; }
+        int sigma = kSigmaMax;
+        __half2 up = __float2half2_rn(pow2f(kSigmaMax)), top = __float2half2_rn(pow2f(kTop + kHeadroom - kSigmaMax));
+
+        const int cells = warp_cells(p, warp), first = (p.u0 * kWarps + warp) * kCellTokens;
+#pragma unroll 1
+        for (int k = 0; k < cells; ++k) {
+            const int slot = used % kStages;
+            const uint32_t bar = smem_addr(&sm.bar[warp][slot]), parity = (used / kStages) & 1;
+            if (!dead && !abar_try(bar, parity) && !abar_wait_long(bar, parity)) dead = true;
+            dead = __any_sync(0xffffffffu, dead);
+            const uint8_t* cell = sm.ring[warp][slot];
+            uint32_t kw[2][G], ks[2][G], vw[2][G], vs[2][G];
+            auto load = [&](uint32_t (&r)[G], const uint8_t* src) {
+                if constexpr (G == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src);
+                    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(src);
+                    r[0] = v.x, r[1] = v.y;
+                }
+            };
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                load(kw[h], cell + (h * 32 + lane) * G * 4);
+                load(ks[h], cell + C::kKs + (h * 4 + i) * G * 4);
+                load(vw[h], cell + C::kV + (h * 32 + lane) * G * 4);
+                load(vs[h], cell + C::kVs + (h * 4 + i) * G * 4);
+            }
+            // scores of rows g (and g + 8), tokens 8h + 2i, + 1
+            float s[2][2 * NT];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int e = 0; e < 2 * NT; ++e) s[h][e] = 0.f;
+#pragma unroll
+                for (int bl = 0; bl < G; ++bl) {
+                    float acc[4] = {corr[bl][0], corr[bl][0], corr[bl][NT - 1], corr[bl][NT - 1]};
+                    const uint32_t w = kw[h][bl], w8 = w >> 8;
+                    const uint32_t a0[4] = {qa[bl][0][0], NT == 2 ? qa[bl][0][2 * NT - 2] : 0u, qa[bl][0][1], NT == 2 ? qa[bl][0][2 * NT - 1] : 0u};
+                    const uint32_t a1[4] = {qa[bl][1][0], NT == 2 ? qa[bl][1][2 * NT - 2] : 0u, qa[bl][1][1], NT == 2 ? qa[bl][1][2 * NT - 1] : 0u};
+                    mma_f16(acc, a0, w & 0x000f000fu, w & 0x00f000f0u);
+                    mma_f16(acc, a1, w8 & 0x000f000fu, w8 & 0x00f000f0u);
+                    const float2 d = __half22float2(u32_as_h2(ks[h][bl]));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        s[h][2 * nt] = fmaf(acc[2 * nt], d.x, s[h][2 * nt]);
+                        s[h][2 * nt + 1] = fmaf(acc[2 * nt + 1], d.y, s[h][2 * nt + 1]);
                     }
                 }
-                s += a * __half2float(*reinterpret_cast<const __half*>(cell + C::kKs + C::scale(tc, bl)));
+            }
+            const int pos0 = first + k * (kWarps * kCellTokens);
+            const bool masked = pos0 + kCellTokens > min_lim;
+            uint32_t keep[2][NT];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float &x0 = s[h][2 * nt], &x1 = s[h][2 * nt + 1];
+                    x0 *= rf[nt];
+                    x1 *= rf[nt];
+                    if (masked) {
+                        const int t = pos0 + 8 * h + 2 * i;
+                        keep[h][nt] = (t < lim[nt] ? 0xffffu : 0u) | (t + 1 < lim[nt] ? 0xffff0000u : 0u);
+                        if (t >= lim[nt]) x0 = -INFINITY;
+                        if (t + 1 >= lim[nt]) x1 = -INFINITY;
+                    }
+                }
+            // the running maximum, and the running scale of the value blocks
+            bool raise = false;
+            float mx[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float v = fmaxf(fmaxf(s[0][2 * nt], s[0][2 * nt + 1]), fmaxf(s[1][2 * nt], s[1][2 * nt + 1]));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                mx[nt] = v;
+                raise |= v > m[nt] + kLazy;
+            }
+            __half2 big = __habs2(u32_as_h2(vs[0][0]));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int bl = 0; bl < G; ++bl) big = __hmax2(big, __habs2(u32_as_h2(vs[h][bl])));
+            raise |= !__hble2(big, top);
+            if (__any_sync(0xffffffffu, raise)) {
+                unsigned bits = max(h2_as_u32(big) & 0x7fffu, (h2_as_u32(big) >> 16) & 0x7fffu);
+                if (bits > 0x7bffu) bits = 0;  // a NaN scale has no size
+                bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
+                bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
+                // 2^(e - 15) <= the largest scale < 2^(e - 14) (e = 0 below the normals)
+                const int e = (int)(bits >> 10), want = min(kSigmaMax, kTop - (e - 14));
+                float move = 1.f;
+                if (e - 14 + sigma > kTop + kHeadroom) {
+                    move = pow2f(want - sigma);
+                    sigma = want;
+                    up = __float2half2_rn(pow2f(sigma));
+                    top = __float2half2_rn(fminf(pow2f(kTop + kHeadroom - sigma), 65504.f));
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float mn = fmaxf(m[nt], mx[nt]);
+                    const float f = mn == m[nt] ? 1.f : ex2(m[nt] - mn);
+                    m[nt] = mn;
+                    l[nt] *= f;
+                    const float f0 = __shfl_sync(0xffffffffu, f, 8 * i) * move, f1 = __shfl_sync(0xffffffffu, f, 8 * i + 4) * move;
+#pragma unroll
+                    for (int bl = 0; bl < G; ++bl)
+#pragma unroll
+                        for (int mu = 0; mu < 2; ++mu) {
+                            o[bl][mu][nt][0] *= f0, o[bl][mu][nt][1] *= f1;
+                            o[bl][mu][nt][2] *= f0, o[bl][mu][nt][3] *= f1;
+                        }
+                }
+            }
+            uint32_t ph[2][NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float mm = (m[nt] == -INFINITY ? 0.f : m[nt]) - kOffset;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float e0 = ex2(s[h][2 * nt] - mm), e1 = ex2(s[h][2 * nt + 1] - mm);
+                    l[nt] += e0 + e1;
+                    ph[h][nt] = pack_h2(e0, e1);
+                }
+            }
+#pragma unroll
+            for (int bl = 0; bl < G; ++bl) {
+                uint32_t pb[2][NT];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const __half2 d = __hmul2(u32_as_h2(vs[h][bl]), up);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        pb[h][nt] = h2_as_u32(__hmul2(u32_as_h2(ph[h][nt]), d));
+                        if (masked) pb[h][nt] &= keep[h][nt];
+                    }
+                }
+                const uint32_t w0 = vw[0][bl], w1 = vw[1][bl], w08 = w0 >> 8, w18 = w1 >> 8;
+                const uint32_t v0[4] = {centred_lo(w0), centred_hi(w0), centred_lo(w1), centred_hi(w1)};
+                const uint32_t v1[4] = {centred_lo(w08), centred_hi(w08), centred_lo(w18), centred_hi(w18)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(o[bl][0][nt], v0, pb[0][nt], pb[1][nt]);
+                    mma_f16(o[bl][1][nt], v1, pb[0][nt], pb[1][nt]);
+                }
+            }
+            ++used;
+            __syncwarp();  // every lane has read the slot
+            if (!dead) issue();
+        }
+
+        // --- the warps' sums into one
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
+            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
+            if (dead) l[nt] = __int_as_float(0x7fc00000);
+            if (i == 0) {
+                sm.m[warp][g + 8 * nt] = m[nt];
+                sm.l[warp][g + 8 * nt] = l[nt];
             }
         }
-        float mx = s;
-        for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const float mn = fmaxf(m, mx);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float f = expf(m - base);
-        const float e = cell ? expf(s - base) : 0.f;
-        float sum = e;
-        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        l = l * f + sum;
-        m = mn;
-        for (int bl = 0; bl < G; ++bl) o[bl] *= f;
-        for (int j = 0; j < 32 && p0 + j < seen; ++j) {
-            const float pj = __shfl_sync(0xffffffffu, e, j);
-            const uint8_t* cj = kv_cell<D>(c, b, seq, p0 + j, head);
-            if (!cj) continue;
-            const int tj = (p0 + j) & (kCellTokens - 1);
-            for (int bl = 0; bl < G; ++bl) {  // dim 32 bl + lane = 32 bl + g + 8 i
-                const uint32_t w = *reinterpret_cast<const uint16_t*>(cj + C::kV + C::v_half(tj, lane & 7, bl));
-                const float d = __half2float(*reinterpret_cast<const __half*>(cj + C::kVs + C::scale(tj, bl)));
-                o[bl] += pj * (d * ((float)((w >> (4 * (lane >> 3))) & 15u) - 8.f));
+        __syncthreads();
+        if (tid < kRows) {
+            float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][tid]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) ll += sm.m[w][tid] == -INFINITY ? (sm.l[w][tid] != sm.l[w][tid] ? sm.l[w][tid] : 0.f)
+                                                                             : sm.l[w][tid] * ex2(sm.m[w][tid] - mm);
+            sm.mrow[tid] = mm;
+            sm.lrow[tid] = ll;
+        }
+        {
+            const float unit = pow2f(24) * pow2f(-sigma);  // codes are q * 2^-24, value scales d * 2^sigma
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * nt + 2 * i + e;
+                    float mm = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
+                    const float f = sm.m[warp][r] == -INFINITY ? 0.f : ex2(sm.m[warp][r] - mm) * unit;
+#pragma unroll
+                    for (int bl = 0; bl < G; ++bl)
+#pragma unroll
+                        for (int mu = 0; mu < 2; ++mu) {
+                            o[bl][mu][nt][e] = o[bl][mu][nt][e] * f;
+                            o[bl][mu][nt][2 + e] = o[bl][mu][nt][2 + e] * (f * 0.0625f);
+                        }
+                }
+        }
+#pragma unroll
+        for (int half = kWarps / 2; half >= 1; half >>= 1) {
+            if (warp >= half && warp < 2 * half) {
+#pragma unroll
+                for (int bl = 0; bl < G; ++bl)
+#pragma unroll
+                    for (int mu = 0; mu < 2; ++mu)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                sm.tree[warp - half][8 * nt + 2 * i + (e & 1)][32 * bl + 16 * mu + g + 8 * (e >> 1)] = o[bl][mu][nt][e];
+            }
+            __syncthreads();
+            if (warp < half) {
+#pragma unroll
+                for (int bl = 0; bl < G; ++bl)
+#pragma unroll
+                    for (int mu = 0; mu < 2; ++mu)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float& t = sm.tree[warp][8 * nt + 2 * i + (e & 1)][32 * bl + 16 * mu + g + 8 * (e >> 1)];
+                                o[bl][mu][nt][e] += t;
+                                if (half == 1) t = o[bl][mu][nt][e];
+                            }
+            }
+            __syncthreads();
+        }
+
+        // --- out, or to the item's other pieces
+        auto put = [&](int r, int d, float4 v, float mm, float ll) {
+            const float inv = 1.0f / ll;
+            float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = mm == -INFINITY && ll == 0.f ? 0.f : x[e] * inv;
+            const long long row = (long long)p.tile * kRows + r;
+            const int tok = (int)(row / group), head = p.head * group + (int)(row - (long long)tok * group);
+            __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0], x[1]), y1 = __floats2bfloat162_rn(x[2], x[3]);
+            *reinterpret_cast<uint2*>(a.out + ((size_t)(t0 + tok) * c.hq + head) * D + d) =
+                make_uint2(*reinterpret_cast<uint32_t*>(&y0), *reinterpret_cast<uint32_t*>(&y1));
+        };
+        const bool whole = p.u0 == 0 && p.u1 == p.s.units;
+        if (whole) {
+            for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
+                const int r = e / (D / 4), d = 4 * (e % (D / 4));
+                put(r, d, *reinterpret_cast<const float4*>(&sm.tree[0][r][d]), sm.mrow[r], sm.lrow[r]);
+            }
+        } else {
+            // CTAs that share the item: the one its first unit falls to .. the one its last falls to
+            const long long x0 = p.x - p.u0, x1 = x0 + p.s.units - 1;
+            const int c0 = (int)(((x0 + 1) * ctas - 1) / total), c1 = (int)(((x1 + 1) * ctas - 1) / total);
+            float* rec = a.partial + ((size_t)blockIdx.x * 2 + (p.u0 == 0 ? 1 : 0)) * kPartFloats(D);
+            for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
+                const int r = e / (D / 4), d = 4 * (e % (D / 4));
+                __stcg(reinterpret_cast<float4*>(rec + r * D + d), *reinterpret_cast<const float4*>(&sm.tree[0][r][d]));
+            }
+            if (tid < rows) {
+                __stcg(rec + 16 * D + tid, sm.mrow[tid]);
+                __stcg(rec + 16 * D + 16 + tid, sm.lrow[tid]);
+            }
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const unsigned n = atomicAdd(a.arrived + c0, 1u) + 1u;
+                sm.last = n == (unsigned)(c1 - c0 + 1);
+                if (sm.last) a.arrived[c0] = 0;  // for the next call
+            }
+            __syncthreads();
+            if (sm.last) {
+                __threadfence();
+                for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
+                    const int r = e / (D / 4), d = 4 * (e % (D / 4));
+                    float mm = -INFINITY, ll = 0.f;
+                    for (int cta = c0; cta <= c1; ++cta)
+                        mm = fmaxf(mm, __ldcg(a.partial + ((size_t)cta * 2 + (cta == c0)) * kPartFloats(D) + 16 * D + r));
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int cta = c0; cta <= c1; ++cta) {
+                        const float* q = a.partial + ((size_t)cta * 2 + (cta == c0)) * kPartFloats(D);
+                        const float qm = __ldcg(q + 16 * D + r), ql = __ldcg(q + 16 * D + 16 + r);
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
+                        const float f = qm == -INFINITY ? 0.f : ex2(qm - mm);
+                        ll += qm == -INFINITY ? (ql != ql ? ql : 0.f) : f * ql;
+                        v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+                    }
+                    put(r, d, v, mm, ll);
+                }
             }
         }
+        __syncthreads();  // tree, m and l are free again
     }
-    bad = __any_sync(0xffffffffu, bad);
-    if (bad && lane == 0) atomicOr(c.err, 1u);
-    for (int bl = 0; bl < G; ++bl) {
-        float r = l > 0.f || l != l ? o[bl] / l : 0.f;
-        if (bad) r = __int_as_float(0x7fc00000);
-        __nv_bfloat16 v = __float2bfloat16_rn(r);
-        out[((size_t)t * c.hq + h) * D + 32 * bl + lane] = *reinterpret_cast<uint16_t*>(&v);
+    if (dead) {
+        if (lane == 0) atomicOr(c.err, 2u);
+        for (; used < issued; ++used)  // nothing of this warp is in flight when it leaves
+            abar_wait_long(smem_addr(&sm.bar[warp][used % kStages]), (used / kStages) & 1);
     }
 }
 
-uint64_t attend_scratch_bytes(int) { return 0; }
+static int sm_count(int device) {
+    static int counts[64] = {};
+    if (device < 0 || device >= 64) return 152;
+    if (!counts[device]) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) n = 152;
+        counts[device] = n;
+    }
+    return counts[device];
+}
+static int max_grid(int device) { return 2 * sm_count(device); }
+
+// Partial records, then the arrival counters.
+uint64_t attend_scratch_bytes(int device) {
+    return (uint64_t)max_grid(device) * (2 * kPartFloats(128) * sizeof(float) + sizeof(unsigned));
+}
+
+template <int D, int NT>
+static void launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, int grid, cudaStream_t st) {
+    static bool set = false;
+    if (!set) {
+        cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT>));
+        set = true;
+    }
+    k_attend<D, NT><<<grid, kAttThreads, sizeof(AttSmem<D, NT>), st>>>(c, b, a);
+}
 
 void launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
-                   uint16_t* out, void*, cudaStream_t st) {
-    const dim3 grid((unsigned)T, (unsigned)((c.hq + kWarps - 1) / kWarps));
-    if (D == 128) k_attend<128><<<grid, 32 * kWarps, 0, st>>>(c, b, q, q_stride, T, scale, out);
-    else k_attend<64><<<grid, 32 * kWarps, 0, st>>>(c, b, q, q_stride, T, scale, out);
+                   uint16_t* out, void* scratch, cudaStream_t st) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int n = max_grid(dev);
+    AttendArgs a = {q, q_stride, T, scale, out, (float*)scratch,
+                    (unsigned*)((uint8_t*)scratch + (size_t)n * 2 * kPartFloats(128) * sizeof(float))};
+    // 16 rows at a time where a head has more than 8 rows in a step: group
+    // heads times the new tokens of an average sequence
+    const bool wide = (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
+    const int grid = wide ? sm_count(dev) : n;
+    if (D == 128) wide ? launch<128, 2>(c, b, a, grid, st) : launch<128, 1>(c, b, a, grid, st);
+    else wide ? launch<64, 2>(c, b, a, grid, st) : launch<64, 1>(c, b, a, grid, st);
 }
 
 }  // namespace moe
