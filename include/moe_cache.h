@@ -472,7 +472,7 @@ moe_status_t moe_kv_append(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
 
 /* Attention of the T newest tokens over the cache: row i of sequence b sees
  * the positions 0 .. its own, out = softmax(scale q k^T) v with the values
- * the cache holds; query head h reads key/value head h / (q_heads /
+ * the cache holds (scale finite, not negative); query head h reads key/value head h / (q_heads /
  * kv_heads). A row that sees no position is zero.
  *   q   : device bf16 rows [T] x q_heads x head_dim (rotated), q_stride apart
  *   out : device bf16 [T x q_heads x head_dim]
@@ -499,9 +499,11 @@ moe_status_t moe_kv_read(moe_kv_t* h, int32_t layer, int32_t T, const moe_kv_bat
  *   cu_q, cu_k : device int32 [num_seqs + 1], first entry 0, not decreasing,
  *             last ones at most Tq and Tk
  *   head_dim 64 or 128; q_heads a multiple of kv_heads, at most 128 times it
+ *   scale   : finite, not negative
  *   out     : device bf16 [Tq x q_heads x head_dim]
  * Runs on the current device, asynchronous on `stream`. MOE_ERR_INVALID for
- * bad arguments. Allocates nothing. */
+ * bad arguments. Allocates nothing. Should a bounded wait inside the kernel
+ * give up (0.2 s), the rows concerned come out as NaN. */
 moe_status_t moe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, int32_t Tq, int32_t Tk, int32_t num_seqs, const int32_t* cu_q,
                              const int32_t* cu_k, int32_t q_heads, int32_t kv_heads, int32_t head_dim, float scale,

@@ -407,6 +407,7 @@ moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
     if (const char* p = batch_problem(batch)) return refuse(p);
     if (T == 0) return MOE_OK;
     if (!q || !out) return refuse("NULL q or out");
+    if (!(scale >= 0.f && scale <= 3.4028235e38f)) return refuse("scale must be finite and not negative");
     if (!rows_ok(q, q_stride, c.q_heads, c.head_dim) || ((uintptr_t)out & 15u))
         return refuse("q and out need 16-byte aligned rows: q_stride a multiple of 8 and not below q_heads * head_dim");
     moe::launch_attend(dev_of(h, layer), batch_of(batch), c.head_dim, (const uint16_t*)q, q_stride, T, scale,
