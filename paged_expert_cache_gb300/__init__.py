@@ -389,10 +389,23 @@ class MoECache:
 # The attention half of a decoder layer: a paged key/value cache in Q4_0
 # blocks, attention over it, and attention of whole prompts.
 # ---------------------------------------------------------------------------
+_torch = None
+
+
+def _need_torch():
+    """The torch module, for the calls that take tensors (kept, so that a call
+    does not pay for the import statement)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _rows(name, t, heads, dim, rows=None):
     """Checks t as bf16 rows [T, heads, dim] (or [T, heads * dim]) on the
     current CUDA device, dense within a row; returns its row stride."""
-    import torch
+    torch = _need_torch()
     if not isinstance(t, torch.Tensor):
         _refuse(f"{name} must be a torch tensor")
     shape = t.shape
@@ -415,13 +428,30 @@ def _dense(name, t, heads, dim, rows):
 
 
 def _on_device(name, t):
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != _torch.cuda.current_device():
         _refuse(f"{name} must be on the current CUDA device")
 
 
+def _all_dense(bf16, *tensors):
+    """Whether every (tensor, shape) is a contiguous bf16 tensor of that shape
+    on the current CUDA device: the usual call, accepted in a few hundred
+    nanoseconds a tensor. Where it is false, _rows says what is wrong or finds
+    the strides."""
+    dev = -1
+    for t, shape in tensors:
+        if t is not None:
+            if t.shape != shape or t.dtype is not bf16 or not t.is_contiguous():
+                return False
+            d = t.get_device()
+            if d != dev:
+                if dev >= 0 or d < 0 or d != _torch.cuda.current_device():
+                    return False
+                dev = d
+    return True
+
+
 def _indexes(name, t, shape=None, dims=1):
-    import torch
+    torch = _need_torch()
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != dims or not t.is_contiguous():
         _refuse(f"{name} must be a contiguous int32 tensor of {dims} dimension(s)")
     if shape is not None and tuple(t.shape) != shape:
@@ -435,10 +465,9 @@ def _batch(batch):
     return batch._ref
 
 
-def _stream(stream):
+def _stream(stream, device):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        return _torch._C._cuda_getCurrentRawStream(device) or None
     return (stream if isinstance(stream, int) else stream.cuda_stream) or None
 
 
@@ -480,6 +509,8 @@ class KVCache:
         L = load()
         self.cfg = cfg
         self.h = None
+        self._dims, self._device = (cfg.q_heads, cfg.kv_heads, cfg.head_dim), cfg.device
+        _need_torch()
         h = vp()
         _check(L.moe_kv_create(ctypes.byref(cfg), ctypes.byref(h)))
         self.h = h.value
@@ -501,48 +532,65 @@ class KVCache:
         head_dim], cosines then sines; None: no rotation) and stored; q bf16
         [T, q_heads, head_dim] rotated into q_out (None: keys and values only).
         Returns q_out."""
-        c = self.cfg
+        hq, hkv, dim = self._dims
+        torch = _torch
+        if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor)):
+            _refuse("k and v must be torch tensors")
+        if q is not None and q_out is None:
+            _refuse("q needs q_out")
         T = k.shape[0]
-        ks = _rows("k", k, c.kv_heads, c.head_dim)
-        vs = _rows("v", v, c.kv_heads, c.head_dim, T)
-        qs = 0
-        if q is not None:
-            qs = _rows("q", q, c.q_heads, c.head_dim, T)
-            if q_out is None:
-                _refuse("q needs q_out")
-            _dense("q_out", q_out, c.q_heads, c.head_dim, T)
-        if k_out is not None:
-            _dense("k_out", k_out, c.kv_heads, c.head_dim, T)
+        qs, ks = hq * dim, hkv * dim
+        vs = ks
+        if not _all_dense(torch.bfloat16, (k, (T, hkv, dim)), (v, (T, hkv, dim)), (k_out, (T, hkv, dim)),
+                          (q, (T, hq, dim)), (q_out, (T, hq, dim))):
+            ks = _rows("k", k, hkv, dim)
+            vs = _rows("v", v, hkv, dim, T)
+            if q is not None:
+                qs = _rows("q", q, hq, dim, T)
+                _dense("q_out", q_out, hq, dim, T)
+            if k_out is not None:
+                _dense("k_out", k_out, hkv, dim, T)
+        rows = 0
         if rope is not None:
-            import torch
-            if rope.dtype is not torch.float32 or rope.dim() != 2 or rope.shape[1] != c.head_dim \
+            if rope.dtype is not torch.float32 or rope.dim() != 2 or rope.shape[1] != dim \
                     or not rope.is_contiguous() or not rope.shape[0]:
-                _refuse(f"rope must be contiguous float32 [positions, {c.head_dim}]")
+                _refuse(f"rope must be contiguous float32 [positions, {dim}]")
             _on_device("rope", rope)
-        _check(load().moe_kv_append(self.h, layer, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, _batch(batch),
-                                    _ptr(rope), 0 if rope is None else rope.shape[0],
-                                    None if q is None else q_out.data_ptr(), _ptr(k_out), _stream(stream)))
+            rows = rope.shape[0]
+        _check(_lib.moe_kv_append(self.h, layer, None if q is None else q.data_ptr(), qs, k.data_ptr(), ks,
+                                  v.data_ptr(), vs, T, _batch(batch), None if rope is None else rope.data_ptr(), rows,
+                                  None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
+                                  _stream(stream, self._device)))
         return q_out
 
     def attend(self, layer, q, batch, out, scale=None, stream=None):
         """moe_kv_attend: attention of the newest tokens, q bf16 [T, q_heads,
         head_dim] (rotated), into out. scale None: head_dim ** -0.5."""
-        c = self.cfg
-        qs = _rows("q", q, c.q_heads, c.head_dim)
+        hq, hkv, dim = self._dims
+        if not isinstance(q, _torch.Tensor) or not isinstance(out, _torch.Tensor):
+            _refuse("q and out must be torch tensors")
         T = q.shape[0]
-        _dense("out", out, c.q_heads, c.head_dim, T)
-        _check(load().moe_kv_attend(self.h, layer, q.data_ptr(), qs, T, _batch(batch),
-                                    c.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), _stream(stream)))
+        qs = hq * dim
+        if not _all_dense(_torch.bfloat16, (q, (T, hq, dim)), (out, (T, hq, dim))):
+            qs = _rows("q", q, hq, dim)
+            _dense("out", out, hq, dim, T)
+        _check(_lib.moe_kv_attend(self.h, layer, q.data_ptr(), qs, T, _batch(batch),
+                                  dim ** -0.5 if scale is None else scale, out.data_ptr(),
+                                  _stream(stream, self._device)))
         return out
 
     def read(self, layer, batch, k_out, v_out, stream=None):
         """moe_kv_read: the batch's rows of the cache as bf16 into k_out, v_out
         [T, kv_heads, head_dim]."""
-        c = self.cfg
+        hq, hkv, dim = self._dims
+        if not isinstance(k_out, _torch.Tensor) or not isinstance(v_out, _torch.Tensor):
+            _refuse("k_out and v_out must be torch tensors")
         T = k_out.shape[0]
-        _dense("k_out", k_out, c.kv_heads, c.head_dim, T)
-        _dense("v_out", v_out, c.kv_heads, c.head_dim, T)
-        _check(load().moe_kv_read(self.h, layer, T, _batch(batch), k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
+        if not _all_dense(_torch.bfloat16, (k_out, (T, hkv, dim)), (v_out, (T, hkv, dim))):
+            _dense("k_out", k_out, hkv, dim, T)
+            _dense("v_out", v_out, hkv, dim, T)
+        _check(_lib.moe_kv_read(self.h, layer, T, _batch(batch), k_out.data_ptr(), v_out.data_ptr(),
+                                _stream(stream, self._device)))
         return k_out, v_out
 
     def info(self):
@@ -559,16 +607,20 @@ def attention_prompt(q, k, v, out, cu_q, cu_k=None, scale=None, stream=None):
     """moe_attn_prompt: causal attention of packed prompts, q bf16 [Tq, q_heads,
     D], k and v bf16 [Tk, kv_heads, D], out [Tq, q_heads, D]; cu_q, cu_k int32
     [B + 1] (cu_k None: cu_q). scale None: D ** -0.5. Returns out."""
-    import torch
-    for name, t in (("q", q), ("k", k), ("v", v)):
+    torch = _need_torch()
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
             _refuse(f"{name} must be a torch tensor [T, heads, head_dim]")
     Tq, hq, dim = q.shape
-    Tk, hkv = k.shape[:2]
-    qs = _rows("q", q, hq, dim)
-    ks = _rows("k", k, hkv, dim)
-    vs = _rows("v", v, hkv, dim, Tk)
-    _dense("out", out, hq, dim, Tq)
+    Tk, hkv, _ = k.shape
+    qs, ks = hq * dim, hkv * dim
+    vs = ks
+    if not _all_dense(torch.bfloat16, (q, (Tq, hq, dim)), (out, (Tq, hq, dim)), (k, (Tk, hkv, dim)),
+                      (v, (Tk, hkv, dim))):
+        qs = _rows("q", q, hq, dim)
+        ks = _rows("k", k, hkv, dim)
+        vs = _rows("v", v, hkv, dim, Tk)
+        _dense("out", out, hq, dim, Tq)
     _indexes("cu_q", cu_q)
     B = cu_q.shape[0] - 1
     if cu_k is None:
@@ -577,5 +629,5 @@ def attention_prompt(q, k, v, out, cu_q, cu_k=None, scale=None, stream=None):
         _indexes("cu_k", cu_k, (B + 1,))
     _check(load().moe_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, Tq, Tk, B, cu_q.data_ptr(),
                                   cu_k.data_ptr(), hq, hkv, dim, dim ** -0.5 if scale is None else scale,
-                                  out.data_ptr(), _stream(stream)))
+                                  out.data_ptr(), _stream(stream, q.get_device())))
     return out

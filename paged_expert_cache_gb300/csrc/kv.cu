@@ -407,6 +407,7 @@ moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
     if (const char* p = batch_problem(batch)) return refuse(p);
     if (T == 0) return MOE_OK;
     if (!q || !out) return refuse("NULL q or out");
+    if ((int64_t)T * (c.q_heads / c.kv_heads) > 0x7fff0000ll) return refuse("T is too large");
     if (!(scale >= 0.f && scale <= 3.4028235e38f)) return refuse("scale must be finite and not negative");
     if (!rows_ok(q, q_stride, c.q_heads, c.head_dim) || ((uintptr_t)out & 15u))
         return refuse("q and out need 16-byte aligned rows: q_stride a multiple of 8 and not below q_heads * head_dim");

@@ -70,6 +70,13 @@ __device__ __forceinline__ uint32_t centred_hi(uint32_t w) {
     return h2_as_u32(__hadd2(u32_as_h2(w & 0x00f000f0u), u32_as_h2(0x80808080u)));
 }
 
+// a / b for a >= 0, b > 0: nearly always both fit 32 bits, where a division
+// takes a fraction of the 64-bit one's time.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if ((((unsigned long long)a | (unsigned long long)b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+
 // What a sequence asks for. cells: of its context (one more than the table
 // has where the length is past it, so that the missing page is met).
 struct SeqWork {
@@ -83,9 +90,9 @@ __device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, in
     s.n = max(t1 - t0, 0);
     s.kv = __ldg(b.kv_lens + seq);
     const long long cap = (long long)b.table_stride * c.page_tokens + 1;
-    s.cells = (int)((min((long long)max(s.kv, 0), cap) + kCellTokens - 1) / kCellTokens);
+    s.cells = (int)((unsigned)((int)min((long long)max(s.kv, 0), cap) + kCellTokens - 1) / kCellTokens);
     s.units = max(1, (s.cells + kWarps - 1) / kWarps);
-    s.tiles = (int)(((long long)s.n * (c.hq / c.hkv) + 8 * NT - 1) / (8 * NT));
+    s.tiles = (s.n * (c.hq / c.hkv) + 8 * NT - 1) / (8 * NT);  // rows fit 31 bits
     s.work = (long long)s.units * c.hkv * s.tiles;
     return s;
 }
@@ -100,10 +107,10 @@ struct Piece {
 // The piece that starts at unit x (x in seq's range), cut at `hi`.
 __device__ __forceinline__ void piece_at(Piece& p, long long x, long long hi) {
     const long long off = x - p.prefix;
-    const long long item = off / p.s.units;
+    const long long item = quotient(off, p.s.units);
     p.u0 = (int)(off - item * p.s.units);
     p.u1 = (int)min((long long)p.s.units, p.u0 + (hi - x));
-    p.head = (int)(item / p.s.tiles);
+    p.head = (int)quotient(item, p.s.tiles);
     p.tile = (int)(item - (long long)p.head * p.s.tiles);
     p.x = x;
 }
@@ -228,8 +235,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             if (b.B <= kAttThreads) total = sum;
             ctas = min(total, (long long)gridDim.x);
             if (blockIdx.x >= ctas) return;
-            lo = (long long)blockIdx.x * total / ctas;
-            hi = (long long)(blockIdx.x + 1) * total / ctas;
+            lo = quotient((long long)blockIdx.x * total, ctas);
+            hi = quotient((long long)(blockIdx.x + 1) * total, ctas);
         }
         incl += base;
         if (incl - w <= lo && lo < incl) {
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         const Piece& p = sm.cur[warp];
         // --- rows of the piece: row r of the tile is query row tile * kRows + r of the head's n * group
         const int t0 = min(max(__ldg(b.cu + p.seq), 0), a.T);
-        const int rows = (int)min((long long)kRows, (long long)p.s.n * group - (long long)p.tile * kRows);
+        const int rows = min(kRows, p.s.n * group - p.tile * kRows);
         uint32_t qa[G][2][2 * NT];  // A registers: k-step s, (a0, a2) of row g, then of row g + 8
         float corr[G][NT], rf[NT];
         int lim[NT];
@@ -320,8 +327,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = g + 8 * nt;
-            const long long row = (long long)p.tile * kRows + (r < rows ? r : 0);
-            const int tok = (int)(row / group), head = p.head * group + (int)(row - (long long)tok * group);
+            const int row = p.tile * kRows + (r < rows ? r : 0);
+            const int tok = (int)((unsigned)row / (unsigned)group), head = p.head * group + row - tok * group;
             lim[nt] = p.s.kv - p.s.n + tok + 1;
             min_lim = min(min_lim, lim[nt]);
             uint4 u[G];
@@ -593,8 +600,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = mm == -INFINITY && ll == 0.f ? 0.f : x[e] * inv;
-            const long long row = (long long)p.tile * kRows + r;
-            const int tok = (int)(row / group), head = p.head * group + (int)(row - (long long)tok * group);
+            const int row = p.tile * kRows + r;
+            const int tok = (int)((unsigned)row / (unsigned)group), head = p.head * group + row - tok * group;
             __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0], x[1]), y1 = __floats2bfloat162_rn(x[2], x[3]);
             *reinterpret_cast<uint2*>(a.out + ((size_t)(t0 + tok) * c.hq + head) * D + d) =
                 make_uint2(*reinterpret_cast<uint32_t*>(&y0), *reinterpret_cast<uint32_t*>(&y1));
@@ -608,7 +615,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         } else {
             // CTAs that share the item: the one its first unit falls to .. the one its last falls to
             const long long x0 = p.x - p.u0, x1 = x0 + p.s.units - 1;
-            const int c0 = (int)(((x0 + 1) * ctas - 1) / total), c1 = (int)(((x1 + 1) * ctas - 1) / total);
+            const int c0 = (int)quotient((x0 + 1) * ctas - 1, total), c1 = (int)quotient((x1 + 1) * ctas - 1, total);
             float* rec = a.partial + ((size_t)blockIdx.x * 2 + (p.u0 == 0 ? 1 : 0)) * kPartFloats(D);
             for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
                 const int r = e / (D / 4), d = 4 * (e % (D / 4));
