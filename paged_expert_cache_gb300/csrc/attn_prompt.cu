@@ -82,13 +82,15 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok;
 }
-__device__ __noinline__ void bar_wait_long(uint32_t bar, uint32_t parity, int* dead) {
-    if (*(volatile int*)dead) return;  // another wait of this CTA gave up: nobody waits any more
-    if (!gbar_wait(bar, parity)) *(volatile int*)dead = 1;
-}
-// Waits for the phase; a wait that gives up marks the CTA, whose rows come out as NaN.
+// Waits for the phase; a wait that gives up marks the CTA, whose rows come out
+// as NaN and whose other waits give up at once.
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, int* dead) {
-    if (!bar_try(bar, parity)) bar_wait_long(bar, parity, dead);
+    if (bar_try(bar, parity)) return;
+    const unsigned long long t0 = globaltimer_ns();
+    while (!bar_try(bar, parity)) {
+        if (*(volatile int*)dead) return;
+        if (globaltimer_ns() - t0 > kGWaitNs) *(volatile int*)dead = 1;
+    }
 }
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -145,6 +147,22 @@ __device__ __forceinline__ float ex2f(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 operations in one instruction (pairs in 64-bit registers).
+__device__ __forceinline__ unsigned long long pair2(float lo, float hi) {
+    return (unsigned long long)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float lo2(unsigned long long v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(unsigned long long v) { return __uint_as_float((uint32_t)(v >> 32)); }
 __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&p);
@@ -260,6 +278,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
         const int seen_by_all = max(min(shift + i0 + 1, lk), 0);  // keys below this are seen by every row
         const int first_masked = seen_by_all / kTile;             // first key tile with a value to be cleaned
 
+        // Registers: the launch gives 168 a thread (64512 in all); the softmax
+        // warpgroups hold a row of scores each and take 208, the third 88.
+        if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
         if (warp == 8) {
             if (lane == 0) {
                 for (int x = 0; x < 2; ++x) {
@@ -330,7 +352,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                 const int e = 2 * n - 1;
                 bar_wait(gsmem(&sm.empty[e % kStages]), (e / kStages) & 1, dead);
             }
-        } else if (warp >= 10) {
+        } else {
             for (int j = first_masked; j < n; ++j) {
                 const int e = 2 * j + 1, st = e % kStages;
                 bar_wait(gsmem(&sm.dirty), (j - first_masked) & 1, dead);
@@ -355,7 +377,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                 fence_async_smem();
                 bar_arrive(gsmem(&sm.clean));
             }
+        }
         } else {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
             // --- softmax of tile x, a thread per row
             const int x = warp >> 2, nx = x ? n1 : n0, row = tid & 127;
             const int tok = row / group, i = i0 + x * tokens + tok;
@@ -381,11 +405,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                         for (int e = 0; e < 32; ++e)
                             if (32 * h + e >= left) s[h][e] = 0xff800000u;
                 }
-                float mx = m;
+                float mx4[4] = {m, m, m, m};
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1])));
+                    for (int e = 0; e < 32; e += 2)
+                        mx4[(e >> 1) & 3] = fmaxf(mx4[(e >> 1) & 3], fmaxf(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1])));
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 const bool raise = (mx - m) * a.c > kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
                     // S of this step was computed after the last step's O, so O is at rest
@@ -405,20 +431,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     }
                 }
                 const float mc = m == -INFINITY ? 0.f : m * a.c;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const unsigned long long c2 = pair2(a.c, a.c), mc2 = pair2(-mc, -mc);
+                unsigned long long sum[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t p[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const float e0 = ex2f(fmaf(__uint_as_float(s[2 * h + (e >> 4)][(2 * e) & 31]), a.c, -mc));
-                        const float e1 = ex2f(fmaf(__uint_as_float(s[2 * h + (e >> 4)][(2 * e + 1) & 31]), a.c, -mc));
-                        sum[e & 3] += e0 + e1;
+                        const uint32_t* z = &s[2 * h + (e >> 4)][(2 * e) & 31];
+                        const unsigned long long y = fma2(pair2(__uint_as_float(z[0]), __uint_as_float(z[1])), c2, mc2);
+                        const float e0 = ex2f(lo2(y)), e1 = ex2f(hi2(y));
+                        sum[e & 3] = add2(sum[e & 3], pair2(e0, e1));
                         p[e] = pack_bf(e0, e1);
                     }
                     tc_st32(ts + 32 * h, p);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                l += lo2(sum[0]) + hi2(sum[0]);
                 tc_st_wait();
                 tc_fence_before();
                 bar_arrive(gsmem(&sm.p_full[x]));
