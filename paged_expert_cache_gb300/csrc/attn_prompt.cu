@@ -142,6 +142,13 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
     return d;
 }
 
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(yes));
+    return yes;
+}
+
 __device__ __forceinline__ float ex2f(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -302,51 +309,69 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                 }
             }
         } else if (warp == 9) {
-            if (lane == 0 && n > 0) {
+            // The whole warp walks the loop and one lane issues, so that the
+            // operands stay in uniform registers; descriptors are one base each
+            // plus constants.
+            if (n > 0) {
                 constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false), id_o = idesc_bf16(kTile, D, true);
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+                const bool leader = elect_one();
+                const uint64_t qd = tc_sdesc(gsmem(sm.q[0])), kd = tc_sdesc(gsmem(sm.kv[0])), vd = sdesc_mn(gsmem(sm.kv[0]));
+                constexpr uint64_t kTileStep = S::kTileBytes >> 4;  // to the next tile, in a descriptor
                 auto scores = [&](int x, int st) {
-                    const uint32_t qa = gsmem(sm.q[x]), ka = gsmem(sm.kv[st]);
+                    const uint64_t qx = qd + x * kTileStep, kx = kd + st * kTileStep;
 #pragma unroll
                     for (int d = 0; d < D / 16; ++d) {
-                        const uint32_t off = (d / 4) * kHalf + (d % 4) * 32;
-                        tc_mma(tmem + x * kTile, tc_sdesc(qa + off), tc_sdesc(ka + off), id_s, d != 0);
+                        const uint32_t off = ((d / 4) * kHalf + (d % 4) * 32) >> 4;
+                        tc_mma(tm + x * kTile, qx + off, kx + off, id_s, d != 0);
                     }
                     tc_commit(gsmem(&sm.s_full[x]));
                 };
                 auto values = [&](int x, int st, bool first) {
-                    const uint32_t va = gsmem(sm.kv[st]);
+                    const uint64_t vx = vd + st * kTileStep;
 #pragma unroll
                     for (int t = 0; t < kTile / 16; ++t)
-                        tc_mma_ta(tmem + 2 * kTile + x * D, tmem + x * kTile + 8 * t, sdesc_mn(va + t * 2048), id_o, !(first && t == 0));
+                        tc_mma_ta(tm + 2 * kTile + x * D, tm + x * kTile + 8 * t, vx + t * (2048 >> 4), id_o, t == 0 ? !first : 1);
                 };
                 bar_wait(gsmem(&sm.full[0]), 0, dead);
-                tc_fence_after();
                 for (int x = 0; x < 2; ++x) {
                     if ((x ? n1 : n0) == 0) continue;
                     bar_wait(gsmem(&sm.q_full[x]), 0, dead);
-                    scores(x, 0);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (leader) scores(x, 0);
                 }
-                tc_commit(gsmem(&sm.empty[0]));
+                if (leader) tc_commit(gsmem(&sm.empty[0]));
+                int sv = 1, sk = 2;               // stages of V_j and K_(j + 1), and their rounds' parities
+                uint32_t pv = 0, pk = 0;
                 for (int j = 0; j < n; ++j) {
-                    const int ev = 2 * j + 1, ek = 2 * j + 2, sv = ev % kStages, sk = ek % kStages;
-                    bar_wait(gsmem(&sm.full[sv]), (ev / kStages) & 1, dead);
-                    if (j >= first_masked) bar_arrive(gsmem(&sm.dirty));  // the cleaning warps cannot tell the ring's rounds apart
-                    if (j + 1 < n) bar_wait(gsmem(&sm.full[sk]), (ek / kStages) & 1, dead);
+                    bar_wait(gsmem(&sm.full[sv]), pv, dead);
+                    // the cleaning warps cannot tell the ring's rounds apart
+                    if (j >= first_masked && leader) bar_arrive(gsmem(&sm.dirty));
+                    if (j + 1 < n) bar_wait(gsmem(&sm.full[sk]), pk, dead);
+                    if (*(volatile int*)dead) break;
+#pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int nx = x ? n1 : n0;
                         if (j < nx) {
                             bar_wait(gsmem(&sm.p_full[x]), j & 1, dead);
                             if (j >= first_masked) bar_wait(gsmem(&sm.clean), (j - first_masked) & 1, dead);
+                            __syncwarp();
                             tc_fence_after();
-                            if (*(volatile int*)dead) break;
-                            values(x, sv, j == 0);
-                            if (j + 1 == nx) tc_commit(gsmem(&sm.o_full[x]));
-                            else scores(x, sk);
+                            if (leader) {
+                                values(x, sv, j == 0);
+                                if (j + 1 == nx) tc_commit(gsmem(&sm.o_full[x]));
+                                else scores(x, sk);
+                            }
                         }
                     }
-                    if (*(volatile int*)dead) break;
-                    tc_commit(gsmem(&sm.empty[sv]));
-                    if (j + 1 < n) tc_commit(gsmem(&sm.empty[sk]));
+                    if (leader) {
+                        tc_commit(gsmem(&sm.empty[sv]));
+                        if (j + 1 < n) tc_commit(gsmem(&sm.empty[sk]));
+                    }
+                    sv += 2, sk += 2;
+                    if (sv >= kStages) sv -= kStages, pv ^= 1;
+                    if (sk >= kStages) sk -= kStages, pk ^= 1;
                 }
                 // the last arrivals, so that none is under way when the CTA ends
                 const int e = 2 * n - 1;
