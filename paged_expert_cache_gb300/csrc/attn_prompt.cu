@@ -11,16 +11,20 @@
 // tiles and runs them through the tensor cores in turn, so that the softmax of
 // one overlaps the products of the other:
 //   warps 0-3, 4-7  softmax of tile 0, 1: a thread per row, scores from tensor
-//                   memory, weights back to it as bf16 over the scores
-//   warp 8          TMA loads: the two query tiles, then K0 V0 K1 V1 ... into a
-//                   ring of 128-key stages (128-byte swizzle)
-//   warp 9          issues the MMAs: S = Q K^T (both from shared memory), and
-//                   O += P V (P from tensor memory, V as the MN-major operand)
-//   warps 10, 11    the values that some row of the CTA does not see: those past
-//                   the sequence's keys are set to zero, and infinities and NaN
-//                   behind the diagonal are replaced by zero (0 * inf would
-//                   reach every row) and added to the rows that do see them at
-//                   the end
+//                   memory, weights back to it as bf16 over the scores, 64 keys
+//                   at a time
+//   warp 8          items and TMA loads: the two query tiles, then K0 V0 K1 V1 ...
+//                   into a ring of 128-key stages (128-byte swizzle)
+//   warps 9, 10     issue the MMAs of tile 0, 1: S = Q K^T (both from shared
+//                   memory), and O += P V (P from tensor memory, V as the
+//                   MN-major operand)
+// CTAs are persistent: one that has finished its pair of tiles takes the work
+// of a CTA that has not started (cluster launch control), so that the next
+// pair's loads and scores run under the last one's outputs.
+// Values that some row of a CTA does not see are cleaned in shared memory
+// before use: those past the sequence's keys are set to zero, and infinities
+// and NaN behind the diagonal are replaced by zero (0 * inf would reach every
+// row) and added to the rows that do see them at the end.
 // Tensor memory: S0 S1 (128 columns each) and O0 O1 (head_dim each), fp32.
 // Weights are bf16 (the tensor cores take one type for both operands, and the
 // values are bf16): an error of the size of the output's own rounding. Maxima
@@ -49,6 +53,16 @@ struct PromptArgs {
     uint16_t* out;
 };
 
+// One item of work: two neighbouring query tiles of a sequence and head.
+struct Item {
+    int q0, lq;   // the sequence's first query row, and its queries
+    int k0, lk;   // its first key row, and its keys
+    int i0, head; // the first token of the pair of tiles; the key/value head
+    int end;      // no item: the CTA's work is done
+};
+
+constexpr int kTable = 256;  // entries of the table of pairs of tiles before a run of sequences
+
 template <int D>
 struct PromptSmem {
     static constexpr int kHalves = D / 64;                 // 64-dim halves of a tile: one swizzled row each
@@ -56,10 +70,15 @@ struct PromptSmem {
     static constexpr int kStages = D == 128 ? 5 : 8;
     uint8_t q[2][kTileBytes];
     uint8_t kv[kStages][kTileBytes];
-    unsigned long long q_full[2], full[kStages], empty[kStages];
-    unsigned long long s_full[2], p_full[2], o_full[2], dirty, clean;
-    int seq_sum[kPromptThreads / 32];
-    int total, seq, pair, flag, dead;
+    ulonglong2 answer;  // of the launch-control request
+    unsigned long long q_full[2], q_empty[2], full[kStages], empty[kStages];
+    unsigned long long s_full[2], p_full[2][2], o_full[2], clean;
+    unsigned long long item_full[2], item_empty[2], asked;
+    Item item[2];
+    int flag[2];        // number of the last item (of each parity) with infinities or NaN among its cleaned values, + 1
+    int prefix[kTable], total;
+    int wsum[kTable / 32];
+    int dead;
     uint32_t tmem;
 };
 
@@ -82,15 +101,39 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok;
 }
-// Waits for the phase; a wait that gives up marks the CTA, whose rows come out
-// as NaN and whose other waits give up at once.
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, int* dead) {
+// Waits for the phase. A wait that gives up marks the CTA, whose rows come out
+// as NaN and whose other waits give up at once, but for those on the items
+// themselves (`always`), which keep their own limit.
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, int* dead, bool always = false) {
     if (bar_try(bar, parity)) return;
     const unsigned long long t0 = globaltimer_ns();
     while (!bar_try(bar, parity)) {
-        if (*(volatile int*)dead) return;
-        if (globaltimer_ns() - t0 > kGWaitNs) *(volatile int*)dead = 1;
+        if (!always && *(volatile int*)dead) return;
+        if (globaltimer_ns() - t0 > kGWaitNs) {
+            *(volatile int*)dead = 1;
+            return;
+        }
     }
+}
+
+// Launch control: asks for the next CTA of the grid that has not started, to
+// run its work here instead. The answer lands in shared memory.
+__device__ __forceinline__ void ask_next_cta(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(answer),
+                 "r"(bar)
+                 : "memory");
+}
+// The CTA that the answer gives, or -1.
+__device__ __forceinline__ int next_cta(uint32_t answer) {
+    uint32_t yes, x;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b128 r;\nld.shared.b128 r, [%2];\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+        : "=r"(yes), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    return yes ? (int)x : -1;
 }
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -122,6 +165,38 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32])
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+// 8 columns of this thread's lane, loaded and waited for; and stored.
+__device__ __forceinline__ void tc_ld8_wait(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\ntcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// Waits for this thread's tensor-memory loads, the one into r among them: its
+// registers are operands, so that no use of them moves before the wait.
+__device__ __forceinline__ void tc_ld_wait32(uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+        "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]),
+        "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        :
         : "memory");
 }
 __device__ __forceinline__ void tc_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
@@ -183,6 +258,38 @@ __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
     return w;
 }
 
+// max of three in one instruction
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// The values of a key tile that some row of the CTA does not see (keys from
+// `from` on): infinities and NaN to zero, and everything from key `end` on. One
+// of 128 threads' share; true if it found some.
+template <int D>
+__device__ __forceinline__ bool clean_values(uint8_t* tile, int t, int from, int end) {
+    constexpr int kChunks = D / 8;  // 16-byte chunks of a key's values
+    from = max(from, 0);
+    end = min(max(end, 0), kTile);
+    bool found = false;
+#pragma unroll 2
+    for (int w = t + from * kChunks; w < kTile * kChunks; w += 128) {
+        const int r = w / kChunks, cc = w % kChunks;
+        uint4* at = reinterpret_cast<uint4*>(tile + (cc >> 3) * (kTile * 128) + r * 128 + (((cc ^ r) & 7) << 4));
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (r < end) {
+            u = *at;
+            if (!(any_nonfinite(u.x) || any_nonfinite(u.y) || any_nonfinite(u.z) || any_nonfinite(u.w))) continue;
+            found = true;
+            u = make_uint4(drop_nonfinite(u.x), drop_nonfinite(u.y), drop_nonfinite(u.z), drop_nonfinite(u.w));
+        }
+        *at = u;
+    }
+    return found;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, const __grid_constant__ CUtensorMap mq,
                                                               const __grid_constant__ CUtensorMap mk,
@@ -193,235 +300,346 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
     S& sm = *reinterpret_cast<S*>(raw + (((gsmem(raw) + 1023u) & ~1023u) - gsmem(raw)));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = a.hq / a.hkv, tokens = kTile / group;  // tokens of a tile
-    const int head = blockIdx.x % a.hkv, which = blockIdx.x / a.hkv;
 
-    if (warp == 8) {
-        tc_alloc(gsmem(&sm.tmem), 512);
-        tc_relinquish();
-    }
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            bar_init_n(gsmem(&sm.q_full[i]), 1);
-            bar_init_n(gsmem(&sm.s_full[i]), 1);
-            bar_init_n(gsmem(&sm.p_full[i]), 128);
-            bar_init_n(gsmem(&sm.o_full[i]), 1);
-        }
-        for (int i = 0; i < kStages; ++i) {
-            bar_init_n(gsmem(&sm.full[i]), 1);
-            bar_init_n(gsmem(&sm.empty[i]), 1);
-        }
-        bar_init_n(gsmem(&sm.dirty), 1);
-        bar_init_n(gsmem(&sm.clean), 64);
-        sm.flag = 0;
-        sm.dead = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    }
-    // --- which pair of tiles: the sequences' pairs are numbered in order, and
-    // the CTAs take them from the last, so that a sequence's longest run first
+    // --- the table: pairs of tiles before sequence t * run
+    const int run = (a.B + kTable - 1) / kTable;
     auto pairs_of = [&](int s) {
         const int n = min(max(__ldg(a.cu_q + s + 1), 0), a.Tq) - min(max(__ldg(a.cu_q + s), 0), a.Tq);
         return n > 0 ? (n + 2 * tokens - 1) / (2 * tokens) : 0;
     };
-    auto scan = [&](int w, int& incl, int& sum) {
-        incl = w;
+    int incl = 0, mine = 0;
+    if (warp < kTable / 32) {
+        for (int s = tid * run; s < min((tid + 1) * run, a.B); ++s) mine += pairs_of(s);
+        incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += v;
         }
-        if (lane == 31) sm.seq_sum[warp] = incl;
-        __syncthreads();
-        sum = 0;
-        int before = 0;
-#pragma unroll
-        for (int w2 = 0; w2 < kPromptThreads / 32; ++w2) {
-            if (w2 == warp) before = sum;
-            sum += sm.seq_sum[w2];
+        if (lane == 31) sm.wsum[warp] = incl;
+    } else if (warp == 8) {
+        tc_alloc(gsmem(&sm.tmem), 512);
+        tc_relinquish();
+    } else if (warp == 9) {
+        if (lane == 0) {
+            for (int x = 0; x < 2; ++x) {
+                bar_init_n(gsmem(&sm.q_full[x]), 1);
+                bar_init_n(gsmem(&sm.q_empty[x]), 1);
+                bar_init_n(gsmem(&sm.s_full[x]), 1);
+                bar_init_n(gsmem(&sm.p_full[x][0]), 128);
+                bar_init_n(gsmem(&sm.p_full[x][1]), 128);
+                bar_init_n(gsmem(&sm.o_full[x]), 1);
+                bar_init_n(gsmem(&sm.item_full[x]), 1);
+                bar_init_n(gsmem(&sm.item_empty[x]), 10);  // the softmax and MMA warps
+                sm.flag[x] = 0;
+            }
+            for (int st = 0; st < kStages; ++st) {
+                bar_init_n(gsmem(&sm.full[st]), 1);
+                bar_init_n(gsmem(&sm.empty[st]), 2);  // both MMA warps
+            }
+            bar_init_n(gsmem(&sm.clean), 128);
+            bar_init_n(gsmem(&sm.asked), 1);
+            sm.dead = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         }
-        incl += before;
-        __syncthreads();
-    };
-    int total = 0, mine = -1, seq = -1, pair = 0;
-    if (a.B > kPromptThreads) {
-        int w = 0, incl;
-        for (int s = tid; s < a.B; s += kPromptThreads) w += pairs_of(s);
-        scan(w, incl, total);
-    }
-    if (tid == 0) sm.seq = -1;
-    for (int s0 = 0, base = 0; s0 < a.B; s0 += kPromptThreads) {
-        const int w = s0 + tid < a.B ? pairs_of(s0 + tid) : 0;
-        int incl, sum;
-        scan(w, incl, sum);
-        if (a.B <= kPromptThreads) total = sum;
-        mine = total - 1 - which;
-        incl += base;
-        if (mine >= 0 && incl - w <= mine && mine < incl) {
-            sm.seq = s0 + tid;
-            sm.pair = mine - (incl - w);
-        }
-        base += sum;
-        if (base > mine) break;
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    seq = sm.seq;
-    pair = sm.pair;
+    if (warp < kTable / 32) {
+        int before = 0, sum = 0;
+#pragma unroll
+        for (int w = 0; w < kTable / 32; ++w) {
+            if (w == warp) before = sum;
+            sum += sm.wsum[w];
+        }
+        sm.prefix[tid] = before + incl - mine;
+        if (tid == 0) sm.total = sum;
+    }
+    __syncthreads();
     const uint32_t tmem = sm.tmem;
     int* dead = &sm.dead;
 
-    if (seq >= 0) {
-        const int q0 = min(max(__ldg(a.cu_q + seq), 0), a.Tq), q1 = min(max(__ldg(a.cu_q + seq + 1), 0), a.Tq);
-        const int k0 = min(max(__ldg(a.cu_k + seq), 0), a.Tk);
-        const int lk = max(min(max(__ldg(a.cu_k + seq + 1), 0), a.Tk) - k0, 0), lq = q1 - q0, shift = lk - lq;
-        // tile x: tokens i0[x] .. ; token i sees the keys below shift + i + 1
-        const int i0 = pair * 2 * tokens;
-        auto tiles_of = [&](int x) {  // key tiles of tile x
-            const int first = i0 + x * tokens, last = min(first + tokens, lq) - 1;
-            const int lim = last < first ? 0 : max(min(shift + last + 1, lk), 0);
+    // What a pair of tiles asks for: token i of the sequence sees the keys below shift + i + 1.
+    struct Span {
+        int shift, n0, n1, n;  // key tiles of tile 0, tile 1, and of the longer one
+        int seen_by_all;       // keys below this are seen by every row
+        int first_masked;      // the first key tile with a value to be cleaned
+    };
+    auto span_of = [&](const Item& it) {
+        Span p;
+        p.shift = it.lk - it.lq;
+        auto tiles_of = [&](int first) {
+            const int last = min(first + tokens, it.lq) - 1;
+            const int lim = last < first ? 0 : max(min(p.shift + last + 1, it.lk), 0);
             return (lim + kTile - 1) / kTile;
         };
-        const int n0 = tiles_of(0), n1 = tiles_of(1), n = max(n0, n1);
-        const int seen_by_all = max(min(shift + i0 + 1, lk), 0);  // keys below this are seen by every row
-        const int first_masked = seen_by_all / kTile;             // first key tile with a value to be cleaned
+        p.n0 = tiles_of(it.i0);
+        p.n1 = tiles_of(it.i0 + tokens);
+        p.n = max(p.n0, p.n1);
+        p.seen_by_all = max(min(p.shift + it.i0 + 1, it.lk), 0);
+        p.first_masked = p.seen_by_all / kTile;
+        return p;
+    };
+    // The next item, for a warp that uses them; false at the end. `number` counts the items taken.
+    auto take = [&](int number) {
+        bar_wait(gsmem(&sm.item_full[number & 1]), (number >> 1) & 1, dead, true);
+        __syncwarp();
+        return !sm.item[number & 1].end;
+    };
+    auto give_back = [&](int number) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(gsmem(&sm.item_empty[number & 1]));
+    };
 
-        // Registers: the launch gives 168 a thread (64512 in all); the softmax
-        // warpgroups hold a row of scores each and take 208, the third 88.
-        if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    // Registers: the launch gives 168 a thread (64512 in all); the softmax
+    // warpgroups hold a row of scores each and take 216, the third 72.
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
         if (warp == 8) {
-            if (lane == 0) {
-                for (int x = 0; x < 2; ++x) {
-                    if ((x ? n1 : n0) == 0) continue;
-                    const uint32_t bar = gsmem(&sm.q_full[x]);
-                    bar_expect(bar, (uint32_t)(kHalves * 128 * group * tokens));
-                    for (int h = 0; h < kHalves; ++h)
-                        tma_4d(gsmem(sm.q[x]) + h * kHalf, &mq, bar, 64 * h, 0, head, q0 + i0 + x * tokens);
+            // --- items and loads. The CTA starts with its own and asks for
+            // others until none is left. Items are numbered from the last pair
+            // of tiles, so that a sequence's longest run first.
+            int which = blockIdx.x, number = 0, st = 0;
+            uint32_t turn = 1, asks = 0;   // the ring's parity of `empty`; parity of `asked`
+            uint32_t q_turn[2] = {1, 1};
+            while (which >= 0) {
+                const bool ask = !*(volatile int*)dead;
+                if (ask && lane == 0) {
+                    bar_expect(gsmem(&sm.asked), 16);
+                    ask_next_cta(gsmem(&sm.answer), gsmem(&sm.asked));
                 }
-                for (int e = 0; e < 2 * n; ++e) {  // K0 V0 K1 V1 ...
-                    const int st = e % kStages;
-                    const uint32_t bar = gsmem(&sm.full[st]);
-                    if (e >= kStages) bar_wait(gsmem(&sm.empty[st]), (e / kStages - 1) & 1, dead);
-                    if (*(volatile int*)dead) break;
-                    bar_expect(bar, S::kTileBytes);
-                    for (int h = 0; h < kHalves; ++h)
-                        tma_3d(gsmem(sm.kv[st]) + h * kHalf, (e & 1) ? &mv : &mk, bar, 64 * h, head, k0 + (e >> 1) * kTile);
+                const int head = which % a.hkv, at = sm.total - 1 - which / a.hkv;
+                if (at >= 0) {
+                    // the last entry of the table that is not above `at`, then the sequence among its run
+                    int below = 0;
+#pragma unroll
+                    for (int e = 0; e < kTable / 32; ++e) below += sm.prefix[32 * e + lane] <= at;
+                    below = __reduce_add_sync(0xffffffffu, below) - 1;
+                    int seq = below * run, base = sm.prefix[below];
+                    if (run > 1) {
+                        for (;; seq += 32) {
+                            const int s = seq + lane, w = s < a.B ? pairs_of(s) : 0;
+                            int upto = w;
+#pragma unroll
+                            for (int off = 1; off < 32; off <<= 1) {
+                                const int v = __shfl_up_sync(0xffffffffu, upto, off);
+                                if (lane >= off) upto += v;
+                            }
+                            const unsigned hit = __ballot_sync(0xffffffffu, base + upto > at);
+                            if (hit) {
+                                const int l = __ffs(hit) - 1;
+                                seq += l;
+                                base += __shfl_sync(0xffffffffu, upto - w, l);
+                                break;
+                            }
+                            base += __shfl_sync(0xffffffffu, upto, 31);
+                            if (seq + 32 >= a.B) break;  // not reached: the table has the pair
+                        }
+                        seq = min(seq, a.B - 1);
+                    }
+                    const int bound = lane < 2 ? min(max(__ldg(a.cu_q + seq + lane), 0), a.Tq)
+                                      : lane < 4 ? min(max(__ldg(a.cu_k + seq + lane - 2), 0), a.Tk) : 0;
+                    Item it;
+                    it.q0 = __shfl_sync(0xffffffffu, bound, 0);
+                    it.lq = __shfl_sync(0xffffffffu, bound, 1) - it.q0;
+                    it.k0 = __shfl_sync(0xffffffffu, bound, 2);
+                    it.lk = max(__shfl_sync(0xffffffffu, bound, 3) - it.k0, 0);
+                    it.i0 = (at - base) * 2 * tokens;
+                    it.head = head;
+                    it.end = 0;
+                    bar_wait(gsmem(&sm.item_empty[number & 1]), ((number >> 1) & 1) ^ 1, dead, true);
+                    if (lane == 0) {
+                        sm.item[number & 1] = it;
+                        bar_arrive(gsmem(&sm.item_full[number & 1]));
+                    }
+                    ++number;
+                    const Span p = span_of(it);
+                    for (int x = 0; x < 2; ++x) {
+                        if ((x ? p.n1 : p.n0) == 0) continue;
+                        const uint32_t bar = gsmem(&sm.q_full[x]);
+                        bar_wait(gsmem(&sm.q_empty[x]), q_turn[x], dead);
+                        q_turn[x] ^= 1;
+                        if (lane == 0 && !*(volatile int*)dead) {
+                            bar_expect(bar, (uint32_t)(kHalves * 128 * group * tokens));
+                            for (int h = 0; h < kHalves; ++h)
+                                tma_4d(gsmem(sm.q[x]) + h * kHalf, &mq, bar, 64 * h, 0, it.head, it.q0 + it.i0 + x * tokens);
+                        }
+                    }
+                    for (int e = 0; e < 2 * p.n; ++e) {  // K0 V0 K1 V1 ...
+                        const uint32_t bar = gsmem(&sm.full[st]);
+                        bar_wait(gsmem(&sm.empty[st]), turn, dead);
+                        if (*(volatile int*)dead) break;
+                        if (lane == 0) {
+                            bar_expect(bar, S::kTileBytes);
+                            for (int h = 0; h < kHalves; ++h)
+                                tma_3d(gsmem(sm.kv[st]) + h * kHalf, (e & 1) ? &mv : &mk, bar, 64 * h, it.head, it.k0 + (e >> 1) * kTile);
+                        }
+                        if (++st == kStages) st = 0, turn ^= 1;
+                    }
+                    __syncwarp();
+                }
+                which = -1;
+                if (ask) {
+                    bar_wait(gsmem(&sm.asked), asks, dead, true);
+                    asks ^= 1;
+                    __syncwarp();
+                    if (!*(volatile int*)dead || bar_try(gsmem(&sm.asked), asks ^ 1)) which = next_cta(gsmem(&sm.answer));
+                    fence_async_smem();  // the answer is read before the next one is asked for
+                    __syncwarp();
                 }
             }
-        } else if (warp == 9) {
-            // The whole warp walks the loop and one lane issues, so that the
-            // operands stay in uniform registers; descriptors are one base each
-            // plus constants.
-            if (n > 0) {
-                constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false), id_o = idesc_bf16(kTile, D, true);
-                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-                const bool leader = elect_one();
-                const uint64_t qd = tc_sdesc(gsmem(sm.q[0])), kd = tc_sdesc(gsmem(sm.kv[0])), vd = sdesc_mn(gsmem(sm.kv[0]));
-                constexpr uint64_t kTileStep = S::kTileBytes >> 4;  // to the next tile, in a descriptor
-                auto scores = [&](int x, int st) {
-                    const uint64_t qx = qd + x * kTileStep, kx = kd + st * kTileStep;
+            bar_wait(gsmem(&sm.item_empty[number & 1]), ((number >> 1) & 1) ^ 1, dead, true);
+            if (lane == 0) {
+                sm.item[number & 1].end = 1;
+                bar_arrive(gsmem(&sm.item_full[number & 1]));
+            }
+            if (*(volatile int*)dead && lane == 0) {  // copies under way land before the CTA leaves
+                for (int e = 0; e < kStages; ++e) gbar_wait(gsmem(&sm.full[e]), e < st ? turn ^ 1 : turn);
+            }
+        } else if (warp < 11) {
+            // --- the MMAs of tile x. A warp each, so that the tensor cores have
+            // the other tile's products while this one waits for its weights. The
+            // whole warp walks the loop and one lane issues, so that the operands
+            // stay in uniform registers; descriptors are one base each plus
+            // constants. Both warps pass every stage of the ring and every
+            // cleaning, needed or not: a wait cannot tell a phase from the next
+            // but one.
+            constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false), id_o = idesc_bf16(kTile, D, true);
+            const int x = __shfl_sync(0xffffffffu, warp - 9, 0);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t ts = tm + x * kTile, to = tm + 2 * kTile + x * D;
+            const bool leader = elect_one();
+            const uint64_t qd = tc_sdesc(gsmem(sm.q[0]) + x * S::kTileBytes), kd = tc_sdesc(gsmem(sm.kv[0])),
+                           vd = sdesc_mn(gsmem(sm.kv[0]));
+            constexpr uint64_t kTileStep = S::kTileBytes >> 4;  // to the next stage, in a descriptor
+            auto scores = [&](int st, bool last) {
+                const uint64_t kx = kd + st * kTileStep;
 #pragma unroll
-                    for (int d = 0; d < D / 16; ++d) {
-                        const uint32_t off = ((d / 4) * kHalf + (d % 4) * 32) >> 4;
-                        tc_mma(tm + x * kTile, qx + off, kx + off, id_s, d != 0);
-                    }
-                    tc_commit(gsmem(&sm.s_full[x]));
-                };
-                auto values = [&](int x, int st, bool first) {
-                    const uint64_t vx = vd + st * kTileStep;
-#pragma unroll
-                    for (int t = 0; t < kTile / 16; ++t)
-                        tc_mma_ta(tm + 2 * kTile + x * D, tm + x * kTile + 8 * t, vx + t * (2048 >> 4), id_o, t == 0 ? !first : 1);
-                };
-                bar_wait(gsmem(&sm.full[0]), 0, dead);
-                for (int x = 0; x < 2; ++x) {
-                    if ((x ? n1 : n0) == 0) continue;
-                    bar_wait(gsmem(&sm.q_full[x]), 0, dead);
-                    __syncwarp();
-                    tc_fence_after();
-                    if (leader) scores(x, 0);
+                for (int d = 0; d < D / 16; ++d) {
+                    const uint32_t off = ((d / 4) * kHalf + (d % 4) * 32) >> 4;
+                    tc_mma(ts, qd + off, kx + off, id_s, d != 0);
                 }
-                if (leader) tc_commit(gsmem(&sm.empty[0]));
-                int sv = 1, sk = 2;               // stages of V_j and K_(j + 1), and their rounds' parities
-                uint32_t pv = 0, pk = 0;
-                for (int j = 0; j < n; ++j) {
-                    bar_wait(gsmem(&sm.full[sv]), pv, dead);
-                    // the cleaning warps cannot tell the ring's rounds apart
-                    if (j >= first_masked && leader) bar_arrive(gsmem(&sm.dirty));
-                    if (j + 1 < n) bar_wait(gsmem(&sm.full[sk]), pk, dead);
-                    if (*(volatile int*)dead) break;
+                tc_commit(gsmem(&sm.s_full[x]));
+                if (last) tc_commit(gsmem(&sm.q_empty[x]));
+            };
+            auto values = [&](int half, int st, bool first) {  // of the tile's keys 64 half ..
+                const uint64_t vx = vd + st * kTileStep;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int nx = x ? n1 : n0;
-                        if (j < nx) {
-                            bar_wait(gsmem(&sm.p_full[x]), j & 1, dead);
-                            if (j >= first_masked) bar_wait(gsmem(&sm.clean), (j - first_masked) & 1, dead);
-                            __syncwarp();
-                            tc_fence_after();
-                            if (leader) {
-                                values(x, sv, j == 0);
-                                if (j + 1 == nx) tc_commit(gsmem(&sm.o_full[x]));
-                                else scores(x, sk);
-                            }
+                for (int t = half * kTile / 32; t < (half + 1) * kTile / 32; ++t)
+                    tc_mma_ta(to, ts + 8 * t, vx + t * (2048 >> 4), id_o, t == 0 ? !first : 1);
+            };
+            auto free_stage = [&](int st, bool used) {
+                if (used) tc_commit(gsmem(&sm.empty[st]));
+                else bar_arrive(gsmem(&sm.empty[st]));
+            };
+            int st = 0;
+            uint32_t round = 0, p_turn = 0, q_turn = 0, c_turn = 0;
+            auto step = [&]() { if (++st == kStages) st = 0, round ^= 1; };
+            for (int number = 0; take(number); ++number) {
+                const Span p = span_of(sm.item[number & 1]);
+                give_back(number);
+                if (p.n == 0) continue;
+                const int nx = x ? p.n1 : p.n0;
+                int sk = st, sv;
+                bar_wait(gsmem(&sm.full[sk]), round, dead);
+                step();
+                if (nx) {
+                    bar_wait(gsmem(&sm.q_full[x]), q_turn, dead);
+                    q_turn ^= 1;
+                }
+                __syncwarp();
+                tc_fence_after();
+                if (leader) {
+                    if (nx) scores(sk, nx == 1);
+                    free_stage(sk, nx);
+                }
+                __syncwarp();
+                for (int j = 0; j < p.n; ++j) {
+                    sv = st;
+                    bar_wait(gsmem(&sm.full[sv]), round, dead);
+                    step();
+                    sk = st;
+                    if (j + 1 < p.n) {
+                        bar_wait(gsmem(&sm.full[sk]), round, dead);
+                        step();
+                    }
+                    if (*(volatile int*)dead) break;
+                    if (j >= p.first_masked) {
+                        bar_wait(gsmem(&sm.clean), c_turn, dead);
+                        c_turn ^= 1;
+                    }
+                    if (j < nx) {
+                        bar_wait(gsmem(&sm.p_full[x][0]), p_turn, dead);
+                        __syncwarp();
+                        tc_fence_after();
+                        if (leader) values(0, sv, j == 0);
+                        __syncwarp();
+                        bar_wait(gsmem(&sm.p_full[x][1]), p_turn, dead);
+                        p_turn ^= 1;
+                        __syncwarp();
+                        tc_fence_after();
+                        if (leader) {
+                            values(1, sv, false);
+                            if (j + 1 == nx) tc_commit(gsmem(&sm.o_full[x]));
+                            else scores(sk, j + 2 == nx);
                         }
                     }
                     if (leader) {
-                        tc_commit(gsmem(&sm.empty[sv]));
-                        if (j + 1 < n) tc_commit(gsmem(&sm.empty[sk]));
+                        free_stage(sv, j < nx);
+                        if (j + 1 < p.n) free_stage(sk, j < nx);
                     }
-                    sv += 2, sk += 2;
-                    if (sv >= kStages) sv -= kStages, pv ^= 1;
-                    if (sk >= kStages) sk -= kStages, pk ^= 1;
+                    __syncwarp();
                 }
-                // the last arrivals, so that none is under way when the CTA ends
-                const int e = 2 * n - 1;
-                bar_wait(gsmem(&sm.empty[e % kStages]), (e / kStages) & 1, dead);
+                if (*(volatile int*)dead) break;
             }
-        } else {
-            for (int j = first_masked; j < n; ++j) {
-                const int e = 2 * j + 1, st = e % kStages;
-                bar_wait(gsmem(&sm.dirty), (j - first_masked) & 1, dead);
-                bar_wait(gsmem(&sm.full[st]), (e / kStages) & 1, dead);
-                const int r0 = max(seen_by_all - j * kTile, 0);
-                bool found = false;
-                constexpr int kChunks = D / 8;  // 16-byte chunks of a key's values
-                for (int w = tid - 320 + r0 * kChunks; w < kTile * kChunks; w += 64) {
-                    const int r = w / kChunks, cc = w % kChunks;
-                    uint4* at = reinterpret_cast<uint4*>(sm.kv[st] + (cc >> 3) * kHalf + r * 128 + (((cc ^ r) & 7) << 4));
-                    if (j * kTile + r >= lk) {
-                        *at = make_uint4(0, 0, 0, 0);
-                    } else {
-                        const uint4 u = *at;
-                        if (any_nonfinite(u.x) || any_nonfinite(u.y) || any_nonfinite(u.z) || any_nonfinite(u.w)) {
-                            found = true;
-                            *at = make_uint4(drop_nonfinite(u.x), drop_nonfinite(u.y), drop_nonfinite(u.z), drop_nonfinite(u.w));
-                        }
-                    }
-                }
-                if (found) sm.flag = 1;
-                fence_async_smem();
-                bar_arrive(gsmem(&sm.clean));
-            }
+            // the last arrivals, so that none is under way when the CTA ends:
+            // a stage's `empty` completes once for each time it was filled
+            for (int e = 0; e < kStages; ++e) bar_wait(gsmem(&sm.empty[e]), e < st ? round : round ^ 1, dead);
         }
-        } else {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-            // --- softmax of tile x, a thread per row
-            const int x = warp >> 2, nx = x ? n1 : n0, row = tid & 127;
-            const int tok = row / group, i = i0 + x * tokens + tok;
-            const bool used = tok < tokens && i < lq;
-            const int lim = used ? max(min(shift + i + 1, lk), 0) : 0;   // keys this row sees
-            const int lim_tile = max(min(shift + i0 + x * tokens + 1, lk), 0);
-            const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-            const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + 2 * kTile + x * D;
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
+        // --- softmax of tile x, a thread per row
+        const int x = warp >> 2, row = tid & 127, tok = row / group;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + 2 * kTile + x * D;
+        uint32_t s_turn = 0, o_turn = 0;
+        int ring = 0;  // stages of the ring used before this item
+        for (int number = 0; take(number); ++number) {
+            // the item stays in shared memory until the warp gives it back; only
+            // what the loop needs is kept in registers
+            const Item& it = sm.item[number & 1];
+            int nx, lim, lim_tile;  // key tiles; keys this row sees, and the first row of the tile
+            int cleans;             // the first key tile whose values this warpgroup cleans
+            {
+                const Span p = span_of(it);
+                const int i = it.i0 + x * tokens + tok;
+                nx = x ? p.n1 : p.n0;
+                cleans = x ? max(p.first_masked, p.n0) : p.first_masked;
+                lim = tok < tokens && i < it.lq ? max(min(p.shift + i + 1, it.lk), 0) : 0;
+                lim_tile = max(min(p.shift + it.i0 + x * tokens + 1, it.lk), 0);
+            }
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < nx; ++j) {
-                bar_wait(gsmem(&sm.s_full[x]), j & 1, dead);
+                bar_wait(gsmem(&sm.s_full[x]), s_turn, dead);
+                s_turn ^= 1;
+                if (j >= cleans) {
+                    // The stage's previous round is over, since these scores came after it.
+                    const int e = ring + 2 * j + 1, st = e % kStages;
+                    bar_wait(gsmem(&sm.full[st]), (e / kStages) & 1, dead);
+                    if (clean_values<D>(sm.kv[st], row, span_of(it).seen_by_all - j * kTile, it.lk - j * kTile))
+                        *(volatile int*)&sm.flag[number & 1] = number + 1;
+                    fence_async_smem();
+                    bar_arrive(gsmem(&sm.clean));
+                }
                 __syncwarp();
                 tc_fence_after();
                 uint32_t s[4][32];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) tc_ld32(ts + 32 * h, s[h]);
-                tc_ld_wait();
+#pragma unroll
+                for (int h = 0; h < 4; ++h) tc_ld_wait32(s[h]);
                 if ((j + 1) * kTile > lim_tile) {
                     const int left = lim - j * kTile;  // columns from here on are hidden
 #pragma unroll
@@ -435,8 +653,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                 for (int h = 0; h < 4; ++h)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
-                        mx4[(e >> 1) & 3] = fmaxf(mx4[(e >> 1) & 3], fmaxf(__uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1])));
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                        mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
+                const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
                 const bool raise = (mx - m) * a.c > kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
                     // S of this step was computed after the last step's O, so O is at rest
@@ -444,14 +662,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     if (raise) m = mx;
                     l *= f;
                     if (j > 0) {
+#pragma unroll 1
+                        for (int h = 0; h < D / 8; ++h) {  // few registers beside the row's
+                            uint32_t o[8];
+                            tc_ld8_wait(to + 8 * h, o);
 #pragma unroll
-                        for (int h = 0; h < D / 32; ++h) {
-                            uint32_t o[32];
-                            tc_ld32(to + 32 * h, o);
-                            tc_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc_st32(to + 32 * h, o);
+                            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc_st8(to + 8 * h, o);
                         }
                     }
                 }
@@ -459,47 +676,54 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                 const unsigned long long c2 = pair2(a.c, a.c), mc2 = pair2(-mc, -mc);
                 unsigned long long sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const uint32_t* z = &s[2 * h + (e >> 4)][(2 * e) & 31];
-                        const unsigned long long y = fma2(pair2(__uint_as_float(z[0]), __uint_as_float(z[1])), c2, mc2);
+                    for (int e = 0; e < 16; ++e) {
+                        const unsigned long long y =
+                            fma2(pair2(__uint_as_float(s[h][2 * e]), __uint_as_float(s[h][2 * e + 1])), c2, mc2);
                         const float e0 = ex2f(lo2(y)), e1 = ex2f(hi2(y));
                         sum[e & 3] = add2(sum[e & 3], pair2(e0, e1));
-                        p[e] = pack_bf(e0, e1);
+                        w[e] = pack_bf(e0, e1);
                     }
-                    tc_st32(ts + 32 * h, p);
+                    tc_st16(ts + 16 * h, w);
+                    if (h & 1) {  // the products with the first 64 keys begin while the other weights are computed
+                        tc_st_wait();
+                        tc_fence_before();
+                        bar_arrive(gsmem(&sm.p_full[x][h >> 1]));
+                    }
                 }
                 sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
                 l += lo2(sum[0]) + hi2(sum[0]);
-                tc_st_wait();
-                tc_fence_before();
-                bar_arrive(gsmem(&sm.p_full[x]));
             }
-            // --- out
-            if (nx) bar_wait(gsmem(&sm.o_full[x]), 0, dead);
+            // --- out. (The next item's first O comes after its first weights, so O stays until this is done.)
+            if (nx) {
+                bar_wait(gsmem(&sm.o_full[x]), o_turn, dead);
+                o_turn ^= 1;
+            }
             __syncwarp();
             tc_fence_after();
-            const bool flag = nx && *(volatile int*)&sm.flag;
+            const bool flag = nx && *(volatile int*)&sm.flag[number & 1] == number + 1;
             const bool lost = *(volatile int*)dead;
             const float inv = l == 0.f ? 0.f : 1.0f / l;
-            uint16_t* dst = a.out + ((size_t)(q0 + i) * a.hq + head * group + (row - tok * group)) * D;
+            const int i = it.i0 + x * tokens + tok;
+            const bool used = tok < tokens && i < it.lq;
+            uint16_t* dst = a.out + ((size_t)(it.q0 + i) * a.hq + it.head * group + (row - tok * group)) * D;
 #pragma unroll
             for (int h = 0; h < D / 32; ++h) {
                 uint32_t o[32];
                 __syncwarp();
                 if (nx) {
                     tc_ld32(to + 32 * h, o);
-                    tc_ld_wait();
+                    tc_ld_wait32(o);
                 }
                 float y[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = lim > 0 ? __uint_as_float(o[e]) * inv : 0.f;
                 if (flag) {  // infinities and NaN that the cleaning took out, where this row sees them
-                    for (int t = first_masked * kTile; t < lim; ++t) {
-                        if (t < seen_by_all) continue;
-                        const uint16_t* vr = a.v + (size_t)(k0 + t) * a.vs + (size_t)head * D + 32 * h;
+                    const Span p = span_of(it);
+                    for (int t = max(p.first_masked * kTile, p.seen_by_all); t < lim; ++t) {
+                        const uint16_t* vr = a.v + (size_t)(it.k0 + t) * a.vs + (size_t)it.head * D + 32 * h;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             const float w = __uint_as_float((uint32_t)__ldg(vr + e) << 16);
@@ -517,11 +741,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     }
                 }
             }
-        }
-        __syncwarp();
-        if (*(volatile int*)dead && warp == 8 && lane == 0) {
-            // copies under way land before the CTA leaves
-            for (int e = 0; e < min(2 * n, kStages); ++e) gbar_wait(gsmem(&sm.full[e]), 0);
+            tc_fence_before();  // the reads of O, before the weights that let it be overwritten
+            ring = (ring + 2 * span_of(it).n) % (2 * kStages);
+            give_back(number);  // only now: the flag of the next item but one shares this one's place
         }
     }
     tc_fence_before();
