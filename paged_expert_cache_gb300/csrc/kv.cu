@@ -181,9 +181,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvDev c, KvBatch b
         *reinterpret_cast<uint16_t*>(vc + C::v_half(tc, 2 * i + 1, b1)) = (uint16_t)(h1 >> 16);
     }
     if (i == 0) {
-        uint8_t* sc = cell + (kind == 1 ? C::kKs : C::kVs);
-        *reinterpret_cast<__half*>(sc + C::scale(tc, b0)) = d0;
-        *reinterpret_cast<__half*>(sc + C::scale(tc, b1)) = d1;
+        *reinterpret_cast<__half*>(cell + (kind == 1 ? C::kKs + C::k_scale(tc, b0) : C::kVs + C::v_scale(tc, b0))) = d0;
+        *reinterpret_cast<__half*>(cell + (kind == 1 ? C::kKs + C::k_scale(tc, b1) : C::kVs + C::v_scale(tc, b1))) = d1;
     }
 }
 
@@ -221,9 +220,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_read(KvDev c, KvBatch b, 
     uint32_t w0 = 0, w1 = 0;  // nibble e: dim 8i + e of the block
     float d0 = __int_as_float(0x7fc00000), d1 = d0;
     if (cell) {
-        const uint8_t* sc = cell + (is_v ? C::kVs : C::kKs);
-        d0 = __half2float(*reinterpret_cast<const __half*>(sc + C::scale(tc, b0)));
-        d1 = __half2float(*reinterpret_cast<const __half*>(sc + C::scale(tc, b1)));
+        d0 = __half2float(*reinterpret_cast<const __half*>(cell + (is_v ? C::kVs + C::v_scale(tc, b0) : C::kKs + C::k_scale(tc, b0))));
+        d1 = __half2float(*reinterpret_cast<const __half*>(cell + (is_v ? C::kVs + C::v_scale(tc, b1) : C::kKs + C::k_scale(tc, b1))));
         if (!is_v) {
             const uint32_t u0 = *reinterpret_cast<const uint32_t*>(cell + C::k_word(tc, i, b0));
             const uint32_t u1 = *reinterpret_cast<const uint32_t*>(cell + C::k_word(tc, i, b1));

@@ -7,9 +7,9 @@
 // reads and no shuffles. With G = head_dim / 32 blocks per token, lane l,
 // g = l / 4 and i = l % 4, a cell is
 //   K codes   words [16 tokens][4 i][G]    word (t, i, b): dims 32b + 8i + 2j (bits 4j) and + 1 (bits 16 + 4j)
-//   K scales  fp16x2 [2 halves][4 i][G]    tokens 8 half + 2i, + 1
+//   K scales  fp16 [16 tokens][G]
 //   V codes   words [2 halves][8 g][4 i][G]  dims 32b + g + 8j of tokens 8 half + 2i (bits 4j) and + 1 (bits 16 + 4j)
-//   V scales  as K scales
+//   V scales  fp16x2 [2 halves][4 i][G]    tokens 8 half + 2i, + 1
 // 576 G bytes, 18 per block. Every token owns whole 16-bit units, so tokens
 // are written without reading their neighbours.
 #pragma once
@@ -30,7 +30,8 @@ struct Cell {
     __device__ static int v_half(int t, int g, int b) {
         return (((t >> 3) * 32 + g * 4 + ((t & 7) >> 1)) * G + b) * 4 + (t & 1) * 2;
     }
-    __device__ static int scale(int t, int b) { return (((t >> 3) * 4 + ((t & 7) >> 1)) * G + b) * 4 + (t & 1) * 2; }
+    __device__ static int k_scale(int t, int b) { return (t * G + b) * 2; }
+    __device__ static int v_scale(int t, int b) { return (((t >> 3) * 4 + ((t & 7) >> 1)) * G + b) * 4 + (t & 1) * 2; }
 };
 
 // What the kernels need of a handle and a batch, by value.

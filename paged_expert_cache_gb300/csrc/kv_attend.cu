@@ -22,16 +22,17 @@
 // Arithmetic. A 4-bit code q masked out of its word is the fp16 subnormal q *
 // 2^-24 (or q * 2^-20 for the upper nibble of a byte), which the tensor cores
 // multiply exactly, so codes become operands with one AND.
-//  scores: A = q (fp16 after the exact power-of-two prescale of its row), B =
-//    key codes without their - 8: a block's sum starts at -8 sum(q) instead
-//    (the sums are then within 8e-7 of a random row's score, measured), and is
-//    multiplied by the block's scale in fp32.
-//  values: A = value codes (transposed), here with the - 8 subtracted (exact in
-//    fp16), since a sum that only cancels would leave a rounding of 8 d p where
-//    the values met are zero; B = p * d for each block, rounded to fp16 twice
-//    (p, then the product: 2^-11 each, an eighth of the output's own rounding
-//    each); d is first brought near 1 by a power of two that follows the
-//    largest scale met, so fp16's range is no limit.
+//  scores: A = key codes (16 tokens), B = q (8 rows; fp16 after the exact
+//    power-of-two prescale of its row). The codes keep their 8: a block's sum
+//    starts at -8 sum(q) instead (the sums are then within 8e-7 of a random
+//    row's score, measured), and is multiplied by the block's scale in fp32.
+//  values: A = value codes (32 dims by 16 tokens), here with the 8 subtracted
+//    (exact in fp16), since a sum that only cancels would leave a rounding of
+//    8 d p where the values met are zero; B = p * d for each block, from the
+//    scores' layout by one 8 x 8 transposition, rounded to fp16 twice (p, then
+//    the product: 2^-11 each, an eighth of the output's own rounding each). Where
+//    the largest scale met is not within fp16's comfort, d is brought there by
+//    a power of two that follows it, so fp16's range is no limit.
 // Softmax statistics, sums and outputs are fp32. A row's running maximum is
 // raised only when a score exceeds it by 2^kLazy, the outputs being rescaled
 // then.
@@ -42,13 +43,14 @@ namespace moe {
 constexpr int kWarps = 8;
 constexpr int kAttThreads = 32 * kWarps;
 constexpr int kStages = 4;
-// fp16's range for the product p * d: a row's largest weight is 2^kOffset when
-// its maximum is set and may grow by 2^kLazy; the value blocks' scales are
-// multiplied by at most 2^kSigmaMax, to below 2^kTop when a new largest one is
-// met, and may grow by 2^kHeadroom. So a product is below 2^15, and weights down
-// to 2^-31 of the largest still count.
+// fp16's range for the product p * d. A row's largest weight is 2^kOffset when
+// its maximum is set and may grow by 2^kLazy. The value blocks' scales are
+// multiplied by 2^sigma: 0 while the largest met is below 1 and was not below
+// 2^kSmall when first met, else at most kSigmaMax and such that it comes to
+// between 2^(kTop - 1) and 2^kTop, and may grow to 1. So a product is below 2^15,
+// and weights down to 2^-26 of the largest still count.
 constexpr float kLazy = 4.0f, kOffset = 11.0f;
-constexpr int kSigmaMax = 15, kTop = -4, kHeadroom = 4;
+constexpr int kSigmaMax = 15, kTop = -4, kSmall = -8;
 constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -146,9 +148,8 @@ template <int D, int NT>
 struct AttSmem {
     static constexpr int kRows = 8 * NT, kPad = D + 4;
     alignas(128) uint8_t ring[kWarps][kStages][Cell<D>::kBytes];
-    float tree[kWarps / 2][kRows][kPad];
-    float m[kWarps][kRows], l[kWarps][kRows];
-    float mrow[kRows], lrow[kRows];
+    float o[kWarps][kRows][kPad];        // the warps' outputs; then factors of an item's pieces
+    float m[kWarps][kRows], l[kWarps][kRows], unit[kWarps];
     alignas(8) unsigned long long bar[kWarps][kStages];
     long long wsum[kWarps];
     Piece cur[kWarps], ask[kWarps];  // a warp's piece at work and the one it asks for: rarely read, so not in registers
@@ -184,6 +185,18 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
+}
+// d = a b + c, c kept.
+__device__ __forceinline__ void mma_f16_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+// Transposes an 8 x 8 matrix of 16-bit values held two a lane (row lane / 4).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+    return r;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return h2_as_u32(__floats2half2_rn(lo, hi)); }
 
@@ -320,17 +333,18 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         // --- rows of the piece: row r of the tile is query row tile * kRows + r of the head's n * group
         const int t0 = min(max(__ldg(b.cu + p.seq), 0), a.T);
         const int rows = min(kRows, p.s.n * group - p.tile * kRows);
-        uint32_t qa[G][2][2 * NT];  // A registers: k-step s, (a0, a2) of row g, then of row g + 8
-        float corr[G][NT], rf[NT];
-        int lim[NT];
+        uint32_t qb[NT][G][2][2];        // B registers of the scores, row 8 nt + g: k-step, (b0, b1)
+        float corr[NT][G][4];            // -8 sum(q) of rows 2i, 2i + 1, 2i, 2i + 1
+        float rf[NT][2];                 // scores to log2 units, rows 2i, 2i + 1
+        int lim[NT][2], lim_row[NT];     // positions seen by rows 2i, 2i + 1, and by row g
         int min_lim = 0x7fffffff;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = g + 8 * nt;
             const int row = p.tile * kRows + (r < rows ? r : 0);
             const int tok = (int)((unsigned)row / (unsigned)group), head = p.head * group + row - tok * group;
-            lim[nt] = p.s.kv - p.s.n + tok + 1;
-            min_lim = min(min_lim, lim[nt]);
+            lim_row[nt] = p.s.kv - p.s.n + tok + 1;
+            min_lim = min(min_lim, lim_row[nt]);
             uint4 u[G];
             const uint16_t* src = a.q + (size_t)(t0 + tok) * a.qs + (size_t)head * D + 8 * i;
             unsigned mx = 0;
@@ -354,245 +368,242 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                     const uint32_t h = pack_h2(x0 * k, x1 * k);
                     const float2 back = __half22float2(u32_as_h2(h));
                     sum += (back.x + back.y) * ((j & 1) ? 16.0f : 1.0f);
-                    qa[bl][j >> 1][2 * nt + (j & 1)] = h;
+                    qb[nt][bl][j >> 1][j & 1] = h;
                 }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                corr[bl][nt] = sum * (-8.0f / 16777216.0f);
+                sum *= -8.0f / 16777216.0f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) corr[nt][bl][e] = corr[nt][bl][2 + e] = __shfl_sync(0xffffffffu, sum, 8 * i + 4 * e);
             }
-            rf[nt] = a.scale * kLog2e * 16777216.0f * pow2f(sh);
+            // a scale of zero still hides what is hidden: -inf times a tiny factor is -inf
+            const float fac = fmaxf(a.scale * kLog2e * 16777216.0f * pow2f(sh), 1e-37f);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                rf[nt][e] = __shfl_sync(0xffffffffu, fac, 8 * i + 4 * e);
+                lim[nt][e] = __shfl_sync(0xffffffffu, lim_row[nt], 8 * i + 4 * e);
+            }
         }
         min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 4));
         min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 8));
         min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, 16));
 
         float o[G][2][NT][4] = {};   // c0, c1: dim 32 bl + 16 mu + g of rows 2i, 2i + 1; c2, c3: dim + 8, times 16
-        float m[NT], l[NT];
+        float m[NT][2], l[NT][2];    // rows 2i, 2i + 1; l: this lane's tokens
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) { m[nt] = -INFINITY; l[nt] = 0.f; }
-        int sigma = kSigmaMax;
-        __half2 up = __float2half2_rn(pow2f(kSigmaMax)), top = __float2half2_rn(pow2f(kTop + kHeadroom - kSigmaMax));
+        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+        int sigma = kSigmaMax + 1;   // none yet
+        __half2 top = __float2half2_rn(0.f);
 
         const int cells = warp_cells(p, warp), first = (p.u0 * kWarps + warp) * kCellTokens;
+        auto words = [&](uint32_t (&r)[G], const uint8_t* src) {
+            if constexpr (G == 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(src);
+                r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(src);
+                r[0] = v.x, r[1] = v.y;
+            }
+        };
 #pragma unroll 1
-        for (int k = 0; k < cells; ++k) {
-            const int slot = used % kStages;
-            const uint32_t bar = smem_addr(&sm.bar[warp][slot]), parity = (used / kStages) & 1;
-            if (!dead && !abar_try(bar, parity) && !abar_wait_long(bar, parity)) dead = true;
-            dead = __any_sync(0xffffffffu, dead);
-            const uint8_t* cell = sm.ring[warp][slot];
-            uint32_t kw[2][G], ks[2][G], vw[2][G], vs[2][G];
-            auto load = [&](uint32_t (&r)[G], const uint8_t* src) {
-                if constexpr (G == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src);
-                    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2*>(src);
-                    r[0] = v.x, r[1] = v.y;
-                }
-            };
+        for (int k = 0; k < cells; k += 2) {
+            // two cells at a time where there are two
+            const int both = k + 1 < cells ? 2 : 1;
+            float s[2][NT][4];       // c0, c1: token g, rows 2i, 2i + 1; c2, c3: token g + 8
+            uint32_t vs[2][2][G];    // value scales
+            __half2 big = __float2half2_rn(0.f);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                load(kw[h], cell + (h * 32 + lane) * G * 4);
-                load(ks[h], cell + C::kKs + (h * 4 + i) * G * 4);
-                load(vw[h], cell + C::kV + (h * 32 + lane) * G * 4);
-                load(vs[h], cell + C::kVs + (h * 4 + i) * G * 4);
-            }
-            // scores of rows g (and g + 8), tokens 8h + 2i, + 1
-            float s[2][2 * NT];
+            for (int z = 0; z < 2; ++z) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2 * NT; ++e) s[h][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) s[z][nt][e] = -INFINITY;
+                if (z < both) {
+                    const int slot = (used + z) % kStages;
+                    const uint32_t bar = smem_addr(&sm.bar[warp][slot]), parity = ((used + z) / kStages) & 1;
+                    if (!dead && !abar_try(bar, parity) && !abar_wait_long(bar, parity)) dead = true;
+                    const uint8_t* cell = sm.ring[warp][slot];
+                    uint32_t kw[2][G];
+                    __half2 ks[2][G / 2];
 #pragma unroll
-                for (int bl = 0; bl < G; ++bl) {
-                    float acc[4] = {corr[bl][0], corr[bl][0], corr[bl][NT - 1], corr[bl][NT - 1]};
-                    const uint32_t w = kw[h][bl], w8 = w >> 8;
-                    const uint32_t a0[4] = {qa[bl][0][0], NT == 2 ? qa[bl][0][2 * NT - 2] : 0u, qa[bl][0][1], NT == 2 ? qa[bl][0][2 * NT - 1] : 0u};
-                    const uint32_t a1[4] = {qa[bl][1][0], NT == 2 ? qa[bl][1][2 * NT - 2] : 0u, qa[bl][1][1], NT == 2 ? qa[bl][1][2 * NT - 1] : 0u};
-                    mma_f16(acc, a0, w & 0x000f000fu, w & 0x00f000f0u);
-                    mma_f16(acc, a1, w8 & 0x000f000fu, w8 & 0x00f000f0u);
-                    const float2 d = __half22float2(u32_as_h2(ks[h][bl]));
+                    for (int h = 0; h < 2; ++h) {
+                        words(kw[h], cell + (h * 32 + lane) * G * 4);
+                        words(vs[z][h], cell + C::kVs + (h * 4 + i) * G * 4);
+                        if constexpr (G == 4) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(cell + C::kKs + (8 * h + g) * G * 2);
+                            ks[h][0] = u32_as_h2(v.x), ks[h][1] = u32_as_h2(v.y);
+                        } else {
+                            ks[h][0] = *reinterpret_cast<const __half2*>(cell + C::kKs + (8 * h + g) * G * 2);
+                        }
+                    }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        s[h][2 * nt] = fmaf(acc[2 * nt], d.x, s[h][2 * nt]);
-                        s[h][2 * nt + 1] = fmaf(acc[2 * nt + 1], d.y, s[h][2 * nt + 1]);
+                    for (int bl = 0; bl < G; ++bl) {
+                        const uint32_t w0 = kw[0][bl], w1 = kw[1][bl], w08 = w0 >> 8, w18 = w1 >> 8;
+                        const uint32_t a0[4] = {w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u};
+                        const uint32_t a1[4] = {w08 & 0x000f000fu, w18 & 0x000f000fu, w08 & 0x00f000f0u, w18 & 0x00f000f0u};
+                        const float d0 = bl & 1 ? __high2float(ks[0][bl / 2]) : __low2float(ks[0][bl / 2]);
+                        const float d1 = bl & 1 ? __high2float(ks[1][bl / 2]) : __low2float(ks[1][bl / 2]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float acc[4];
+                            mma_f16_c(acc, a0, qb[nt][bl][0][0], qb[nt][bl][0][1], corr[nt][bl]);
+                            mma_f16(acc, a1, qb[nt][bl][1][0], qb[nt][bl][1][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                s[z][nt][e] = bl ? fmaf(acc[e], e < 2 ? d0 : d1, s[z][nt][e]) : acc[e] * (e < 2 ? d0 : d1);
+                        }
+                        big = __hmax2(big, __hmax2(__habs2(u32_as_h2(vs[z][0][bl])), __habs2(u32_as_h2(vs[z][1][bl]))));
+                    }
+                    const int pos0 = first + (k + z) * (kWarps * kCellTokens);
+                    if (pos0 + kCellTokens > min_lim) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (pos0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) s[z][nt][e] = -INFINITY;
                     }
                 }
             }
-            const int pos0 = first + k * (kWarps * kCellTokens);
-            const bool masked = pos0 + kCellTokens > min_lim;
-            uint32_t keep[2][NT];
+            // Do the running maxima and the running scale of the value blocks
+            // still do? A lane looks at its own scores; only if one does not are
+            // the maxima shared.
+            bool raise = !__hble2(big, top);
+            float mx[NT][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float &x0 = s[h][2 * nt], &x1 = s[h][2 * nt + 1];
-                    x0 *= rf[nt];
-                    x1 *= rf[nt];
-                    if (masked) {
-                        const int t = pos0 + 8 * h + 2 * i;
-                        keep[h][nt] = (t < lim[nt] ? 0xffffu : 0u) | (t + 1 < lim[nt] ? 0xffff0000u : 0u);
-                        if (t >= lim[nt]) x0 = -INFINITY;
-                        if (t + 1 >= lim[nt]) x1 = -INFINITY;
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    mx[nt][e] = rf[nt][e] * fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+                    raise |= mx[nt][e] > m[nt][e] + kLazy;
                 }
-            // the running maximum, and the running scale of the value blocks
-            bool raise = false;
-            float mx[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float v = fmaxf(fmaxf(s[0][2 * nt], s[0][2 * nt + 1]), fmaxf(s[1][2 * nt], s[1][2 * nt + 1]));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                mx[nt] = v;
-                raise |= v > m[nt] + kLazy;
-            }
-            __half2 big = __habs2(u32_as_h2(vs[0][0]));
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int bl = 0; bl < G; ++bl) big = __hmax2(big, __habs2(u32_as_h2(vs[h][bl])));
-            raise |= !__hble2(big, top);
             if (__any_sync(0xffffffffu, raise)) {
                 unsigned bits = max(h2_as_u32(big) & 0x7fffu, (h2_as_u32(big) >> 16) & 0x7fffu);
                 if (bits > 0x7bffu) bits = 0;  // a NaN scale has no size
                 bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
                 bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
-                // 2^(e - 15) <= the largest scale < 2^(e - 14) (e = 0 below the normals)
-                const int e = (int)(bits >> 10), want = min(kSigmaMax, kTop - (e - 14));
+                // 2^(e - 1) <= the largest scale < 2^e (or below, for a subnormal one)
+                const int e = (int)(bits >> 10) - 14;
                 float move = 1.f;
-                if (e - 14 + sigma > kTop + kHeadroom) {
-                    move = pow2f(want - sigma);
+                if (bits && (sigma > kSigmaMax || e + sigma > 0)) {
+                    const int want = e <= 0 && e > kSmall && (sigma > kSigmaMax || sigma > 0) ? 0 : min(kSigmaMax, kTop - e);
+                    if (sigma <= kSigmaMax) move = pow2f(want - sigma);
                     sigma = want;
-                    up = __float2half2_rn(pow2f(sigma));
-                    top = __float2half2_rn(fminf(pow2f(kTop + kHeadroom - sigma), 65504.f));
+                    top = __float2half2_rn(fminf(pow2f(-sigma), 65504.f));
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float mn = fmaxf(m[nt], mx[nt]);
-                    const float f = mn == m[nt] ? 1.f : ex2(m[nt] - mn);
-                    m[nt] = mn;
-                    l[nt] *= f;
-                    const float f0 = __shfl_sync(0xffffffffu, f, 8 * i) * move, f1 = __shfl_sync(0xffffffffu, f, 8 * i + 4) * move;
+                    float f[2];
+#pragma unroll
+                    for (int e2 = 0; e2 < 2; ++e2) {
+                        float v = mx[nt][e2];
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                        v = fmaxf(v, m[nt][e2]);
+                        f[e2] = v == m[nt][e2] ? 1.f : ex2(m[nt][e2] - v);
+                        m[nt][e2] = v;
+                        l[nt][e2] *= f[e2];
+                        f[e2] *= move;
+                    }
 #pragma unroll
                     for (int bl = 0; bl < G; ++bl)
 #pragma unroll
-                        for (int mu = 0; mu < 2; ++mu) {
-                            o[bl][mu][nt][0] *= f0, o[bl][mu][nt][1] *= f1;
-                            o[bl][mu][nt][2] *= f0, o[bl][mu][nt][3] *= f1;
-                        }
+                        for (int mu = 0; mu < 2; ++mu)
+#pragma unroll
+                            for (int c4 = 0; c4 < 4; ++c4) o[bl][mu][nt][c4] *= f[c4 & 1];
                 }
             }
-            uint32_t ph[2][NT];
+            float mm[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float mm = (m[nt] == -INFINITY ? 0.f : m[nt]) - kOffset;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float e0 = ex2(s[h][2 * nt] - mm), e1 = ex2(s[h][2 * nt + 1] - mm);
-                    l[nt] += e0 + e1;
-                    ph[h][nt] = pack_h2(e0, e1);
+                for (int e = 0; e < 2; ++e) mm[nt][e] = (m[nt][e] == -INFINITY ? 0.f : m[nt][e]) - kOffset;
+            const int lift = sigma > kSigmaMax ? 0 : sigma;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                if (z >= both) break;
+                const uint8_t* cell = sm.ring[warp][(used + z) % kStages];
+                uint32_t ph[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float e0 = ex2(fmaf(s[z][nt][2 * h], rf[nt][0], -mm[nt][0]));
+                        const float e1 = ex2(fmaf(s[z][nt][2 * h + 1], rf[nt][1], -mm[nt][1]));
+                        l[nt][0] += e0;
+                        l[nt][1] += e1;
+                        ph[nt][h] = transpose8(pack_h2(e0, e1));  // row g, tokens 8h + 2i, + 1
+                    }
+                const int pos0 = first + (k + z) * (kWarps * kCellTokens);
+                const bool masked = pos0 + kCellTokens > min_lim;
+                if (lift) {
+                    const __half2 up = __float2half2_rn(pow2f(lift));
+#pragma unroll
+                    for (int bl = 0; bl < G; ++bl)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) vs[z][h][bl] = h2_as_u32(__hmul2(u32_as_h2(vs[z][h][bl]), up));
                 }
-            }
+                uint32_t vw[2][G];
+                words(vw[0], cell + C::kV + lane * G * 4);
+                words(vw[1], cell + C::kV + (32 + lane) * G * 4);
 #pragma unroll
-            for (int bl = 0; bl < G; ++bl) {
-                uint32_t pb[2][NT];
+                for (int bl = 0; bl < G; ++bl) {
+                    uint32_t pb[NT][2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const __half2 d = __hmul2(u32_as_h2(vs[h][bl]), up);
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) pb[nt][h] = h2_as_u32(__hmul2(u32_as_h2(ph[nt][h]), u32_as_h2(vs[z][h][bl])));
+                    if (masked) {  // a hidden token's scale may be NaN
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int t = pos0 + 8 * h + 2 * i;
+                                pb[nt][h] &= (t < lim_row[nt] ? 0xffffu : 0u) | (t + 1 < lim_row[nt] ? 0xffff0000u : 0u);
+                            }
+                    }
+                    const uint32_t w0 = vw[0][bl], w1 = vw[1][bl], w08 = w0 >> 8, w18 = w1 >> 8;
+                    const uint32_t v0[4] = {centred_lo(w0), centred_hi(w0), centred_lo(w1), centred_hi(w1)};
+                    const uint32_t v1[4] = {centred_lo(w08), centred_hi(w08), centred_lo(w18), centred_hi(w18)};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        pb[h][nt] = h2_as_u32(__hmul2(u32_as_h2(ph[h][nt]), d));
-                        if (masked) pb[h][nt] &= keep[h][nt];
+                        mma_f16(o[bl][0][nt], v0, pb[nt][0], pb[nt][1]);
+                        mma_f16(o[bl][1][nt], v1, pb[nt][0], pb[nt][1]);
                     }
                 }
-                const uint32_t w0 = vw[0][bl], w1 = vw[1][bl], w08 = w0 >> 8, w18 = w1 >> 8;
-                const uint32_t v0[4] = {centred_lo(w0), centred_hi(w0), centred_lo(w1), centred_hi(w1)};
-                const uint32_t v1[4] = {centred_lo(w08), centred_hi(w08), centred_lo(w18), centred_hi(w18)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(o[bl][0][nt], v0, pb[0][nt], pb[1][nt]);
-                    mma_f16(o[bl][1][nt], v1, pb[0][nt], pb[1][nt]);
-                }
             }
-            ++used;
-            __syncwarp();  // every lane has read the slot
-            if (!dead) issue();
+            used += both;
+            dead = __any_sync(0xffffffffu, dead);  // and every lane has read the slots
+            if (!dead) {
+                issue();
+                if (both == 2) issue();
+            }
         }
 
         // --- the warps' sums into one
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
-            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
-            if (dead) l[nt] = __int_as_float(0x7fc00000);
-            if (i == 0) {
-                sm.m[warp][g + 8 * nt] = m[nt];
-                sm.l[warp][g + 8 * nt] = l[nt];
-            }
-        }
-        __syncthreads();
-        if (tid < kRows) {
-            float mm = -INFINITY, ll = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][tid]);
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) ll += sm.m[w][tid] == -INFINITY ? (sm.l[w][tid] != sm.l[w][tid] ? sm.l[w][tid] : 0.f)
-                                                                             : sm.l[w][tid] * ex2(sm.m[w][tid] - mm);
-            sm.mrow[tid] = mm;
-            sm.lrow[tid] = ll;
-        }
-        {
-            const float unit = pow2f(24) * pow2f(-sigma);  // codes are q * 2^-24, value scales d * 2^sigma
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 8 * nt + 2 * i + e;
-                    float mm = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
-                    const float f = sm.m[warp][r] == -INFINITY ? 0.f : ex2(sm.m[warp][r] - mm) * unit;
-#pragma unroll
-                    for (int bl = 0; bl < G; ++bl)
-#pragma unroll
-                        for (int mu = 0; mu < 2; ++mu) {
-                            o[bl][mu][nt][e] = o[bl][mu][nt][e] * f;
-                            o[bl][mu][nt][2 + e] = o[bl][mu][nt][2 + e] * (f * 0.0625f);
-                        }
+                for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
+                if (dead) l[nt][e] = __int_as_float(0x7fc00000);
+                if (g == 0) {
+                    sm.m[warp][8 * nt + 2 * i + e] = m[nt][e];
+                    sm.l[warp][8 * nt + 2 * i + e] = l[nt][e];
                 }
-        }
-#pragma unroll
-        for (int half = kWarps / 2; half >= 1; half >>= 1) {
-            if (warp >= half && warp < 2 * half) {
-#pragma unroll
-                for (int bl = 0; bl < G; ++bl)
-#pragma unroll
-                    for (int mu = 0; mu < 2; ++mu)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                sm.tree[warp - half][8 * nt + 2 * i + (e & 1)][32 * bl + 16 * mu + g + 8 * (e >> 1)] = o[bl][mu][nt][e];
             }
-            __syncthreads();
-            if (warp < half) {
+        if (lane == 0) sm.unit[warp] = pow2f(24) * pow2f(sigma > kSigmaMax ? 0 : -sigma);  // of codes and scales
 #pragma unroll
-                for (int bl = 0; bl < G; ++bl)
+        for (int bl = 0; bl < G; ++bl)
 #pragma unroll
-                    for (int mu = 0; mu < 2; ++mu)
+            for (int mu = 0; mu < 2; ++mu)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float& t = sm.tree[warp][8 * nt + 2 * i + (e & 1)][32 * bl + 16 * mu + g + 8 * (e >> 1)];
-                                o[bl][mu][nt][e] += t;
-                                if (half == 1) t = o[bl][mu][nt][e];
-                            }
-            }
-            __syncthreads();
-        }
+                    for (int e = 0; e < 4; ++e)
+                        sm.o[warp][8 * nt + 2 * i + (e & 1)][32 * bl + 16 * mu + g + 8 * (e >> 1)] =
+                            e < 2 ? o[bl][mu][nt][e] : o[bl][mu][nt][e] * 0.0625f;
+        __syncthreads();
 
         // --- out, or to the item's other pieces
         auto put = [&](int r, int d, float4 v, float mm, float ll) {
@@ -607,24 +618,35 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 make_uint2(*reinterpret_cast<uint32_t*>(&y0), *reinterpret_cast<uint32_t*>(&y1));
         };
         const bool whole = p.u0 == 0 && p.u1 == p.s.units;
-        if (whole) {
-            for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
-                const int r = e / (D / 4), d = 4 * (e % (D / 4));
-                put(r, d, *reinterpret_cast<const float4*>(&sm.tree[0][r][d]), sm.mrow[r], sm.lrow[r]);
+        float* rec = a.partial + ((size_t)blockIdx.x * 2 + (p.u0 == 0 ? 1 : 0)) * kPartFloats(D);
+        for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
+            const int r = e / (D / 4), d = 4 * (e % (D / 4));
+            float mm = -INFINITY, ll = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float wm = sm.m[w][r], wl = sm.l[w][r];
+                const float f = wm == -INFINITY ? 0.f : ex2(wm - mm), fu = f * sm.unit[w];
+                const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][d]);
+                ll += wm == -INFINITY ? (wl != wl ? wl : 0.f) : f * wl;
+                v.x = fmaf(fu, x.x, v.x), v.y = fmaf(fu, x.y, v.y), v.z = fmaf(fu, x.z, v.z), v.w = fmaf(fu, x.w, v.w);
             }
-        } else {
+            if (whole) {
+                put(r, d, v, mm, ll);
+            } else {
+                __stcg(reinterpret_cast<float4*>(rec + r * D + d), v);
+                if (d == 0) {
+                    __stcg(rec + 16 * D + r, mm);
+                    __stcg(rec + 16 * D + 16 + r, ll);
+                }
+            }
+        }
+        if (!whole) {
             // CTAs that share the item: the one its first unit falls to .. the one its last falls to
             const long long x0 = p.x - p.u0, x1 = x0 + p.s.units - 1;
             const int c0 = (int)quotient((x0 + 1) * ctas - 1, total), c1 = (int)quotient((x1 + 1) * ctas - 1, total);
-            float* rec = a.partial + ((size_t)blockIdx.x * 2 + (p.u0 == 0 ? 1 : 0)) * kPartFloats(D);
-            for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
-                const int r = e / (D / 4), d = 4 * (e % (D / 4));
-                __stcg(reinterpret_cast<float4*>(rec + r * D + d), *reinterpret_cast<const float4*>(&sm.tree[0][r][d]));
-            }
-            if (tid < rows) {
-                __stcg(rec + 16 * D + tid, sm.mrow[tid]);
-                __stcg(rec + 16 * D + 16 + tid, sm.lrow[tid]);
-            }
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -635,26 +657,42 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             __syncthreads();
             if (sm.last) {
                 __threadfence();
+                auto record = [&](int cta) { return a.partial + ((size_t)cta * 2 + (cta == c0)) * kPartFloats(D); };
+                float* fac = &sm.o[0][0][0];  // [piece][row]: maxima, then factors
+                const int pieces = c1 - c0 + 1;
+                for (int e = tid; e < pieces * rows; e += kAttThreads)
+                    fac[(e / rows) * kRows + e % rows] = __ldcg(record(c0 + e / rows) + 16 * D + e % rows);
+                __syncthreads();
+                for (int r = warp; r < rows; r += kWarps) {  // a warp per row, lanes over the pieces
+                    float mm = -INFINITY, ll = 0.f;
+                    for (int q = lane; q < pieces; q += 32) mm = fmaxf(mm, fac[q * kRows + r]);
+#pragma unroll
+                    for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
+                    for (int q = lane; q < pieces; q += 32) {
+                        const float qm = fac[q * kRows + r], ql = __ldcg(record(c0 + q) + 16 * D + 16 + r);
+                        const float f = qm == -INFINITY ? 0.f : ex2(qm - mm);
+                        fac[q * kRows + r] = f;
+                        ll += qm == -INFINITY ? (ql != ql ? ql : 0.f) : f * ql;
+                    }
+#pragma unroll
+                    for (int off = 16; off; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
+                    if (lane == 0) sm.m[0][r] = mm, sm.l[0][r] = ll;
+                }
+                __syncthreads();
                 for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
                     const int r = e / (D / 4), d = 4 * (e % (D / 4));
-                    float mm = -INFINITY, ll = 0.f;
-                    for (int cta = c0; cta <= c1; ++cta)
-                        mm = fmaxf(mm, __ldcg(a.partial + ((size_t)cta * 2 + (cta == c0)) * kPartFloats(D) + 16 * D + r));
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int cta = c0; cta <= c1; ++cta) {
-                        const float* q = a.partial + ((size_t)cta * 2 + (cta == c0)) * kPartFloats(D);
-                        const float qm = __ldcg(q + 16 * D + r), ql = __ldcg(q + 16 * D + 16 + r);
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(q + r * D + d));
-                        const float f = qm == -INFINITY ? 0.f : ex2(qm - mm);
-                        ll += qm == -INFINITY ? (ql != ql ? ql : 0.f) : f * ql;
+#pragma unroll 8
+                    for (int q = 0; q < pieces; ++q) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(record(c0 + q) + r * D + d));
+                        const float f = fac[q * kRows + r];
                         v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
                     }
-                    put(r, d, v, mm, ll);
+                    put(r, d, v, sm.m[0][r], sm.l[0][r]);
                 }
             }
         }
-        __syncthreads();  // tree, m and l are free again
+        __syncthreads();  // o, m and l are free again
     }
     if (dead) {
         if (lane == 0) atomicOr(c.err, 2u);
