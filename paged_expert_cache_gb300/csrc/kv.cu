@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvDev c, KvBatch b
     }
     __half d0, d1;
     const uint32_t w0 = quantise8(x, d0), w1 = quantise8(y, d1);
-    uint8_t* cell = seq >= 0 && kind != 0 ? kv_cell<D>(c, b, seq, pos, head) : nullptr;
+    uint8_t* cell = seq >= 0 && kind != 0 ? kv_cell<D>(c, b, seq, pos >> 4, head) : nullptr;
     bad |= seq >= 0 && kind != 0 && !cell;
     if (bad) atomicOr(c.err, 1u);
     const int tc = pos & (kCellTokens - 1), i = lane & 3, b0 = lane >> 2, b1 = b0 + G / 2;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_read(KvDev c, KvBatch b, 
     }
     const int seq = live ? seq_of_row(cu, b.B, t) : -1;
     const int pos = seq >= 0 ? __ldg(b.kv_lens + seq) - (cu[seq + 1] - t) : -1;
-    const uint8_t* cell = seq >= 0 ? kv_cell<D>(c, b, seq, pos, head) : nullptr;
+    const uint8_t* cell = seq >= 0 ? kv_cell<D>(c, b, seq, pos >> 4, head) : nullptr;
     if (seq >= 0 && !cell) atomicOr(c.err, 1u);
     const int tc = pos & (kCellTokens - 1), i = lane & 3, b0 = lane >> 2, b1 = b0 + G / 2;
     uint32_t w0 = 0, w1 = 0;  // nibble e: dim 8i + e of the block
@@ -303,6 +303,7 @@ moe::KvDev dev_of(const moe_kv_t* h, int layer) {
     d.page_tokens = h->cfg.page_tokens;
     d.hq = h->cfg.q_heads;
     d.hkv = h->cfg.kv_heads;
+    d.cells_div = moe::fast_div((uint32_t)h->cfg.page_tokens / moe::kCellTokens);
     return d;
 }
 moe::KvBatch batch_of(const moe_kv_batch_t* b) {
@@ -405,7 +406,8 @@ moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
     if (const char* p = batch_problem(batch)) return refuse(p);
     if (T == 0) return MOE_OK;
     if (!q || !out) return refuse("NULL q or out");
-    if ((int64_t)T * (c.q_heads / c.kv_heads) > 0x7fff0000ll) return refuse("T is too large");
+    if (!moe::attend_fits(dev_of(h, layer), batch_of(batch), T))
+        return refuse("the batch is too large: more than 2^30 units of 128 cache tokens and 8 rows are possible");
     if (!(scale >= 0.f && scale <= 3.4028235e38f)) return refuse("scale must be finite and not negative");
     if (!rows_ok(q, q_stride, c.q_heads, c.head_dim) || ((uintptr_t)out & 15u))
         return refuse("q and out need 16-byte aligned rows: q_stride a multiple of 8 and not below q_heads * head_dim");

@@ -34,28 +34,42 @@ struct Cell {
     __device__ static int v_scale(int t, int b) { return (((t >> 3) * 4 + ((t & 7) >> 1)) * G + b) * 4 + (t & 1) * 2; }
 };
 
+// Division of 0 <= x < 2^31 by a divisor fixed on the host: with 2^(l - 1) < d
+// <= 2^l, x / d = (x + hi(x m)) / 2^l for m = 2^32 (2^l - d) / d + 1, rounded
+// down.
+struct FastDiv {
+    uint32_t m, l;
+    __device__ int div(int x) const { return (int)((__umulhi((uint32_t)x, m) + (uint32_t)x) >> l); }
+};
+inline FastDiv fast_div(uint32_t d) {
+    uint32_t l = 0;
+    while ((1u << l) < d) ++l;
+    return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l};
+}
+
 // What the kernels need of a handle and a batch, by value.
 struct KvDev {
     uint8_t* pool;        // this layer's pages
     unsigned* err;        // sticky bits: 1 a position or page out of range, 2 a wait gave up
     uint64_t page_bytes;
     int num_pages, page_tokens, hq, hkv;
+    FastDiv cells_div;    // by the cells of a page and head
 };
 struct KvBatch {
     const int *cu, *kv_lens, *table;
     int B, table_stride;
 };
 
-// The cell of position `pos` for head `head`, or null where the table or the
-// pool has no such page.
+// Cell `n` of a sequence (positions 16 n ..) for head `head`, or null where the
+// table or the pool has no such page.
 template <int D>
-__device__ __forceinline__ uint8_t* kv_cell(const KvDev& c, const KvBatch& b, int seq, int pos, int head) {
-    if (pos < 0) return nullptr;
-    const int pg = pos / c.page_tokens;
+__device__ __forceinline__ uint8_t* kv_cell(const KvDev& c, const KvBatch& b, int seq, int n, int head) {
+    if (n < 0) return nullptr;
+    const int pg = c.cells_div.div(n);
     if (pg >= b.table_stride) return nullptr;
     const int page = __ldg(b.table + (size_t)seq * b.table_stride + pg);
     if ((unsigned)page >= (unsigned)c.num_pages) return nullptr;
-    const int cells = c.page_tokens / kCellTokens, in = (pos - pg * c.page_tokens) / kCellTokens;
+    const int cells = c.page_tokens / kCellTokens, in = n - pg * cells;
     return c.pool + (size_t)page * c.page_bytes + (size_t)(head * cells + in) * Cell<D>::kBytes;
 }
 
@@ -74,6 +88,8 @@ __device__ __forceinline__ int seq_of_row(const int* cu, int B, int t) {
 
 // Device scratch of the attention kernel on `device`, zeroed once.
 uint64_t attend_scratch_bytes(int device);
+// Whether every piece of work of such a call can be numbered in 31 bits.
+bool attend_fits(const KvDev& c, const KvBatch& b, int T);
 void launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
                    uint16_t* out, void* scratch, cudaStream_t st);
 

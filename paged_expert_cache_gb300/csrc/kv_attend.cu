@@ -36,6 +36,9 @@
 // Softmax statistics, sums and outputs are fp32. A row's running maximum is
 // raised only when a score exceeds it by 2^kLazy, the outputs being rescaled
 // then.
+#include <algorithm>
+#include <type_traits>
+
 #include "kv.cuh"
 
 namespace moe {
@@ -43,14 +46,15 @@ namespace moe {
 constexpr int kWarps = 8;
 constexpr int kAttThreads = 32 * kWarps;
 constexpr int kStages = 4;
+constexpr int kMaxCtas = 304;             // two per SM
 // fp16's range for the product p * d. A row's largest weight is 2^kOffset when
 // its maximum is set and may grow by 2^kLazy. The value blocks' scales are
-// multiplied by 2^sigma: 0 while the largest met is below 1 and was not below
+// multiplied by 2^sigma: 0 while the largest met is below 2 and was not below
 // 2^kSmall when first met, else at most kSigmaMax and such that it comes to
-// between 2^(kTop - 1) and 2^kTop, and may grow to 1. So a product is below 2^15,
-// and weights down to 2^-26 of the largest still count.
-constexpr float kLazy = 4.0f, kOffset = 11.0f;
-constexpr int kSigmaMax = 15, kTop = -4, kSmall = -8;
+// between 2^(kTop - 1) and 2^kTop, and may grow to 2. So a product is below 2^15,
+// and weights down to 2^-25 of the largest still count.
+constexpr float kLazy = 4.0f, kOffset = 10.0f;
+constexpr int kSigmaMax = 15, kTop = -3, kSmall = -8;
 constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -60,6 +64,7 @@ struct AttendArgs {
     int T;
     float scale;
     uint16_t* out;
+    FastDiv group_div;
     float* partial;       // [grid][2] records: first and last piece of each CTA
     unsigned* arrived;    // [grid] pieces arrived at the item that starts in a CTA and ends elsewhere
 };
@@ -82,20 +87,19 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // What a sequence asks for. cells: of its context (one more than the table
 // has where the length is past it, so that the missing page is met).
 struct SeqWork {
-    int n, kv, cells, units, tiles;
-    long long work;
+    int t0, n, kv, cells, units, tiles, work;
 };
 template <int NT>
-__device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, int T, int seq) {
+__device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, int T, int group, int seq) {
     SeqWork s;
-    const int t0 = min(max(__ldg(b.cu + seq), 0), T), t1 = min(max(__ldg(b.cu + seq + 1), 0), T);
-    s.n = max(t1 - t0, 0);
+    s.t0 = min(max(__ldg(b.cu + seq), 0), T);
+    s.n = max(min(max(__ldg(b.cu + seq + 1), 0), T) - s.t0, 0);
     s.kv = __ldg(b.kv_lens + seq);
     const long long cap = (long long)b.table_stride * c.page_tokens + 1;
     s.cells = (int)((unsigned)((int)min((long long)max(s.kv, 0), cap) + kCellTokens - 1) / kCellTokens);
     s.units = max(1, (s.cells + kWarps - 1) / kWarps);
-    s.tiles = (s.n * (c.hq / c.hkv) + 8 * NT - 1) / (8 * NT);  // rows fit 31 bits
-    s.work = (long long)s.units * c.hkv * s.tiles;
+    s.tiles = (s.n * group + 8 * NT - 1) / (8 * NT);
+    s.work = s.units * c.hkv * s.tiles;
     return s;
 }
 
@@ -103,23 +107,22 @@ __device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, in
 struct Piece {
     int seq, head, tile, u0, u1;
     SeqWork s;
-    long long x, prefix;  // number of its first unit, and of its sequence's first
+    int x, prefix;  // number of its first unit, and of its sequence's first
 };
 
 // The piece that starts at unit x (x in seq's range), cut at `hi`.
-__device__ __forceinline__ void piece_at(Piece& p, long long x, long long hi) {
-    const long long off = x - p.prefix;
-    const long long item = quotient(off, p.s.units);
+__device__ __forceinline__ void piece_at(Piece& p, int x, int hi) {
+    const unsigned off = x - p.prefix, item = off / (unsigned)p.s.units;
     p.u0 = (int)(off - item * p.s.units);
-    p.u1 = (int)min((long long)p.s.units, p.u0 + (hi - x));
-    p.head = (int)quotient(item, p.s.tiles);
-    p.tile = (int)(item - (long long)p.head * p.s.tiles);
+    p.u1 = min(p.s.units, p.u0 + (hi - x));
+    p.head = p.s.tiles == 1 ? (int)item : (int)(item / (unsigned)p.s.tiles);
+    p.tile = (int)item - p.head * p.s.tiles;
     p.x = x;
 }
 // Steps to the next piece; false at `hi`. Whole warps.
 template <int NT>
-__device__ __forceinline__ bool next_piece(Piece& p, long long hi, const KvDev& c, const KvBatch& b, int T, int lane) {
-    const long long x = p.x + (p.u1 - p.u0);
+__device__ __forceinline__ bool next_piece(Piece& p, int hi, const KvDev& c, const KvBatch& b, int T, int group, int lane) {
+    const int x = p.x + (p.u1 - p.u0);
     if (x >= hi) return false;
     if (x >= p.prefix + p.s.work) {
         p.prefix += p.s.work;
@@ -132,7 +135,7 @@ __device__ __forceinline__ bool next_piece(Piece& p, long long hi, const KvDev& 
             if (s + 32 >= b.B) return false;
         }
         p.seq = s;
-        p.s = seq_work<NT>(c, b, T, s);
+        p.s = seq_work<NT>(c, b, T, group, s);
     }
     piece_at(p, x, hi);
     return true;
@@ -148,13 +151,15 @@ template <int D, int NT>
 struct AttSmem {
     static constexpr int kRows = 8 * NT, kPad = D + 4;
     alignas(128) uint8_t ring[kWarps][kStages][Cell<D>::kBytes];
-    float o[kWarps][kRows][kPad];        // the warps' outputs; then factors of an item's pieces
+    union {
+        float o[kWarps][kRows][kPad];    // the warps' outputs
+        float join[2][kMaxCtas * kRows]; // then maxima (factors) and sums of an item's pieces
+    };
     float m[kWarps][kRows], l[kWarps][kRows], unit[kWarps];
     alignas(8) unsigned long long bar[kWarps][kStages];
-    long long wsum[kWarps];
+    int wsum[kWarps];
     Piece cur[kWarps], ask[kWarps];  // a warp's piece at work and the one it asks for: rarely read, so not in registers
-    long long prefix;
-    int seq, last;
+    int prefix, seq, last;
 };
 
 constexpr int kPartFloats(int D) { return 16 * D + 32; }  // output rows, maxima, sums
@@ -186,11 +191,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
-// d = a b + c, c kept.
-__device__ __forceinline__ void mma_f16_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+// d = a b.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Transposes an 8 x 8 matrix of 16-bit values held two a lane (row lane / 4).
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -209,149 +214,214 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, i = lane & 3;
     const int group = c.hq / c.hkv;
 
-    // --- this CTA's run of units [lo, hi), and the sequence that lo falls in
     if (lane < kStages) abar_init(smem_addr(&sm.bar[warp][lane]));
-    long long total = 0;
-    auto block_scan = [&](long long w, long long& incl, long long& sum) {
-        incl = w;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    __syncwarp();
+
+    // --- this CTA's run of units [lo, hi), and the sequence that lo falls in.
+    // CTA x takes base units, the first `extra` CTAs one more.
+    int total = 0, ctas = 0, base = 0, extra = 0, lo = 0, hi = 0, seq = -1, prefix = 0;
+    auto share = [&]() {
+        ctas = min(total, (int)gridDim.x);
+        if ((int)blockIdx.x >= ctas) return false;
+        base = (unsigned)total / (unsigned)ctas;
+        extra = total - base * ctas;
+        lo = blockIdx.x * base + min((int)blockIdx.x, extra);
+        hi = lo + base + ((int)blockIdx.x < extra);
+        return true;
+    };
+    auto cta_of = [&](int x) {
+        const int wide = extra * (base + 1);
+        return x < wide ? (int)((unsigned)x / (unsigned)(base + 1)) : extra + (int)((unsigned)(x - wide) / (unsigned)base);
+    };
+    if (b.B <= 8 * 32) {
+        // every warp by itself: a lane takes a few neighbouring sequences
+        const int per = (b.B + 31) / 32, s0 = min(lane * per, b.B), s1 = min(s0 + per, b.B);
+        int mine = 0;
+        for (int s = s0; s < s1; ++s) mine += seq_work<NT>(c, b, a.T, group, s).work;
+        int upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += v;
+            const int v = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += v;
         }
-        if (lane == 31) sm.wsum[warp] = incl;
-        __syncthreads();
-        sum = 0;
-        long long before = 0;
+        total = __shfl_sync(0xffffffffu, upto, 31);
+        if (!share()) return;
+        const unsigned hit = __ballot_sync(0xffffffffu, lo < upto);
+        const int l = __ffs(hit) - 1;
+        seq = l * per;
+        prefix = __shfl_sync(0xffffffffu, upto - mine, l);
+        if (per > 1)
+            for (;; ++seq) {
+                const int w = seq_work<NT>(c, b, a.T, group, seq).work;
+                if (lo < prefix + w) break;
+                prefix += w;
+            }
+    } else {
+        auto block_scan = [&](int w, int& incl, int& sum) {
+            incl = w;
 #pragma unroll
-        for (int w2 = 0; w2 < kWarps; ++w2) {
-            if (w2 == warp) before = sum;
-            sum += sm.wsum[w2];
-        }
-        incl += before;
-        __syncthreads();
-    };
-    if (b.B > kAttThreads) {
-        long long mine = 0;
-        for (int s = tid; s < b.B; s += kAttThreads) mine += seq_work<NT>(c, b, a.T, s).work;
-        long long incl;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += v;
+            }
+            if (lane == 31) sm.wsum[warp] = incl;
+            __syncthreads();
+            sum = 0;
+            int before = 0;
+#pragma unroll
+            for (int w2 = 0; w2 < kWarps; ++w2) {
+                if (w2 == warp) before = sum;
+                sum += sm.wsum[w2];
+            }
+            incl += before;
+            __syncthreads();
+        };
+        int mine = 0, incl, sum, below = 0;
+        for (int s = tid; s < b.B; s += kAttThreads) mine += seq_work<NT>(c, b, a.T, group, s).work;
         block_scan(mine, incl, total);
-    }
-    long long lo = 0, hi = 0, base = 0;
-    long long ctas = 0;
-    for (int s0 = 0; s0 < b.B; s0 += kAttThreads) {
-        const int s = s0 + tid;
-        const long long w = s < b.B ? seq_work<NT>(c, b, a.T, s).work : 0;
-        long long incl, sum;
-        block_scan(w, incl, sum);
-        if (s0 == 0) {
-            if (b.B <= kAttThreads) total = sum;
-            ctas = min(total, (long long)gridDim.x);
-            if (blockIdx.x >= ctas) return;
-            lo = quotient((long long)blockIdx.x * total, ctas);
-            hi = quotient((long long)(blockIdx.x + 1) * total, ctas);
+        if (!share()) return;
+        for (int s0 = 0; s0 < b.B; s0 += kAttThreads) {
+            const int s = s0 + tid, w = s < b.B ? seq_work<NT>(c, b, a.T, group, s).work : 0;
+            block_scan(w, incl, sum);
+            incl += below;
+            if (incl - w <= lo && lo < incl) {
+                sm.seq = s;
+                sm.prefix = incl - w;
+            }
+            below += sum;
+            if (below > lo) break;
         }
-        incl += base;
-        if (incl - w <= lo && lo < incl) {
-            sm.seq = s;
-            sm.prefix = incl - w;
-        }
-        base += sum;
-        if (base > lo) break;
+        __syncthreads();
+        seq = sm.seq;
+        prefix = sm.prefix;
     }
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    __syncthreads();
 
-    // --- the warp's ring: `ask` is the piece being asked for, `p` the one at work
+    // --- the warp's ring: sm.ask is the piece being asked for, sm.cur the one at work
     auto keep_piece = [&](Piece& to, const Piece& from) {
         __syncwarp();
         if (lane == 0) to = from;
         __syncwarp();
     };
+    // steps a kept piece on; false (and the piece as it was) at the end of the run
+    auto step = [&](Piece& at) {
+        Piece p = at;
+        const bool there = next_piece<NT>(p, hi, c, b, a.T, group, lane);
+        if (there) keep_piece(at, p);
+        return there;
+    };
+    // row r of a piece's tile: new token and query head
+    auto token_head = [&](const Piece& p, int r, int& tok, int& head) {
+        const int row = p.tile * kRows + r;
+        tok = a.group_div.div(row);
+        head = p.head * group + row - tok * group;
+    };
+    auto rows_of = [&](const Piece& p) { return min(kRows, p.s.n * group - p.tile * kRows); };
+    uint4 u[NT][G];  // this lane's part of q: row 8 nt + g, dims 32 bl + 8 i ..
+    auto load_q = [&](const Piece& p) {
+        const int rows = rows_of(p);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = g + 8 * nt;
+            int tok, head;
+            token_head(p, r < rows ? r : 0, tok, head);
+            const uint16_t* src = a.q + (size_t)(p.s.t0 + tok) * a.qs + (size_t)head * D + 8 * i;
+#pragma unroll
+            for (int bl = 0; bl < G; ++bl) u[nt][bl] = __ldg(reinterpret_cast<const uint4*>(src + 32 * bl));
+        }
+    };
     int ask_n, ask_k = 0;
     {
         Piece p;
-        p.seq = sm.seq;
-        p.prefix = sm.prefix;
-        p.s = seq_work<NT>(c, b, a.T, p.seq);
+        p.seq = seq;
+        p.prefix = prefix;
+        p.s = seq_work<NT>(c, b, a.T, group, seq);
         piece_at(p, lo, hi);
+        load_q(p);
         ask_n = warp_cells(p, warp);
         keep_piece(sm.cur[warp], p);
         keep_piece(sm.ask[warp], p);
     }
-    // steps a kept piece on; false (and the piece as it was) at the end of the run
-    auto step = [&](Piece& at) {
-        Piece p = at;
-        const bool there = next_piece<NT>(p, hi, c, b, a.T, lane);
-        if (there) keep_piece(at, p);
-        return there;
-    };
     unsigned issued = 0, used = 0;
     bool more = true, dead = false;
     const uint8_t* addr = nullptr;
-    auto issue = [&]() {  // asks for the warp's next cell, if there is one
-        while (more && ask_k == ask_n) {
-            more = step(sm.ask[warp]);
-            ask_n = more ? warp_cells(sm.ask[warp], warp) : 0;
-            ask_k = 0;
-        }
-        if (!more) return;
-        if ((ask_k & 31) == 0) {
-            const int k = ask_k + lane;
-            const Piece& q = sm.ask[warp];
-            addr = k < ask_n ? kv_cell<D>(c, b, q.seq, ((q.u0 + k) * kWarps + warp) * kCellTokens, q.head) : nullptr;
-        }
-        if (lane == (ask_k & 31)) {
-            const int slot = issued % kStages;
-            const uint32_t bar = smem_addr(&sm.bar[warp][slot]);
-            if (addr) {
-                asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n" ::"r"(bar),
-                             "r"((uint32_t)C::kBytes)
-                             : "memory");
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                        smem_addr(sm.ring[warp][slot])),
-                    "l"(addr), "r"((uint32_t)C::kBytes), "r"(bar)
-                    : "memory");
-            } else {  // no such page: its values are NaN
-                atomicOr(c.err, 1u);
-                uint4* s = reinterpret_cast<uint4*>(sm.ring[warp][slot]);
-                for (int e = 0; e < C::kBytes / 16; ++e) s[e] = make_uint4(0, 0, 0, 0);
-                for (int e = C::kVs / 16; e < C::kBytes / 16; ++e) s[e] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-                asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.shared::cta.b64 st, [%0];\n}\n" ::"r"(bar) : "memory");
+    // Asks for the warp's next `want` cells, as far as there are some; a lane each.
+    auto issue = [&](int want) {
+        while (want > 0) {
+            while (more && ask_k == ask_n) {
+                more = step(sm.ask[warp]);
+                ask_n = more ? warp_cells(sm.ask[warp], warp) : 0;
+                ask_k = 0;
+                if (more && warp == 0) {  // the next piece's q on its way to L2
+                    const Piece& p = sm.ask[0];
+                    const int r = lane / (D / 64);
+                    if (r < rows_of(p)) {
+                        int tok, head;
+                        token_head(p, r, tok, head);
+                        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(
+                            a.q + (size_t)(p.s.t0 + tok) * a.qs + (size_t)head * D + 64 * (lane % (D / 64))));
+                    }
+                }
             }
+            if (!more) return;
+            if ((ask_k & 31) == 0) {  // the next 32 cells' places
+                const int k = ask_k + lane;
+                const Piece& q = sm.ask[warp];
+                addr = k < ask_n ? kv_cell<D>(c, b, q.seq, (q.u0 + k) * kWarps + warp, q.head) : nullptr;
+            }
+            const int now = min(min(want, ask_n - ask_k), 32 - (ask_k & 31)), nth = lane - (ask_k & 31);
+            if ((unsigned)nth < (unsigned)now) {
+                const int slot = (issued + nth) % kStages;
+                const uint32_t bar = smem_addr(&sm.bar[warp][slot]);
+                if (addr) {
+                    asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n" ::"r"(bar),
+                                 "r"((uint32_t)C::kBytes)
+                                 : "memory");
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                            smem_addr(sm.ring[warp][slot])),
+                        "l"(addr), "r"((uint32_t)C::kBytes), "r"(bar)
+                        : "memory");
+                } else {  // no such page: its values are NaN
+                    atomicOr(c.err, 1u);
+                    uint4* s = reinterpret_cast<uint4*>(sm.ring[warp][slot]);
+                    for (int e = 0; e < C::kVs / 16; ++e) s[e] = make_uint4(0, 0, 0, 0);
+                    for (int e = C::kVs / 16; e < C::kBytes / 16; ++e) s[e] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                    asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.shared::cta.b64 st, [%0];\n}\n" ::"r"(bar) : "memory");
+                }
+            }
+            issued += now;
+            ask_k += now;
+            want -= now;
         }
-        ++issued;
-        ++ask_k;
     };
-#pragma unroll 1
-    for (int k = 0; k < kStages; ++k) issue();
+    issue(kStages);
 
-    for (bool any = true; any; any = step(sm.cur[warp])) {
+    for (bool first_piece = true;; first_piece = false) {
+        if (!first_piece) {
+            if (!step(sm.cur[warp])) break;
+            load_q(sm.cur[warp]);
+        }
         const Piece& p = sm.cur[warp];
-        // --- rows of the piece: row r of the tile is query row tile * kRows + r of the head's n * group
-        const int t0 = min(max(__ldg(b.cu + p.seq), 0), a.T);
-        const int rows = min(kRows, p.s.n * group - p.tile * kRows);
+        const int rows = rows_of(p);
         uint32_t qb[NT][G][2][2];        // B registers of the scores, row 8 nt + g: k-step, (b0, b1)
-        float corr[NT][G][4];            // -8 sum(q) of rows 2i, 2i + 1, 2i, 2i + 1
+        float corr[NT][G][2];            // -8 sum(q) of rows 2i, 2i + 1, for codes of 2^-24
         float rf[NT][2];                 // scores to log2 units, rows 2i, 2i + 1
         int lim[NT][2], lim_row[NT];     // positions seen by rows 2i, 2i + 1, and by row g
         int min_lim = 0x7fffffff;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = g + 8 * nt;
-            const int row = p.tile * kRows + (r < rows ? r : 0);
-            const int tok = (int)((unsigned)row / (unsigned)group), head = p.head * group + row - tok * group;
+            int tok, head;
+            token_head(p, r < rows ? r : 0, tok, head);
             lim_row[nt] = p.s.kv - p.s.n + tok + 1;
             min_lim = min(min_lim, lim_row[nt]);
-            uint4 u[G];
-            const uint16_t* src = a.q + (size_t)(t0 + tok) * a.qs + (size_t)head * D + 8 * i;
             unsigned mx = 0;
 #pragma unroll
             for (int bl = 0; bl < G; ++bl) {
-                u[bl] = __ldg(reinterpret_cast<const uint4*>(src + 32 * bl));
-                mx = max(max(mx, bf16x2_absmax(u[bl].x)), max(bf16x2_absmax(u[bl].y), max(bf16x2_absmax(u[bl].z), bf16x2_absmax(u[bl].w))));
+                const uint4 w = u[nt][bl];
+                mx = max(max(mx, bf16x2_absmax(w.x)), max(bf16x2_absmax(w.y), max(bf16x2_absmax(w.z), bf16x2_absmax(w.w))));
             }
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -359,7 +429,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             const float f = pow2f(-sh);
 #pragma unroll
             for (int bl = 0; bl < G; ++bl) {
-                const uint32_t w[4] = {u[bl].x, u[bl].y, u[bl].z, u[bl].w};
+                const uint32_t w[4] = {u[nt][bl].x, u[nt][bl].y, u[nt][bl].z, u[nt][bl].w};
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -374,7 +444,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 sum *= -8.0f / 16777216.0f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) corr[nt][bl][e] = corr[nt][bl][2 + e] = __shfl_sync(0xffffffffu, sum, 8 * i + 4 * e);
+                for (int e = 0; e < 2; ++e) corr[nt][bl][e] = __shfl_sync(0xffffffffu, sum, 8 * i + 4 * e);
             }
             // a scale of zero still hides what is hidden: -inf times a tiny factor is -inf
             const float fac = fmaxf(a.scale * kLog2e * 16777216.0f * pow2f(sh), 1e-37f);
@@ -393,7 +463,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
         int sigma = kSigmaMax + 1;   // none yet
-        __half2 top = __float2half2_rn(0.f);
+        uint32_t watch = ~0u;        // bits of a value scale that call for a look at sigma
 
         const int cells = warp_cells(p, warp), first = (p.u0 * kWarps + warp) * kCellTokens;
         auto words = [&](uint32_t (&r)[G], const uint8_t* src) {
@@ -405,90 +475,99 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 r[0] = v.x, r[1] = v.y;
             }
         };
-#pragma unroll 1
-        for (int k = 0; k < cells; k += 2) {
-            // two cells at a time where there are two
-            const int both = k + 1 < cells ? 2 : 1;
-            float s[2][NT][4];       // c0, c1: token g, rows 2i, 2i + 1; c2, c3: token g + 8
-            uint32_t vs[2][2][G];    // value scales
-            __half2 big = __float2half2_rn(0.f);
+        // Z cells, from the warp's k-th
+        auto cells_step = [&](int k, auto count) {
+            constexpr int Z = decltype(count)::value;
+            float s[Z][NT][4];       // c0, c1: token g, rows 2i, 2i + 1; c2, c3: token g + 8
+            uint32_t vs[Z][2][G];    // value scales
+            uint32_t seen = 0;       // their bits
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
+            for (int z = 0; z < Z; ++z) {
+                const int slot = (used + z) % kStages;
+                const uint32_t bar = smem_addr(&sm.bar[warp][slot]), parity = ((used + z) / kStages) & 1;
+                if (!abar_try(bar, parity) && !dead && !abar_wait_long(bar, parity)) dead = true;
+            }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int z = 0; z < Z; ++z) {
+                const uint8_t* cell = sm.ring[warp][(used + z) % kStages];
+                uint32_t kw[2][G];
+                __half2 ks[2][G / 2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[z][nt][e] = -INFINITY;
-                if (z < both) {
-                    const int slot = (used + z) % kStages;
-                    const uint32_t bar = smem_addr(&sm.bar[warp][slot]), parity = ((used + z) / kStages) & 1;
-                    if (!dead && !abar_try(bar, parity) && !abar_wait_long(bar, parity)) dead = true;
-                    const uint8_t* cell = sm.ring[warp][slot];
-                    uint32_t kw[2][G];
-                    __half2 ks[2][G / 2];
+                for (int h = 0; h < 2; ++h) {
+                    words(kw[h], cell + (h * 32 + lane) * G * 4);
+                    words(vs[z][h], cell + C::kVs + (h * 4 + i) * G * 4);
+                    if constexpr (G == 4) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(cell + C::kKs + (8 * h + g) * G * 2);
+                        ks[h][0] = u32_as_h2(v.x), ks[h][1] = u32_as_h2(v.y);
+                    } else {
+                        ks[h][0] = *reinterpret_cast<const __half2*>(cell + C::kKs + (8 * h + g) * G * 2);
+                    }
+                }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        words(kw[h], cell + (h * 32 + lane) * G * 4);
-                        words(vs[z][h], cell + C::kVs + (h * 4 + i) * G * 4);
-                        if constexpr (G == 4) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(cell + C::kKs + (8 * h + g) * G * 2);
-                            ks[h][0] = u32_as_h2(v.x), ks[h][1] = u32_as_h2(v.y);
-                        } else {
-                            ks[h][0] = *reinterpret_cast<const __half2*>(cell + C::kKs + (8 * h + g) * G * 2);
+                for (int bl = 0; bl < G; ++bl) {
+                    const uint32_t w0 = kw[0][bl], w1 = kw[1][bl], w08 = w0 >> 8, w18 = w1 >> 8;
+                    const uint32_t a0[4] = {w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u};
+                    const uint32_t a1[4] = {w08 & 0x000f000fu, w18 & 0x000f000fu, w08 & 0x00f000f0u, w18 & 0x00f000f0u};
+                    const float d0 = bl & 1 ? __high2float(ks[0][bl / 2]) : __low2float(ks[0][bl / 2]);
+                    const float d1 = bl & 1 ? __high2float(ks[1][bl / 2]) : __low2float(ks[1][bl / 2]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float acc[4];
+                        mma_f16_zero(acc, a0, qb[nt][bl][0][0], qb[nt][bl][0][1]);
+                        mma_f16(acc, a1, qb[nt][bl][1][0], qb[nt][bl][1][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float d = e < 2 ? d0 : d1, x = acc[e] + corr[nt][bl][e & 1];
+                            s[z][nt][e] = bl ? fmaf(x, d, s[z][nt][e]) : x * d;
                         }
                     }
+                    seen |= vs[z][0][bl] | vs[z][1][bl];
+                }
+                const int pos0 = first + (k + z) * (kWarps * kCellTokens);
+                if (pos0 + kCellTokens > min_lim) {
 #pragma unroll
-                    for (int bl = 0; bl < G; ++bl) {
-                        const uint32_t w0 = kw[0][bl], w1 = kw[1][bl], w08 = w0 >> 8, w18 = w1 >> 8;
-                        const uint32_t a0[4] = {w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u};
-                        const uint32_t a1[4] = {w08 & 0x000f000fu, w18 & 0x000f000fu, w08 & 0x00f000f0u, w18 & 0x00f000f0u};
-                        const float d0 = bl & 1 ? __high2float(ks[0][bl / 2]) : __low2float(ks[0][bl / 2]);
-                        const float d1 = bl & 1 ? __high2float(ks[1][bl / 2]) : __low2float(ks[1][bl / 2]);
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float acc[4];
-                            mma_f16_c(acc, a0, qb[nt][bl][0][0], qb[nt][bl][0][1], corr[nt][bl]);
-                            mma_f16(acc, a1, qb[nt][bl][1][0], qb[nt][bl][1][1]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                s[z][nt][e] = bl ? fmaf(acc[e], e < 2 ? d0 : d1, s[z][nt][e]) : acc[e] * (e < 2 ? d0 : d1);
-                        }
-                        big = __hmax2(big, __hmax2(__habs2(u32_as_h2(vs[z][0][bl])), __habs2(u32_as_h2(vs[z][1][bl]))));
-                    }
-                    const int pos0 = first + (k + z) * (kWarps * kCellTokens);
-                    if (pos0 + kCellTokens > min_lim) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (pos0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) s[z][nt][e] = -INFINITY;
-                    }
+                        for (int e = 0; e < 4; ++e)
+                            if (pos0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) s[z][nt][e] = -INFINITY;
                 }
             }
             // Do the running maxima and the running scale of the value blocks
             // still do? A lane looks at its own scores; only if one does not are
             // the maxima shared.
-            bool raise = !__hble2(big, top);
+            bool raise = (seen & watch) != 0;
             float mx[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    mx[nt][e] = rf[nt][e] * fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+                    float v = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
+                    if (Z == 2) v = fmaxf(v, fmaxf(s[Z - 1][nt][e], s[Z - 1][nt][e + 2]));
+                    mx[nt][e] = rf[nt][e] * v;
                     raise |= mx[nt][e] > m[nt][e] + kLazy;
                 }
             if (__any_sync(0xffffffffu, raise)) {
-                unsigned bits = max(h2_as_u32(big) & 0x7fffu, (h2_as_u32(big) >> 16) & 0x7fffu);
-                if (bits > 0x7bffu) bits = 0;  // a NaN scale has no size
+                float move = 1.f;
+                unsigned bits = 0;
+#pragma unroll
+                for (int z = 0; z < Z; ++z)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int bl = 0; bl < G; ++bl) {
+                            const unsigned x = vs[z][h][bl] & 0x7fffu, y = (vs[z][h][bl] >> 16) & 0x7fffu;
+                            bits = max(bits, max(x > 0x7bffu ? 0u : x, y > 0x7bffu ? 0u : y));  // NaN has no size
+                        }
                 bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
                 bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
                 // 2^(e - 1) <= the largest scale < 2^e (or below, for a subnormal one)
                 const int e = (int)(bits >> 10) - 14;
-                float move = 1.f;
-                if (bits && (sigma > kSigmaMax || e + sigma > 0)) {
-                    const int want = e <= 0 && e > kSmall && (sigma > kSigmaMax || sigma > 0) ? 0 : min(kSigmaMax, kTop - e);
+                if (bits && (sigma > kSigmaMax || e + sigma > 1)) {
+                    const int want = e <= 1 && e > kSmall && (sigma > kSigmaMax || sigma > 0) ? 0 : min(kSigmaMax, kTop - e);
                     if (sigma <= kSigmaMax) move = pow2f(want - sigma);
                     sigma = want;
-                    top = __float2half2_rn(fminf(pow2f(-sigma), 65504.f));
+                    // at sigma 0 a scale of 2 or more has its top exponent bit set; elsewhere every step looks
+                    watch = want == 0 ? 0x40004000u : ~0u;
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -498,7 +577,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                         float v = mx[nt][e2];
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-                        v = fmaxf(v, m[nt][e2]);
+                        // raised where it is exceeded by enough, so that a look at sigma alone changes no row
+                        v = v > m[nt][e2] + kLazy ? v : m[nt][e2];
                         f[e2] = v == m[nt][e2] ? 1.f : ex2(m[nt][e2] - v);
                         m[nt][e2] = v;
                         l[nt][e2] *= f[e2];
@@ -518,9 +598,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 #pragma unroll
                 for (int e = 0; e < 2; ++e) mm[nt][e] = (m[nt][e] == -INFINITY ? 0.f : m[nt][e]) - kOffset;
             const int lift = sigma > kSigmaMax ? 0 : sigma;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                if (z >= both) break;
+            // values of cell z; `masked`: some row does not see all of it
+            auto values = [&](int z, auto masked) {
                 const uint8_t* cell = sm.ring[warp][(used + z) % kStages];
                 uint32_t ph[NT][2];
 #pragma unroll
@@ -533,34 +612,23 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                         l[nt][1] += e1;
                         ph[nt][h] = transpose8(pack_h2(e0, e1));  // row g, tokens 8h + 2i, + 1
                     }
-                const int pos0 = first + (k + z) * (kWarps * kCellTokens);
-                const bool masked = pos0 + kCellTokens > min_lim;
-                if (lift) {
-                    const __half2 up = __float2half2_rn(pow2f(lift));
-#pragma unroll
-                    for (int bl = 0; bl < G; ++bl)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) vs[z][h][bl] = h2_as_u32(__hmul2(u32_as_h2(vs[z][h][bl]), up));
-                }
                 uint32_t vw[2][G];
                 words(vw[0], cell + C::kV + lane * G * 4);
                 words(vw[1], cell + C::kV + (32 + lane) * G * 4);
+                const int pos0 = first + (k + z) * (kWarps * kCellTokens);
 #pragma unroll
                 for (int bl = 0; bl < G; ++bl) {
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) pb[nt][h] = h2_as_u32(__hmul2(u32_as_h2(ph[nt][h]), u32_as_h2(vs[z][h][bl])));
-                    if (masked) {  // a hidden token's scale may be NaN
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
+                        for (int h = 0; h < 2; ++h) {
+                            pb[nt][h] = h2_as_u32(__hmul2(u32_as_h2(ph[nt][h]), u32_as_h2(vs[z][h][bl])));
+                            if (decltype(masked)::value) {  // a hidden token's scale may be NaN
                                 const int t = pos0 + 8 * h + 2 * i;
                                 pb[nt][h] &= (t < lim_row[nt] ? 0xffffu : 0u) | (t + 1 < lim_row[nt] ? 0xffff0000u : 0u);
                             }
-                    }
+                        }
                     const uint32_t w0 = vw[0][bl], w1 = vw[1][bl], w08 = w0 >> 8, w18 = w1 >> 8;
                     const uint32_t v0[4] = {centred_lo(w0), centred_hi(w0), centred_lo(w1), centred_hi(w1)};
                     const uint32_t v1[4] = {centred_lo(w08), centred_hi(w08), centred_lo(w18), centred_hi(w18)};
@@ -570,14 +638,31 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                         mma_f16(o[bl][1][nt], v1, pb[nt][0], pb[nt][1]);
                     }
                 }
+            };
+            if (lift) {
+                const __half2 up = __float2half2_rn(pow2f(lift));
+#pragma unroll
+                for (int z = 0; z < Z; ++z)
+#pragma unroll
+                    for (int bl = 0; bl < G; ++bl)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) vs[z][h][bl] = h2_as_u32(__hmul2(u32_as_h2(vs[z][h][bl]), up));
             }
-            used += both;
+            if (first + (k + Z - 1) * (kWarps * kCellTokens) + kCellTokens > min_lim) {
+#pragma unroll
+                for (int z = 0; z < Z; ++z) values(z, std::true_type{});
+            } else {
+#pragma unroll
+                for (int z = 0; z < Z; ++z) values(z, std::false_type{});
+            }
+            used += Z;
             dead = __any_sync(0xffffffffu, dead);  // and every lane has read the slots
-            if (!dead) {
-                issue();
-                if (both == 2) issue();
-            }
-        }
+            if (!dead) issue(Z);
+        };
+        int k = 0;
+#pragma unroll 1
+        for (; k + 1 < cells; k += 2) cells_step(k, std::integral_constant<int, 2>{});
+        if (k < cells) cells_step(k, std::integral_constant<int, 1>{});
 
         // --- the warps' sums into one
 #pragma unroll
@@ -611,10 +696,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = mm == -INFINITY && ll == 0.f ? 0.f : x[e] * inv;
-            const int row = p.tile * kRows + r;
-            const int tok = (int)((unsigned)row / (unsigned)group), head = p.head * group + row - tok * group;
+            int tok, head;
+            token_head(p, r, tok, head);
             __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0], x[1]), y1 = __floats2bfloat162_rn(x[2], x[3]);
-            *reinterpret_cast<uint2*>(a.out + ((size_t)(t0 + tok) * c.hq + head) * D + d) =
+            *reinterpret_cast<uint2*>(a.out + ((size_t)(p.s.t0 + tok) * c.hq + head) * D + d) =
                 make_uint2(*reinterpret_cast<uint32_t*>(&y0), *reinterpret_cast<uint32_t*>(&y1));
         };
         const bool whole = p.u0 == 0 && p.u1 == p.s.units;
@@ -645,50 +730,79 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         }
         if (!whole) {
             // CTAs that share the item: the one its first unit falls to .. the one its last falls to
-            const long long x0 = p.x - p.u0, x1 = x0 + p.s.units - 1;
-            const int c0 = (int)quotient((x0 + 1) * ctas - 1, total), c1 = (int)quotient((x1 + 1) * ctas - 1, total);
-            __threadfence();
+            const int x0 = p.x - p.u0, c0 = cta_of(x0), pieces = cta_of(x0 + p.s.units - 1) - c0 + 1;
             __syncthreads();
             if (tid == 0) {
+                __threadfence();  // the CTA's record, then its arrival
                 const unsigned n = atomicAdd(a.arrived + c0, 1u) + 1u;
-                sm.last = n == (unsigned)(c1 - c0 + 1);
-                if (sm.last) a.arrived[c0] = 0;  // for the next call
+                sm.last = n == (unsigned)pieces;
+                if (sm.last) {
+                    a.arrived[c0] = 0;  // for the next call
+                    __threadfence();
+                }
             }
             __syncthreads();
             if (sm.last) {
-                __threadfence();
-                auto record = [&](int cta) { return a.partial + ((size_t)cta * 2 + (cta == c0)) * kPartFloats(D); };
-                float* fac = &sm.o[0][0][0];  // [piece][row]: maxima, then factors
-                const int pieces = c1 - c0 + 1;
-                for (int e = tid; e < pieces * rows; e += kAttThreads)
-                    fac[(e / rows) * kRows + e % rows] = __ldcg(record(c0 + e / rows) + 16 * D + e % rows);
-                __syncthreads();
-                for (int r = warp; r < rows; r += kWarps) {  // a warp per row, lanes over the pieces
-                    float mm = -INFINITY, ll = 0.f;
-                    for (int q = lane; q < pieces; q += 32) mm = fmaxf(mm, fac[q * kRows + r]);
+                auto record = [&](int q) { return a.partial + ((size_t)(c0 + q) * 2 + (q == 0)) * kPartFloats(D); };
+                if (pieces <= 8) {
+                    for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
+                        const int r = e / (D / 4), d = 4 * (e % (D / 4));
+                        float qm[8], ql[8];
+                        float4 x[8];
 #pragma unroll
-                    for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
-                    for (int q = lane; q < pieces; q += 32) {
-                        const float qm = fac[q * kRows + r], ql = __ldcg(record(c0 + q) + 16 * D + 16 + r);
-                        const float f = qm == -INFINITY ? 0.f : ex2(qm - mm);
-                        fac[q * kRows + r] = f;
-                        ll += qm == -INFINITY ? (ql != ql ? ql : 0.f) : f * ql;
-                    }
+                        for (int q = 0; q < 8; ++q) {
+                            const float* at = record(min(q, pieces - 1));
+                            qm[q] = __ldcg(at + 16 * D + r);
+                            ql[q] = __ldcg(at + 16 * D + 16 + r);
+                            x[q] = __ldcg(reinterpret_cast<const float4*>(at + r * D + d));
+                        }
+                        float mm = -INFINITY, ll = 0.f;
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int off = 16; off; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
-                    if (lane == 0) sm.m[0][r] = mm, sm.l[0][r] = ll;
-                }
-                __syncthreads();
-                for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
-                    const int r = e / (D / 4), d = 4 * (e % (D / 4));
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int q = 0; q < pieces; ++q) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(record(c0 + q) + r * D + d));
-                        const float f = fac[q * kRows + r];
-                        v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+                        for (int q = 0; q < 8; ++q) mm = fmaxf(mm, qm[q]);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            if (q >= pieces) break;
+                            const float f = qm[q] == -INFINITY ? 0.f : ex2(qm[q] - mm);
+                            ll += qm[q] == -INFINITY ? (ql[q] != ql[q] ? ql[q] : 0.f) : f * ql[q];
+                            v.x = fmaf(f, x[q].x, v.x), v.y = fmaf(f, x[q].y, v.y), v.z = fmaf(f, x[q].z, v.z), v.w = fmaf(f, x[q].w, v.w);
+                        }
+                        put(r, d, v, mm, ll);
                     }
-                    put(r, d, v, sm.m[0][r], sm.l[0][r]);
+                } else {
+                    float *fac = sm.join[0], *sum = sm.join[1];  // [piece][row]
+                    for (int e = tid; e < pieces * kRows; e += kAttThreads) {
+                        const float* at = record(e / kRows) + 16 * D + e % kRows;
+                        if (e % kRows < rows) fac[e] = __ldcg(at), sum[e] = __ldcg(at + 16);
+                    }
+                    __syncthreads();
+                    for (int r = warp; r < rows; r += kWarps) {  // a warp per row, lanes over the pieces
+                        float mm = -INFINITY, ll = 0.f;
+                        for (int q = lane; q < pieces; q += 32) mm = fmaxf(mm, fac[q * kRows + r]);
+#pragma unroll
+                        for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
+                        for (int q = lane; q < pieces; q += 32) {
+                            const float qm = fac[q * kRows + r], ql = sum[q * kRows + r];
+                            const float f = qm == -INFINITY ? 0.f : ex2(qm - mm);
+                            fac[q * kRows + r] = f;
+                            ll += qm == -INFINITY ? (ql != ql ? ql : 0.f) : f * ql;
+                        }
+#pragma unroll
+                        for (int off = 16; off; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
+                        if (lane == 0) sm.m[0][r] = mm, sm.l[0][r] = ll;
+                    }
+                    __syncthreads();
+                    for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
+                        const int r = e / (D / 4), d = 4 * (e % (D / 4));
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 16
+                        for (int q = 0; q < pieces; ++q) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4*>(record(q) + r * D + d));
+                            const float f = fac[q * kRows + r];
+                            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+                        }
+                        put(r, d, v, sm.m[0][r], sm.l[0][r]);
+                    }
                 }
             }
         }
@@ -701,6 +815,12 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
     }
 }
 
+bool attend_fits(const KvDev& c, const KvBatch& b, int T) {
+    const int64_t rows = (int64_t)T * (c.hq / c.hkv), tiles = rows / 8 + std::min<int64_t>(b.B, T);
+    const int64_t units = ((int64_t)b.table_stride * c.page_tokens + 1) / (kCellTokens * kWarps) + 1;
+    return rows < (1ll << 30) && (double)tiles * (double)units * (double)c.hkv < (double)(1ll << 30);
+}
+
 static int sm_count(int device) {
     static int counts[64] = {};
     if (device < 0 || device >= 64) return 152;
@@ -711,7 +831,7 @@ static int sm_count(int device) {
     }
     return counts[device];
 }
-static int max_grid(int device) { return 2 * sm_count(device); }
+static int max_grid(int device) { return std::min(2 * sm_count(device), kMaxCtas); }
 
 // Partial records, then the arrival counters.
 uint64_t attend_scratch_bytes(int device) {
@@ -733,12 +853,12 @@ void launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, i
     int dev = 0;
     cudaGetDevice(&dev);
     const int n = max_grid(dev);
-    AttendArgs a = {q, q_stride, T, scale, out, (float*)scratch,
+    AttendArgs a = {q, q_stride, T, scale, out, fast_div((uint32_t)(c.hq / c.hkv)), (float*)scratch,
                     (unsigned*)((uint8_t*)scratch + (size_t)n * 2 * kPartFloats(128) * sizeof(float))};
     // 16 rows at a time where a head has more than 8 rows in a step: group
     // heads times the new tokens of an average sequence
     const bool wide = (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
-    const int grid = wide ? sm_count(dev) : n;
+    const int grid = wide ? (n + 1) / 2 : n;
     if (D == 128) wide ? launch<128, 2>(c, b, a, grid, st) : launch<128, 1>(c, b, a, grid, st);
     else wide ? launch<64, 2>(c, b, a, grid, st) : launch<64, 1>(c, b, a, grid, st);
 }
