@@ -12,8 +12,10 @@
 // and every CTA takes an equal run of them, whatever the lengths are: the
 // lengths are read on the device, and a long sequence is spread over the whole
 // GPU. A run's pieces that cover an item only in part leave a partial sum
-// (maximum, sum, unnormalised output); the CTA that arrives last at the item
-// adds them in order, so the result does not depend on who is last.
+// (maximum, sum, unnormalised output), and a second small kernel, launched
+// behind the first, adds an item's pieces in order. (The last CTA to arrive
+// doing it instead cost each piece a fence and an atomic, about 2000 cycles, and
+// a long sequence one CTA's walk over 76 pieces, about 20000.)
 //
 // A warp owns every kWarps-th cell of the run: it asks for its cells kStages
 // ahead with bulk copies into a ring of its own, and never waits for another
@@ -66,7 +68,14 @@ struct AttendArgs {
     uint16_t* out;
     FastDiv group_div;
     float* partial;       // [grid][2] records: first and last piece of each CTA
-    unsigned* arrived;    // [grid] pieces arrived at the item that starts in a CTA and ends elsewhere
+    struct Split* split;  // [grid] the item that starts in a CTA and ends in another
+};
+
+// An item in several pieces, for the kernel that joins them: the last piece of
+// its CTA and the first ones of the next pieces - 1.
+struct Split {
+    int pieces;           // 0: none
+    int t0, head, tile, rows;
 };
 
 // (q - 8) 2^-24 of the codes at bits 0-3 and 16-19, (q - 8) 2^-20 of those at 4-7 and 20-23, as fp16 pairs.
@@ -151,15 +160,12 @@ template <int D, int NT>
 struct AttSmem {
     static constexpr int kRows = 8 * NT, kPad = D + 4;
     alignas(128) uint8_t ring[kWarps][kStages][Cell<D>::kBytes];
-    union {
-        float o[kWarps][kRows][kPad];    // the warps' outputs
-        float join[2][kMaxCtas * kRows]; // then maxima (factors) and sums of an item's pieces
-    };
+    float o[kWarps][kRows][kPad];    // the warps' outputs
     float m[kWarps][kRows], l[kWarps][kRows], unit[kWarps];
     alignas(8) unsigned long long bar[kWarps][kStages];
     int wsum[kWarps];
     Piece cur[kWarps], ask[kWarps];  // a warp's piece at work and the one it asks for: rarely read, so not in registers
-    int prefix, seq, last;
+    int prefix, seq;
 };
 
 constexpr int kPartFloats(int D) { return 16 * D + 32; }  // output rows, maxima, sums
@@ -205,6 +211,20 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return h2_as_u32(__floats2half2_rn(lo, hi)); }
 
+// Four dims of a row's output: sums v of weights times values over the sum l of
+// weights (m their maximum).
+template <int D>
+__device__ __forceinline__ void put_row(const KvDev& c, const AttendArgs& a, int t0, int head, int row, int d, float4 v, float m, float l) {
+    const int group = c.hq / c.hkv, tok = a.group_div.div(row);
+    const float inv = 1.0f / l;
+    float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = m == -INFINITY && l == 0.f ? 0.f : x[e] * inv;
+    __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0], x[1]), y1 = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2*>(a.out + ((size_t)(t0 + tok) * c.hq + head * group + row - tok * group) * D + d) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&y0), *reinterpret_cast<uint32_t*>(&y1));
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a) {
     constexpr int G = D / 32, kRows = 8 * NT;
@@ -218,12 +238,17 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     __syncwarp();
 
+    griddep_wait();    // the batch's arrays, and the last call's records
+    griddep_launch();  // k_join may be set up meanwhile
     // --- this CTA's run of units [lo, hi), and the sequence that lo falls in.
     // CTA x takes base units, the first `extra` CTAs one more.
     int total = 0, ctas = 0, base = 0, extra = 0, lo = 0, hi = 0, seq = -1, prefix = 0;
     auto share = [&]() {
         ctas = min(total, (int)gridDim.x);
-        if ((int)blockIdx.x >= ctas) return false;
+        if ((int)blockIdx.x >= ctas) {
+            if (tid == 0) a.split[blockIdx.x].pieces = 0;
+            return false;
+        }
         base = (unsigned)total / (unsigned)ctas;
         extra = total - base * ctas;
         lo = blockIdx.x * base + min((int)blockIdx.x, extra);
@@ -343,7 +368,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         keep_piece(sm.ask[warp], p);
     }
     unsigned issued = 0, used = 0;
-    bool more = true, dead = false;
+    bool more = true, dead = false, split_here = false;
     const uint8_t* addr = nullptr;
     // Asks for the warp's next `want` cells, as far as there are some; a lane each.
     auto issue = [&](int want) {
@@ -691,17 +716,6 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         __syncthreads();
 
         // --- out, or to the item's other pieces
-        auto put = [&](int r, int d, float4 v, float mm, float ll) {
-            const float inv = 1.0f / ll;
-            float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = mm == -INFINITY && ll == 0.f ? 0.f : x[e] * inv;
-            int tok, head;
-            token_head(p, r, tok, head);
-            __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0], x[1]), y1 = __floats2bfloat162_rn(x[2], x[3]);
-            *reinterpret_cast<uint2*>(a.out + ((size_t)(p.s.t0 + tok) * c.hq + head) * D + d) =
-                make_uint2(*reinterpret_cast<uint32_t*>(&y0), *reinterpret_cast<uint32_t*>(&y1));
-        };
         const bool whole = p.u0 == 0 && p.u1 == p.s.units;
         float* rec = a.partial + ((size_t)blockIdx.x * 2 + (p.u0 == 0 ? 1 : 0)) * kPartFloats(D);
         for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
@@ -719,7 +733,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 v.x = fmaf(fu, x.x, v.x), v.y = fmaf(fu, x.y, v.y), v.z = fmaf(fu, x.z, v.z), v.w = fmaf(fu, x.w, v.w);
             }
             if (whole) {
-                put(r, d, v, mm, ll);
+                put_row<D>(c, a, p.s.t0, p.head, p.tile * kRows + r, d, v, mm, ll);
             } else {
                 __stcg(reinterpret_cast<float4*>(rec + r * D + d), v);
                 if (d == 0) {
@@ -728,91 +742,66 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 }
             }
         }
-        if (!whole) {
-            // CTAs that share the item: the one its first unit falls to .. the one its last falls to
-            const int x0 = p.x - p.u0, c0 = cta_of(x0), pieces = cta_of(x0 + p.s.units - 1) - c0 + 1;
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();  // the CTA's record, then its arrival
-                const unsigned n = atomicAdd(a.arrived + c0, 1u) + 1u;
-                sm.last = n == (unsigned)pieces;
-                if (sm.last) {
-                    a.arrived[c0] = 0;  // for the next call
-                    __threadfence();
-                }
-            }
-            __syncthreads();
-            if (sm.last) {
-                auto record = [&](int q) { return a.partial + ((size_t)(c0 + q) * 2 + (q == 0)) * kPartFloats(D); };
-                if (pieces <= 8) {
-                    for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
-                        const int r = e / (D / 4), d = 4 * (e % (D / 4));
-                        float qm[8], ql[8];
-                        float4 x[8];
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float* at = record(min(q, pieces - 1));
-                            qm[q] = __ldcg(at + 16 * D + r);
-                            ql[q] = __ldcg(at + 16 * D + 16 + r);
-                            x[q] = __ldcg(reinterpret_cast<const float4*>(at + r * D + d));
-                        }
-                        float mm = -INFINITY, ll = 0.f;
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) mm = fmaxf(mm, qm[q]);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            if (q >= pieces) break;
-                            const float f = qm[q] == -INFINITY ? 0.f : ex2(qm[q] - mm);
-                            ll += qm[q] == -INFINITY ? (ql[q] != ql[q] ? ql[q] : 0.f) : f * ql[q];
-                            v.x = fmaf(f, x[q].x, v.x), v.y = fmaf(f, x[q].y, v.y), v.z = fmaf(f, x[q].z, v.z), v.w = fmaf(f, x[q].w, v.w);
-                        }
-                        put(r, d, v, mm, ll);
-                    }
-                } else {
-                    float *fac = sm.join[0], *sum = sm.join[1];  // [piece][row]
-                    for (int e = tid; e < pieces * kRows; e += kAttThreads) {
-                        const float* at = record(e / kRows) + 16 * D + e % kRows;
-                        if (e % kRows < rows) fac[e] = __ldcg(at), sum[e] = __ldcg(at + 16);
-                    }
-                    __syncthreads();
-                    for (int r = warp; r < rows; r += kWarps) {  // a warp per row, lanes over the pieces
-                        float mm = -INFINITY, ll = 0.f;
-                        for (int q = lane; q < pieces; q += 32) mm = fmaxf(mm, fac[q * kRows + r]);
-#pragma unroll
-                        for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
-                        for (int q = lane; q < pieces; q += 32) {
-                            const float qm = fac[q * kRows + r], ql = sum[q * kRows + r];
-                            const float f = qm == -INFINITY ? 0.f : ex2(qm - mm);
-                            fac[q * kRows + r] = f;
-                            ll += qm == -INFINITY ? (ql != ql ? ql : 0.f) : f * ql;
-                        }
-#pragma unroll
-                        for (int off = 16; off; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
-                        if (lane == 0) sm.m[0][r] = mm, sm.l[0][r] = ll;
-                    }
-                    __syncthreads();
-                    for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
-                        const int r = e / (D / 4), d = 4 * (e % (D / 4));
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 16
-                        for (int q = 0; q < pieces; ++q) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4*>(record(q) + r * D + d));
-                            const float f = fac[q * kRows + r];
-                            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
-                        }
-                        put(r, d, v, sm.m[0][r], sm.l[0][r]);
-                    }
-                }
-            }
+        if (tid == 0 && p.u0 == 0 && p.u1 < p.s.units) {
+            const int x0 = p.x, c1 = cta_of(x0 + p.s.units - 1);
+            a.split[blockIdx.x] = {c1 - (int)blockIdx.x + 1, p.s.t0, p.head, p.tile, rows};
+            split_here = true;
         }
         __syncthreads();  // o, m and l are free again
     }
+    if (tid == 0 && !split_here) a.split[blockIdx.x].pieces = 0;
     if (dead) {
         if (lane == 0) atomicOr(c.err, 2u);
         for (; used < issued; ++used)  // nothing of this warp is in flight when it leaves
             abar_wait_long(smem_addr(&sm.bar[warp][used % kStages]), (used / kStages) & 1);
     }
+}
+
+// Joins the pieces of split items: a block takes two rows of the item that
+// starts in CTA blockIdx.x, a warp a quarter of its pieces, a lane four dims.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
+    constexpr int kLanes = D / 4;                 // lanes of a row's dims
+    constexpr int kSets = 4 * 32 / kLanes;        // pieces taken side by side, of each row
+    __shared__ float4 part[2][kSets][kLanes];
+    __shared__ float lpart[2][kSets];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int half = warp >> 2, set = (warp & 3) * (32 / kLanes) + lane / kLanes, d = 4 * (lane % kLanes);
+    const int r = 2 * blockIdx.y + half;
+    griddep_wait();
+    const Split* at = a.split + blockIdx.x;
+    const Split s = {__ldcg(&at->pieces), __ldcg(&at->t0), __ldcg(&at->head), __ldcg(&at->tile), __ldcg(&at->rows)};
+    if (2 * (int)blockIdx.y >= s.rows || s.pieces == 0) return;
+    const bool mine = r < s.rows;
+    auto record = [&](int q) { return a.partial + ((size_t)(blockIdx.x + q) * 2 + (q == 0)) * kPartFloats(D); };
+    float m = -INFINITY;  // of all pieces
+    for (int q = lane; q < s.pieces; q += 32)
+        if (mine) m = fmaxf(m, __ldcg(record(q) + 16 * D + r));
+#pragma unroll
+    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    if (mine) {
+#pragma unroll 4
+        for (int q = set; q < s.pieces; q += kSets) {
+            const float* at = record(q);
+            const float qm = __ldcg(at + 16 * D + r), ql = __ldcg(at + 16 * D + 16 + r);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(at + r * D + d));
+            const float f = qm == -INFINITY ? 0.f : ex2(qm - m);
+            l += qm == -INFINITY ? (ql != ql ? ql : 0.f) : f * ql;
+            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+        }
+    }
+    part[half][set][lane % kLanes] = v;
+    if (lane % kLanes == 0) lpart[half][set] = l;
+    __syncthreads();
+    if (set != 0 || !mine) return;
+    for (int q = 1; q < kSets; ++q) {
+        const float4 x = part[half][q][lane % kLanes];
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        l += lpart[half][q];
+    }
+    put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
 }
 
 bool attend_fits(const KvDev& c, const KvBatch& b, int T) {
@@ -833,9 +822,9 @@ static int sm_count(int device) {
 }
 static int max_grid(int device) { return std::min(2 * sm_count(device), kMaxCtas); }
 
-// Partial records, then the arrival counters.
+// Partial records, then the split items.
 uint64_t attend_scratch_bytes(int device) {
-    return (uint64_t)max_grid(device) * (2 * kPartFloats(128) * sizeof(float) + sizeof(unsigned));
+    return (uint64_t)max_grid(device) * (2 * kPartFloats(128) * sizeof(float) + sizeof(Split));
 }
 
 template <int D, int NT>
@@ -845,7 +834,8 @@ static void launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, int gr
         cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT>));
         set = true;
     }
-    k_attend<D, NT><<<grid, kAttThreads, sizeof(AttSmem<D, NT>), st>>>(c, b, a);
+    launch_ex(k_attend<D, NT>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
+    launch_ex(k_join<D, NT>, dim3(grid, 4 * NT), dim3(256), 0, st, true, c, a);
 }
 
 void launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
@@ -854,7 +844,7 @@ void launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, i
     cudaGetDevice(&dev);
     const int n = max_grid(dev);
     AttendArgs a = {q, q_stride, T, scale, out, fast_div((uint32_t)(c.hq / c.hkv)), (float*)scratch,
-                    (unsigned*)((uint8_t*)scratch + (size_t)n * 2 * kPartFloats(128) * sizeof(float))};
+                    (Split*)((uint8_t*)scratch + (size_t)n * 2 * kPartFloats(128) * sizeof(float))};
     // 16 rows at a time where a head has more than 8 rows in a step: group
     // heads times the new tokens of an average sequence
     const bool wide = (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
