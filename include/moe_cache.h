@@ -514,7 +514,7 @@ moe_status_t moe_kv_info(const moe_kv_t* h, moe_kv_info_t* out);
 
 /* Synchronises and reports (then forgets) what the handle's kernels found:
  * MOE_ERR_INVALID if a call met a position or page out of range,
- * MOE_ERR_TIMEOUT if a bounded wait gave up, MOE_ERR_CUDA for a CUDA error. */
+ * MOE_ERR_CUDA for a CUDA error. */
 moe_status_t moe_kv_status(moe_kv_t* h);
 
 /* Synchronises and frees everything the handle owns. NULL is accepted. */

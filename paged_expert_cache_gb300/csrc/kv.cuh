@@ -50,7 +50,7 @@ inline FastDiv fast_div(uint32_t d) {
 // What the kernels need of a handle and a batch, by value.
 struct KvDev {
     uint8_t* pool;        // this layer's pages
-    unsigned* err;        // sticky bits: 1 a position or page out of range, 2 a wait gave up
+    unsigned* err;        // sticky: 1 once a position or page was out of range
     uint64_t page_bytes;
     int num_pages, page_tokens, hq, hkv;
     FastDiv cells_div;    // by the cells of a page and head

@@ -18,8 +18,10 @@
 // a long sequence one CTA's walk over 76 pieces, about 20000.)
 //
 // A warp owns every kWarps-th cell of the run: it asks for its cells kStages
-// ahead with bulk copies into a ring of its own, and never waits for another
-// warp before the end of an item. A cell is 2304 bytes at head_dim 128.
+// ahead with 16-byte asynchronous copies into a ring of its own, and never waits
+// for another warp before the end of an item. A cell is 2304 bytes at head_dim
+// 128. (One bulk copy and mbarrier per cell in their place cost a warp about
+// 1000 of 3200 cycles for every two cells: the issue alone 760.)
 //
 // Arithmetic. A 4-bit code q masked out of its word is the fp16 subnormal q *
 // 2^-24 (or q * 2^-20 for the upper nibble of a byte), which the tensor cores
@@ -49,6 +51,11 @@ constexpr int kWarps = 8;
 constexpr int kAttThreads = 32 * kWarps;
 constexpr int kStages = 4;
 constexpr int kMaxCtas = 304;             // two per SM
+// What beginning an item costs, in units: its rows to be fetched and laid out,
+// the warps' sums to be joined and written (about 7000 cycles, a unit 1500). Items
+// are numbered with so many idle units before their first, so that CTAs with
+// many short sequences get fewer cells.
+constexpr int kBegin = 4;
 // fp16's range for the product p * d. A row's largest weight is 2^kOffset when
 // its maximum is set and may grow by 2^kLazy. The value blocks' scales are
 // multiplied by 2^sigma: 0 while the largest met is below 2 and was not below
@@ -57,7 +64,6 @@ constexpr int kMaxCtas = 304;             // two per SM
 // and weights down to 2^-25 of the largest still count.
 constexpr float kLazy = 4.0f, kOffset = 10.0f;
 constexpr int kSigmaMax = 15, kTop = -3, kSmall = -8;
-constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -108,30 +114,34 @@ __device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, in
     s.cells = (int)((unsigned)((int)min((long long)max(s.kv, 0), cap) + kCellTokens - 1) / kCellTokens);
     s.units = max(1, (s.cells + kWarps - 1) / kWarps);
     s.tiles = (s.n * group + 8 * NT - 1) / (8 * NT);
-    s.work = s.units * c.hkv * s.tiles;
+    s.work = (s.units + kBegin) * c.hkv * s.tiles;
     return s;
 }
 
-// A piece of an item: units [u0, u1) of (sequence, head, row tile).
+// A piece of an item: units [u0, u1) of (sequence, head, row tile); none (u0 ==
+// u1) where the run ends in the item's idle units.
 struct Piece {
     int seq, head, tile, u0, u1;
     SeqWork s;
-    int x, prefix;  // number of its first unit, and of its sequence's first
+    int first, next, prefix;  // numbers of the item's first unit, of the one after the piece, of the sequence's first
 };
 
-// The piece that starts at unit x (x in seq's range), cut at `hi`.
+// The piece that starts at number x (x in seq's range), cut at `hi`.
 __device__ __forceinline__ void piece_at(Piece& p, int x, int hi) {
-    const unsigned off = x - p.prefix, item = off / (unsigned)p.s.units;
-    p.u0 = (int)(off - item * p.s.units);
-    p.u1 = min(p.s.units, p.u0 + (hi - x));
+    const int len = p.s.units + kBegin;
+    const unsigned off = x - p.prefix, item = off / (unsigned)len;
+    const int in = (int)(off - item * len), to = min(len, in + (hi - x));
+    p.u0 = max(in - kBegin, 0);
+    p.u1 = max(to - kBegin, 0);
     p.head = p.s.tiles == 1 ? (int)item : (int)(item / (unsigned)p.s.tiles);
     p.tile = (int)item - p.head * p.s.tiles;
-    p.x = x;
+    p.first = x - in + kBegin;
+    p.next = x - in + to;
 }
 // Steps to the next piece; false at `hi`. Whole warps.
 template <int NT>
 __device__ __forceinline__ bool next_piece(Piece& p, int hi, const KvDev& c, const KvBatch& b, int T, int group, int lane) {
-    const int x = p.x + (p.u1 - p.u0);
+    const int x = p.next;
     if (x >= hi) return false;
     if (x >= p.prefix + p.s.work) {
         p.prefix += p.s.work;
@@ -162,35 +172,12 @@ struct AttSmem {
     alignas(128) uint8_t ring[kWarps][kStages][Cell<D>::kBytes];
     float o[kWarps][kRows][kPad];    // the warps' outputs
     float m[kWarps][kRows], l[kWarps][kRows], unit[kWarps];
-    alignas(8) unsigned long long bar[kWarps][kStages];
     int wsum[kWarps];
     Piece cur[kWarps], ask[kWarps];  // a warp's piece at work and the one it asks for: rarely read, so not in registers
     int prefix, seq;
 };
 
 constexpr int kPartFloats(int D) { return 16 * D + 32; }  // output rows, maxima, sums
-
-__device__ __forceinline__ void abar_init(uint32_t bar) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool abar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok;
-}
-__device__ __noinline__ bool abar_wait_long(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = globaltimer_ns();
-    for (unsigned it = 0; it < (1u << 26); ++it) {
-        if (abar_try(bar, parity)) return true;
-        if (globaltimer_ns() - t0 > kWaitNs) break;
-    }
-    return false;
-}
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -233,10 +220,6 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
     AttSmem<D, NT>& sm = *reinterpret_cast<AttSmem<D, NT>*>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, i = lane & 3;
     const int group = c.hq / c.hkv;
-
-    if (lane < kStages) abar_init(smem_addr(&sm.bar[warp][lane]));
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    __syncwarp();
 
     griddep_wait();    // the batch's arrays, and the last call's records
     griddep_launch();  // k_join may be set up meanwhile
@@ -328,10 +311,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         if (lane == 0) to = from;
         __syncwarp();
     };
-    // steps a kept piece on; false (and the piece as it was) at the end of the run
+    // steps a kept piece on; false (and the piece as it was) at the end of the run, an item's idle units among it
     auto step = [&](Piece& at) {
         Piece p = at;
-        const bool there = next_piece<NT>(p, hi, c, b, a.T, group, lane);
+        const bool there = next_piece<NT>(p, hi, c, b, a.T, group, lane) && p.u1 > p.u0;
         if (there) keep_piece(at, p);
         return there;
     };
@@ -362,15 +345,43 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         p.prefix = prefix;
         p.s = seq_work<NT>(c, b, a.T, group, seq);
         piece_at(p, lo, hi);
+        if (p.u1 == p.u0) {  // a run of idle units only
+            if (tid == 0) a.split[blockIdx.x].pieces = 0;
+            return;
+        }
         load_q(p);
         ask_n = warp_cells(p, warp);
         keep_piece(sm.cur[warp], p);
         keep_piece(sm.ask[warp], p);
     }
     unsigned issued = 0, used = 0;
-    bool more = true, dead = false, split_here = false;
+    bool more = true, split_here = false;
     const uint8_t* addr = nullptr;
-    // Asks for the warp's next `want` cells, as far as there are some; a lane each.
+    const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(sm.ring[warp][0]) + 16 * lane;
+    // Copies the cell whose place lane `from` has into the ring.
+    auto copy_cell = [&](int from, int slot) {
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(addr), from));
+        constexpr int kChunks = C::kBytes / 16;
+        if (src) {
+            const uint8_t* at = src + 16 * lane;
+            const uint32_t to = ring0 + slot * C::kBytes;
+#pragma unroll
+            for (int e = 0; e < kChunks; e += 32)
+                if (e + 32 <= kChunks || lane < kChunks - e)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to + 16 * e), "l"(at + 16 * e) : "memory");
+        } else {  // no such page: its values are NaN
+            if (lane == 0) atomicOr(c.err, 1u);
+            uint8_t* dst = sm.ring[warp][slot];
+            for (int e = lane; e < kChunks; e += 32) {
+                const uint32_t w = e < C::kVs / 16 ? 0u : 0x7fff7fffu;
+                *reinterpret_cast<uint4*>(dst + 16 * e) = make_uint4(w, w, w, w);
+            }
+        }
+    };
+    // Asks for the warp's next `want` cells, as far as there are some, and closes
+    // the group of these copies. All groups but the last one hold all but the
+    // last one or two of the ring's cells: a step waits for those.
     auto issue = [&](int want) {
         while (want > 0) {
             while (more && ask_k == ask_n) {
@@ -388,40 +399,21 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                     }
                 }
             }
-            if (!more) return;
+            if (!more) break;
             if ((ask_k & 31) == 0) {  // the next 32 cells' places
                 const int k = ask_k + lane;
                 const Piece& q = sm.ask[warp];
                 addr = k < ask_n ? kv_cell<D>(c, b, q.seq, (q.u0 + k) * kWarps + warp, q.head) : nullptr;
             }
-            const int now = min(min(want, ask_n - ask_k), 32 - (ask_k & 31)), nth = lane - (ask_k & 31);
-            if ((unsigned)nth < (unsigned)now) {
-                const int slot = (issued + nth) % kStages;
-                const uint32_t bar = smem_addr(&sm.bar[warp][slot]);
-                if (addr) {
-                    asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}\n" ::"r"(bar),
-                                 "r"((uint32_t)C::kBytes)
-                                 : "memory");
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                            smem_addr(sm.ring[warp][slot])),
-                        "l"(addr), "r"((uint32_t)C::kBytes), "r"(bar)
-                        : "memory");
-                } else {  // no such page: its values are NaN
-                    atomicOr(c.err, 1u);
-                    uint4* s = reinterpret_cast<uint4*>(sm.ring[warp][slot]);
-                    for (int e = 0; e < C::kVs / 16; ++e) s[e] = make_uint4(0, 0, 0, 0);
-                    for (int e = C::kVs / 16; e < C::kBytes / 16; ++e) s[e] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-                    asm volatile("{\n.reg .b64 st;\nmbarrier.arrive.shared::cta.b64 st, [%0];\n}\n" ::"r"(bar) : "memory");
-                }
-            }
-            issued += now;
-            ask_k += now;
-            want -= now;
+            copy_cell(ask_k & 31, issued % kStages);
+            ++issued;
+            ++ask_k;
+            --want;
         }
+        cp_async_commit();
     };
-    issue(kStages);
+    issue(kStages / 2);
+    issue(kStages / 2);
 
     for (bool first_piece = true;; first_piece = false) {
         if (!first_piece) {
@@ -506,12 +498,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             float s[Z][NT][4];       // c0, c1: token g, rows 2i, 2i + 1; c2, c3: token g + 8
             uint32_t vs[Z][2][G];    // value scales
             uint32_t seen = 0;       // their bits
-#pragma unroll
-            for (int z = 0; z < Z; ++z) {
-                const int slot = (used + z) % kStages;
-                const uint32_t bar = smem_addr(&sm.bar[warp][slot]), parity = ((used + z) / kStages) & 1;
-                if (!abar_try(bar, parity) && !dead && !abar_wait_long(bar, parity)) dead = true;
-            }
+            cp_async_wait_but_last();
+            __syncwarp();
 #pragma unroll
             for (int z = 0; z < Z; ++z) {
                 const uint8_t* cell = sm.ring[warp][(used + z) % kStages];
@@ -681,8 +669,17 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 for (int z = 0; z < Z; ++z) values(z, std::false_type{});
             }
             used += Z;
-            dead = __any_sync(0xffffffffu, dead);  // and every lane has read the slots
-            if (!dead) issue(Z);
+            __syncwarp();  // every lane has read the slots
+            const int at = ask_k & 31;
+            if (at && at + Z <= 32 && ask_k + Z <= ask_n) {
+#pragma unroll
+                for (int z = 0; z < Z; ++z) copy_cell(at + z, (issued + z) % kStages);
+                issued += Z;
+                ask_k += Z;
+                cp_async_commit();
+            } else {
+                issue(Z);
+            }
         };
         int k = 0;
 #pragma unroll 1
@@ -696,7 +693,6 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
-                if (dead) l[nt][e] = __int_as_float(0x7fc00000);
                 if (g == 0) {
                     sm.m[warp][8 * nt + 2 * i + e] = m[nt][e];
                     sm.l[warp][8 * nt + 2 * i + e] = l[nt][e];
@@ -716,7 +712,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         __syncthreads();
 
         // --- out, or to the item's other pieces
-        const bool whole = p.u0 == 0 && p.u1 == p.s.units;
+        const bool whole = p.u1 - p.u0 == p.s.units;
         float* rec = a.partial + ((size_t)blockIdx.x * 2 + (p.u0 == 0 ? 1 : 0)) * kPartFloats(D);
         for (int e = tid; e < rows * (D / 4); e += kAttThreads) {
             const int r = e / (D / 4), d = 4 * (e % (D / 4));
@@ -729,7 +725,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 const float wm = sm.m[w][r], wl = sm.l[w][r];
                 const float f = wm == -INFINITY ? 0.f : ex2(wm - mm), fu = f * sm.unit[w];
                 const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][d]);
-                ll += wm == -INFINITY ? (wl != wl ? wl : 0.f) : f * wl;
+                ll += f * wl;
                 v.x = fmaf(fu, x.x, v.x), v.y = fmaf(fu, x.y, v.y), v.z = fmaf(fu, x.z, v.z), v.w = fmaf(fu, x.w, v.w);
             }
             if (whole) {
@@ -743,71 +739,93 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             }
         }
         if (tid == 0 && p.u0 == 0 && p.u1 < p.s.units) {
-            const int x0 = p.x, c1 = cta_of(x0 + p.s.units - 1);
+            const int c1 = cta_of(p.first + p.s.units - 1);
             a.split[blockIdx.x] = {c1 - (int)blockIdx.x + 1, p.s.t0, p.head, p.tile, rows};
             split_here = true;
         }
         __syncthreads();  // o, m and l are free again
     }
     if (tid == 0 && !split_here) a.split[blockIdx.x].pieces = 0;
-    if (dead) {
-        if (lane == 0) atomicOr(c.err, 2u);
-        for (; used < issued; ++used)  // nothing of this warp is in flight when it leaves
-            abar_wait_long(smem_addr(&sm.bar[warp][used % kStages]), (used / kStages) & 1);
-    }
 }
 
-// Joins the pieces of split items: a block takes two rows of the item that
-// starts in CTA blockIdx.x, a warp a quarter of its pieces, a lane four dims.
+// Joins the pieces of the split item that starts in CTA blockIdx.x. Up to
+// kFewPieces of them, a warp takes a row; more, four warps take one. A lane has
+// four dims and asks for eight pieces at once, so that few pieces are one trip to
+// L2 and the longest sequence's 76 are three.
+constexpr int kFewPieces = 16;
 template <int D, int NT>
 __global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
-    constexpr int kLanes = D / 4;                 // lanes of a row's dims
-    constexpr int kSets = 4 * 32 / kLanes;        // pieces taken side by side, of each row
-    __shared__ float4 part[2][kSets][kLanes];
-    __shared__ float lpart[2][kSets];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int half = warp >> 2, set = (warp & 3) * (32 / kLanes) + lane / kLanes, d = 4 * (lane % kLanes);
-    const int r = 2 * blockIdx.y + half;
+    constexpr int kLanes = D / 4, kSide = 32 / kLanes;  // lanes of a row's dims; pieces a warp takes side by side
+    constexpr int kAhead = 8;
+    __shared__ float4 part[8][kSide][kLanes];
+    __shared__ float mpart[8][kSide], lpart[8][kSide];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, side = lane / kLanes, d = 4 * (lane % kLanes);
     griddep_wait();
     const Split* at = a.split + blockIdx.x;
     const Split s = {__ldcg(&at->pieces), __ldcg(&at->t0), __ldcg(&at->head), __ldcg(&at->tile), __ldcg(&at->rows)};
-    if (2 * (int)blockIdx.y >= s.rows || s.pieces == 0) return;
-    const bool mine = r < s.rows;
-    auto record = [&](int q) { return a.partial + ((size_t)(blockIdx.x + q) * 2 + (q == 0)) * kPartFloats(D); };
-    float m = -INFINITY;  // of all pieces
-    for (int q = lane; q < s.pieces; q += 32)
-        if (mine) m = fmaxf(m, __ldcg(record(q) + 16 * D + r));
-#pragma unroll
-    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const int per = s.pieces <= kFewPieces ? 1 : 4;     // warps a row
+    const int first_row = blockIdx.y * (8 / per), r = first_row + warp / per;
+    if (s.pieces == 0 || first_row >= s.rows) return;
+    const int set = (warp % per) * kSide + side, sets = per * kSide;
+    float m = -INFINITY, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    if (mine) {
-#pragma unroll 4
-        for (int q = set; q < s.pieces; q += kSets) {
-            const float* at = record(q);
-            const float qm = __ldcg(at + 16 * D + r), ql = __ldcg(at + 16 * D + 16 + r);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(at + r * D + d));
-            const float f = qm == -INFINITY ? 0.f : ex2(qm - m);
-            l += qm == -INFINITY ? (ql != ql ? ql : 0.f) : f * ql;
-            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+    if (r < s.rows) {
+        for (int q0 = set; q0 < s.pieces; q0 += kAhead * sets) {
+            float qm[kAhead], ql[kAhead], high = m;
+            float4 x[kAhead];
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                // (volatile: left alone, the compiler moves each load to its use, and each use waits)
+                const int q = min(q0 + e * sets, s.pieces - 1);
+                const float* rec = a.partial + ((size_t)(blockIdx.x + q) * 2 + (q == 0)) * kPartFloats(D);
+                asm volatile("ld.global.cg.f32 %0, [%1];\n" : "=f"(qm[e]) : "l"(rec + 16 * D + r));
+                asm volatile("ld.global.cg.f32 %0, [%1];\n" : "=f"(ql[e]) : "l"(rec + 16 * D + 16 + r));
+                asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                             : "=f"(x[e].x), "=f"(x[e].y), "=f"(x[e].z), "=f"(x[e].w)
+                             : "l"(rec + r * D + d));
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                if (q0 + e * sets >= s.pieces) qm[e] = -INFINITY;  // weight 0
+                high = fmaxf(high, qm[e]);
+            }
+            const float f0 = m == high ? 1.f : ex2(m - high);
+            m = high;
+            l *= f0;
+            v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const float f = qm[e] == -INFINITY ? 0.f : ex2(qm[e] - m);
+                l = fmaf(f, ql[e], l);
+                v.x = fmaf(f, x[e].x, v.x), v.y = fmaf(f, x[e].y, v.y), v.z = fmaf(f, x[e].z, v.z), v.w = fmaf(f, x[e].w, v.w);
+            }
         }
     }
-    part[half][set][lane % kLanes] = v;
-    if (lane % kLanes == 0) lpart[half][set] = l;
-    __syncthreads();
-    if (set != 0 || !mine) return;
-    for (int q = 1; q < kSets; ++q) {
-        const float4 x = part[half][q][lane % kLanes];
-        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-        l += lpart[half][q];
+    if (sets > 1) {
+        part[warp][side][lane % kLanes] = v;
+        if (lane % kLanes == 0) mpart[warp][side] = m, lpart[warp][side] = l;
+        __syncthreads();
+        if (set != 0) return;
+        float high = m;
+        for (int q = 1; q < sets; ++q) high = fmaxf(high, mpart[warp + q / kSide][q % kSide]);
+        const float f0 = m == -INFINITY ? 0.f : ex2(m - high);
+        l *= f0;
+        v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+        for (int q = 1; q < sets; ++q) {
+            const float qm = mpart[warp + q / kSide][q % kSide], f = qm == -INFINITY ? 0.f : ex2(qm - high);
+            const float4 x = part[warp + q / kSide][q % kSide][lane % kLanes];
+            l = fmaf(f, lpart[warp + q / kSide][q % kSide], l);
+            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+        }
+        m = high;
     }
-    put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
+    if (r < s.rows) put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
 }
 
 bool attend_fits(const KvDev& c, const KvBatch& b, int T) {
     const int64_t rows = (int64_t)T * (c.hq / c.hkv), tiles = rows / 8 + std::min<int64_t>(b.B, T);
     const int64_t units = ((int64_t)b.table_stride * c.page_tokens + 1) / (kCellTokens * kWarps) + 1;
-    return rows < (1ll << 30) && (double)tiles * (double)units * (double)c.hkv < (double)(1ll << 30);
+    return rows < (1ll << 30) && (double)tiles * (double)(units + kBegin) * (double)c.hkv < (double)(1ll << 30);
 }
 
 static int sm_count(int device) {
@@ -832,6 +850,9 @@ static void launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, int gr
     static bool set = false;
     if (!set) {
         cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT>));
+        // the same division of L1 and shared memory for both: an SM is idle while it changes
+        cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        cudaFuncSetAttribute(k_join<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         set = true;
     }
     launch_ex(k_attend<D, NT>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
