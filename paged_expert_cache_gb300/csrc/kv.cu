@@ -1,6 +1,7 @@
 // kv.cu -- the paged key/value cache: its handle and C entry points, the
 // kernel that rotates and stores new tokens, and the one that reads tokens
 // back.
+#include <algorithm>
 #include <new>
 
 #include "kv.cuh"
@@ -8,8 +9,7 @@
 
 namespace moe {
 
-constexpr int kAppendThreads = 256;
-constexpr int kCuShared = 1024;  // batches up to this many sequences are searched in shared memory
+constexpr int kAppendThreads = 128;
 
 struct AppendArgs {
     const uint16_t *q, *k, *v;
@@ -35,9 +35,9 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// One Q4_0 block held as 8 values in each of four neighbouring lanes: this
-// lane's eight codes (nibble e is value e) and the block's scale.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half& d) {
+// One Q4_0 block held as 8 values in each of a quad's four lanes: this lane's
+// eight codes (q - 8, as integers) and the block's scale.
+__device__ __forceinline__ void quantise8(const float (&x)[8], int (&q)[8], __half& d) {
     float hi = x[0], lo = x[0];
     bool bad = false;
 #pragma unroll
@@ -56,134 +56,241 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half& d) {
     d = __float2half_rn(fminf(fmaxf(m * -0.125f, -65504.0f), 65504.0f));
     if (bad) d = __ushort_as_half(0x7fff);  // the block reads as NaN
     const float f = __half2float(d);
-    uint32_t w = 0;
+    const float inv = f == 0.0f || bad ? 0.0f : __frcp_rn(f);
+    // rint(x / d) without a division for each value. x is a bf16 and d an fp16
+    // value, so a quotient that is no tie n + 1/2 is at least 2^-16 away from
+    // one (x - d (n + 1/2) is a whole number of units in 8 + 11 + 4 bits), while
+    // x * inv is within 2^-20 of it: rounded to multiples of 2^-17 (the spacing
+    // of fp32 about 96) ties become exact and nothing else does, and the second
+    // rounding is the quotient's own, ties to even.
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        // the quotient of a bf16 value and an fp16 scale is never within an
-        // fp32 rounding of a tie it does not hit, so this is the exact rounding
-        const float r = f == 0.0f || bad ? 0.0f : rintf(__fdiv_rn(x[e], f));
-        w |= (uint32_t)(int)(fminf(fmaxf(r, -8.0f), 7.0f) + 8.0f) << (4 * e);
+        const float y = __fsub_rn(__fmaf_rn(x[e], inv, 96.0f), 96.0f);
+        q[e] = __float2int_rn(bad ? 0.0f : fminf(fmaxf(y, -8.0f), 7.0f));
     }
-    return w;
 }
 
-// nibbles 0..7 -> the word of a K cell: nibble 2j at bits 4j, 2j + 1 at 16 + 4j
-__device__ __forceinline__ uint32_t spread_pairs(uint32_t w) {
-    uint32_t r = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r |= ((w >> (8 * j)) & 15u) << (4 * j) | ((w >> (8 * j + 4)) & 15u) << (16 + 4 * j);
-    return r;
+// The position of packed row t, its sequence in `seq` (-1: none). In a decode
+// step row t is sequence t's, so that is looked at first: one trip to memory
+// instead of a search's several.
+__device__ __forceinline__ int row_position(const KvBatch& b, int t, bool live, int& seq) {
+    seq = -1;
+    if (!live) return -1;
+    const int guess = min(t, b.B - 1), c0 = __ldg(b.cu + guess);
+    int c1 = __ldg(b.cu + guess + 1), len = __ldg(b.kv_lens + guess);
+    seq = guess;
+    if (!(c0 <= t && t < c1)) {
+        seq = seq_of_row(b.cu, b.B, t);
+        if (seq < 0) return -1;
+        c1 = __ldg(b.cu + seq + 1);
+        len = __ldg(b.kv_lens + seq);
+    }
+    return len - (c1 - t);
 }
 
 // ---------------------------------------------------------------------------
 // New tokens into the cache.
 //
-// One row (a head of q, k or v of a token) is D / 16 lanes: lane c holds
-// dims 8c .. 8c + 7 and the same of the upper half, which are whole rotation
-// pairs, and four neighbouring lanes hold one Q4_0 block of each half. The
-// kernel moves each value once (18 of 32 bytes for k and v on the way out);
-// what bounds a prompt is the q rows' bytes, what bounds a decode step is the
-// launch and the chain batch -> position -> page.
+// A row is a head of a token; four lanes (a quad) hold one, lane i the dims 32b
+// + 8i .. + 7 of every block b: whole rotation pairs, and a block across the
+// quad. Warps of queries have one token and heads in steps of eight, so its
+// rotation is read once; warps of keys or values have eight neighbouring tokens
+// of one head, so a cell's bytes are written 16 at a time: a key row's words lie
+// together, and a value word holds two neighbouring tokens, put together from
+// two quads where both are in the warp.
+//
+// The kernel moves each value once (18 of 64 bytes for keys and values on the
+// way to the cache); what bounds a prompt is the queries' bytes, what bounds a
+// decode step is the launch and the chain batch -> position -> page.
 // ---------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvDev c, KvBatch b, AppendArgs a) {
-    constexpr int kLanes = D / 16, G = D / 32;
-    __shared__ int cu_s[kCuShared + 1];
-    const int tid = threadIdx.x;
-    const int rows = (a.q ? c.hq : 0) + 2 * c.hkv;
-    const unsigned long long item = (unsigned long long)blockIdx.x * (kAppendThreads / kLanes) + tid / kLanes;
-    const int lane = tid % kLanes;
-    const unsigned long long total = (unsigned long long)a.T * rows;
-    const bool live = item < total;
-    const int t = !live ? 0 : total <= 0xffffffffull ? (int)((unsigned)item / (unsigned)rows) : (int)(item / rows);
-    int r = live ? (int)(item - (unsigned long long)t * rows) : 0;
-    int kind = 2, head;  // 0 q, 1 k, 2 v
-    if (!a.q) r += c.hq;
-    if (r < c.hq) { kind = 0; head = r; }
-    else if (r < c.hq + c.hkv) { kind = 1; head = r - c.hq; }
-    else head = r - c.hq - c.hkv;
-    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-    if (live) {
-        const uint16_t* src = kind == 0 ? a.q + (size_t)t * a.qs : kind == 1 ? a.k + (size_t)t * a.ks : a.v + (size_t)t * a.vs;
-        src += (size_t)head * D + 8 * lane;
-        ua = *reinterpret_cast<const uint4*>(src);
-        ub = *reinterpret_cast<const uint4*>(src + D / 2);
+struct RotaryRow {
+    static constexpr int P = D / 64;  // blocks of the lower half
+    float c[P][8], s[P][8];
+    bool bad;
+    __device__ void load(const AppendArgs& a, int pos, int i) {
+        bad = pos < 0 || pos >= a.rope_rows;
+        const float* row = a.rope + (size_t)(bad ? 0 : pos) * D + 8 * i;
+#pragma unroll
+        for (int b = 0; b < P; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(row + 32 * b + 4 * h));
+                const float4 y = __ldg(reinterpret_cast<const float4*>(row + D / 2 + 32 * b + 4 * h));
+                c[b][4 * h] = x.x, c[b][4 * h + 1] = x.y, c[b][4 * h + 2] = x.z, c[b][4 * h + 3] = x.w;
+                s[b][4 * h] = y.x, s[b][4 * h + 1] = y.y, s[b][4 * h + 2] = y.z, s[b][4 * h + 3] = y.w;
+            }
+        if (bad) {
+#pragma unroll
+            for (int b = 0; b < P; ++b)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) c[b][e] = s[b][e] = __int_as_float(0x7fc00000);
+        }
     }
-    const int* cu = b.cu;
-    if (b.B <= kCuShared) {
-        for (int i = tid; i <= b.B; i += kAppendThreads) cu_s[i] = __ldg(b.cu + i);
-        cu = cu_s;
-        __syncthreads();
-    }
-    const int seq = live ? seq_of_row(cu, b.B, t) : -1;
-    const int pos = seq >= 0 ? __ldg(b.kv_lens + seq) - (cu[seq + 1] - t) : -1;
-    float x[8], y[8];
-    unpack8(ua, x);
-    unpack8(ub, y);
-    bool bad = false;
-    if (kind != 2) {
-        if (a.rope && seq >= 0) {
-            bad = pos < 0 || pos >= a.rope_rows;
-            const float4* row = reinterpret_cast<const float4*>(a.rope + (size_t)(bad ? 0 : pos) * D) + 2 * lane;
-            const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row + D / 8), s1 = __ldg(row + D / 8 + 1);
-            const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    // rotates a row; products and sum each rounded to fp32, as a program of
+    // separate multiplies and adds computes them, then once to bf16
+    __device__ void turn(uint4 (&u)[D / 32]) const {
+#pragma unroll
+        for (int b = 0; b < P; ++b) {
+            float x[8], y[8];
+            unpack8(u[b], x);
+            unpack8(u[b + P], y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // products and sum each rounded to fp32, as a program of
-                // separate multiplies and adds computes them
-                const float u = x[e], w = y[e];
-                x[e] = __fsub_rn(__fmul_rn(u, cs[e]), __fmul_rn(w, sn[e]));
-                y[e] = __fadd_rn(__fmul_rn(w, cs[e]), __fmul_rn(u, sn[e]));
-                if (bad) x[e] = y[e] = __int_as_float(0x7fc00000);
+                const float p = x[e], q = y[e];
+                x[e] = __fsub_rn(__fmul_rn(p, c[b][e]), __fmul_rn(q, s[b][e]));
+                y[e] = __fadd_rn(__fmul_rn(q, c[b][e]), __fmul_rn(p, s[b][e]));
             }
-            ua = pack8(x);
-            ub = pack8(y);
+            u[b] = pack8(x);
+            u[b + P] = pack8(y);
         }
-        uint16_t* dst = kind == 0 ? a.q_out : a.k_out;
-        if (seq >= 0 && dst) {
-            dst += ((size_t)t * (kind == 0 ? c.hq : c.hkv) + head) * D + 8 * lane;
-            *reinterpret_cast<uint4*>(dst) = ua;
-            *reinterpret_cast<uint4*>(dst + D / 2) = ub;
-        }
-        unpack8(ua, x);  // the block holds the rounded key
-        unpack8(ub, y);
     }
-    if (!__any_sync(0xffffffffu, kind != 0)) {  // a warp of q rows is done
-        if (bad) atomicOr(c.err, 1u);
+};
+
+// HB: steps of eight heads that a warp of queries takes
+template <int D, int HB>
+__global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvDev c, KvBatch b, AppendArgs a, int q_warps, int q_chunks) {
+    constexpr int G = D / 32;
+    using C = Cell<D>;
+    const int tid = threadIdx.x, lane = tid & 31, quad = lane >> 2, i = lane & 3;
+    const int w = blockIdx.x * (kAppendThreads / 32) + (tid >> 5);
+    const bool is_q = w < q_warps;
+    // --- the rows, asked for before anything about them is known
+    int t, head;
+    bool live, is_k = false;
+    uint4 u[HB][G];
+    if (is_q) {
+        t = q_chunks == 1 ? w : (int)((unsigned)w / (unsigned)q_chunks);
+        head = (w - t * q_chunks) * 8 * HB + quad;
+        live = true;
+#pragma unroll
+        for (int e = 0; e < HB; ++e)
+            if (head + 8 * e < c.hq) {
+#pragma unroll
+                for (int bl = 0; bl < G; ++bl)
+                    u[e][bl] = __ldcs(reinterpret_cast<const uint4*>(a.q + (size_t)t * a.qs + (size_t)(head + 8 * e) * D + 32 * bl + 8 * i));
+            }
+    } else {
+        const int v = w - q_warps, kv = (int)((unsigned)v / (unsigned)c.hkv);  // keys and values in turn
+        head = v - kv * c.hkv;
+        is_k = (kv & 1) == 0;
+        t = (kv >> 1) * 8 + quad;
+        live = t < a.T;
+        const uint16_t* src = is_k ? a.k + (size_t)(live ? t : 0) * a.ks : a.v + (size_t)(live ? t : 0) * a.vs;
+#pragma unroll
+        for (int bl = 0; bl < G; ++bl)
+            u[0][bl] = live ? __ldcs(reinterpret_cast<const uint4*>(src + (size_t)head * D + 32 * bl + 8 * i)) : make_uint4(0, 0, 0, 0);
+    }
+    if (!is_q && (w - q_warps) >= 2 * c.hkv * ((a.T + 7) / 8)) return;  // past the last warp of work
+    int seq;
+    const int pos = row_position(b, t, live, seq);
+    RotaryRow<D> rot;
+    if (a.rope && (is_q || is_k)) {
+        rot.load(a, seq >= 0 ? pos : 0, i);
+        if (seq >= 0 && rot.bad && i == 0) atomicOr(c.err, 1u);
+    }
+    if (is_q) {
+        if (seq < 0) return;
+#pragma unroll
+        for (int e = 0; e < HB; ++e)
+            if (head + 8 * e < c.hq) {
+                if (a.rope) rot.turn(u[e]);
+                uint16_t* dst = a.q_out + ((size_t)t * c.hq + head + 8 * e) * D + 8 * i;
+#pragma unroll
+                for (int bl = 0; bl < G; ++bl) *reinterpret_cast<uint4*>(dst + 32 * bl) = u[e][bl];
+            }
         return;
     }
-    __half d0, d1;
-    const uint32_t w0 = quantise8(x, d0), w1 = quantise8(y, d1);
-    uint8_t* cell = seq >= 0 && kind != 0 ? kv_cell<D>(c, b, seq, pos >> 4, head) : nullptr;
-    bad |= seq >= 0 && kind != 0 && !cell;
-    if (bad) atomicOr(c.err, 1u);
-    const int tc = pos & (kCellTokens - 1), i = lane & 3, b0 = lane >> 2, b1 = b0 + G / 2;
-    // v: the four lanes' words, of which this lane stores dims g = 2i, 2i + 1 (+ 8j)
-    uint32_t h0 = 0, h1 = 0;  // halfwords of g = 2i (low) and 2i + 1 (high)
+    if (is_k && a.rope) rot.turn(u[0]);
+    if (is_k && a.k_out && seq >= 0) {
+        uint16_t* dst = a.k_out + ((size_t)t * c.hkv + head) * D + 8 * i;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int from = (threadIdx.x & 28) + j;
-        const uint32_t v0 = __shfl_sync(0xffffffffu, w0, from) >> (8 * i), v1 = __shfl_sync(0xffffffffu, w1, from) >> (8 * i);
-        h0 |= (v0 & 15u) << (4 * j) | ((v0 >> 4) & 15u) << (16 + 4 * j);
-        h1 |= (v1 & 15u) << (4 * j) | ((v1 >> 4) & 15u) << (16 + 4 * j);
+        for (int bl = 0; bl < G; ++bl) *reinterpret_cast<uint4*>(dst + 32 * bl) = u[0][bl];
+    }
+    uint8_t* cell = seq >= 0 ? kv_cell<D>(c, b, seq, pos >> 4, head) : nullptr;
+    if (seq >= 0 && !cell && i == 0) atomicOr(c.err, 1u);
+    const int tc = pos & (kCellTokens - 1);
+    uint32_t code[G];    // keys: the word of each block; values: nibble e of dim 8i + e
+    __half d[G];
+#pragma unroll
+    for (int bl = 0; bl < G; ++bl) {
+        float x[8];
+        int q[8];
+        unpack8(u[0][bl], x);
+        quantise8(x, q, d[bl]);
+        uint32_t r = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r |= (uint32_t)(q[e] + 8) << (is_k ? (e >> 1) * 4 + (e & 1) * 16 : 4 * e);
+        code[bl] = r;
+    }
+    auto store_words = [&](uint8_t* to, const uint32_t (&x)[G]) {
+        if constexpr (G == 4) *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
+        else *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[1]);
+    };
+    uint32_t scale[G];  // this token's, in the low half
+#pragma unroll
+    for (int bl = 0; bl < G; ++bl) scale[bl] = __half_as_ushort(d[bl]);
+    if (is_k) {
+        if (!cell) return;
+        store_words(cell + C::k_word(tc, i, 0), code);
+        if (i == 0) {
+            if constexpr (G == 4)
+                *reinterpret_cast<uint2*>(cell + C::kKs + C::k_scale(tc, 0)) = make_uint2(scale[0] | scale[1] << 16, scale[2] | scale[3] << 16);
+            else
+                *reinterpret_cast<uint32_t*>(cell + C::kKs + C::k_scale(tc, 0)) = scale[0] | scale[1] << 16;
+        }
+        return;
+    }
+    // the neighbouring token of this one's value words, if its quad is here
+    const bool odd = pos & 1;
+    const int other = odd ? lane - 4 : lane + 4, from = other & 31;
+    const bool pair = __shfl_sync(0xffffffffu, cell ? seq : -2, from) == seq && (unsigned)other < 32u && cell;
+    uint32_t word[G], half[G], swap[G];
+#pragma unroll
+    for (int bl = 0; bl < G; ++bl) {
+        uint32_t h = 0;  // dims g = 2i (low half) and 2i + 1 (high half), + 8j at nibble j
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t v = __shfl_sync(0xffffffffu, code[bl], (lane & 28) + j) >> (8 * i);
+            h |= (v & 15u) << (4 * j) | ((v >> 4) & 15u) << (16 + 4 * j);
+        }
+        half[bl] = h;
+        const uint32_t theirs = __shfl_sync(0xffffffffu, h, from);
+        word[bl] = odd ? (theirs >> 16) | (h & 0xffff0000u) : (h & 0xffffu) | theirs << 16;
+        swap[bl] = __shfl_sync(0xffffffffu, scale[bl], from);
     }
     if (!cell) return;
-    using C = Cell<D>;
-    if (kind == 1) {
-        *reinterpret_cast<uint32_t*>(cell + C::k_word(tc, i, b0)) = spread_pairs(w0);
-        *reinterpret_cast<uint32_t*>(cell + C::k_word(tc, i, b1)) = spread_pairs(w1);
+    uint8_t* vc = cell + C::kV;
+    if (pair) {
+        store_words(vc + C::v_half(tc & ~1, 2 * i + odd, 0), word);
+        if (i == 0 && !odd) {
+#pragma unroll
+            for (int bl = 0; bl < G; ++bl) scale[bl] |= swap[bl] << 16;
+            store_words(cell + C::kVs + C::v_scale(tc, 0), scale);
+        }
     } else {
-        uint8_t* vc = cell + C::kV;
-        *reinterpret_cast<uint16_t*>(vc + C::v_half(tc, 2 * i, b0)) = (uint16_t)h0;
-        *reinterpret_cast<uint16_t*>(vc + C::v_half(tc, 2 * i + 1, b0)) = (uint16_t)(h0 >> 16);
-        *reinterpret_cast<uint16_t*>(vc + C::v_half(tc, 2 * i, b1)) = (uint16_t)h1;
-        *reinterpret_cast<uint16_t*>(vc + C::v_half(tc, 2 * i + 1, b1)) = (uint16_t)(h1 >> 16);
+#pragma unroll
+        for (int bl = 0; bl < G; ++bl) {
+            *reinterpret_cast<uint16_t*>(vc + C::v_half(tc, 2 * i, bl)) = (uint16_t)half[bl];
+            *reinterpret_cast<uint16_t*>(vc + C::v_half(tc, 2 * i + 1, bl)) = (uint16_t)(half[bl] >> 16);
+            if (i == 0) *reinterpret_cast<uint16_t*>(cell + C::kVs + C::v_scale(tc, bl)) = (uint16_t)scale[bl];
+        }
     }
-    if (i == 0) {
-        *reinterpret_cast<__half*>(cell + (kind == 1 ? C::kKs + C::k_scale(tc, b0) : C::kVs + C::v_scale(tc, b0))) = d0;
-        *reinterpret_cast<__half*>(cell + (kind == 1 ? C::kKs + C::k_scale(tc, b1) : C::kVs + C::v_scale(tc, b1))) = d1;
-    }
+}
+
+template <int D>
+static cudaError_t launch_append(const KvDev& d, const KvBatch& b, const AppendArgs& a, cudaStream_t st) {
+    // A warp of queries takes 32 heads of a token (the rotation is read once for
+    // them), but 8 where there are too few tokens to fill the GPU that way.
+    const int hq = a.q ? d.hq : 0;
+    const bool deep = (int64_t)a.T * ((hq + 31) / 32) >= 152 * 16;
+    const int chunk = deep ? 32 : 8, q_chunks = std::max((hq + chunk - 1) / chunk, 1);
+    const int64_t q_warps = hq ? (int64_t)a.T * q_chunks : 0, warps = q_warps + 2 * (int64_t)d.hkv * ((a.T + 7) / 8);
+    if (warps > 0x7ffffff0ll) return cudaErrorInvalidValue;
+    const unsigned blocks = (unsigned)((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
+    if (deep) k_kv_append<D, 4><<<blocks, kAppendThreads, 0, st>>>(d, b, a, (int)q_warps, q_chunks);
+    else k_kv_append<D, 1><<<blocks, kAppendThreads, 0, st>>>(d, b, a, (int)q_warps, q_chunks);
+    return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -195,7 +302,6 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_read(KvDev c, KvBatch b, 
                                                             uint16_t* __restrict__ v_out) {
     constexpr int kLanes = D / 16, G = D / 32;
     using C = Cell<D>;
-    __shared__ int cu_s[kCuShared + 1];
     const int tid = threadIdx.x;
     const int rows = 2 * c.hkv;
     const unsigned long long item = (unsigned long long)blockIdx.x * (kAppendThreads / kLanes) + tid / kLanes;
@@ -206,14 +312,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_read(KvDev c, KvBatch b, 
     int head = live ? (int)(item - (unsigned long long)t * rows) : 0;
     const bool is_v = head >= c.hkv;
     if (is_v) head -= c.hkv;
-    const int* cu = b.cu;
-    if (b.B <= kCuShared) {
-        for (int i = tid; i <= b.B; i += kAppendThreads) cu_s[i] = __ldg(b.cu + i);
-        cu = cu_s;
-        __syncthreads();
-    }
-    const int seq = live ? seq_of_row(cu, b.B, t) : -1;
-    const int pos = seq >= 0 ? __ldg(b.kv_lens + seq) - (cu[seq + 1] - t) : -1;
+    int seq;
+    const int pos = row_position(b, t, live, seq);
     const uint8_t* cell = seq >= 0 ? kv_cell<D>(c, b, seq, pos >> 4, head) : nullptr;
     if (seq >= 0 && !cell) atomicOr(c.err, 1u);
     const int tc = pos & (kCellTokens - 1), i = lane & 3, b0 = lane >> 2, b1 = b0 + G / 2;
@@ -385,15 +485,10 @@ moe_status_t moe_kv_append(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
     if (rope && rope_rows < 1) return refuse("rope_rows must be >= 1");
     moe::AppendArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, q_stride, k_stride, v_stride, T,
                          rope, rope_rows, (uint16_t*)q_out, (uint16_t*)k_out};
-    const uint64_t items = (uint64_t)T * ((q ? c.q_heads : 0) + 2 * c.kv_heads);
-    const uint64_t per = moe::kAppendThreads / (c.head_dim / 16), blocks = (items + per - 1) / per;
-    if (blocks > 0x7fffffffull) return refuse("T is too large");
     const moe::KvDev d = dev_of(h, layer);
-    if (c.head_dim == 128)
-        moe::k_kv_append<128><<<(unsigned)blocks, moe::kAppendThreads, 0, (cudaStream_t)stream>>>(d, batch_of(batch), a);
-    else
-        moe::k_kv_append<64><<<(unsigned)blocks, moe::kAppendThreads, 0, (cudaStream_t)stream>>>(d, batch_of(batch), a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = c.head_dim == 128 ? moe::launch_append<128>(d, batch_of(batch), a, (cudaStream_t)stream)
+                                            : moe::launch_append<64>(d, batch_of(batch), a, (cudaStream_t)stream);
+    if (e == cudaErrorInvalidValue) return refuse("T is too large");
     return e == cudaSuccess ? MOE_OK : cuda_refuse(e);
 }
 

@@ -74,7 +74,7 @@ __device__ __forceinline__ uint8_t* kv_cell(const KvDev& c, const KvBatch& b, in
 }
 
 // The sequence of packed row t: the last b with cu[b] <= t, or -1 where t is
-// at or past cu[B]. cu may be in shared memory.
+// at or past cu[B].
 __device__ __forceinline__ int seq_of_row(const int* cu, int B, int t) {
     if (t >= cu[B]) return -1;
     int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
