@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
     };
     int incl = 0, mine = 0;
     if (warp < kTable / 32) {
+        griddep_wait();
         for (int s = tid * run; s < min((tid + 1) * run, a.B); ++s) mine += pairs_of(s);
         incl = mine;
 #pragma unroll
@@ -320,6 +321,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
     } else if (warp == 8) {
         tc_alloc(gsmem(&sm.tmem), 512);
         tc_relinquish();
+        griddep_wait();
     } else if (warp == 9) {
         if (lane == 0) {
             for (int x = 0; x < 2; ++x) {
@@ -782,8 +784,7 @@ static cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& mq, con
     constexpr int bytes = (int)sizeof(PromptSmem<D>) + 1024;
     static const cudaError_t set = cudaFuncSetAttribute(k_prompt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (set != cudaSuccess) return set;
-    k_prompt<D><<<(unsigned)grid, kPromptThreads, bytes, st>>>(a, mq, mk, mv);
-    return cudaGetLastError();
+    return launch_ex(k_prompt<D>, dim3((unsigned)grid), dim3(kPromptThreads), bytes, st, true, a, mq, mk, mv);
 }
 
 }  // namespace moe

@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvDev c, KvBatch b
     const int tid = threadIdx.x, lane = tid & 31, quad = lane >> 2, i = lane & 3;
     const int w = blockIdx.x * (kAppendThreads / 32) + (tid >> 5);
     const bool is_q = w < q_warps;
+    griddep_wait();
+    griddep_launch();
     // --- the rows, asked for before anything about them is known
     int t, head;
     bool live, is_k = false;
@@ -288,76 +290,80 @@ static cudaError_t launch_append(const KvDev& d, const KvBatch& b, const AppendA
     const int64_t q_warps = hq ? (int64_t)a.T * q_chunks : 0, warps = q_warps + 2 * (int64_t)d.hkv * ((a.T + 7) / 8);
     if (warps > 0x7ffffff0ll) return cudaErrorInvalidValue;
     const unsigned blocks = (unsigned)((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
-    if (deep) k_kv_append<D, 4><<<blocks, kAppendThreads, 0, st>>>(d, b, a, (int)q_warps, q_chunks);
-    else k_kv_append<D, 1><<<blocks, kAppendThreads, 0, st>>>(d, b, a, (int)q_warps, q_chunks);
-    return cudaGetLastError();
+    return launch_ex(deep ? k_kv_append<D, 4> : k_kv_append<D, 1>, dim3(blocks), dim3(kAppendThreads), 0, st, true, d, b, a,
+                     (int)q_warps, q_chunks);
 }
 
 // ---------------------------------------------------------------------------
-// Tokens of the cache back as bf16: the same rows and lanes, the other way.
-// d * (q - 8) is exact in fp32 (11 + 4 bits), then rounded once.
+// Tokens of the cache back as bf16: a warp takes eight neighbouring rows of a
+// head's keys or values, a quad each, as they were written. d * (q - 8) is exact
+// in fp32 (11 + 4 bits), then rounded once.
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_read(KvDev c, KvBatch b, int T, uint16_t* __restrict__ k_out,
                                                             uint16_t* __restrict__ v_out) {
-    constexpr int kLanes = D / 16, G = D / 32;
+    constexpr int G = D / 32;
     using C = Cell<D>;
-    const int tid = threadIdx.x;
-    const int rows = 2 * c.hkv;
-    const unsigned long long item = (unsigned long long)blockIdx.x * (kAppendThreads / kLanes) + tid / kLanes;
-    const int lane = tid % kLanes;
-    const unsigned long long total = (unsigned long long)T * rows;
-    const bool live = item < total;
-    const int t = !live ? 0 : total <= 0xffffffffull ? (int)((unsigned)item / (unsigned)rows) : (int)(item / rows);
-    int head = live ? (int)(item - (unsigned long long)t * rows) : 0;
-    const bool is_v = head >= c.hkv;
-    if (is_v) head -= c.hkv;
+    const int lane = threadIdx.x & 31, quad = lane >> 2, i = lane & 3;
+    const int w = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    griddep_wait();
+    griddep_launch();
+    if (w >= 2 * c.hkv * ((T + 7) / 8)) return;
+    const int kv = (int)((unsigned)w / (unsigned)c.hkv), head = w - kv * c.hkv, t = (kv >> 1) * 8 + quad;
+    const bool is_k = (kv & 1) == 0;
     int seq;
-    const int pos = row_position(b, t, live, seq);
+    const int pos = row_position(b, t, t < T, seq);
     const uint8_t* cell = seq >= 0 ? kv_cell<D>(c, b, seq, pos >> 4, head) : nullptr;
-    if (seq >= 0 && !cell) atomicOr(c.err, 1u);
-    const int tc = pos & (kCellTokens - 1), i = lane & 3, b0 = lane >> 2, b1 = b0 + G / 2;
-    uint32_t w0 = 0, w1 = 0;  // nibble e: dim 8i + e of the block
-    float d0 = __int_as_float(0x7fc00000), d1 = d0;
-    if (cell) {
-        d0 = __half2float(*reinterpret_cast<const __half*>(cell + (is_v ? C::kVs + C::v_scale(tc, b0) : C::kKs + C::k_scale(tc, b0))));
-        d1 = __half2float(*reinterpret_cast<const __half*>(cell + (is_v ? C::kVs + C::v_scale(tc, b1) : C::kKs + C::k_scale(tc, b1))));
-        if (!is_v) {
-            const uint32_t u0 = *reinterpret_cast<const uint32_t*>(cell + C::k_word(tc, i, b0));
-            const uint32_t u1 = *reinterpret_cast<const uint32_t*>(cell + C::k_word(tc, i, b1));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w0 |= ((u0 >> (4 * j)) & 15u) << (8 * j) | ((u0 >> (16 + 4 * j)) & 15u) << (8 * j + 4);
-                w1 |= ((u1 >> (4 * j)) & 15u) << (8 * j) | ((u1 >> (16 + 4 * j)) & 15u) << (8 * j + 4);
-            }
+    if (seq >= 0 && !cell && i == 0) atomicOr(c.err, 1u);
+    const int tc = pos & (kCellTokens - 1);
+    auto words = [&](uint32_t (&r)[G], const uint8_t* src) {
+        if constexpr (G == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src);
+            r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
         } else {
-            const uint8_t* vc = cell + C::kV;
-            w0 = *reinterpret_cast<const uint16_t*>(vc + C::v_half(tc, 2 * i, b0)) |
-                 (uint32_t)*reinterpret_cast<const uint16_t*>(vc + C::v_half(tc, 2 * i + 1, b0)) << 16;
-            w1 = *reinterpret_cast<const uint16_t*>(vc + C::v_half(tc, 2 * i, b1)) |
-                 (uint32_t)*reinterpret_cast<const uint16_t*>(vc + C::v_half(tc, 2 * i + 1, b1)) << 16;
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            r[0] = v.x, r[1] = v.y;
+        }
+    };
+    uint32_t code[G] = {};  // keys: the block's word; values: dims g = 2i (low half) and 2i + 1 (high half)
+    float d[G];
+#pragma unroll
+    for (int bl = 0; bl < G; ++bl) d[bl] = __int_as_float(0x7fc00000);
+    if (cell && is_k) {
+        words(code, cell + C::k_word(tc, i, 0));
+#pragma unroll
+        for (int bl = 0; bl < G; ++bl) d[bl] = __half2float(*reinterpret_cast<const __half*>(cell + C::kKs + C::k_scale(tc, bl)));
+    } else if (cell) {
+        uint32_t lo[G], hi[G], sc[G];
+        words(lo, cell + C::kV + C::v_half(tc & ~1, 2 * i, 0));
+        words(hi, cell + C::kV + C::v_half(tc & ~1, 2 * i + 1, 0));
+        words(sc, cell + C::kVs + C::v_scale(tc & ~1, 0));
+        const int shift = 16 * (tc & 1);
+#pragma unroll
+        for (int bl = 0; bl < G; ++bl) {
+            code[bl] = ((lo[bl] >> shift) & 0xffffu) | (hi[bl] >> shift) << 16;
+            d[bl] = __half2float(__ushort_as_half((unsigned short)(sc[bl] >> shift)));
         }
     }
-    // v: lane j of the quad holds dims g = 2j, 2j + 1 (+ 8i'); gather dims 8i + g
-    uint32_t g0 = 0, g1 = 0;
+    uint16_t* dst = (is_k ? k_out : v_out) + ((size_t)t * c.hkv + head) * D + 8 * i;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int from = (threadIdx.x & 28) + j;
-        const uint32_t v0 = __shfl_sync(0xffffffffu, w0, from) >> (4 * i), v1 = __shfl_sync(0xffffffffu, w1, from) >> (4 * i);
-        g0 |= (v0 & 15u) << (8 * j) | ((v0 >> 16) & 15u) << (8 * j + 4);
-        g1 |= (v1 & 15u) << (8 * j) | ((v1 >> 16) & 15u) << (8 * j + 4);
-    }
-    if (is_v) { w0 = g0; w1 = g1; }
-    if (seq < 0) return;
-    float x[8], y[8];
+    for (int bl = 0; bl < G; ++bl) {
+        float x[8];
+        if (is_k) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        x[e] = d0 * ((float)((w0 >> (4 * e)) & 15u) - 8.0f);
-        y[e] = d1 * ((float)((w1 >> (4 * e)) & 15u) - 8.0f);
+            for (int e = 0; e < 8; ++e) x[e] = (float)((code[bl] >> ((e >> 1) * 4 + (e & 1) * 16)) & 15u);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // dims 8i + 2j, + 1 are nibble i of lane j's halves
+                const uint32_t v = __shfl_sync(0xffffffffu, code[bl], (lane & 28) + j) >> (4 * i);
+                x[2 * j] = (float)(v & 15u);
+                x[2 * j + 1] = (float)((v >> 16) & 15u);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = d[bl] * (x[e] - 8.0f);
+        if (seq >= 0) *reinterpret_cast<uint4*>(dst + 32 * bl) = pack8(x);
     }
-    uint16_t* dst = (is_v ? v_out : k_out) + ((size_t)t * c.hkv + head) * D + 8 * lane;
-    *reinterpret_cast<uint4*>(dst) = pack8(x);
-    *reinterpret_cast<uint4*>(dst + D / 2) = pack8(y);
 }
 
 }  // namespace moe
@@ -506,9 +512,8 @@ moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
     if (!(scale >= 0.f && scale <= 3.4028235e38f)) return refuse("scale must be finite and not negative");
     if (!rows_ok(q, q_stride, c.q_heads, c.head_dim) || ((uintptr_t)out & 15u))
         return refuse("q and out need 16-byte aligned rows: q_stride a multiple of 8 and not below q_heads * head_dim");
-    moe::launch_attend(dev_of(h, layer), batch_of(batch), c.head_dim, (const uint16_t*)q, q_stride, T, scale,
-                       (uint16_t*)out, h->scratch, (cudaStream_t)stream);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = moe::launch_attend(dev_of(h, layer), batch_of(batch), c.head_dim, (const uint16_t*)q, q_stride, T,
+                                             scale, (uint16_t*)out, h->scratch, (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : cuda_refuse(e);
 }
 
@@ -522,17 +527,12 @@ moe_status_t moe_kv_read(moe_kv_t* h, int32_t layer, int32_t T, const moe_kv_bat
     if (T == 0) return MOE_OK;
     if (!k_out || !v_out || (((uintptr_t)k_out | (uintptr_t)v_out) & 15u))
         return refuse("k_out and v_out must not be NULL, and 16-byte aligned");
-    const uint64_t items = (uint64_t)T * 2 * c.kv_heads;
-    const uint64_t per = moe::kAppendThreads / (c.head_dim / 16), blocks = (items + per - 1) / per;
-    if (blocks > 0x7fffffffull) return refuse("T is too large");
-    const moe::KvDev d = dev_of(h, layer);
-    if (c.head_dim == 128)
-        moe::k_kv_read<128><<<(unsigned)blocks, moe::kAppendThreads, 0, (cudaStream_t)stream>>>(
-            d, batch_of(batch), T, (uint16_t*)k_out, (uint16_t*)v_out);
-    else
-        moe::k_kv_read<64><<<(unsigned)blocks, moe::kAppendThreads, 0, (cudaStream_t)stream>>>(
-            d, batch_of(batch), T, (uint16_t*)k_out, (uint16_t*)v_out);
-    const cudaError_t e = cudaGetLastError();
+    const uint64_t warps = 2 * (uint64_t)c.kv_heads * (((uint64_t)T + 7) / 8), per = moe::kAppendThreads / 32;
+    if (warps > 0x7ffffff0ull) return refuse("T is too large");
+    const uint64_t blocks = (warps + per - 1) / per;
+    const cudaError_t e = moe::launch_ex(c.head_dim == 128 ? moe::k_kv_read<128> : moe::k_kv_read<64>, dim3((unsigned)blocks),
+                                         dim3(moe::kAppendThreads), 0, (cudaStream_t)stream, true, dev_of(h, layer),
+                                         batch_of(batch), T, (uint16_t*)k_out, (uint16_t*)v_out);
     return e == cudaSuccess ? MOE_OK : cuda_refuse(e);
 }
 

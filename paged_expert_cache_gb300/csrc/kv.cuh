@@ -90,7 +90,7 @@ __device__ __forceinline__ int seq_of_row(const int* cu, int B, int t) {
 uint64_t attend_scratch_bytes(int device);
 // Whether every piece of work of such a call can be numbered in 31 bits.
 bool attend_fits(const KvDev& c, const KvBatch& b, int T);
-void launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
-                   uint16_t* out, void* scratch, cudaStream_t st);
+cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
+                          uint16_t* out, void* scratch, cudaStream_t st);
 
 }  // namespace moe

@@ -846,23 +846,25 @@ uint64_t attend_scratch_bytes(int device) {
 }
 
 template <int D, int NT>
-static void launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, int grid, cudaStream_t st) {
-    static bool set = false;
-    if (!set) {
-        cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT>));
+static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, int grid, cudaStream_t st) {
+    static const cudaError_t set = [] {
+        cudaError_t e = cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT>));
         // the same division of L1 and shared memory for both: an SM is idle while it changes
-        cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-        cudaFuncSetAttribute(k_join<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-        set = true;
-    }
-    launch_ex(k_attend<D, NT>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
-    launch_ex(k_join<D, NT>, dim3(grid, 4 * NT), dim3(256), 0, st, true, c, a);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k_join<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        return e;
+    }();
+    if (set != cudaSuccess) return set;
+    const cudaError_t e = launch_ex(k_attend<D, NT>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
+    return e != cudaSuccess ? e : launch_ex(k_join<D, NT>, dim3(grid, 4 * NT), dim3(256), 0, st, true, c, a);
 }
 
-void launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
-                   uint16_t* out, void* scratch, cudaStream_t st) {
+cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
+                          uint16_t* out, void* scratch, cudaStream_t st) {
     int dev = 0;
-    cudaGetDevice(&dev);
+    if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     const int n = max_grid(dev);
     AttendArgs a = {q, q_stride, T, scale, out, fast_div((uint32_t)(c.hq / c.hkv)), (float*)scratch,
                     (Split*)((uint8_t*)scratch + (size_t)n * 2 * kPartFloats(128) * sizeof(float))};
@@ -870,8 +872,8 @@ void launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, i
     // heads times the new tokens of an average sequence
     const bool wide = (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
     const int grid = wide ? (n + 1) / 2 : n;
-    if (D == 128) wide ? launch<128, 2>(c, b, a, grid, st) : launch<128, 1>(c, b, a, grid, st);
-    else wide ? launch<64, 2>(c, b, a, grid, st) : launch<64, 1>(c, b, a, grid, st);
+    if (D == 128) return wide ? launch<128, 2>(c, b, a, grid, st) : launch<128, 1>(c, b, a, grid, st);
+    return wide ? launch<64, 2>(c, b, a, grid, st) : launch<64, 1>(c, b, a, grid, st);
 }
 
 }  // namespace moe
