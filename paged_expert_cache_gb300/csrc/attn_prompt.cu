@@ -51,6 +51,8 @@ struct PromptArgs {
     int Tq, Tk, B, hq, hkv;
     float c;  // scale * log2 e
     uint16_t* out;
+    int out32;  // out is 32-byte aligned
+    int single; // items are one tile: too few pairs to fill the GPU
 };
 
 // One item of work: two neighbouring query tiles of a sequence and head.
@@ -301,11 +303,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = a.hq / a.hkv, tokens = kTile / group;  // tokens of a tile
 
-    // --- the table: pairs of tiles before sequence t * run
+    const int reach = a.single ? tokens : 2 * tokens;  // tokens of an item
+    // --- the table: items before sequence t * run
     const int run = (a.B + kTable - 1) / kTable;
     auto pairs_of = [&](int s) {
         const int n = min(max(__ldg(a.cu_q + s + 1), 0), a.Tq) - min(max(__ldg(a.cu_q + s), 0), a.Tq);
-        return n > 0 ? (n + 2 * tokens - 1) / (2 * tokens) : 0;
+        return n > 0 ? (n + reach - 1) / reach : 0;
     };
     int incl = 0, mine = 0;
     if (warp < kTable / 32) {
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
             return (lim + kTile - 1) / kTile;
         };
         p.n0 = tiles_of(it.i0);
-        p.n1 = tiles_of(it.i0 + tokens);
+        p.n1 = a.single ? 0 : tiles_of(it.i0 + tokens);
         p.n = max(p.n0, p.n1);
         p.seen_by_all = max(min(p.shift + it.i0 + 1, it.lk), 0);
         p.first_masked = p.seen_by_all / kTile;
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     it.lq = __shfl_sync(0xffffffffu, bound, 1) - it.q0;
                     it.k0 = __shfl_sync(0xffffffffu, bound, 2);
                     it.lk = max(__shfl_sync(0xffffffffu, bound, 3) - it.k0, 0);
-                    it.i0 = (at - base) * 2 * tokens;
+                    it.i0 = (at - base) * reach;
                     it.head = head;
                     it.end = 0;
                     bar_wait(gsmem(&sm.item_empty[number & 1]), ((number >> 1) & 1) ^ 1, dead, true);
@@ -709,7 +712,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
             const bool lost = *(volatile int*)dead;
             const float inv = l == 0.f ? 0.f : 1.0f / l;
             const int i = it.i0 + x * tokens + tok;
-            const bool used = tok < tokens && i < it.lq;
+            const bool used = tok < tokens && i < it.lq && !(x && a.single);
             uint16_t* dst = a.out + ((size_t)(it.q0 + i) * a.hq + it.head * group + (row - tok * group)) * D;
 #pragma unroll
             for (int h = 0; h < D / 32; ++h) {
@@ -735,11 +738,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                 }
                 if (used) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 u = make_uint4(pack_bf(y[e], y[e + 1]), pack_bf(y[e + 2], y[e + 3]), pack_bf(y[e + 4], y[e + 5]),
-                                             pack_bf(y[e + 6], y[e + 7]));
-                        if (lost) u = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-                        *reinterpret_cast<uint4*>(dst + 32 * h + e) = u;
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) w[q] = lost ? 0x7fc07fc0u : pack_bf(y[e + 2 * q], y[e + 2 * q + 1]);
+                        uint16_t* at = dst + 32 * h + e;
+                        // a lane's row is a line of its own: whole sectors halve the stores' trips
+                        if (a.out32) {
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(at), "r"(w[0]), "r"(w[1]),
+                                         "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                         : "memory");
+                        } else {
+                            *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4*>(at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
                 }
             }
@@ -834,9 +846,13 @@ extern "C" moe_status_t moe_attn_prompt(const void* q, int64_t q_stride, const v
     }
     // a scale of zero still hides what is hidden: -inf times a tiny factor is -inf
     const float c = std::fmax(scale * 1.4426950408889634f, 1e-37f);
-    const moe::PromptArgs a = {(const uint16_t*)v, v_stride, cu_q, cu_k, Tq, Tk, num_seqs, q_heads, kv_heads, c, (uint16_t*)out};
-    // at most this many pairs of tiles, whatever the lengths on the device are
-    const int64_t pairs = (int64_t)Tq / (2 * tokens) + std::min(num_seqs, Tq);
+    // Pairs of tiles, or single ones where the pairs would leave half of the SMs
+    // idle (a chunk of 526 tokens over 3487 keys, 2 of them, 2 heads: 60 -> 46
+    // us). At most this many, whatever the lengths on the device are.
+    auto items = [&](int n) { return (int64_t)Tq / (n * tokens) + std::min(num_seqs, Tq); };
+    const int single = items(2) * kv_heads <= 76;
+    const int64_t pairs = items(single ? 1 : 2);
+    const moe::PromptArgs a = {(const uint16_t*)v, v_stride, cu_q, cu_k, Tq, Tk, num_seqs, q_heads, kv_heads, c, (uint16_t*)out, ((uintptr_t)out & 31u) == 0, single};
     if (pairs * kv_heads > 0x7fffffffll) return refuse("too many rows");
     const cudaError_t e = head_dim == 128 ? moe::launch_prompt<128>(a, mq, mk, mv, pairs * kv_heads, (cudaStream_t)stream)
                                           : moe::launch_prompt<64>(a, mq, mk, mv, pairs * kv_heads, (cudaStream_t)stream);

@@ -213,7 +213,7 @@ __device__ __forceinline__ void put_row(const KvDev& c, const AttendArgs& a, int
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a) {
+__global__ void __launch_bounds__(kAttThreads, NT == 1 || D == 64 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a) {
     constexpr int G = D / 32, kRows = 8 * NT;
     using C = Cell<D>;
     extern __shared__ uint8_t raw[];
@@ -871,7 +871,7 @@ cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_
     // 16 rows at a time where a head has more than 8 rows in a step: group
     // heads times the new tokens of an average sequence
     const bool wide = (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
-    const int grid = wide ? (n + 1) / 2 : n;
+    const int grid = wide && D == 128 ? (n + 1) / 2 : n;  // as many as fit the registers
     if (D == 128) return wide ? launch<128, 2>(c, b, a, grid, st) : launch<128, 1>(c, b, a, grid, st);
     return wide ? launch<64, 2>(c, b, a, grid, st) : launch<64, 1>(c, b, a, grid, st);
 }
