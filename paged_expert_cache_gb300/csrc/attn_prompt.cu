@@ -251,9 +251,6 @@ __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&p);
 }
-__device__ __forceinline__ bool any_nonfinite(uint32_t w) {  // of two bf16
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
 __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
     if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
     if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
@@ -269,27 +266,51 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // The values of a key tile that some row of the CTA does not see (keys from
 // `from` on): infinities and NaN to zero, and everything from key `end` on. One
-// of 128 threads' share; true if it found some.
+// of 128 threads' share; true if it found some. Rows 8 apart have the same
+// swizzle, so a thread keeps its 16-byte column and steps through the rows.
 template <int D>
 __device__ __forceinline__ bool clean_values(uint8_t* tile, int t, int from, int end) {
-    constexpr int kChunks = D / 8;  // 16-byte chunks of a key's values
-    from = max(from, 0);
+    constexpr int kChunks = D / 8, kRowsAtOnce = 128 / kChunks;  // chunks of a key's values; keys of a pass
     end = min(max(end, 0), kTile);
-    bool found = false;
-#pragma unroll 2
-    for (int w = t + from * kChunks; w < kTile * kChunks; w += 128) {
-        const int r = w / kChunks, cc = w % kChunks;
-        uint4* at = reinterpret_cast<uint4*>(tile + (cc >> 3) * (kTile * 128) + r * 128 + (((cc ^ r) & 7) << 4));
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (r < end) {
-            u = *at;
-            if (!(any_nonfinite(u.x) || any_nonfinite(u.y) || any_nonfinite(u.z) || any_nonfinite(u.w))) continue;
-            found = true;
-            u = make_uint4(drop_nonfinite(u.x), drop_nonfinite(u.y), drop_nonfinite(u.z), drop_nonfinite(u.w));
+    const int cc = t % kChunks;
+    int r = max(from, 0) + t / kChunks;
+    uint4* at = reinterpret_cast<uint4*>(tile + (cc >> 3) * (kTile * 128) + r * 128 + (((cc ^ r) & 7) << 4));
+    bool found = false, wrote = false;
+#pragma unroll 4
+    for (; r < end; r += kRowsAtOnce, at += kRowsAtOnce * 8) {
+        const uint4 u = *at;
+        const uint32_t top = __vmaxu2(__vmaxu2(u.x & 0x7f807f80u, u.y & 0x7f807f80u), __vmaxu2(u.z & 0x7f807f80u, u.w & 0x7f807f80u));
+        if ((top & 0xffffu) == 0x7f80u || (top >> 16) == 0x7f80u) {  // an exponent of all ones
+            found = wrote = true;
+            *at = make_uint4(drop_nonfinite(u.x), drop_nonfinite(u.y), drop_nonfinite(u.z), drop_nonfinite(u.w));
         }
-        *at = u;
     }
+    for (; r < kTile; r += kRowsAtOnce, at += kRowsAtOnce * 8) {
+        wrote = true;
+        *at = make_uint4(0, 0, 0, 0);
+    }
+    if (wrote) fence_async_smem();
     return found;
+}
+
+// Scores of a row's columns from `left` on to -inf, in tensor memory, 32 columns
+// at a time where some row of the warp hides one. A loop of few instructions:
+// written out for a row in registers, the rarely run code took about 4000 cycles
+// to fetch.
+__device__ __forceinline__ void hide_scores(uint32_t ts, int left) {
+    const int first = __reduce_min_sync(0xffffffffu, max(left, 0)) / 32;
+#pragma unroll 1
+    for (int h = first; h < kTile / 32; ++h) {
+        const int k = left - 32 * h;
+        const uint32_t keep = k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
+        uint32_t r[32];
+        tc_ld32(ts + 32 * h, r);
+        tc_ld_wait32(r);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = keep & (1u << e) ? r[e] : 0xff800000u;
+        tc_st32(ts + 32 * h, r);
+    }
+    tc_st_wait();
 }
 
 template <int D>
@@ -635,24 +656,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     bar_wait(gsmem(&sm.full[st]), (e / kStages) & 1, dead);
                     if (clean_values<D>(sm.kv[st], row, span_of(it).seen_by_all - j * kTile, it.lk - j * kTile))
                         *(volatile int*)&sm.flag[number & 1] = number + 1;
-                    fence_async_smem();
                     bar_arrive(gsmem(&sm.clean));
                 }
                 __syncwarp();
                 tc_fence_after();
+                if ((j + 1) * kTile > lim_tile) hide_scores(ts, lim - j * kTile);
                 uint32_t s[4][32];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) tc_ld32(ts + 32 * h, s[h]);
 #pragma unroll
                 for (int h = 0; h < 4; ++h) tc_ld_wait32(s[h]);
-                if ((j + 1) * kTile > lim_tile) {
-                    const int left = lim - j * kTile;  // columns from here on are hidden
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * h + e >= left) s[h][e] = 0xff800000u;
-                }
                 float mx4[4] = {m, m, m, m};
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
@@ -714,7 +727,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
             const int i = it.i0 + x * tokens + tok;
             const bool used = tok < tokens && i < it.lq && !(x && a.single);
             uint16_t* dst = a.out + ((size_t)(it.q0 + i) * a.hq + it.head * group + (row - tok * group)) * D;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
                 uint32_t o[32];
                 __syncwarp();
