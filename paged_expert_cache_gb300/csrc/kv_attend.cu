@@ -52,10 +52,11 @@ constexpr int kAttThreads = 32 * kWarps;
 constexpr int kStages = 4;
 constexpr int kMaxCtas = 304;             // two per SM
 // What beginning an item costs, in units: its rows to be fetched and laid out,
-// the warps' sums to be joined and written (about 7000 cycles, a unit 1500). Items
+// the warps' sums to be joined and written (about 8000 cycles, a unit 1400). Items
 // are numbered with so many idle units before their first, so that CTAs with
-// many short sequences get fewer cells.
-constexpr int kBegin = 4;
+// many short sequences get fewer cells (2, 4, 6, 9: 20.6, 20.0, 19.7, 20.7 us for
+// 32 streams of up to 4095 tokens).
+constexpr int kBegin = 6;
 // fp16's range for the product p * d. A row's largest weight is 2^kOffset when
 // its maximum is set and may grow by 2^kLazy. The value blocks' scales are
 // multiplied by 2^sigma: 0 while the largest met is below 2 and was not below
@@ -213,7 +214,7 @@ __device__ __forceinline__ void put_row(const KvDev& c, const AttendArgs& a, int
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttThreads, NT == 1 || D == 64 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a) {
+__global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a) {
     constexpr int G = D / 32, kRows = 8 * NT;
     using C = Cell<D>;
     extern __shared__ uint8_t raw[];
@@ -868,12 +869,14 @@ cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_
     const int n = max_grid(dev);
     AttendArgs a = {q, q_stride, T, scale, out, fast_div((uint32_t)(c.hq / c.hkv)), (float*)scratch,
                     (Split*)((uint8_t*)scratch + (size_t)n * 2 * kPartFloats(128) * sizeof(float))};
-    // 16 rows at a time where a head has more than 8 rows in a step: group
-    // heads times the new tokens of an average sequence
-    const bool wide = (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
-    const int grid = wide && D == 128 ? (n + 1) / 2 : n;  // as many as fit the registers
-    if (D == 128) return wide ? launch<128, 2>(c, b, a, grid, st) : launch<128, 1>(c, b, a, grid, st);
-    return wide ? launch<64, 2>(c, b, a, grid, st) : launch<64, 1>(c, b, a, grid, st);
+    // 16 rows at a time where a head has more than 8 in a step (its group times
+    // the new tokens of an average sequence), although only half as many warps
+    // fit: 8 streams of 4000 tokens, 4 new ones and 8 heads a group 23.1 us, 8
+    // rows at a time 26.4. Not at head_dim 64, where a row's part is smaller: 7
+    // streams of 5000-54000 tokens 60.2 and 57.8 us.
+    const bool wide = D == 128 && (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
+    if (wide) return launch<128, 2>(c, b, a, (n + 1) / 2, st);
+    return D == 128 ? launch<128, 1>(c, b, a, n, st) : launch<64, 1>(c, b, a, n, st);
 }
 
 }  // namespace moe
