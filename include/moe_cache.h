@@ -415,7 +415,8 @@ moe_status_t moe_route_topk_noalloc(const void* hidden, int32_t T, const void* r
  * concerned come out as NaN, and moe_kv_status reports it.
  *
  * Errors of these entry points leave their message with moe_last_error(NULL).
- * Calls on one handle must not overlap (one stream, or ordered streams).
+ * Calls on one handle must not overlap (one stream, or ordered streams), and
+ * are made with the handle's device current.
  */
 typedef struct moe_kv moe_kv_t;
 

@@ -419,7 +419,7 @@ def _rows(name, t, heads, dim, rows=None):
     if st[-1] != 1 or len(shape) == 3 and heads > 1 and st[1] != dim:
         _refuse(f"the heads and dims of a row of {name} must be contiguous")
     _on_device(name, t)
-    return st[0] if shape[0] > 1 else max(st[0], heads * dim)
+    return st[0] if shape[0] > 1 else heads * dim  # the stride of a single row means nothing
 
 
 def _dense(name, t, heads, dim, rows):

@@ -400,6 +400,16 @@ const char* batch_problem(const moe_kv_batch_t* b) {
     return nullptr;
 }
 
+// What is wrong with a call on the handle, or null.
+const char* call_problem(const moe_kv_t* h, int32_t layer, int32_t T, const moe_kv_batch_t* b) {
+    if (!h) return "handle is NULL";
+    if (layer < 0 || layer >= h->cfg.num_layers) return "layer out of range";
+    if (T < 0) return "T must be >= 0";
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != h->cfg.device) return "the handle's device is not the current one";
+    return batch_problem(b);
+}
+
 moe::KvDev dev_of(const moe_kv_t* h, int layer) {
     moe::KvDev d;
     d.pool = h->pool + (size_t)layer * h->layer_bytes;
@@ -447,7 +457,7 @@ moe_status_t moe_kv_create(const moe_kv_config_t* cfg, moe_kv_t** out) {
     h->cfg = c;
     h->page_bytes = (uint64_t)c.page_tokens * c.kv_heads * (c.head_dim / 32) * 36;
     h->layer_bytes = h->page_bytes * (uint64_t)c.num_pages;
-    const uint64_t pool = h->layer_bytes * (uint64_t)c.num_layers;
+    const uint64_t pool = h->layer_bytes <= (1ull << 40) / (uint64_t)c.num_layers ? h->layer_bytes * (uint64_t)c.num_layers : ~0ull;
     if (cudaError_t e = cudaSetDevice(c.device); e != cudaSuccess) { delete h; return cuda_refuse(e); }
     h->scratch_bytes = moe::attend_scratch_bytes(c.device);
     void *p = nullptr, *s = nullptr;
@@ -477,11 +487,8 @@ moe_status_t moe_kv_append(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
                            int64_t k_stride, const void* v, int64_t v_stride, int32_t T,
                            const moe_kv_batch_t* batch, const float* rope, int32_t rope_rows, void* q_out,
                            void* k_out, void* stream) {
-    if (!h) return refuse("handle is NULL");
+    if (const char* p = call_problem(h, layer, T, batch)) return refuse(p);
     const moe_kv_config_t& c = h->cfg;
-    if (layer < 0 || layer >= c.num_layers) return refuse("layer out of range");
-    if (T < 0) return refuse("T must be >= 0");
-    if (const char* p = batch_problem(batch)) return refuse(p);
     if (T == 0) return MOE_OK;
     if (!k || !v || (q && !q_out)) return refuse("NULL k, v or q_out");
     if ((q && !rows_ok(q, q_stride, c.q_heads, c.head_dim)) || !rows_ok(k, k_stride, c.kv_heads, c.head_dim) ||
@@ -500,11 +507,8 @@ moe_status_t moe_kv_append(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
 
 moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_stride, int32_t T,
                            const moe_kv_batch_t* batch, float scale, void* out, void* stream) {
-    if (!h) return refuse("handle is NULL");
+    if (const char* p = call_problem(h, layer, T, batch)) return refuse(p);
     const moe_kv_config_t& c = h->cfg;
-    if (layer < 0 || layer >= c.num_layers) return refuse("layer out of range");
-    if (T < 0) return refuse("T must be >= 0");
-    if (const char* p = batch_problem(batch)) return refuse(p);
     if (T == 0) return MOE_OK;
     if (!q || !out) return refuse("NULL q or out");
     if (!moe::attend_fits(dev_of(h, layer), batch_of(batch), T))
@@ -519,11 +523,8 @@ moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
 
 moe_status_t moe_kv_read(moe_kv_t* h, int32_t layer, int32_t T, const moe_kv_batch_t* batch, void* k_out,
                          void* v_out, void* stream) {
-    if (!h) return refuse("handle is NULL");
+    if (const char* p = call_problem(h, layer, T, batch)) return refuse(p);
     const moe_kv_config_t& c = h->cfg;
-    if (layer < 0 || layer >= c.num_layers) return refuse("layer out of range");
-    if (T < 0) return refuse("T must be >= 0");
-    if (const char* p = batch_problem(batch)) return refuse(p);
     if (T == 0) return MOE_OK;
     if (!k_out || !v_out || (((uintptr_t)k_out | (uintptr_t)v_out) & 15u))
         return refuse("k_out and v_out must not be NULL, and 16-byte aligned");

@@ -74,9 +74,9 @@ __device__ __forceinline__ uint8_t* kv_cell(const KvDev& c, const KvBatch& b, in
 }
 
 // The sequence of packed row t: the last b with cu[b] <= t, or -1 where t is
-// at or past cu[B].
+// before cu[0], or at or past cu[B].
 __device__ __forceinline__ int seq_of_row(const int* cu, int B, int t) {
-    if (t >= cu[B]) return -1;
+    if (t < cu[0] || t >= cu[B]) return -1;
     int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;

@@ -21,6 +21,14 @@ def test_bad_cache_configurations_are_refused(kw):
     assert e.value.status == pec.ERR_INVALID and str(e.value)
 
 
+def test_a_pool_whose_size_overflows_is_refused():
+    # 2^31 - 1 layers of pages of 150 MB: the product does not fit 64 bits
+    c = pec.make_kv_config(2 ** 31 - 1, 2 ** 31 - 1, 1024, 1024, 128, page_tokens=1024)
+    with pytest.raises(pec.MoeError) as e:
+        pec.KVCache(c)
+    assert e.value.status in (pec.ERR_OOM, pec.ERR_CUDA)  # no device here, or no such memory
+
+
 def test_config_defaults():
     c = pec.KvConfig()
     pec.load().moe_kv_config_default(ctypes.byref(c))
@@ -44,13 +52,14 @@ def test_null_handles_are_refused():
 @pytest.mark.parametrize("change,what", [
     (dict(Tq=-1), "Tq"), (dict(B=0), "num_seqs"), (dict(cu_q=None), "cu_q"), (dict(dim=80), "head_dim"),
     (dict(hq=3, hkv=2), "kv_heads"), (dict(hq=130, hkv=1), "kv_heads"), (dict(q=None), "NULL"), (dict(v=None), "NULL"),
+    (dict(scale=-1.0), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"),
     (dict(q=8), "aligned"), (dict(qs=64), "aligned"), (dict(ks=260), "aligned"), (dict(out=24), "aligned"),
 ])
 def test_prompt_entry_refuses_bad_arguments_before_any_launch(change, what):
-    a = dict(q=16, qs=1024, k=16, ks=256, v=16, vs=256, Tq=4, Tk=4, B=1, cu_q=16, cu_k=16, hq=8, hkv=2, dim=128, out=16)
+    a = dict(q=16, qs=1024, k=16, ks=256, v=16, vs=256, Tq=4, Tk=4, B=1, cu_q=16, cu_k=16, hq=8, hkv=2, dim=128, out=16, scale=1.0)
     a.update(change)
     st = pec.load().moe_attn_prompt(a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["Tq"], a["Tk"], a["B"],
-                                    a["cu_q"], a["cu_k"], a["hq"], a["hkv"], a["dim"], 1.0, a["out"], None)
+                                    a["cu_q"], a["cu_k"], a["hq"], a["hkv"], a["dim"], a["scale"], a["out"], None)
     assert st == pec.ERR_INVALID
     assert what in pec.load().moe_last_error(None).decode()
 

@@ -181,6 +181,48 @@ def test_rows_past_the_batch_and_empty_calls_change_nothing():
     P.cache.status()
 
 
+def test_rows_before_the_first_sequence_belong_to_none():
+    P = Paged([10, 5], 2, 1, 64, seed=6).fill()
+    q = P.q([2, 1])
+    clean = P.attend(q, [2, 1])
+    batch = pec.KVBatch(i32([1, 3, 4]), P.lens, P.table)
+    out = torch.full((4, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    P.cache.attend(0, torch.cat([q[:1], q]), batch, out)
+    assert (out[0] == 7.0).all() and torch.equal(out[1:], clean)
+    before = [torch.empty(15, 1, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    after = [torch.empty_like(b) for b in before]
+    P.cache.read(0, P.whole, *before)
+    k = torch.cat([P.k[:1] * 3, P.k[8:10], P.k[14:]])  # the row of no sequence, then what is there already
+    v = torch.cat([P.v[:1] * 3, P.v[8:10], P.v[14:]])
+    P.cache.append(0, None, k, v, batch)
+    P.cache.read(0, P.whole, *after)
+    assert torch.equal(before[0], after[0]) and torch.equal(before[1], after[1])
+    P.cache.status()
+
+
+def test_the_stride_of_a_single_row_does_not_matter():
+    P = Paged([77], 8, 2, 128, seed=7).fill()
+    q = P.q([1])
+    odd = torch.empty(1, 1, 8, 131, dtype=torch.bfloat16, device="cuda")[..., :128]  # not rows of this layout
+    with pytest.raises(pec.MoeError):
+        P.attend(odd[0], [1])
+    view = q.as_strided((1, 8, 128), (3, 128, 1))
+    assert torch.equal(P.attend(view, [1]), P.attend(q, [1]))
+
+
+def test_a_scale_of_zero_averages_what_is_seen():
+    P = Paged([300, 20], 4, 2, 64, page=32, seed=8).fill()
+    q = P.q([2, 1])
+    want, bound = ref.attend(q, P.split(ref.held(P.k)), P.split(ref.held(P.v)), [2, 1], 0.0)
+    check(P.attend(q, [2, 1], scale=0.0), want, bound)
+    lens = [40, 150]
+    q, k, v = prompt_inputs(lens, lens, 4, 2, 64, seed=9)
+    out = torch.empty_like(q)
+    pec.attention_prompt(q, k, v, out, cumulative(lens), scale=0.0)
+    want, bound = ref.attend(q, parts(k, lens), parts(v, lens), lens, 0.0)
+    check(out, want, bound)
+
+
 # ---------------------------------------------------------------------------
 # attention over the cache
 # ---------------------------------------------------------------------------
