@@ -432,21 +432,13 @@ def _on_device(name, t):
         _refuse(f"{name} must be on the current CUDA device")
 
 
-def _all_dense(bf16, *tensors):
+def _all_dense(bf16, dev, *tensors):
     """Whether every (tensor, shape) is a contiguous bf16 tensor of that shape
-    on the current CUDA device: the usual call, accepted in a few hundred
-    nanoseconds a tensor. Where it is false, _rows says what is wrong or finds
-    the strides."""
-    dev = -1
+    on CUDA device dev: the usual call, accepted in a few hundred nanoseconds a
+    tensor. Where it is false, _rows says what is wrong or finds the strides."""
     for t, shape in tensors:
-        if t is not None:
-            if t.shape != shape or t.dtype is not bf16 or not t.is_contiguous():
-                return False
-            d = t.get_device()
-            if d != dev:
-                if dev >= 0 or d < 0 or d != _torch.cuda.current_device():
-                    return False
-                dev = d
+        if t is not None and not (t.shape == shape and t.dtype is bf16 and t.is_contiguous() and t.get_device() == dev):
+            return False
     return True
 
 
@@ -541,8 +533,9 @@ class KVCache:
         T = k.shape[0]
         qs, ks = hq * dim, hkv * dim
         vs = ks
-        if not _all_dense(torch.bfloat16, (k, (T, hkv, dim)), (v, (T, hkv, dim)), (k_out, (T, hkv, dim)),
-                          (q, (T, hq, dim)), (q_out, (T, hq, dim))):
+        q_shape, kv_shape, dev = (T, hq, dim), (T, hkv, dim), self._device
+        if not _all_dense(torch.bfloat16, dev, (k, kv_shape), (v, kv_shape), (k_out, kv_shape), (q, q_shape),
+                          (q_out, q_shape)):
             ks = _rows("k", k, hkv, dim)
             vs = _rows("v", v, hkv, dim, T)
             if q is not None:
@@ -555,7 +548,8 @@ class KVCache:
             if rope.dtype is not torch.float32 or rope.dim() != 2 or rope.shape[1] != dim \
                     or not rope.is_contiguous() or not rope.shape[0]:
                 _refuse(f"rope must be contiguous float32 [positions, {dim}]")
-            _on_device("rope", rope)
+            if rope.get_device() != dev:
+                _refuse(f"rope must be on CUDA device {dev}")
             rows = rope.shape[0]
         _check(_lib.moe_kv_append(self.h, layer, None if q is None else q.data_ptr(), qs, k.data_ptr(), ks,
                                   v.data_ptr(), vs, T, _batch(batch), None if rope is None else rope.data_ptr(), rows,
@@ -571,7 +565,7 @@ class KVCache:
             _refuse("q and out must be torch tensors")
         T = q.shape[0]
         qs = hq * dim
-        if not _all_dense(_torch.bfloat16, (q, (T, hq, dim)), (out, (T, hq, dim))):
+        if not _all_dense(_torch.bfloat16, self._device, (q, (T, hq, dim)), (out, (T, hq, dim))):
             qs = _rows("q", q, hq, dim)
             _dense("out", out, hq, dim, T)
         _check(_lib.moe_kv_attend(self.h, layer, q.data_ptr(), qs, T, _batch(batch),
@@ -586,7 +580,7 @@ class KVCache:
         if not isinstance(k_out, _torch.Tensor) or not isinstance(v_out, _torch.Tensor):
             _refuse("k_out and v_out must be torch tensors")
         T = k_out.shape[0]
-        if not _all_dense(_torch.bfloat16, (k_out, (T, hkv, dim)), (v_out, (T, hkv, dim))):
+        if not _all_dense(_torch.bfloat16, self._device, (k_out, (T, hkv, dim)), (v_out, (T, hkv, dim))):
             _dense("k_out", k_out, hkv, dim, T)
             _dense("v_out", v_out, hkv, dim, T)
         _check(_lib.moe_kv_read(self.h, layer, T, _batch(batch), k_out.data_ptr(), v_out.data_ptr(),
@@ -608,26 +602,31 @@ def attention_prompt(q, k, v, out, cu_q, cu_k=None, scale=None, stream=None):
     D], k and v bf16 [Tk, kv_heads, D], out [Tq, q_heads, D]; cu_q, cu_k int32
     [B + 1] (cu_k None: cu_q). scale None: D ** -0.5. Returns out."""
     torch = _need_torch()
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            _refuse(f"{name} must be a torch tensor [T, heads, head_dim]")
+    T = torch.Tensor
+    if not (isinstance(q, T) and isinstance(k, T) and isinstance(v, T) and isinstance(out, T)
+            and q.dim() == k.dim() == v.dim() == out.dim() == 3):
+        _refuse("q, k, v and out must be torch tensors [T, heads, head_dim]")
     Tq, hq, dim = q.shape
     Tk, hkv, _ = k.shape
     qs, ks = hq * dim, hkv * dim
     vs = ks
-    if not _all_dense(torch.bfloat16, (q, (Tq, hq, dim)), (out, (Tq, hq, dim)), (k, (Tk, hkv, dim)),
-                      (v, (Tk, hkv, dim))):
+    dev = q.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice() or not _all_dense(
+            torch.bfloat16, dev, (q, (Tq, hq, dim)), (out, (Tq, hq, dim)), (k, (Tk, hkv, dim)), (v, (Tk, hkv, dim))):
         qs = _rows("q", q, hq, dim)
         ks = _rows("k", k, hkv, dim)
         vs = _rows("v", v, hkv, dim, Tk)
         _dense("out", out, hq, dim, Tq)
-    _indexes("cu_q", cu_q)
-    B = cu_q.shape[0] - 1
     if cu_k is None:
         cu_k = cu_q
-    else:
-        _indexes("cu_k", cu_k, (B + 1,))
+    for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):  # the usual tensor first, as in _all_dense
+        if not (isinstance(t, T) and t.dtype is torch.int32 and t.dim() == 1 and t.is_contiguous()
+                and t.get_device() == dev):
+            _indexes(name, t)
+    B = cu_q.shape[0] - 1
+    if cu_k.shape[0] != B + 1:
+        _refuse(f"cu_k must have shape {(B + 1,)}, got {tuple(cu_k.shape)}")
     _check(load().moe_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, Tq, Tk, B, cu_q.data_ptr(),
                                   cu_k.data_ptr(), hq, hkv, dim, dim ** -0.5 if scale is None else scale,
-                                  out.data_ptr(), _stream(stream, q.get_device())))
+                                  out.data_ptr(), _stream(stream, dev)))
     return out

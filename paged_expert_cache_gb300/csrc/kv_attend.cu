@@ -185,11 +185,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
-// d = a b.
-__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+// d = a b + c, c kept.
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};\n"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 // Transposes an 8 x 8 matrix of 16-bit values held two a lane (row lane / 4).
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -527,12 +527,12 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float acc[4];
-                        mma_f16_zero(acc, a0, qb[nt][bl][0][0], qb[nt][bl][0][1]);
+                        mma_f16_from(acc, a0, qb[nt][bl][0][0], qb[nt][bl][0][1], corr[nt][bl][0], corr[nt][bl][1]);
                         mma_f16(acc, a1, qb[nt][bl][1][0], qb[nt][bl][1][1]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float d = e < 2 ? d0 : d1, x = acc[e] + corr[nt][bl][e & 1];
-                            s[z][nt][e] = bl ? fmaf(x, d, s[z][nt][e]) : x * d;
+                            const float d = e < 2 ? d0 : d1;
+                            s[z][nt][e] = bl ? fmaf(acc[e], d, s[z][nt][e]) : acc[e] * d;
                         }
                     }
                     seen |= vs[z][0][bl] | vs[z][1][bl];

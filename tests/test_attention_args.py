@@ -83,6 +83,13 @@ def test_prompt_wrapper_refuses_mismatched_tensors():
             assert what in str(e.value) or "CUDA device" in str(e.value), (what, str(e.value))
 
 
+def test_dense_tensors_off_the_device_are_not_taken_for_usable_ones():
+    x = torch.zeros(4, 2, 64).bfloat16()
+    pec._need_torch()
+    assert not pec._all_dense(torch.bfloat16, 0, (x, (4, 2, 64)), (x, (4, 2, 64)))
+    assert pec._all_dense(torch.bfloat16, 0, (None, (4, 2, 64)))
+
+
 def test_batch_refuses_wrong_arrays():
     cu, lens, table = (torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                        torch.zeros(2, 4, dtype=torch.int32))

@@ -210,6 +210,23 @@ def test_the_stride_of_a_single_row_does_not_matter():
     assert torch.equal(P.attend(view, [1]), P.attend(q, [1]))
 
 
+def test_tensors_off_the_device_are_refused():
+    P = Paged([20], 4, 2, 64, seed=10).fill()
+    q, out = P.q([1]), torch.empty(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = P.k[19:]
+    batch = P.batch([1])
+    calls = [lambda: P.cache.attend(0, q.cpu(), batch, out), lambda: P.cache.attend(0, q.cpu(), batch, out.cpu()),
+             lambda: P.cache.append(0, None, k.cpu(), k.cpu(), batch), lambda: P.cache.append(0, q, k, k, batch, q_out=out.cpu()),
+             lambda: P.cache.append(0, q, k, k, batch, rope=torch.zeros(32, 64), q_out=out),
+             lambda: P.cache.read(0, batch, k.cpu(), k.cpu()), lambda: P.cache.attend(0, q, None, out),
+             lambda: pec.attention_prompt(q, k, k, out, batch.cu_tokens.cpu()),
+             lambda: pec.attention_prompt(q.cpu(), k.cpu(), k.cpu(), out.cpu(), batch.cu_tokens.cpu())]
+    for call in calls:
+        with pytest.raises(pec.MoeError) as e:
+            call()
+        assert e.value.status == pec.ERR_INVALID
+
+
 def test_a_scale_of_zero_averages_what_is_seen():
     P = Paged([300, 20], 4, 2, 64, page=32, seed=8).fill()
     q = P.q([2, 1])
