@@ -69,7 +69,7 @@ template <int D>
 struct PromptSmem {
     static constexpr int kHalves = D / 64;                 // 64-dim halves of a tile: one swizzled row each
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kStages = D == 128 ? 4 : 6;       // (one more of 32 KB: 1 to 5% slower)
     uint8_t q[2][kTileBytes];
     uint8_t kv[kStages][kTileBytes];
     ulonglong2 answer;  // of the launch-control request
@@ -291,6 +291,22 @@ __device__ __forceinline__ bool clean_values(uint8_t* tile, int t, int from, int
     }
     if (wrote) fence_async_smem();
     return found;
+}
+
+// Adds the infinities and NaN among the values of keys first .. end - 1, which
+// the cleaning took out, to a row that sees them. Out of line: it hardly runs.
+template <int D>
+__device__ __noinline__ void add_nonfinite(const PromptArgs& a, uint16_t* row, int k0, int head, int first, int end) {
+    for (int t = first; t < end; ++t) {
+        const uint16_t* v = a.v + (size_t)(k0 + t) * a.vs + (size_t)head * D;
+        for (int d = 0; d < D; ++d) {
+            const float x = __uint_as_float((uint32_t)__ldg(v + d) << 16);
+            if (!(fabsf(x) <= 3.4028235e38f)) {
+                const __nv_bfloat16 y = __float2bfloat16_rn(__uint_as_float((uint32_t)row[d] << 16) + x);
+                row[d] = *reinterpret_cast<const uint16_t*>(&y);
+            }
+        }
+    }
 }
 
 // Scores of a row's columns from `left` on to -inf, in tensor memory, 32 columns
@@ -723,7 +739,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
             tc_fence_after();
             const bool flag = nx && *(volatile int*)&sm.flag[number & 1] == number + 1;
             const bool lost = *(volatile int*)dead;
-            const float inv = l == 0.f ? 0.f : 1.0f / l;
+            const float inv = lost ? __int_as_float(0x7fc00000) : l == 0.f ? 0.f : 1.0f / l;
+            const bool seen = lim > 0 || lost;
             const int i = it.i0 + x * tokens + tok;
             const bool used = tok < tokens && i < it.lq && !(x && a.single);
             uint16_t* dst = a.out + ((size_t)(it.q0 + i) * a.hq + it.head * group + (row - tok * group)) * D;
@@ -735,26 +752,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     tc_ld32(to + 32 * h, o);
                     tc_ld_wait32(o);
                 }
-                float y[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) y[e] = lim > 0 ? __uint_as_float(o[e]) * inv : 0.f;
-                if (flag) {  // infinities and NaN that the cleaning took out, where this row sees them
-                    const Span p = span_of(it);
-                    for (int t = max(p.first_masked * kTile, p.seen_by_all); t < lim; ++t) {
-                        const uint16_t* vr = a.v + (size_t)(it.k0 + t) * a.vs + (size_t)it.head * D + 32 * h;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float w = __uint_as_float((uint32_t)__ldg(vr + e) << 16);
-                            if (!(fabsf(w) <= 3.4028235e38f)) y[e] += w;
-                        }
-                    }
-                }
                 if (used) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 16) {
                         uint32_t w[8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) w[q] = lost ? 0x7fc07fc0u : pack_bf(y[e + 2 * q], y[e + 2 * q + 1]);
+                        for (int q = 0; q < 8; ++q)
+                            w[q] = seen ? pack_bf(__uint_as_float(o[e + 2 * q]) * inv, __uint_as_float(o[e + 2 * q + 1]) * inv) : 0u;
                         uint16_t* at = dst + 32 * h + e;
                         // a lane's row is a line of its own: whole sectors halve the stores' trips
                         if (a.out32) {
@@ -767,6 +771,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                         }
                     }
                 }
+            }
+            if (flag && used) {
+                const Span p = span_of(it);
+                add_nonfinite<D>(a, dst, it.k0, it.head, max(p.first_masked * kTile, p.seen_by_all), lim);
             }
             tc_fence_before();  // the reads of O, before the weights that let it be overwritten
             ring = (ring + 2 * span_of(it).n) % (2 * kStages);
