@@ -443,6 +443,8 @@ PROMPT = [  # queries, keys, hq, hkv, dim
     ([130], None, 128, 1, 128),
     ([520], [900], 5, 5, 128),
     ([1100], None, 2, 1, 64),
+    ([700, 0, 300, 129], None, 16, 16, 64),      # enough pairs of tiles for every SM
+    ([260, 400, 77], [900, 400, 1], 24, 12, 128),
 ]
 
 
@@ -483,7 +485,8 @@ def test_prompt_strided_rows_and_rows_of_no_sequence(dim, hq, hkv):
     assert (out[171:] == 7.0).all()
 
 
-@pytest.mark.parametrize("dim,hq,hkv,what", [(128, 8, 2, math.nan), (64, 4, 4, math.inf), (128, 1, 1, -math.inf)])
+@pytest.mark.parametrize("dim,hq,hkv,what", [(128, 8, 2, math.nan), (64, 4, 4, math.inf), (128, 1, 1, -math.inf),
+                                             (64, 32, 32, math.nan), (128, 24, 12, math.inf)])
 def test_prompt_keys_and_values_a_row_does_not_see_do_not_touch_it(dim, hq, hkv, what):
     lens = [150, 90, 300]
     q, k, v = prompt_inputs(lens, lens, hq, hkv, dim, seed=32)
@@ -508,13 +511,14 @@ def test_prompt_keys_and_values_a_row_does_not_see_do_not_touch_it(dim, hq, hkv,
     assert hit.isnan().all() if what != what else (hit == what).all()
 
 
-def test_prompt_scores_that_climb_and_fall():
+@pytest.mark.parametrize("hkv", [1, 16])  # one tile with two halves of its keys, and two tiles an item
+def test_prompt_scores_that_climb_and_fall(hkv):
     lens = [640, 640]
-    q, k, v = prompt_inputs(lens, lens, 4, 1, 64, seed=33)
+    q, k, v = prompt_inputs(lens, lens, 4 * hkv, hkv, 64, seed=33)
     ramp = torch.linspace(-60, 60, 640, device="cuda")
     q.zero_(), k.zero_()
     q[..., 0] = 8.0
-    k[:640, 0, 0], k[640:, 0, 0] = ramp.bfloat16(), ramp.flip(0).bfloat16()
+    k[:640, :, 0], k[640:, :, 0] = ramp.bfloat16()[:, None], ramp.flip(0).bfloat16()[:, None]
     out = torch.empty_like(q)
     pec.attention_prompt(q, k, v, out, cumulative(lens), scale=0.125)
     want, bound = ref.attend(q, parts(k, lens), parts(v, lens), lens, 0.125)
