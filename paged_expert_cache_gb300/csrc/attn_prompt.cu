@@ -33,8 +33,8 @@
 // when a score exceeds it by 2^8.
 //
 // Measured: 8192 tokens, 32 query heads over 4, head_dim 128: 353 us in a graph
-// (1556 TFLOP/s, 0.80 of cuBLAS's bf16 rate); 20 sequences of up to 1500 tokens at
-// head_dim 64 106 us. A key tile of a pair takes 2058 cycles of the tensor cores
+// (1557 TFLOP/s, 0.80 of cuBLAS's bf16 rate); 20 sequences of up to 1500 tokens at
+// head_dim 64 105 us. A key tile of a pair takes 2058 cycles of the tensor cores
 // at head_dim 128 and about 2900 here; at 64 it takes 1538 (N = 64 products run at
 // half rate) and 2240.
 #include <cuda.h>
@@ -986,7 +986,8 @@ extern "C" moe_status_t moe_attn_prompt(const void* q, int64_t q_stride, const v
     auto items = [&](int n) { return (int64_t)Tq / (n * tokens) + std::min(num_seqs, Tq); };
     const bool single = items(2) * kv_heads <= (Tk / num_seqs >= 1000 ? 380 : 76);
     const int64_t pairs = items(single ? 1 : 2);
-    const moe::PromptArgs a = {(const uint16_t*)v, v_stride, cu_q, cu_k, Tq, Tk, num_seqs, q_heads, kv_heads, c, (uint16_t*)out, ((uintptr_t)out & 31u) == 0};
+    const moe::PromptArgs a = {(const uint16_t*)v, v_stride, cu_q, cu_k, Tq, Tk, num_seqs, q_heads, kv_heads, c,
+                               (uint16_t*)out, ((uintptr_t)out & 31u) == 0};
     if (pairs * kv_heads > 0x7fffffffll) return refuse("too many rows");
     const auto launch = head_dim == 128 ? (single ? moe::launch_prompt<128, true> : moe::launch_prompt<128, false>)
                                         : (single ? moe::launch_prompt<64, true> : moe::launch_prompt<64, false>);

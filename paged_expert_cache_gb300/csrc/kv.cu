@@ -101,7 +101,10 @@ __device__ __forceinline__ int row_position(const KvBatch& b, int t, bool live, 
 //
 // The kernel moves each value once (18 of 64 bytes for keys and values on the
 // way to the cache); what bounds a prompt is the queries' bytes, what bounds a
-// decode step is the launch and the chain batch -> position -> page.
+// decode step is the launch and the chain batch -> position -> page. Measured in a
+// graph: 13296 tokens of 64 query heads over 8, head_dim 64, 52.5 us (5.1 TB/s, three
+// quarters of a copy's rate); 32 heads over 4, head_dim 128: 2451 tokens 10.6 us, one
+// token 2.9.
 // ---------------------------------------------------------------------------
 template <int D>
 struct RotaryRow {
@@ -297,7 +300,8 @@ static cudaError_t launch_append(const KvDev& d, const KvBatch& b, const AppendA
 // ---------------------------------------------------------------------------
 // Tokens of the cache back as bf16: a warp takes eight neighbouring rows of a
 // head's keys or values, a quad each, as they were written. d * (q - 8) is exact
-// in fp32 (11 + 4 bits), then rounded once.
+// in fp32 (11 + 4 bits), then rounded once. 13296 tokens of 8 heads, head_dim 64:
+// 10.8 us in a graph (3.2 TB/s: few bytes for its start and its chain); one token 2.1.
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_read(KvDev c, KvBatch b, int T, uint16_t* __restrict__ k_out,

