@@ -42,9 +42,9 @@
 // then.
 //
 // Measured in a graph at head_dim 128: 64 sequences of 4000 to 12000 tokens, 64
-// query heads over 8, 121 us (4.9 TB/s, 0.72 of a copy's rate; the warps' issue slots
+// query heads over 8, 120 us (5.0 TB/s, 0.73 of a copy's rate; the warps' issue slots
 // and latencies bound it, not the memory). 28 or 32 heads over 4: 32 sequences of up
-// to 4095 tokens 20.5 us, one of 100003 tokens 26.5, one of 513 tokens 8.7, where the
+// to 4095 tokens 19.8 us, one of 100003 tokens 25.0, one of 513 tokens 8.5, where the
 // two launches, an item's start and the join are most of it.
 #include <algorithm>
 #include <type_traits>
@@ -84,12 +84,22 @@ struct AttendArgs {
     struct Split* split;  // [grid] the item that starts in a CTA and ends in another
 };
 
-// An item in several pieces, for the kernel that joins them: the last piece of
-// its CTA and the first ones of the next pieces - 1.
-struct Split {
-    int pieces;           // 0: none
-    int t0, head, tile, rows;
+// What a CTA leaves for the kernel that joins the pieces of an item: the last
+// piece of CTA `from` and the first ones of the next pieces - 1. The CTA where
+// the item starts leaves all rows to join or, if there are many pieces, the
+// first one, and CTAs in the item's middle the others.
+struct alignas(16) Split {
+    int pieces;            // 0: none
+    int from, row, rows;   // rows `row` to rows - 1
+    int t0, head, tile;
 };
+constexpr int kJoinAhead = 5;  // pieces that a lane of k_join asks for at once
+// Whether a block takes a row instead of a warp. (pieces - 2 CTAs are in the item's
+// middle, and rows - 1 of them are needed.)
+template <int D>
+__device__ __forceinline__ bool many_pieces(int pieces, int rows) {
+    return pieces > kJoinAhead * (128 / D) && pieces > rows;
+}
 
 // (q - 8) 2^-24 of the codes at bits 0-3 and 16-19, (q - 8) 2^-20 of those at 4-7 and 20-23, as fp16 pairs.
 __device__ __forceinline__ uint32_t centred_lo(uint32_t w) {
@@ -184,7 +194,7 @@ struct AttSmem {
     int prefix, seq;
 };
 
-constexpr int kPartFloats(int D) { return 16 * D + 32; }  // output rows, maxima, sums
+constexpr int kPartFloats(int D) { return 16 * D + 32; }  // output rows, then each row's maximum and sum
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -740,59 +750,62 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             } else {
                 __stcg(reinterpret_cast<float4*>(rec + r * D + d), v);
                 if (d == 0) {
-                    __stcg(rec + 16 * D + r, mm);
-                    __stcg(rec + 16 * D + 16 + r, ll);
+                    __stcg(reinterpret_cast<float2*>(rec + 16 * D + 2 * r), make_float2(mm, ll));
                 }
             }
         }
-        if (tid == 0 && p.u0 == 0 && p.u1 < p.s.units) {
-            const int c1 = cta_of(p.first + p.s.units - 1);
-            a.split[blockIdx.x] = {c1 - (int)blockIdx.x + 1, p.s.t0, p.head, p.tile, rows};
-            split_here = true;
+        if (tid == 0 && p.u1 < p.s.units) {
+            const int c0 = cta_of(p.first), c1 = cta_of(p.first + p.s.units - 1), row = (int)blockIdx.x - c0;
+            const bool many = many_pieces<D>(c1 - c0 + 1, rows);
+            if (row < (many ? rows : 1)) {
+                a.split[blockIdx.x] = {c1 - c0 + 1, c0, row, many ? row + 1 : rows, p.s.t0, p.head, p.tile};
+                split_here = true;
+            }
         }
         __syncthreads();  // o, m and l are free again
     }
     if (tid == 0 && !split_here) a.split[blockIdx.x].pieces = 0;
 }
 
-// Joins the pieces of the split item that starts in CTA blockIdx.x. Up to
-// kFewPieces of them, a warp takes a row; more, four warps take one. A lane has
-// four dims and asks for eight pieces at once, so that few pieces are one trip to
-// L2 and the longest sequence's 76 are three.
-constexpr int kFewPieces = 16;
+// Joins the pieces of split items, as k_attend's CTA of the same number says: a
+// warp takes a row of few pieces, a block one of many. A lane has four dims and
+// asks for kJoinAhead pieces at once, each a trip to L2; more of them (8, 10) are
+// fewer trips, but also more code, which a kernel this short fetches as it goes:
+// one of 513 tokens 8.5 us (8.6, 8.9), one of 100003 25.0 (25.4, 24.5), 32 of up to
+// 4095 19.8 (20.2, 20.3). One wave of blocks: with four for each CTA, a quarter of
+// the rows each, the last two of these were 26.4 and 20.3 us.
 template <int D, int NT>
 __global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
     constexpr int kLanes = D / 4, kSide = 32 / kLanes;  // lanes of a row's dims; pieces a warp takes side by side
-    constexpr int kAhead = 8;
     __shared__ float4 part[8][kSide][kLanes];
     __shared__ float mpart[8][kSide], lpart[8][kSide];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, side = lane / kLanes, d = 4 * (lane % kLanes);
     griddep_wait();
-    const Split* at = a.split + blockIdx.x;
-    const Split s = {__ldcg(&at->pieces), __ldcg(&at->t0), __ldcg(&at->head), __ldcg(&at->tile), __ldcg(&at->rows)};
-    const int per = s.pieces <= kFewPieces ? 1 : 4;     // warps a row
-    const int first_row = blockIdx.y * (8 / per), r = first_row + warp / per;
-    if (s.pieces == 0 || first_row >= s.rows) return;
-    const int set = (warp % per) * kSide + side, sets = per * kSide;
-    float m = -INFINITY, l = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < s.rows) {
-        for (int q0 = set; q0 < s.pieces; q0 += kAhead * sets) {
-            float qm[kAhead], ql[kAhead], high = m;
-            float4 x[kAhead];
+    const int4* at = reinterpret_cast<const int4*>(a.split + blockIdx.x);
+    const int4 s0 = __ldcg(at), s1 = __ldcg(at + 1);
+    const Split s = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z};
+    if (s.pieces == 0) return;
+    const bool many = s.row + 1 == s.rows;  // one row: all warps take it (few pieces of a single row as well)
+    const float* base = a.partial + (size_t)s.from * 2 * kPartFloats(D);
+    const int set = (many ? warp * kSide : 0) + side, sets = many ? 8 * kSide : kSide;
+    for (int r = many ? s.row : warp; r < s.rows; r += 8) {
+        float m = -INFINITY, l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q0 = set; q0 < s.pieces; q0 += kJoinAhead * sets) {
+            float qm[kJoinAhead], ql[kJoinAhead], high = m;
+            float4 x[kJoinAhead];
 #pragma unroll
-            for (int e = 0; e < kAhead; ++e) {
+            for (int e = 0; e < kJoinAhead; ++e) {
                 // (volatile: left alone, the compiler moves each load to its use, and each use waits)
                 const int q = min(q0 + e * sets, s.pieces - 1);
-                const float* rec = a.partial + ((size_t)(blockIdx.x + q) * 2 + (q == 0)) * kPartFloats(D);
-                asm volatile("ld.global.cg.f32 %0, [%1];\n" : "=f"(qm[e]) : "l"(rec + 16 * D + r));
-                asm volatile("ld.global.cg.f32 %0, [%1];\n" : "=f"(ql[e]) : "l"(rec + 16 * D + 16 + r));
+                const float* rec = base + (unsigned)(2 * q + (q == 0)) * kPartFloats(D);
+                asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];\n" : "=f"(qm[e]), "=f"(ql[e]) : "l"(rec + 16 * D + 2 * r));
                 asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n"
                              : "=f"(x[e].x), "=f"(x[e].y), "=f"(x[e].z), "=f"(x[e].w)
                              : "l"(rec + r * D + d));
             }
 #pragma unroll
-            for (int e = 0; e < kAhead; ++e) {
+            for (int e = 0; e < kJoinAhead; ++e) {
                 if (q0 + e * sets >= s.pieces) qm[e] = -INFINITY;  // weight 0
                 high = fmaxf(high, qm[e]);
             }
@@ -801,32 +814,36 @@ __global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
             l *= f0;
             v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
 #pragma unroll
-            for (int e = 0; e < kAhead; ++e) {
+            for (int e = 0; e < kJoinAhead; ++e) {
                 const float f = qm[e] == -INFINITY ? 0.f : ex2(qm[e] - m);
                 l = fmaf(f, ql[e], l);
                 v.x = fmaf(f, x[e].x, v.x), v.y = fmaf(f, x[e].y, v.y), v.z = fmaf(f, x[e].z, v.z), v.w = fmaf(f, x[e].w, v.w);
             }
         }
-    }
-    if (sets > 1) {
-        part[warp][side][lane % kLanes] = v;
-        if (lane % kLanes == 0) mpart[warp][side] = m, lpart[warp][side] = l;
-        __syncthreads();
-        if (set != 0) return;
-        float high = m;
-        for (int q = 1; q < sets; ++q) high = fmaxf(high, mpart[warp + q / kSide][q % kSide]);
-        const float f0 = m == -INFINITY ? 0.f : ex2(m - high);
-        l *= f0;
-        v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
-        for (int q = 1; q < sets; ++q) {
-            const float qm = mpart[warp + q / kSide][q % kSide], f = qm == -INFINITY ? 0.f : ex2(qm - high);
-            const float4 x = part[warp + q / kSide][q % kSide][lane % kLanes];
-            l = fmaf(f, lpart[warp + q / kSide][q % kSide], l);
-            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+        if (sets > 1) {
+            part[warp][side][lane % kLanes] = v;
+            if (lane % kLanes == 0) mpart[warp][side] = m, lpart[warp][side] = l;
+            if (many) __syncthreads();
+            else __syncwarp();
+            if (set == 0) {
+                float high = m;
+                for (int q = 1; q < sets; ++q) high = fmaxf(high, mpart[warp + q / kSide][q % kSide]);
+                const float f0 = m == -INFINITY ? 0.f : ex2(m - high);
+                l *= f0;
+                v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+                for (int q = 1; q < sets; ++q) {
+                    const float qm = mpart[warp + q / kSide][q % kSide], f = qm == -INFINITY ? 0.f : ex2(qm - high);
+                    const float4 x = part[warp + q / kSide][q % kSide][lane % kLanes];
+                    l = fmaf(f, lpart[warp + q / kSide][q % kSide], l);
+                    v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+                }
+                m = high;
+            }
         }
-        m = high;
+        if (set == 0) put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
+        if (many) break;
+        __syncwarp();  // the sums are free again
     }
-    if (r < s.rows) put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
 }
 
 bool attend_fits(const KvDev& c, const KvBatch& b, int T) {
@@ -865,7 +882,7 @@ static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a,
     }();
     if (set != cudaSuccess) return set;
     const cudaError_t e = launch_ex(k_attend<D, NT>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
-    return e != cudaSuccess ? e : launch_ex(k_join<D, NT>, dim3(grid, 4 * NT), dim3(256), 0, st, true, c, a);
+    return e != cudaSuccess ? e : launch_ex(k_join<D, NT>, dim3(grid), dim3(256), 0, st, true, c, a);
 }
 
 cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
