@@ -32,10 +32,10 @@
 // and sums are fp32; a row's maximum is raised, and its output rescaled, only
 // when a score exceeds it by 2^8.
 //
-// Measured: 8192 tokens, 32 query heads over 4, head_dim 128: 353 us in a graph
-// (1557 TFLOP/s, 0.80 of cuBLAS's bf16 rate); 20 sequences of up to 1500 tokens at
+// Measured: 8192 tokens, 32 query heads over 4, head_dim 128: 333 us in a graph
+// (1651 TFLOP/s, 0.85 of cuBLAS's bf16 rate); 20 sequences of up to 1500 tokens at
 // head_dim 64 105 us. A key tile of a pair takes 2058 cycles of the tensor cores
-// at head_dim 128 and about 2900 here; at 64 it takes 1538 (N = 64 products run at
+// at head_dim 128 and about 2770 here; at 64 it takes 1538 (N = 64 products run at
 // half rate) and 2240.
 #include <cuda.h>
 
@@ -670,15 +670,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     free_stage(sk, nx);
                 }
                 __syncwarp();
+                // The next keys are waited for after the values' products at head_dim
+                // 128, whose ring of four stages may not have them any earlier (8192
+                // tokens 333 us, before them 349); at 64 before them, so that the next
+                // scores follow the values with no other product between (20 sequences
+                // of up to 1500 tokens 105 us, after them 110).
+                constexpr bool kLate = D == 128;
                 for (int j = 0; j < p.n; ++j) {
+                    auto next_keys = [&]() {
+                        sk = st;
+                        if (j + 1 == p.n) return;
+                        bar_wait(gsmem(&sm.full[sk]), round, dead);
+                        step();
+                    };
                     sv = st;
                     bar_wait(gsmem(&sm.full[sv]), round, dead);
                     step();
-                    sk = st;
-                    if (j + 1 < p.n) {
-                        bar_wait(gsmem(&sm.full[sk]), round, dead);
-                        step();
-                    }
+                    if (!kLate) next_keys();
                     if (*(volatile int*)dead) break;
                     if (j >= p.first_masked) {
                         bar_wait(gsmem(&sm.clean[2]), c_turn, dead);
@@ -697,13 +705,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                         if (leader) {
                             values(1, sv, false);
                             if (j + 1 == nx) tc_commit(gsmem(&sm.o_full[x]));
-                            else scores(sk, j + 2 == nx);
+                            else if (!kLate) scores(sk, j + 2 == nx);
                         }
                     }
-                    if (leader) {
-                        free_stage(sv, j < nx);
-                        if (j + 1 < p.n) free_stage(sk, j < nx);
+                    if (leader) free_stage(sv, j < nx);
+                    if (kLate) {
+                        __syncwarp();
+                        next_keys();
+                        __syncwarp();
+                        tc_fence_after();
+                        if (leader && j + 1 < nx) scores(sk, j + 2 == nx);
                     }
+                    if (leader && j + 1 < p.n) free_stage(sk, j < nx);
                     __syncwarp();
                 }
                 if (*(volatile int*)dead) break;
@@ -754,16 +767,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                 tc_fence_after();
                 if ((kt + 1) * kTile > lim_tile) hide_scores(ts, lim - kt * kTile);
                 uint32_t s[4][32];
-#pragma unroll
-                for (int h = 0; h < 4; ++h) tc_ld32(ts + 32 * h, s[h]);
-#pragma unroll
-                for (int h = 0; h < 4; ++h) tc_ld_wait32(s[h]);
                 float mx4[4] = {m, m, m, m};
+                // half of the row at a time: one half's maximum is found while the other is loaded
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
+                for (int h = 0; h < 2; ++h) tc_ld32(ts + 32 * h, s[h]);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
+                for (int b = 0; b < 4; b += 2) {
+#pragma unroll
+                    for (int h = b; h < b + 2; ++h) tc_ld_wait32(s[h]);
+                    if (b == 0) {
+#pragma unroll
+                        for (int h = 2; h < 4; ++h) tc_ld32(ts + 32 * h, s[h]);
+                    }
+#pragma unroll
+                    for (int h = b; h < b + 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
+                }
                 const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
                 const bool raise = (mx - m) * a.c > kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
@@ -979,12 +1000,14 @@ extern "C" moe_status_t moe_attn_prompt(const void* q, int64_t q_stride, const v
     // Items of two tiles, or of one with its keys in two halves. The latter are
     // twice as many and half as long, but each loads its keys for itself: taken
     // where pairs would leave half of the SMs idle (600 tokens, 32 heads over 4:
-    // 11.3 us, in pairs 16.2), and up to two and a half pairs per SM for long
-    // sequences, whose pairs differ most (2451 tokens 52.2 and 58.8 us; 4000, 500
-    // pairs, 112 and 103; 4 of 300, 88 pairs, 12.7 and 11.9). At most this many
-    // items, whatever the lengths on the device are.
+    // 11.6 us, in pairs 16.0), and at head_dim 128 up to two and a half pairs per
+    // SM for long sequences, whose pairs differ most (2451 tokens 53.0 and 61.1 us;
+    // 3000, 376 pairs, 71.5 and 75.3; 3400, 428 pairs, 88.1 and 82.6). Not at 64 (1500
+    // tokens 23.3 and 22.2 us, 2451 44.6 and 40.0), nor for shorter ones (4 of 600
+    // tokens at 64: 23.3 and 19.7). At most this many items, whatever the lengths on
+    // the device are.
     auto items = [&](int n) { return (int64_t)Tq / (n * tokens) + std::min(num_seqs, Tq); };
-    const bool single = items(2) * kv_heads <= (Tk / num_seqs >= 1000 ? 380 : 76);
+    const bool single = items(2) * kv_heads <= (head_dim == 128 && Tk / num_seqs >= 1000 ? 380 : 76);
     const int64_t pairs = items(single ? 1 : 2);
     const moe::PromptArgs a = {(const uint16_t*)v, v_stride, cu_q, cu_k, Tq, Tk, num_seqs, q_heads, kv_heads, c,
                                (uint16_t*)out, ((uintptr_t)out & 31u) == 0};
