@@ -81,7 +81,13 @@ struct PromptSmem {
     uint8_t kv[kStages][kTileBytes];
     ulonglong2 answer;  // of the launch-control request
     unsigned long long q_full[2], q_empty[2], full[kStages], empty[kStages];
-    unsigned long long s_full[2], p_full[2][2], o_full[2], clean[3];  // clean: of slot 0's and 1's own values, and of shared ones
+    unsigned long long s_full[2], p_full[2][2], o_full[2];
+    // The values of a stage are cleaned. One barrier a stage, so that a stage's
+    // next cleaning comes only after both MMA warps have passed this one (they
+    // free the stage) and a wait cannot be a phase behind. Halves of one tile's
+    // keys have one a slot, in the first two: there the slot's own MMA warp alone
+    // waits, and its next scores come after.
+    unsigned long long clean[kStages];
     unsigned long long item_full[2], item_empty[2], asked, half_done, half_read;
     float half[kTile][2];  // maximum and sum of a row's second half of keys
     Item item[2];
@@ -387,8 +393,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
             for (int st = 0; st < kStages; ++st) {
                 bar_init_n(gsmem(&sm.full[st]), 1);
                 bar_init_n(gsmem(&sm.empty[st]), 2);  // both MMA warps
+                bar_init_n(gsmem(&sm.clean[st]), 128);
             }
-            for (int x = 0; x < 3; ++x) bar_init_n(gsmem(&sm.clean[x]), 128);
             bar_init_n(gsmem(&sm.half_done), 128);
             bar_init_n(gsmem(&sm.half_read), 128);
             bar_init_n(gsmem(&sm.asked), 1);
@@ -565,7 +571,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
             // stay in uniform registers; descriptors are one base each plus
             // constants. Both warps pass every stage of the ring and every
             // cleaning, needed or not: a wait cannot tell a phase from the next
-            // but one.
+            // but one, and so no barrier may complete twice before both have passed.
             constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false), id_o = idesc_bf16(kTile, D, true);
             const int x = __shfl_sync(0xffffffffu, warp - 9, 0);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                 else bar_arrive(gsmem(&sm.empty[st]));
             };
             int st = 0;
-            uint32_t round = 0, p_turn = 0, q_turn = 0, c_turn = 0, c_own = 0;
+            uint32_t round = 0, p_turn = 0, q_turn = 0, c_turn = 0;  // c_turn: a bit a stage (halves: a bit)
             auto step = [&]() { if (++st == kStages) st = 0, round ^= 1; };
             for (int number = 0; take(number); ++number) {
                 const Span p = span_of(sm.item[number & 1]);
@@ -619,8 +625,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                             step();
                             if (*(volatile int*)dead) break;
                             if ((x ? p.n0 : 0) + j - 1 >= p.first_masked) {
-                                bar_wait(gsmem(&sm.clean[x]), c_own, dead);
-                                c_own ^= 1;
+                                bar_wait(gsmem(&sm.clean[x]), c_turn, dead);
+                                c_turn ^= 1;
                             }
                             for (int half = 0; half < 2; ++half) {
                                 bar_wait(gsmem(&sm.p_full[x][half]), p_turn, dead);
@@ -689,8 +695,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     if (!kLate) next_keys();
                     if (*(volatile int*)dead) break;
                     if (j >= p.first_masked) {
-                        bar_wait(gsmem(&sm.clean[2]), c_turn, dead);
-                        c_turn ^= 1;
+                        bar_wait(gsmem(&sm.clean[sv]), (c_turn >> sv) & 1, dead);
+                        c_turn ^= 1u << sv;
                     }
                     if (j < nx) {
                         bar_wait(gsmem(&sm.p_full[x][0]), p_turn, dead);
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     bar_wait(gsmem(&sm.full[st]), (e / kStages) & 1, dead);
                     if (clean_values<D>(sm.kv[st], row, span_of(it).seen_by_all - kt * kTile, it.lk - kt * kTile))
                         *(volatile int*)&sm.flag[number & 1] = number + 1;
-                    bar_arrive(gsmem(&sm.clean[kSingle ? x : 2]));
+                    bar_arrive(gsmem(&sm.clean[kSingle ? x : st]));
                 }
                 __syncwarp();
                 tc_fence_after();

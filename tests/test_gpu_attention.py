@@ -525,6 +525,36 @@ def test_prompt_scores_that_climb_and_fall(hkv):
     check(out, want, bound, l2=False)
 
 
+@pytest.mark.parametrize("lq,lk,hq,hkv,dim", [
+    ([1500], None, 28, 4, 64),            # 18 tokens a tile: some tiles straddle a multiple of 128 keys
+    ([700, 400], None, 12, 4, 64),        # 42 tokens a tile
+    ([640, 320], [717, 397], 16, 4, 64),  # 32 tokens a tile after a context of 77
+    ([1500, 900], None, 28, 4, 128),
+])
+def test_prompt_tiles_that_clean_several_key_tiles(lq, lk, hq, hkv, dim):
+    # The first tile of an item cleans the values of two key tiles in a row, while the second, whose maxima climb in
+    # every key tile, lags behind it: each cleaning still has to be met by both.
+    lk = lk or lq
+    q, k, v = prompt_inputs(lq, lk, hq, hkv, dim, seed=36)
+    tokens = 128 // (hq // hkv)
+    q.zero_(), k.zero_()
+    for n, at in zip(lq, [0] + lq):
+        second = torch.arange(n, device="cuda") // tokens % 2 == 1
+        q[at:at + n, :, 0] = torch.where(second, 8.0, 0.0).bfloat16()[:, None]
+    at = 0
+    for n in lk:
+        k[at:at + n, :, 0] = torch.linspace(-n / 20, n / 20, n, device="cuda").bfloat16()[:, None]
+        at += n
+    out, again = torch.empty_like(q), torch.empty_like(q)
+    cu, cu_k = cumulative(lq), cumulative(lk)
+    pec.attention_prompt(q, k, v, out, cu, cu_k, scale=0.125)
+    want, bound = ref.attend(q, parts(k, lk), parts(v, lk), lq, 0.125)
+    check(out, want, bound, l2=False)
+    for _ in range(30):
+        pec.attention_prompt(q, k, v, again, cu, cu_k, scale=0.125)
+        assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("scale_q,scale_v", [(1e-6, 1e-6), (1e4, 1e4), (1e15, 1e30)])
 def test_prompt_magnitudes(scale_q, scale_v):
     lens = [200, 77]
