@@ -34,9 +34,17 @@
 //    (exact in fp16), since a sum that only cancels would leave a rounding of
 //    8 d p where the values met are zero; B = p * d for each block, from the
 //    scores' layout by one 8 x 8 transposition, rounded to fp16 twice (p, then
-//    the product: 2^-11 each, an eighth of the output's own rounding each). Where
-//    the largest scale met is not within fp16's comfort, d is brought there by
-//    a power of two that follows it, so fp16's range is no limit.
+//    the product: 2^-11 each, an eighth of the output's own rounding each).
+//    fp16's range does not hold every product. What a row sees of a block of
+//    dimensions is `far` from the first product past kMost on, or from a warp's
+//    first step on where its scales there are below kQuiet: such products are
+//    formed in fp32 and taken as two bf16 operands (16 bits, fp32's range), in
+//    matrix products of their own to which the other rows give zeros. So neither
+//    other blocks, nor what other rows see, nor what no row sees touch a bit of it.
+//    (One power of two for all of a warp's scales is faster where values are large,
+//    157 us in place of 258 for the 64 sequences below with values 20 times as
+//    large, 236 with ones 1000 times as small; but a block 2^11 below the largest
+//    one met, hidden or not, loses bits by it.)
 // Softmax statistics, sums and outputs are fp32. A row's running maximum is
 // raised only when a score exceeds it by 2^kLazy, the outputs being rescaled
 // then.
@@ -64,13 +72,11 @@ constexpr int kMaxCtas = 304;             // two per SM
 // 32 streams of up to 4095 tokens).
 constexpr int kBegin = 6;
 // fp16's range for the product p * d. A row's largest weight is 2^kOffset when
-// its maximum is set and may grow by 2^kLazy. The value blocks' scales are
-// multiplied by 2^sigma: 0 while the largest met is below 2 and was not below
-// 2^kSmall when first met, else at most kSigmaMax and such that it comes to
-// between 2^(kTop - 1) and 2^kTop, and may grow to 2. So a product is below 2^15,
-// and weights down to 2^-25 of the largest still count.
+// its maximum is set and may grow by 2^kLazy, so with scales below 2 a product is
+// below 2^15, and with scales of kQuiet and more weights down to 2^-14 of the
+// largest keep all bits and down to 2^-24 count.
 constexpr float kLazy = 4.0f, kOffset = 10.0f;
-constexpr int kSigmaMax = 15, kTop = -3, kSmall = -8;
+constexpr uint32_t kMost = 0x7800, kQuiet = 0x1400;  // 2^15 and 2^-10 as fp16
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -107,6 +113,15 @@ __device__ __forceinline__ uint32_t centred_lo(uint32_t w) {
 }
 __device__ __forceinline__ uint32_t centred_hi(uint32_t w) {
     return h2_as_u32(__hadd2(u32_as_h2(w & 0x00f000f0u), u32_as_h2(0x80808080u)));
+}
+
+// q - 8, or 16 (q - 8), of the codes at bits 0-3 and 16-19 as bf16 pairs: 128 + q
+// is a bf16 with the code as its last bits.
+__device__ __forceinline__ uint32_t centred_bf16(uint32_t w, float times) {
+    const uint32_t u = (w & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(times),
+                                     __float2bfloat162_rn(-136.0f * times));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // a / b for a >= 0, b > 0: nearly always both fit 32 bits, where a division
@@ -188,7 +203,7 @@ struct AttSmem {
     static constexpr int kRows = 8 * NT, kPad = D + 4;
     alignas(128) uint8_t ring[kWarps][kStages][Cell<D>::kBytes];
     float o[kWarps][kRows][kPad];    // the warps' outputs
-    float m[kWarps][kRows], l[kWarps][kRows], unit[kWarps];
+    float m[kWarps][kRows], l[kWarps][kRows];
     int wsum[kWarps];
     Piece cur[kWarps], ask[kWarps];  // a warp's piece at work and the one it asks for: rarely read, so not in registers
     int prefix, seq;
@@ -496,8 +511,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         float m[NT][2], l[NT][2];    // rows 2i, 2i + 1; l: this lane's tokens
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
-        int sigma = kSigmaMax + 1;   // none yet
-        uint32_t watch = ~0u;        // bits of a value scale that call for a look at sigma
+        unsigned far = 0;            // bit nt G + bl: row 8 nt + g's products in block bl are
 
         const int cells = warp_cells(p, warp), first = (p.u0 * kWarps + warp) * kCellTokens;
         auto words = [&](uint32_t (&r)[G], const uint8_t* src) {
@@ -509,9 +523,40 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 r[0] = v.x, r[1] = v.y;
             }
         };
-        // Z cells, from the warp's k-th
-        auto cells_step = [&](int k, auto count) {
+        // The blocks of which row g sees small scales only in the warp's first step
+        // (bits of `far`): of this lane's tokens, or of all.
+        auto small_blocks = [&](const auto& vs, auto count, bool all) {
+            unsigned bits = 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                uint32_t x[G] = {};
+#pragma unroll
+                for (int z = 0; z < decltype(count)::value; ++z)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = first + z * (kWarps * kCellTokens) + 8 * h + 2 * i;
+                        const uint32_t sees = (t < lim_row[nt] ? 0x7fffu : 0u) | (t + 1 < lim_row[nt] ? 0x7fff0000u : 0u);
+#pragma unroll
+                        for (int bl = 0; bl < G; ++bl) x[bl] = __vmaxu2(x[bl], vs[z][h][bl] & sees);
+                    }
+#pragma unroll
+                for (int bl = 0; bl < G; ++bl) {
+                    uint32_t big = max(x[bl] & 0xffffu, x[bl] >> 16);
+                    if (all) {
+                        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    }
+                    if (big - 1u < kQuiet - 1u) bits |= 1u << (nt * G + bl);  // not zero, and below
+                }
+            }
+            return bits;
+        };
+        // Z cells, from the warp's k-th. Until a scale of 2 or more or a small block
+        // is met, fp16 holds all products: then nothing is done, and the rest of the
+        // piece goes by `wide` steps, which look at each product's range.
+        auto cells_step = [&](int k, auto count, auto wide) {
             constexpr int Z = decltype(count)::value;
+            constexpr bool kWide = decltype(wide)::value;
             float s[Z][NT][4];       // c0, c1: token g, rows 2i, 2i + 1; c2, c3: token g + 8
             uint32_t vs[Z][2][G];    // value scales
             uint32_t seen = 0;       // their bits
@@ -562,10 +607,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                             if (pos0 + g + 8 * (e >> 1) >= lim[nt][e & 1]) s[z][nt][e] = -INFINITY;
                 }
             }
-            // Do the running maxima and the running scale of the value blocks
-            // still do? A lane looks at its own scores; only if one does not are
-            // the maxima shared.
-            bool raise = (seen & watch) != 0;
+            // Do the running maxima and fp16's range still do? A lane looks at its
+            // own scores and scales; only if one does not are the maxima shared.
+            // (A scale of 2 or more, and NaN, have the top exponent bit.)
+            bool raise = !kWide && (seen & 0x40004000u) != 0;
             float mx[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -577,28 +622,9 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                     raise |= mx[nt][e] > m[nt][e] + kLazy;
                 }
             if (__any_sync(0xffffffffu, raise)) {
-                float move = 1.f;
-                unsigned bits = 0;
-#pragma unroll
-                for (int z = 0; z < Z; ++z)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int bl = 0; bl < G; ++bl) {
-                            const unsigned x = vs[z][h][bl] & 0x7fffu, y = (vs[z][h][bl] >> 16) & 0x7fffu;
-                            bits = max(bits, max(x > 0x7bffu ? 0u : x, y > 0x7bffu ? 0u : y));  // NaN has no size
-                        }
-                bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
-                bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
-                // 2^(e - 1) <= the largest scale < 2^e (or below, for a subnormal one)
-                const int e = (int)(bits >> 10) - 14;
-                if (bits && (sigma > kSigmaMax || e + sigma > 1)) {
-                    const int want = e <= 1 && e > kSmall && (sigma > kSigmaMax || sigma > 0) ? 0 : min(kSigmaMax, kTop - e);
-                    if (sigma <= kSigmaMax) move = pow2f(want - sigma);
-                    sigma = want;
-                    // at sigma 0 a scale of 2 or more has its top exponent bit set; elsewhere every step looks
-                    watch = want == 0 ? 0x40004000u : ~0u;
-                }
+                if (kWide && k == 0) far = small_blocks(vs, count, true);
+                if (!kWide && __any_sync(0xffffffffu, (seen & 0x40004000u) != 0 || (k == 0 && small_blocks(vs, count, false) != 0)))
+                    return false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float f[2];
@@ -607,12 +633,11 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                         float v = mx[nt][e2];
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-                        // raised where it is exceeded by enough, so that a look at sigma alone changes no row
+                        // raised where it is exceeded by enough, so that a row is raised by its own scores alone
                         v = v > m[nt][e2] + kLazy ? v : m[nt][e2];
                         f[e2] = v == m[nt][e2] ? 1.f : ex2(m[nt][e2] - v);
                         m[nt][e2] = v;
                         l[nt][e2] *= f[e2];
-                        f[e2] *= move;
                     }
 #pragma unroll
                     for (int bl = 0; bl < G; ++bl)
@@ -627,11 +652,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) mm[nt][e] = (m[nt][e] == -INFINITY ? 0.f : m[nt][e]) - kOffset;
-            const int lift = sigma > kSigmaMax ? 0 : sigma;
-            // values of cell z; `masked`: some row does not see all of it
-            auto values = [&](int z, auto masked) {
-                const uint8_t* cell = sm.ring[warp][(used + z) % kStages];
-                uint32_t ph[NT][2];
+            // the weights of cell z for the values: row g, tokens 8h + 2i, + 1
+            auto weights = [&](int z, uint32_t (&ph)[NT][2]) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -640,12 +662,20 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                         const float e1 = ex2(fmaf(s[z][nt][2 * h + 1], rf[nt][1], -mm[nt][1]));
                         l[nt][0] += e0;
                         l[nt][1] += e1;
-                        ph[nt][h] = transpose8(pack_h2(e0, e1));  // row g, tokens 8h + 2i, + 1
+                        ph[nt][h] = transpose8(pack_h2(e0, e1));
                     }
+            };
+            // which of them row 8 nt + g sees
+            auto sees = [&](int z, int nt, int h) {
+                const int t = first + (k + z) * (kWarps * kCellTokens) + 8 * h + 2 * i;
+                return (t < lim_row[nt] ? 0xffffu : 0u) | (t + 1 < lim_row[nt] ? 0xffff0000u : 0u);
+            };
+            // values of cell z; `masked`: some row does not see all of it
+            auto values = [&](int z, const uint32_t (&ph)[NT][2], auto masked) {
+                const uint8_t* cell = sm.ring[warp][(used + z) % kStages];
                 uint32_t vw[2][G];
                 words(vw[0], cell + C::kV + lane * G * 4);
                 words(vw[1], cell + C::kV + (32 + lane) * G * 4);
-                const int pos0 = first + (k + z) * (kWarps * kCellTokens);
 #pragma unroll
                 for (int bl = 0; bl < G; ++bl) {
                     uint32_t pb[NT][2];
@@ -654,10 +684,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             pb[nt][h] = h2_as_u32(__hmul2(u32_as_h2(ph[nt][h]), u32_as_h2(vs[z][h][bl])));
-                            if (decltype(masked)::value) {  // a hidden token's scale may be NaN
-                                const int t = pos0 + 8 * h + 2 * i;
-                                pb[nt][h] &= (t < lim_row[nt] ? 0xffffu : 0u) | (t + 1 < lim_row[nt] ? 0xffff0000u : 0u);
-                            }
+                            if (decltype(masked)::value) pb[nt][h] &= sees(z, nt, h);  // a hidden token's scale may be NaN
                         }
                     const uint32_t w0 = vw[0][bl], w1 = vw[1][bl], w08 = w0 >> 8, w18 = w1 >> 8;
                     const uint32_t v0[4] = {centred_lo(w0), centred_hi(w0), centred_lo(w1), centred_hi(w1)};
@@ -669,21 +696,105 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                     }
                 }
             };
-            if (lift) {
-                const __half2 up = __float2half2_rn(pow2f(lift));
+            // the same where some rows and blocks are far
+            auto far_values = [&](int z, const uint32_t (&ph)[NT][2]) {
+                const uint8_t* cell = sm.ring[warp][(used + z) % kStages];
+                float pf[NT][4];  // the weights in fp32
 #pragma unroll
-                for (int z = 0; z < Z; ++z)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int bl = 0; bl < G; ++bl)
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t e0 = __float_as_uint(ex2(fmaf(s[z][nt][2 * h], rf[nt][0], -mm[nt][0])));
+                        const uint32_t e1 = __float_as_uint(ex2(fmaf(s[z][nt][2 * h + 1], rf[nt][1], -mm[nt][1])));
+                        const uint32_t lo = transpose8(__byte_perm(e0, e1, 0x5410)), hi = transpose8(__byte_perm(e0, e1, 0x7632));
+                        pf[nt][2 * h] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
+                        pf[nt][2 * h + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+                    }
+                uint32_t vw[2][G];
+                words(vw[0], cell + C::kV + lane * G * 4);
+                words(vw[1], cell + C::kV + (32 + lane) * G * 4);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) vs[z][h][bl] = h2_as_u32(__hmul2(u32_as_h2(vs[z][h][bl]), up));
-            }
-            if (first + (k + Z - 1) * (kWarps * kCellTokens) + kCellTokens > min_lim) {
+                for (int bl = 0; bl < G; ++bl) {
+                    bool is_far = false, is_near = false;
+                    uint32_t near[NT][2], hi[NT][2], lo[NT][2];
 #pragma unroll
-                for (int z = 0; z < Z; ++z) values(z, std::true_type{});
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const bool f = far & 1u << (nt * G + bl);
+                        is_far |= f, is_near |= !f;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t scale = vs[z][h][bl] & sees(z, nt, h);  // a hidden token's may be NaN, or large
+                            const float2 d = __half22float2(u32_as_h2(scale));
+                            const float x0 = pf[nt][2 * h] * d.x * 0x1p-24f, x1 = pf[nt][2 * h + 1] * d.y * 0x1p-24f;
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+                            const float2 back = __bfloat1622float2(b);
+                            const __nv_bfloat162 rest = __floats2bfloat162_rn(x0 - back.x, x1 - back.y);
+                            near[nt][h] = f ? 0u : h2_as_u32(__hmul2(u32_as_h2(ph[nt][h]), u32_as_h2(scale)));
+                            hi[nt][h] = f ? *reinterpret_cast<const uint32_t*>(&b) : 0u;
+                            lo[nt][h] = f ? *reinterpret_cast<const uint32_t*>(&rest) : 0u;
+                        }
+                    }
+                    const uint32_t w0 = vw[0][bl], w1 = vw[1][bl], w08 = w0 >> 8, w18 = w1 >> 8;
+                    if (__any_sync(0xffffffffu, is_near)) {
+                        const uint32_t v0[4] = {centred_lo(w0), centred_hi(w0), centred_lo(w1), centred_hi(w1)};
+                        const uint32_t v1[4] = {centred_lo(w08), centred_hi(w08), centred_lo(w18), centred_hi(w18)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(o[bl][0][nt], v0, near[nt][0], near[nt][1]);
+                            mma_f16(o[bl][1][nt], v1, near[nt][0], near[nt][1]);
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, is_far)) {
+                        const uint32_t v0[4] = {centred_bf16(w0, 1.f), centred_bf16(w0 >> 4, 16.f), centred_bf16(w1, 1.f),
+                                                centred_bf16(w1 >> 4, 16.f)};
+                        const uint32_t v1[4] = {centred_bf16(w08, 1.f), centred_bf16(w08 >> 4, 16.f), centred_bf16(w18, 1.f),
+                                                centred_bf16(w18 >> 4, 16.f)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_bf16(o[bl][0][nt], v0, hi[nt][0], hi[nt][1]);
+                            mma_bf16(o[bl][1][nt], v1, hi[nt][0], hi[nt][1]);
+                            mma_bf16(o[bl][0][nt], v0, lo[nt][0], lo[nt][1]);
+                            mma_bf16(o[bl][1][nt], v1, lo[nt][0], lo[nt][1]);
+                        }
+                    }
+                }
+            };
+            // the same by the products' range
+            auto wide_values = [&](int z) {
+                uint32_t ph[NT][2];
+                weights(z, ph);
+                unsigned over = 0;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int bl = 0; bl < G; ++bl) {
+                        uint32_t x = 0;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t v = h2_as_u32(__hmul2(u32_as_h2(ph[nt][h]), u32_as_h2(vs[z][h][bl])));
+                            x = __vmaxu2(x, v & sees(z, nt, h) & 0x7fff7fffu);
+                        }
+                        if ((x & 0xffffu) > kMost || (x >> 16) > kMost) over |= 1u << (nt * G + bl);
+                    }
+                over |= __shfl_xor_sync(0xffffffffu, over, 1);
+                far |= over | __shfl_xor_sync(0xffffffffu, over, 2);
+                if (__any_sync(0xffffffffu, far != 0)) far_values(z, ph);
+                else values(z, ph, std::true_type{});
+            };
+            auto plain_values = [&](int z, auto masked) {
+                uint32_t ph[NT][2];
+                weights(z, ph);
+                values(z, ph, masked);
+            };
+            if constexpr (kWide) {
+#pragma unroll
+                for (int z = 0; z < Z; ++z) wide_values(z);
+            } else if (first + (k + Z - 1) * (kWarps * kCellTokens) + kCellTokens > min_lim) {
+#pragma unroll
+                for (int z = 0; z < Z; ++z) plain_values(z, std::true_type{});
             } else {
 #pragma unroll
-                for (int z = 0; z < Z; ++z) values(z, std::false_type{});
+                for (int z = 0; z < Z; ++z) plain_values(z, std::false_type{});
             }
             used += Z;
             __syncwarp();  // every lane has read the slots
@@ -697,11 +808,17 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             } else {
                 issue(Z);
             }
+            return true;
         };
         int k = 0;
+        auto run = [&](auto wide) {
+            bool did = true;
 #pragma unroll 1
-        for (; k + 1 < cells; k += 2) cells_step(k, std::integral_constant<int, 2>{});
-        if (k < cells) cells_step(k, std::integral_constant<int, 1>{});
+            for (; did && k + 1 < cells; k += did ? 2 : 0) did = cells_step(k, std::integral_constant<int, 2>{}, wide);
+            if (did && k + 1 == cells && cells_step(k, std::integral_constant<int, 1>{}, wide)) ++k;
+        };
+        run(std::false_type{});
+        if (k < cells) run(std::true_type{});
 
         // --- the warps' sums into one
 #pragma unroll
@@ -715,7 +832,6 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                     sm.l[warp][8 * nt + 2 * i + e] = l[nt][e];
                 }
             }
-        if (lane == 0) sm.unit[warp] = pow2f(24) * pow2f(sigma > kSigmaMax ? 0 : -sigma);  // of codes and scales
 #pragma unroll
         for (int bl = 0; bl < G; ++bl)
 #pragma unroll
@@ -740,7 +856,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float wm = sm.m[w][r], wl = sm.l[w][r];
-                const float f = wm == -INFINITY ? 0.f : ex2(wm - mm), fu = f * sm.unit[w];
+                const float f = wm == -INFINITY ? 0.f : ex2(wm - mm), fu = f * 0x1p24f;  // of the codes
                 const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][d]);
                 ll += f * wl;
                 v.x = fmaf(fu, x.x, v.x), v.y = fmaf(fu, x.y, v.y), v.z = fmaf(fu, x.z, v.z), v.w = fmaf(fu, x.w, v.w);

@@ -1,0 +1,107 @@
+"""Attention over the cache where value blocks lie far apart: between blocks of
+dimensions, between tokens that some rows of a call see and others do not, and
+in places that no row sees. Elementwise within the bound of the definition
+(attn_reference.py), which counts a dimension's own values only; what a row does
+not see must not change a bit of it.
+"""
+import pytest
+
+from harness import cuda_available
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_available(), reason="needs a CUDA GPU")]
+
+torch = pytest.importorskip("torch")
+import attn_reference as ref  # noqa: E402
+from test_gpu_attention import Paged, check, i32  # noqa: E402
+
+
+def expect(P, q, new, scale, **kw):
+    want, bound = ref.attend(q, P.split(ref.held(P.k)), P.split(ref.held(P.v)), new, scale)
+    check(P.attend(q, new, scale=scale), want, bound, **kw)
+    P.cache.status()
+
+
+@pytest.mark.parametrize("quiet", [1.0, 0.05, 1e-4])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_finite_values_past_the_lengths_do_not_touch_a_row(dim, quiet):
+    # what an earlier sequence left behind in the last cell of a page
+    P = Paged([100, 37, 64, 1], 8, 2, dim, page=32, seed=61, scale_v=quiet).fill()
+    used = set(P.table.flatten().tolist())
+    P.table[P.table < 0] = next(i for i in range(P.pages) if i not in used)
+    q = P.q([1, 1, 1, 1])
+    clean = P.attend(q, [1, 1, 1, 1])
+    for loud in (4e5, 30.0, 1e-6):
+        left = torch.full((4 * 4, 2, dim), loud, device="cuda").bfloat16()
+        left[::2, :, ::3] *= -1
+        P.lens.add_(4)
+        P.cache.append(0, None, left, left, P.batch([4] * 4))
+        P.lens.sub_(4)
+        assert torch.equal(P.attend(q, [1, 1, 1, 1]), clean)
+
+
+@pytest.mark.parametrize("dim,hq", [(64, 8), (128, 8), (128, 1)])
+def test_values_of_a_later_row_do_not_touch_an_earlier_one(dim, hq):
+    # rows of one call that share their tiles: the last token's values are 4e5, the earlier rows do not see it
+    new = [4, 3]
+    outs = []
+    for loud in (1.0, 4e5, 1e-7):
+        P = Paged([300, 43], hq, 1, dim, page=16, seed=62, scale_v=0.05)
+        P.v[299] *= loud
+        P.v[342] *= loud
+        P.fill()
+        q = P.q(new)
+        expect(P, q, new, dim ** -0.5)
+        outs.append(P.attend(q, new))
+    for out in outs[1:]:
+        assert torch.equal(out[:3], outs[0][:3]) and torch.equal(out[4:6], outs[0][4:6])
+
+
+@pytest.mark.parametrize("loud", [30.0, 1e4, 1e5, 1e7])
+@pytest.mark.parametrize("dim,hq,new", [(64, 8, 1), (128, 8, 1), (128, 8, 4), (64, 2, 1)])
+def test_a_loud_block_of_dimensions_beside_quiet_ones(dim, hq, new, loud):
+    P = Paged([700, 90, 5], hq, 1, dim, page=16, seed=63, scale_v=0.01)
+    P.v[..., 32:64] *= loud
+    P.fill()
+    expect(P, P.q([new] * 3), [new] * 3, dim ** -0.5)
+
+
+@pytest.mark.parametrize("quiet", [1e-3, 1e-5])
+def test_quiet_blocks_in_a_long_context(quiet):
+    # weights far apart as well: scores of spread 3, so that most of a row's mass may lie on light tokens
+    P = Paged([6000], 4, 1, 128, page=64, seed=64)
+    P.v[..., 64:] *= quiet
+    P.fill()
+    expect(P, P.q([1]), [1], 3 * 128 ** -0.5)
+
+
+def test_loud_tokens_that_later_ones_outweigh():
+    # the loud tokens come first, and the scores climb until their weight is nothing
+    P = Paged([900, 900], 4, 1, 128, page=32, seed=65, scale_v=0.02)
+    P.v[:40] *= 1e7
+    P.v[900:940, :, :32] *= 1e6
+    q = torch.zeros(2, 4, 128, device="cuda").bfloat16()
+    q[..., 0] = 8.0
+    P.k.zero_()
+    P.k[:, 0, 0] = torch.linspace(-60, 60, 900, device="cuda").bfloat16().repeat(2)
+    P.fill()
+    expect(P, q, [1, 1], 0.125, l2=False)
+
+
+@pytest.mark.parametrize("at", [3, 450])
+def test_a_loud_token_that_one_head_weighs_and_another_does_not(at):
+    P = Paged([800], 8, 1, 128, page=32, seed=66, scale_v=0.02)
+    P.v[at] *= 1e7
+    P.k[at, 0, 0] = 40.0
+    P.fill()
+    q = P.q([1])
+    q[0, ::2, 0], q[0, 1::2, 0] = 8.0, -8.0
+    expect(P, q, [1], 128 ** -0.5)
+
+
+@pytest.mark.parametrize("loud", [100.0, 1e5])
+def test_one_loud_dimension_of_one_token(loud):
+    # its block's other dimensions are zero in that token, and keep the other tokens' precision
+    P = Paged([500, 20], 8, 1, 64, page=16, seed=67, scale_v=0.05)
+    P.v[7, 0, 3] = P.v[510, 0, 40] = loud
+    P.fill()
+    expect(P, P.q([1, 1]), [1, 1], 64 ** -0.5)
