@@ -406,7 +406,8 @@ moe_status_t moe_route_topk_noalloc(const void* hidden, int32_t T, const void* r
  * tokens it holds in the cache with those included, so row i sits at position
  * kv_lens[b] - (cu_tokens[b + 1] - i). A sequence may have no new token.
  * Position p lives in page block_table[b][p / page_tokens]. Rows at or past
- * cu_tokens[num_seqs] belong to no sequence and are left alone. These arrays
+ * cu_tokens[num_seqs] belong to no sequence and are left alone; a call of fewer
+ * rows (T below it) does the first T. These arrays
  * are read on the device when the kernels run, never on the host, so a CUDA
  * graph of the calls can be replayed with other contents.
  *

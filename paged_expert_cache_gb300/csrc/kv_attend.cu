@@ -132,15 +132,18 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 }
 
 // What a sequence asks for. cells: of its context (one more than the table
-// has where the length is past it, so that the missing page is met).
+// has where the length is past it, so that the missing page is met). end: the row
+// after the sequence's last one, which sits at kv - 1, whether the call has all
+// of the rows (t0 to t0 + n - 1) or not.
 struct SeqWork {
-    int t0, n, kv, cells, units, tiles, work;
+    int t0, n, end, kv, cells, units, tiles, work;
 };
 template <int NT>
 __device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, int T, int group, int seq) {
     SeqWork s;
     s.t0 = min(max(__ldg(b.cu + seq), 0), T);
-    s.n = max(min(max(__ldg(b.cu + seq + 1), 0), T) - s.t0, 0);
+    s.end = __ldg(b.cu + seq + 1);
+    s.n = max(min(max(s.end, 0), T) - s.t0, 0);
     s.kv = __ldg(b.kv_lens + seq);
     const long long cap = (long long)b.table_stride * c.page_tokens + 1;
     s.cells = (int)((unsigned)((int)min((long long)max(s.kv, 0), cap) + kCellTokens - 1) / kCellTokens);
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             const int r = g + 8 * nt;
             int tok, head;
             token_head(p, r < rows ? r : 0, tok, head);
-            lim_row[nt] = p.s.kv - p.s.n + tok + 1;
+            lim_row[nt] = p.s.kv - (p.s.end - p.s.t0) + tok + 1;
             min_lim = min(min_lim, lim_row[nt]);
             unsigned mx = 0;
 #pragma unroll

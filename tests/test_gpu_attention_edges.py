@@ -1,8 +1,11 @@
-"""Attention over the cache where value blocks lie far apart: between blocks of
+"""Edges of the attention operators' contracts.
+
+Attention over the cache where value blocks lie far apart: between blocks of
 dimensions, between tokens that some rows of a call see and others do not, and
 in places that no row sees. Elementwise within the bound of the definition
 (attn_reference.py), which counts a dimension's own values only; what a row does
-not see must not change a bit of it.
+not see must not change a bit of it. Then calls of fewer rows than the batch
+describes.
 """
 import pytest
 
@@ -105,3 +108,21 @@ def test_one_loud_dimension_of_one_token(loud):
     P.v[7, 0, 3] = P.v[510, 0, 40] = loud
     P.fill()
     expect(P, P.q([1, 1]), [1, 1], 64 ** -0.5)
+
+
+@pytest.mark.parametrize("dim,new", [(64, [1, 4, 2]), (128, [3, 4]), (128, [9])])
+def test_the_first_rows_of_a_batch_see_what_they_see_in_the_whole_call(dim, new):
+    P = Paged([100, 64, 9][:len(new)], 8, 2, dim, page=32, seed=70).fill()
+    q = P.q(new)
+    want, bound = ref.attend(q, P.split(ref.held(P.k)), P.split(ref.held(P.v)), new, dim ** -0.5)
+    for T in range(1, sum(new) + 1):
+        out = torch.full((T, 8, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+        P.cache.attend(0, q[:T], P.batch(new), out)
+        check(out, want[:T], bound[:T])
+        # the same rows are written and read back by calls of as many
+        k, v = (x[P.cu_list[1] - new[0]:P.cu_list[1]][:T] for x in (P.k, P.v))
+        kh, vh = torch.empty_like(k), torch.empty_like(v)
+        P.cache.append(0, None, k, v, P.batch(new))
+        P.cache.read(0, P.batch(new), kh, vh)
+        assert torch.equal(kh, ref.held(k).bfloat16()) and torch.equal(vh, ref.held(v).bfloat16())
+    P.cache.status()
