@@ -25,7 +25,7 @@
 // Values that some row of a CTA does not see are cleaned in shared memory
 // before use: those past the sequence's keys are set to zero, and infinities
 // and NaN behind the diagonal are replaced by zero (0 * inf would reach every
-// row) and added to the rows that do see them at the end.
+// row) and added, times their weights, to the rows that do see them at the end.
 // Tensor memory: S0 S1 (128 columns each) and O0 O1 (head_dim each), fp32.
 // Weights are bf16 (the tensor cores take one type for both operands, and the
 // values are bf16): an error of the size of the output's own rounding. Maxima
@@ -52,8 +52,8 @@ constexpr int kPromptThreads = 384;
 constexpr float kRaise = 8.0f;       // log2 of the growth a row's weights may reach before a rescale
 
 struct PromptArgs {
-    const uint16_t* v;
-    int64_t vs;
+    const uint16_t *q, *k, *v;
+    int64_t qs, ks, vs;
     const int *cu_q, *cu_k;
     int Tq, Tk, B, hq, hkv;
     float c;  // scale * log2 e
@@ -308,15 +308,26 @@ __device__ __forceinline__ bool clean_values(uint8_t* tile, int t, int from, int
 }
 
 // Adds the infinities and NaN among the values of keys first .. end - 1, which
-// the cleaning took out, to a row that sees them. Out of line: it hardly runs.
+// the cleaning took out, to a row that sees them (queries q, mc its maximum),
+// each times its weight as the tensor cores would have: infinity, or NaN where
+// the weight is 0 in fp32. Out of line: it hardly runs.
 template <int D>
-__device__ __noinline__ void add_nonfinite(const PromptArgs& a, uint16_t* row, int k0, int head, int first, int end) {
+__device__ __noinline__ void add_nonfinite(const PromptArgs& a, uint16_t* row, const uint16_t* q, float mc, int k0, int head, int first,
+                                           int end) {
+    auto value = [](const uint16_t* p) { return __uint_as_float((uint32_t)__ldg(p) << 16); };
     for (int t = first; t < end; ++t) {
         const uint16_t* v = a.v + (size_t)(k0 + t) * a.vs + (size_t)head * D;
+        const uint16_t* k = a.k + (size_t)(k0 + t) * a.ks + (size_t)head * D;
+        float weight = -1.f;  // not known yet
         for (int d = 0; d < D; ++d) {
-            const float x = __uint_as_float((uint32_t)__ldg(v + d) << 16);
+            const float x = value(v + d);
             if (!(fabsf(x) <= 3.4028235e38f)) {
-                const __nv_bfloat16 y = __float2bfloat16_rn(__uint_as_float((uint32_t)row[d] << 16) + x);
+                if (weight < 0.f) {
+                    float s = 0.f;
+                    for (int e = 0; e < D; ++e) s = fmaf(value(q + e), value(k + e), s);
+                    weight = ex2f(fmaf(s, a.c, -mc));
+                }
+                const __nv_bfloat16 y = __float2bfloat16_rn(__uint_as_float((uint32_t)row[d] << 16) + x * weight);
                 row[d] = *reinterpret_cast<const uint16_t*>(&y);
             }
         }
@@ -345,7 +356,8 @@ __device__ __forceinline__ void hide_scores(uint32_t ts, int left) {
 
 // kSingle: items are one tile, its keys in two halves, in place of two tiles.
 template <int D, bool kSingle>
-__global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, const __grid_constant__ CUtensorMap mq,
+__global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_constant__ PromptArgs a,
+                                                              const __grid_constant__ CUtensorMap mq,
                                                               const __grid_constant__ CUtensorMap mk,
                                                               const __grid_constant__ CUtensorMap mv) {
     using S = PromptSmem<D>;
@@ -861,6 +873,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
                     scale1 = m1 == -INFINITY ? 0.f : ex2f((m1 - high) * a.c);
                     l = l * f + sm.half[row][1] * scale1;
                     scale0 = f;
+                    m = high;
                 }
                 half_turn ^= 1;
             }
@@ -909,7 +922,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(PromptArgs a, cons
             }
             if (flag && used) {
                 const Span p = span_of(it);
-                add_nonfinite<D>(a, dst, it.k0, it.head, max(p.first_masked * kTile, p.seen_by_all), lim);
+                add_nonfinite<D>(a, dst, a.q + (size_t)(it.q0 + i) * a.qs + (size_t)(it.head * group + (row - tok * group)) * D,
+                                 m == -INFINITY ? 0.f : m * a.c, it.k0, it.head, max(p.first_masked * kTile, p.seen_by_all), lim);
             }
             tc_fence_before();  // the reads of O, before the weights that let it be overwritten
             if (halves && !x) bar_arrive(gsmem(&sm.half_read));
@@ -1015,7 +1029,7 @@ extern "C" moe_status_t moe_attn_prompt(const void* q, int64_t q_stride, const v
     auto items = [&](int n) { return (int64_t)Tq / (n * tokens) + std::min(num_seqs, Tq); };
     const bool single = items(2) * kv_heads <= (head_dim == 128 && Tk / num_seqs >= 1000 ? 380 : 76);
     const int64_t pairs = items(single ? 1 : 2);
-    const moe::PromptArgs a = {(const uint16_t*)v, v_stride, cu_q, cu_k, Tq, Tk, num_seqs, q_heads, kv_heads, c,
+    const moe::PromptArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, q_stride, k_stride, v_stride, cu_q, cu_k, Tq, Tk, num_seqs, q_heads, kv_heads, c,
                                (uint16_t*)out, ((uintptr_t)out & 31u) == 0};
     if (pairs * kv_heads > 0x7fffffffll) return refuse("too many rows");
     const auto launch = head_dim == 128 ? (single ? moe::launch_prompt<128, true> : moe::launch_prompt<128, false>)

@@ -5,8 +5,10 @@ dimensions, between tokens that some rows of a call see and others do not, and
 in places that no row sees. Elementwise within the bound of the definition
 (attn_reference.py), which counts a dimension's own values only; what a row does
 not see must not change a bit of it. Then calls of fewer rows than the batch
-describes.
+describes, and infinite values of prompts wherever they lie.
 """
+import math
+
 import pytest
 
 from harness import cuda_available
@@ -15,7 +17,8 @@ pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_available(), reason="
 
 torch = pytest.importorskip("torch")
 import attn_reference as ref  # noqa: E402
-from test_gpu_attention import Paged, check, i32  # noqa: E402
+import paged_expert_cache_gb300 as pec  # noqa: E402
+from test_gpu_attention import Paged, check, cumulative, prompt_inputs  # noqa: E402
 
 
 def expect(P, q, new, scale, **kw):
@@ -126,3 +129,24 @@ def test_the_first_rows_of_a_batch_see_what_they_see_in_the_whole_call(dim, new)
         P.cache.read(0, P.batch(new), kh, vh)
         assert torch.equal(kh, ref.held(k).bfloat16()) and torch.equal(vh, ref.held(v).bfloat16())
     P.cache.status()
+
+
+@pytest.mark.parametrize("dim,hkv", [(64, 1), (64, 64), (128, 1), (128, 40)])  # halves of one tile's keys, and pairs
+@pytest.mark.parametrize("low,what", [(-60.0, math.inf), (40.0, math.inf), (40.0, -math.inf), (-60.0, math.nan)])
+def test_an_infinite_value_meets_its_weight_wherever_it_lies(dim, hkv, low, what):
+    # token 10's score is 20 or 120 below the others': its weight is 2^-29, or 2^-173, which is 0 in fp32. Its value is
+    # behind the diagonal of the first rows' tile, and in a tile that later rows see all of.
+    n = 300
+    q, k, v = prompt_inputs([n], [n], hkv, hkv, dim, seed=71)
+    q.zero_(), k.zero_()
+    q[..., 0] = 8.0
+    k[..., 0] = 60.0
+    k[10, :, 0] = low
+    clean, out = torch.empty_like(q), torch.empty_like(q)
+    pec.attention_prompt(q, k, v, clean, cumulative([n]), scale=0.125)
+    v[10, :, 5] = what
+    pec.attention_prompt(q, k, v, out, cumulative([n]), scale=0.125)
+    assert torch.equal(out[:10], clean[:10])
+    assert torch.equal(out[:, :, :5], clean[:, :, :5]) and torch.equal(out[:, :, 6:], clean[:, :, 6:])
+    hit = out[10:, :, 5]
+    assert (hit == what).all() if low > 0 else hit.isnan().all()
