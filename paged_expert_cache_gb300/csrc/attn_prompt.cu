@@ -963,9 +963,12 @@ static bool encode(CUtensorMap* m, const void* p, int rank, const cuuint64_t* di
 
 template <int D, bool kSingle>
 static cudaError_t launch_prompt(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                                 int64_t grid, cudaStream_t st) {
+                                 int dev, int64_t grid, cudaStream_t st) {
     constexpr int bytes = (int)sizeof(PromptSmem<D>) + 1024;
-    static const cudaError_t set = cudaFuncSetAttribute(k_prompt<D, kSingle>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static DeviceOnce once;
+    const cudaError_t set = once.run(dev, [] {
+        return cudaFuncSetAttribute(k_prompt<D, kSingle>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
     if (set != cudaSuccess) return set;
     return launch_ex(k_prompt<D, kSingle>, dim3((unsigned)grid), dim3(kPromptThreads), bytes, st, true, a, mq, mk, mv);
 }
@@ -1034,7 +1037,9 @@ extern "C" moe_status_t moe_attn_prompt(const void* q, int64_t q_stride, const v
     if (pairs * kv_heads > 0x7fffffffll) return refuse("too many rows");
     const auto launch = head_dim == 128 ? (single ? moe::launch_prompt<128, true> : moe::launch_prompt<128, false>)
                                         : (single ? moe::launch_prompt<64, true> : moe::launch_prompt<64, false>);
-    const cudaError_t e = launch(a, mq, mk, mv, pairs * kv_heads, (cudaStream_t)stream);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = launch(a, mq, mk, mv, dev, pairs * kv_heads, (cudaStream_t)stream);
     if (e == cudaSuccess) return MOE_OK;
     moe::set_last_error(cudaGetErrorString(e));
     return MOE_ERR_CUDA;

@@ -15,6 +15,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "device_policy.h"
 
 namespace moe {
 

@@ -989,8 +989,9 @@ uint64_t attend_scratch_bytes(int device) {
 }
 
 template <int D, int NT>
-static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, int grid, cudaStream_t st) {
-    static const cudaError_t set = [] {
+static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, int dev, int grid, cudaStream_t st) {
+    static DeviceOnce once;
+    const cudaError_t set = once.run(dev, [] {
         cudaError_t e = cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT>));
         // the same division of L1 and shared memory for both: an SM is idle while it changes
         if (e == cudaSuccess)
@@ -998,7 +999,7 @@ static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a,
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(k_join<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         return e;
-    }();
+    });
     if (set != cudaSuccess) return set;
     const cudaError_t e = launch_ex(k_attend<D, NT>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
     return e != cudaSuccess ? e : launch_ex(k_join<D, NT>, dim3(grid), dim3(256), 0, st, true, c, a);
@@ -1017,8 +1018,8 @@ cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_
     // rows at a time 26.4. Not at head_dim 64, where a row's part is smaller: 7
     // streams of 5000-54000 tokens 60.2 and 57.8 us.
     const bool wide = D == 128 && (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
-    if (wide) return launch<128, 2>(c, b, a, (n + 1) / 2, st);
-    return D == 128 ? launch<128, 1>(c, b, a, n, st) : launch<64, 1>(c, b, a, n, st);
+    if (wide) return launch<128, 2>(c, b, a, dev, (n + 1) / 2, st);
+    return D == 128 ? launch<128, 1>(c, b, a, dev, n, st) : launch<64, 1>(c, b, a, dev, n, st);
 }
 
 }  // namespace moe

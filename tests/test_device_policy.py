@@ -1,0 +1,42 @@
+"""What the attention entry points keep of a device (device_policy.h), compiled
+with the host compiler and fed cases: no GPU is needed.
+
+  * a kernel's settings are made once on every device that it runs on, not once
+    in a process, and a setting that failed is tried again;
+"""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def policy(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    exe = str(tmp_path_factory.mktemp("policy") / "device_policy_check")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", "-Werror",
+                    "-I", os.path.join(ROOT, "paged_expert_cache_gb300", "csrc"),
+                    os.path.join(ROOT, "tests", "native", "device_policy_check.cpp"), "-o", exe], check=True)
+
+    def run(lines):
+        r = subprocess.run([exe], input="\n".join(lines) + "\n", capture_output=True, text=True, check=True)
+        return r.stdout.split("\n")[:len(lines)]
+    return run
+
+
+def test_settings_are_made_on_every_device(policy):
+    lines = ["once 0 0", "once 0 0", "once 1 0", "once 0 0", "once 1 0", "once 63 0", "once 63 0"]
+    assert policy(lines) == ["1 0", "1 0", "2 0", "2 0", "2 0", "3 0", "3 0"]
+
+
+def test_a_failed_setting_is_tried_again(policy):
+    assert policy(["once 0 7", "once 0 7", "once 0 0", "once 0 7"]) == ["1 7", "2 7", "3 0", "3 0"]
+
+
+def test_devices_past_the_table_are_set_each_time(policy):
+    assert policy(["once 64 0", "once 64 0", "once -1 0"]) == ["1 0", "2 0", "3 0"]

@@ -150,3 +150,21 @@ def test_an_infinite_value_meets_its_weight_wherever_it_lies(dim, hkv, low, what
     assert torch.equal(out[:, :, :5], clean[:, :, :5]) and torch.equal(out[:, :, 6:], clean[:, :, 6:])
     hit = out[10:, :, 5]
     assert (hit == what).all() if low > 0 else hit.isnan().all()
+
+
+@pytest.mark.skipif(cuda_available() and torch.cuda.device_count() < 2, reason="needs two CUDA devices")
+@pytest.mark.parametrize("dim", [64, 128])
+def test_one_process_runs_the_kernels_on_each_device(dim):
+    outs = []
+    for dev in (0, 1):
+        with torch.cuda.device(dev):
+            g = torch.Generator().manual_seed(80)
+            q, k, v = (torch.randn(40, h, dim, generator=g).bfloat16().cuda() for h in (8, 2, 2))
+            batch = pec.KVBatch(*(torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 40], [40], [[0]])))
+            cache = pec.KVCache(pec.make_kv_config(1, 1, 8, 2, dim, device=dev))
+            cache.append(0, None, k, v, batch)
+            both = torch.empty(2, 40, 8, dim, dtype=torch.bfloat16, device="cuda")
+            cache.attend(0, q, batch, both[0])
+            pec.attention_prompt(q, k, v, both[1], batch.cu_tokens)
+            outs.append(both.cpu())
+    assert torch.equal(outs[0], outs[1])
