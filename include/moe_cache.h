@@ -417,7 +417,8 @@ moe_status_t moe_route_topk_noalloc(const void* hidden, int32_t T, const void* r
  *
  * Errors of these entry points leave their message with moe_last_error(NULL).
  * Calls on one handle must not overlap (one stream, or ordered streams), and
- * are made with the handle's device current.
+ * those that enqueue work are made with the handle's device current; the others
+ * leave the current device as it is.
  */
 typedef struct moe_kv moe_kv_t;
 

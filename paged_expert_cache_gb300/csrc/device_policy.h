@@ -24,4 +24,24 @@ struct DeviceOnce {
     }
 };
 
+// Makes a device current while it lives, and then the caller's again. Runtime
+// has get(int*) and set(int), with statuses whose zero is success.
+template <class Runtime>
+struct DeviceScope {
+    using Status = decltype(Runtime::set(0));
+    int before = -1;
+    Status status;
+    explicit DeviceScope(int device) {
+        status = Runtime::get(&before);
+        if (status != Status{}) before = -1;
+        else if (before != device) status = Runtime::set(device);
+    }
+    ~DeviceScope() {
+        int now = -1;
+        if (before >= 0 && Runtime::get(&now) == Status{} && now != before) Runtime::set(before);
+    }
+    DeviceScope(const DeviceScope&) = delete;
+    DeviceScope& operator=(const DeviceScope&) = delete;
+};
+
 }  // namespace moe

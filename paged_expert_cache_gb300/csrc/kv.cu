@@ -385,6 +385,12 @@ struct moe_kv {
 
 namespace {
 
+struct CudaDevices {
+    static cudaError_t get(int* device) { return cudaGetDevice(device); }
+    static cudaError_t set(int device) { return cudaSetDevice(device); }
+};
+using DeviceScope = moe::DeviceScope<CudaDevices>;
+
 moe_status_t refuse(const char* msg) {
     moe::set_last_error(msg);
     return MOE_ERR_INVALID;
@@ -462,7 +468,8 @@ moe_status_t moe_kv_create(const moe_kv_config_t* cfg, moe_kv_t** out) {
     h->page_bytes = (uint64_t)c.page_tokens * c.kv_heads * (c.head_dim / 32) * 36;
     h->layer_bytes = h->page_bytes * (uint64_t)c.num_pages;
     const uint64_t pool = h->layer_bytes <= (1ull << 40) / (uint64_t)c.num_layers ? h->layer_bytes * (uint64_t)c.num_layers : ~0ull;
-    if (cudaError_t e = cudaSetDevice(c.device); e != cudaSuccess) { delete h; return cuda_refuse(e); }
+    const DeviceScope scope(c.device);
+    if (scope.status != cudaSuccess) { delete h; return cuda_refuse(scope.status); }
     h->scratch_bytes = moe::attend_scratch_bytes(c.device);
     void *p = nullptr, *s = nullptr;
     if (pool > (1ull << 40) || cudaMalloc(&p, pool) != cudaSuccess ||
@@ -552,7 +559,8 @@ moe_status_t moe_kv_info(const moe_kv_t* h, moe_kv_info_t* out) {
 moe_status_t moe_kv_status(moe_kv_t* h) {
     if (!h) return refuse("handle is NULL");
     unsigned bits = 0;
-    cudaError_t e = cudaSetDevice(h->cfg.device);
+    const DeviceScope scope(h->cfg.device);
+    cudaError_t e = scope.status;
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = cudaMemcpy(&bits, h->err, sizeof bits, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess && bits) e = cudaMemset(h->err, 0, sizeof bits);
@@ -563,7 +571,7 @@ moe_status_t moe_kv_status(moe_kv_t* h) {
 
 moe_status_t moe_kv_destroy(moe_kv_t* h) {
     if (!h) return MOE_OK;
-    cudaSetDevice(h->cfg.device);
+    const DeviceScope scope(h->cfg.device);
     cudaDeviceSynchronize();
     cudaFree(h->pool);
     cudaFree(h->err);

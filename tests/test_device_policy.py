@@ -3,6 +3,7 @@ with the host compiler and fed cases: no GPU is needed.
 
   * a kernel's settings are made once on every device that it runs on, not once
     in a process, and a setting that failed is tried again;
+  * calls that make a cache's device current leave the caller's current again.
 """
 import os
 import shutil
@@ -40,3 +41,9 @@ def test_a_failed_setting_is_tried_again(policy):
 
 def test_devices_past_the_table_are_set_each_time(policy):
     assert policy(["once 64 0", "once 64 0", "once -1 0"]) == ["1 0", "2 0", "3 0"]
+
+
+def test_a_scope_gives_the_callers_device_back(policy):
+    # current, the scope's, the one that cannot be set -> status, inside, after
+    lines = ["scope 0 1 9", "scope 1 0 9", "scope 2 2 9", "scope 0 5 5", "scope -1 1 9"]
+    assert policy(lines) == ["0 1 0", "0 0 1", "0 2 2", "101 0 0", "3 -1 -1"]

@@ -168,3 +168,9 @@ def test_one_process_runs_the_kernels_on_each_device(dim):
             pec.attention_prompt(q, k, v, both[1], batch.cu_tokens)
             outs.append(both.cpu())
     assert torch.equal(outs[0], outs[1])
+    # a call on a cache of another device leaves the current one as it is
+    with torch.cuda.device(0):
+        cache.status()
+        other = pec.KVCache(pec.make_kv_config(1, 1, 8, 2, dim, device=1))
+        other.close()
+        assert torch._C._cuda_getDevice() == 0
