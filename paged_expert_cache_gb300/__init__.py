@@ -451,9 +451,11 @@ def _indexes(name, t, shape=None, dims=1):
     _on_device(name, t)
 
 
-def _batch(batch):
+def _batch(batch, device):
     if not isinstance(batch, KVBatch):
         _refuse("batch must be a KVBatch")
+    if batch._device != device:
+        _refuse(f"the batch is on CUDA device {batch._device}, the cache on {device}")
     return batch._ref
 
 
@@ -489,7 +491,7 @@ class KVBatch:
         self.cu_tokens, self.kv_lens, self.block_table = cu_tokens, kv_lens, block_table
         self.args = KvBatchArgs(B, block_table.shape[1], cu_tokens.data_ptr(), kv_lens.data_ptr(),
                                 block_table.data_ptr())
-        self._ref = ctypes.addressof(self.args)
+        self._ref, self._device = ctypes.addressof(self.args), kv_lens.get_device()
 
 
 class KVCache:
@@ -552,7 +554,7 @@ class KVCache:
                 _refuse(f"rope must be on CUDA device {dev}")
             rows = rope.shape[0]
         _check(_lib.moe_kv_append(self.h, layer, None if q is None else q.data_ptr(), qs, k.data_ptr(), ks,
-                                  v.data_ptr(), vs, T, _batch(batch), None if rope is None else rope.data_ptr(), rows,
+                                  v.data_ptr(), vs, T, _batch(batch, self._device), None if rope is None else rope.data_ptr(), rows,
                                   None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
                                   _stream(stream, self._device)))
         return q_out
@@ -568,7 +570,7 @@ class KVCache:
         if not _all_dense(_torch.bfloat16, self._device, (q, (T, hq, dim)), (out, (T, hq, dim))):
             qs = _rows("q", q, hq, dim)
             _dense("out", out, hq, dim, T)
-        _check(_lib.moe_kv_attend(self.h, layer, q.data_ptr(), qs, T, _batch(batch),
+        _check(_lib.moe_kv_attend(self.h, layer, q.data_ptr(), qs, T, _batch(batch, self._device),
                                   dim ** -0.5 if scale is None else scale, out.data_ptr(),
                                   _stream(stream, self._device)))
         return out
@@ -583,7 +585,7 @@ class KVCache:
         if not _all_dense(_torch.bfloat16, self._device, (k_out, (T, hkv, dim)), (v_out, (T, hkv, dim))):
             _dense("k_out", k_out, hkv, dim, T)
             _dense("v_out", v_out, hkv, dim, T)
-        _check(_lib.moe_kv_read(self.h, layer, T, _batch(batch), k_out.data_ptr(), v_out.data_ptr(),
+        _check(_lib.moe_kv_read(self.h, layer, T, _batch(batch, self._device), k_out.data_ptr(), v_out.data_ptr(),
                                 _stream(stream, self._device)))
         return k_out, v_out
 

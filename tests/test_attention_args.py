@@ -98,3 +98,13 @@ def test_batch_refuses_wrong_arrays():
         with pytest.raises(pec.MoeError) as e:
             pec.KVBatch(*bad)
         assert e.value.status == pec.ERR_INVALID and what in str(e.value)
+
+
+def test_a_batch_of_another_device_is_refused():
+    # made without tensors, as one whose arrays are on device 1
+    batch = pec.KVBatch.__new__(pec.KVBatch)
+    batch._ref, batch._device = 16, 1
+    assert pec._batch(batch, 1) == 16
+    with pytest.raises(pec.MoeError) as e:
+        pec._batch(batch, 0)
+    assert e.value.status == pec.ERR_INVALID and "batch is on CUDA device 1" in str(e.value)
