@@ -314,7 +314,7 @@ __device__ __forceinline__ bool clean_values(uint8_t* tile, int t, int from, int
 template <int D>
 __device__ __noinline__ void add_nonfinite(const PromptArgs& a, uint16_t* row, const uint16_t* q, float mc, int k0, int head, int first,
                                            int end) {
-    auto value = [](const uint16_t* p) { return __uint_as_float((uint32_t)__ldg(p) << 16); };
+    auto value = [](const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); };
     for (int t = first; t < end; ++t) {
         const uint16_t* v = a.v + (size_t)(k0 + t) * a.vs + (size_t)head * D;
         const uint16_t* k = a.k + (size_t)(k0 + t) * a.ks + (size_t)head * D;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
     // --- the table: items before sequence t * run
     const int run = (a.B + kTable - 1) / kTable;
     auto pairs_of = [&](int s) {
-        const int n = min(max(__ldg(a.cu_q + s + 1), 0), a.Tq) - min(max(__ldg(a.cu_q + s), 0), a.Tq);
+        const int n = min(max(a.cu_q[s + 1], 0), a.Tq) - min(max(a.cu_q[s], 0), a.Tq);
         return n > 0 ? (n + reach - 1) / reach : 0;
     };
     int incl = 0, mine = 0;
@@ -516,8 +516,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
                         }
                         seq = min(seq, a.B - 1);
                     }
-                    const int bound = lane < 2 ? min(max(__ldg(a.cu_q + seq + lane), 0), a.Tq)
-                                      : lane < 4 ? min(max(__ldg(a.cu_k + seq + lane - 2), 0), a.Tk) : 0;
+                    const int bound = lane < 2 ? min(max(a.cu_q[seq + lane], 0), a.Tq)
+                                      : lane < 4 ? min(max(a.cu_k[seq + lane - 2], 0), a.Tk) : 0;
                     Item it;
                     it.q0 = __shfl_sync(0xffffffffu, bound, 0);
                     it.lq = __shfl_sync(0xffffffffu, bound, 1) - it.q0;

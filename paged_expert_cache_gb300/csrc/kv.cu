@@ -76,14 +76,14 @@ __device__ __forceinline__ void quantise8(const float (&x)[8], int (&q)[8], __ha
 __device__ __forceinline__ int row_position(const KvBatch& b, int t, bool live, int& seq) {
     seq = -1;
     if (!live) return -1;
-    const int guess = min(t, b.B - 1), c0 = __ldg(b.cu + guess);
-    int c1 = __ldg(b.cu + guess + 1), len = __ldg(b.kv_lens + guess);
+    const int guess = min(t, b.B - 1), c0 = b.cu[guess];
+    int c1 = b.cu[guess + 1], len = b.kv_lens[guess];
     seq = guess;
     if (!(c0 <= t && t < c1)) {
         seq = seq_of_row(b.cu, b.B, t);
         if (seq < 0) return -1;
-        c1 = __ldg(b.cu + seq + 1);
-        len = __ldg(b.kv_lens + seq);
+        c1 = b.cu[seq + 1];
+        len = b.kv_lens[seq];
     }
     return len - (c1 - t);
 }
@@ -118,8 +118,8 @@ struct RotaryRow {
         for (int b = 0; b < P; ++b)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float4 x = __ldg(reinterpret_cast<const float4*>(row + 32 * b + 4 * h));
-                const float4 y = __ldg(reinterpret_cast<const float4*>(row + D / 2 + 32 * b + 4 * h));
+                const float4 x = *reinterpret_cast<const float4*>(row + 32 * b + 4 * h);
+                const float4 y = *reinterpret_cast<const float4*>(row + D / 2 + 32 * b + 4 * h);
                 c[b][4 * h] = x.x, c[b][4 * h + 1] = x.y, c[b][4 * h + 2] = x.z, c[b][4 * h + 3] = x.w;
                 s[b][4 * h] = y.x, s[b][4 * h + 1] = y.y, s[b][4 * h + 2] = y.z, s[b][4 * h + 3] = y.w;
             }

@@ -48,7 +48,11 @@ inline FastDiv fast_div(uint32_t d) {
     return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l};
 }
 
-// What the kernels need of a handle and a batch, by value.
+// What the kernels need of a handle and a batch, by value. They start before the
+// kernel in front of them has ended (griddep_wait waits for it), and that one may
+// write the batch's arrays, the rotation table and the queries: so all of these
+// are read with ordinary loads, the read-only path being for what does not change
+// while a kernel runs.
 struct KvDev {
     uint8_t* pool;        // this layer's pages
     unsigned* err;        // sticky: 1 once a position or page was out of range
@@ -68,7 +72,7 @@ __device__ __forceinline__ uint8_t* kv_cell(const KvDev& c, const KvBatch& b, in
     if (n < 0) return nullptr;
     const int pg = c.cells_div.div(n);
     if (pg >= b.table_stride) return nullptr;
-    const int page = __ldg(b.table + (size_t)seq * b.table_stride + pg);
+    const int page = b.table[(size_t)seq * b.table_stride + pg];
     if ((unsigned)page >= (unsigned)c.num_pages) return nullptr;
     const int cells = c.page_tokens / kCellTokens, in = n - pg * cells;
     return c.pool + (size_t)page * c.page_bytes + (size_t)(head * cells + in) * Cell<D>::kBytes;

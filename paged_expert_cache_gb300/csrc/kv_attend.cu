@@ -141,10 +141,10 @@ struct SeqWork {
 template <int NT>
 __device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, int T, int group, int seq) {
     SeqWork s;
-    s.t0 = min(max(__ldg(b.cu + seq), 0), T);
-    s.end = __ldg(b.cu + seq + 1);
+    s.t0 = min(max(b.cu[seq], 0), T);
+    s.end = b.cu[seq + 1];
     s.n = max(min(max(s.end, 0), T) - s.t0, 0);
-    s.kv = __ldg(b.kv_lens + seq);
+    s.kv = b.kv_lens[seq];
     const long long cap = (long long)b.table_stride * c.page_tokens + 1;
     s.cells = (int)((unsigned)((int)min((long long)max(s.kv, 0), cap) + kCellTokens - 1) / kCellTokens);
     s.units = max(1, (s.cells + kWarps - 1) / kWarps);
@@ -183,7 +183,7 @@ __device__ __forceinline__ bool next_piece(Piece& p, int hi, const KvDev& c, con
         int s = p.seq + 1;
         for (;; s += 32) {  // the next sequence with new tokens: there is one, since x < hi
             const int e = min(s + lane, b.B - 1);
-            const bool has = s + lane < b.B && min(max(__ldg(b.cu + e + 1), 0), T) > min(max(__ldg(b.cu + e), 0), T);
+            const bool has = s + lane < b.B && min(max(b.cu[e + 1], 0), T) > min(max(b.cu[e], 0), T);
             const unsigned any = __ballot_sync(0xffffffffu, has);
             if (any) { s += __ffs(any) - 1; break; }
             if (s + 32 >= b.B) return false;
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             token_head(p, r < rows ? r : 0, tok, head);
             const uint16_t* src = a.q + (size_t)(p.s.t0 + tok) * a.qs + (size_t)head * D + 8 * i;
 #pragma unroll
-            for (int bl = 0; bl < G; ++bl) u[nt][bl] = __ldg(reinterpret_cast<const uint4*>(src + 32 * bl));
+            for (int bl = 0; bl < G; ++bl) u[nt][bl] = *reinterpret_cast<const uint4*>(src + 32 * bl);
         }
     };
     int ask_n, ask_k = 0;

@@ -5,7 +5,8 @@ dimensions, between tokens that some rows of a call see and others do not, and
 in places that no row sees. Elementwise within the bound of the definition
 (attn_reference.py), which counts a dimension's own values only; what a row does
 not see must not change a bit of it. Then calls of fewer rows than the batch
-describes, and infinite values of prompts wherever they lie.
+describes, infinite values of prompts wherever they lie, and calls one behind
+the other.
 """
 import math
 
@@ -150,6 +151,46 @@ def test_an_infinite_value_meets_its_weight_wherever_it_lies(dim, hkv, low, what
     assert torch.equal(out[:, :, :5], clean[:, :, :5]) and torch.equal(out[:, :, 6:], clean[:, :, 6:])
     hit = out[10:, :, 5]
     assert (hit == what).all() if low > 0 else hit.isnan().all()
+
+
+@pytest.mark.parametrize("dim,B", [(128, 1), (64, 24)])
+def test_calls_in_a_row_read_what_the_call_before_wrote(dim, B):
+    # 60 steps in one graph, each with its own lengths, pages and queries in the same buffers, as a decode loop has them
+    steps, hq, hkv, page = 60, 8, 2, 16
+    kv = [100 + 3 * b for b in range(B)]
+    P = Paged([n + steps for n in kv], hq, hkv, dim, page, seed=72)
+    tables = torch.stack([P.table[torch.randperm(B, generator=P.g, device="cuda")] for _ in range(steps)])
+    lens = torch.randint(20, 100, (steps, B), generator=P.g, device="cuda").to(torch.int32)
+    qkv = torch.randn(steps, B, hq + 2 * hkv, dim, generator=P.g, device="cuda").bfloat16()
+    rope = ref.rope_table(400, dim).cuda()
+    table, kv_lens, x = torch.empty_like(tables[0]), torch.empty_like(lens[0]), torch.empty_like(qkv[0])
+    batch = pec.KVBatch(torch.arange(B + 1, dtype=torch.int32, device="cuda"), kv_lens, table)
+    turned, out = (torch.empty(B, hq, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def run(outs, wait):
+        P.fill()
+        for s in range(steps):
+            table.copy_(tables[s]), kv_lens.copy_(lens[s]), x.copy_(qkv[s])
+            wait()
+            P.cache.append(0, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], batch, rope=rope, q_out=turned)
+            wait()
+            P.cache.attend(0, turned, batch, out)
+            pec.attention_prompt(turned, x[:, hq:hq + hkv], x[:, hq + hkv:], x[:, :hq].contiguous(), batch.cu_tokens)
+            wait()
+            outs[s].copy_(out)
+
+    want, got = (torch.zeros(steps, B, hq, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    run(want, torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(got, lambda: None)
+    for _ in range(5):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    P.cache.status()
 
 
 @pytest.mark.skipif(cuda_available() and torch.cuda.device_count() < 2, reason="needs two CUDA devices")
