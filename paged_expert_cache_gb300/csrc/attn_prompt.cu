@@ -1020,26 +1020,18 @@ extern "C" moe_status_t moe_attn_prompt(const void* q, int64_t q_stride, const v
     }
     // a scale of zero still hides what is hidden: -inf times a tiny factor is -inf
     const float c = std::fmax(scale * 1.4426950408889634f, 1e-37f);
-    // Items of two tiles, or of one with its keys in two halves. The latter are
-    // twice as many and half as long, but each loads its keys for itself: taken
-    // where pairs would leave half of the SMs idle (600 tokens, 32 heads over 4:
-    // 11.6 us, in pairs 16.0), and at head_dim 128 up to two and a half pairs per
-    // SM for long sequences, whose pairs differ most (2451 tokens 53.0 and 61.1 us;
-    // 3000, 376 pairs, 71.5 and 75.3; 3400, 428 pairs, 88.1 and 82.6). Not at 64 (1500
-    // tokens 23.3 and 22.2 us, 2451 44.6 and 40.0), nor for shorter ones (4 of 600
-    // tokens at 64: 23.3 and 19.7). At most this many items, whatever the lengths on
-    // the device are.
-    auto items = [&](int n) { return (int64_t)Tq / (n * tokens) + std::min(num_seqs, Tq); };
-    const bool single = items(2) * kv_heads <= (head_dim == 128 && Tk / num_seqs >= 1000 ? 380 : 76);
-    const int64_t pairs = items(single ? 1 : 2);
-    const moe::PromptArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, q_stride, k_stride, v_stride, cu_q, cu_k, Tq, Tk, num_seqs, q_heads, kv_heads, c,
-                               (uint16_t*)out, ((uintptr_t)out & 31u) == 0};
-    if (pairs * kv_heads > 0x7fffffffll) return refuse("too many rows");
-    const auto launch = head_dim == 128 ? (single ? moe::launch_prompt<128, true> : moe::launch_prompt<128, false>)
-                                        : (single ? moe::launch_prompt<64, true> : moe::launch_prompt<64, false>);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = launch(a, mq, mk, mv, dev, pairs * kv_heads, (cudaStream_t)stream);
+    // At most this many items of n tiles, whatever the lengths on the device are.
+    auto items = [&](int n) { return (int64_t)Tq / (n * tokens) + std::min(num_seqs, Tq); };
+    const bool single = moe::prompt_in_halves(items(2) * kv_heads, head_dim, Tk / num_seqs, moe::sm_count(dev));
+    const int64_t ctas = items(single ? 1 : 2) * kv_heads;
+    const moe::PromptArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, q_stride, k_stride, v_stride,
+                               cu_q, cu_k, Tq, Tk, num_seqs, q_heads, kv_heads, c, (uint16_t*)out, ((uintptr_t)out & 31u) == 0};
+    if (ctas > 0x7fffffffll) return refuse("too many rows");
+    const auto launch = head_dim == 128 ? (single ? moe::launch_prompt<128, true> : moe::launch_prompt<128, false>)
+                                        : (single ? moe::launch_prompt<64, true> : moe::launch_prompt<64, false>);
+    if (e == cudaSuccess) e = launch(a, mq, mk, mv, dev, ctas, (cudaStream_t)stream);
     if (e == cudaSuccess) return MOE_OK;
     moe::set_last_error(cudaGetErrorString(e));
     return MOE_ERR_CUDA;

@@ -284,11 +284,9 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvDev c, KvBatch b
 }
 
 template <int D>
-static cudaError_t launch_append(const KvDev& d, const KvBatch& b, const AppendArgs& a, cudaStream_t st) {
-    // A warp of queries takes 32 heads of a token (the rotation is read once for
-    // them), but 8 where there are too few tokens to fill the GPU that way.
+static cudaError_t launch_append(const KvDev& d, const KvBatch& b, const AppendArgs& a, int device, cudaStream_t st) {
     const int hq = a.q ? d.hq : 0;
-    const bool deep = (int64_t)a.T * ((hq + 31) / 32) >= 152 * 16;
+    const bool deep = append_takes_32_heads((int64_t)a.T * ((hq + 31) / 32), sm_count(device));
     const int chunk = deep ? 32 : 8, q_chunks = std::max((hq + chunk - 1) / chunk, 1);
     const int64_t q_warps = hq ? (int64_t)a.T * q_chunks : 0, warps = q_warps + 2 * (int64_t)d.hkv * ((a.T + 7) / 8);
     if (warps > 0x7ffffff0ll) return cudaErrorInvalidValue;
@@ -510,8 +508,8 @@ moe_status_t moe_kv_append(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
     moe::AppendArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, q_stride, k_stride, v_stride, T,
                          rope, rope_rows, (uint16_t*)q_out, (uint16_t*)k_out};
     const moe::KvDev d = dev_of(h, layer);
-    const cudaError_t e = c.head_dim == 128 ? moe::launch_append<128>(d, batch_of(batch), a, (cudaStream_t)stream)
-                                            : moe::launch_append<64>(d, batch_of(batch), a, (cudaStream_t)stream);
+    const cudaError_t e = c.head_dim == 128 ? moe::launch_append<128>(d, batch_of(batch), a, c.device, (cudaStream_t)stream)
+                                            : moe::launch_append<64>(d, batch_of(batch), a, c.device, (cudaStream_t)stream);
     if (e == cudaErrorInvalidValue) return refuse("T is too large");
     return e == cudaSuccess ? MOE_OK : cuda_refuse(e);
 }

@@ -91,6 +91,8 @@ __device__ __forceinline__ int seq_of_row(const int* cu, int B, int t) {
     return lo;
 }
 
+// SMs of a device (asked for once; a GB300's where that fails).
+int sm_count(int device);
 // Device scratch of the attention kernel on `device`, zeroed once.
 uint64_t attend_scratch_bytes(int device);
 // Whether every piece of work of such a call can be numbered in 31 bits.

@@ -971,15 +971,15 @@ bool attend_fits(const KvDev& c, const KvBatch& b, int T) {
     return rows < (1ll << 30) && (double)tiles * (double)(units + kBegin) * (double)c.hkv < (double)(1ll << 30);
 }
 
-static int sm_count(int device) {
-    static int counts[64] = {};
-    if (device < 0 || device >= 64) return 152;
-    if (!counts[device]) {
-        int n = 0;
+int sm_count(int device) {
+    static std::atomic<int> counts[kMaxDevices] = {};
+    if (device < 0 || device >= kMaxDevices) return 152;
+    int n = counts[device].load(std::memory_order_relaxed);
+    if (!n) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) n = 152;
-        counts[device] = n;
+        counts[device].store(n, std::memory_order_relaxed);
     }
-    return counts[device];
+    return n;
 }
 static int max_grid(int device) { return std::min(2 * sm_count(device), kMaxCtas); }
 

@@ -5,6 +5,9 @@
 //   scope <current> <device> <fails>  a scope of the device while another is
 //     current, with a runtime that refuses to set device <fails>; prints the
 //     scope's status, the device current inside, and the one after it
+//   heads <tasks> <sms>               whether append takes 32 heads a warp
+//   halves <pairs> <head_dim> <keys per sequence> <sms>   whether a prompt's
+//     items are one tile with its keys in halves
 #include <cstdio>
 #include <cstring>
 
@@ -27,6 +30,7 @@ int main() {
     static moe::DeviceOnce once;
     char what[16];
     int device, status, made = 0;
+    long long n, keys;
     while (std::scanf(" %15s", what) == 1) {
         if (std::strcmp(what, "once") == 0 && std::scanf("%d %d", &device, &status) == 2) {
             const int got = once.run(device, [&] {
@@ -42,6 +46,10 @@ int main() {
                 inside = current;
             }
             std::printf("%d %d %d\n", status, inside, current);
+        } else if (std::strcmp(what, "heads") == 0 && std::scanf("%lld %d", &n, &device) == 2) {
+            std::printf("%d\n", moe::append_takes_32_heads(n, device));
+        } else if (std::strcmp(what, "halves") == 0 && std::scanf("%lld %d %lld %d", &n, &status, &keys, &device) == 4) {
+            std::printf("%d\n", moe::prompt_in_halves(n, status, keys, device));
         } else {
             return 1;
         }

@@ -3,7 +3,8 @@ with the host compiler and fed cases: no GPU is needed.
 
   * a kernel's settings are made once on every device that it runs on, not once
     in a process, and a setting that failed is tried again;
-  * calls that make a cache's device current leave the caller's current again.
+  * calls that make a cache's device current leave the caller's current again;
+  * the append and prompt kernels choose their forms by the device's SMs.
 """
 import os
 import shutil
@@ -47,3 +48,14 @@ def test_a_scope_gives_the_callers_device_back(policy):
     # current, the scope's, the one that cannot be set -> status, inside, after
     lines = ["scope 0 1 9", "scope 1 0 9", "scope 2 2 9", "scope 0 5 5", "scope -1 1 9"]
     assert policy(lines) == ["0 1 0", "0 0 1", "0 2 2", "101 0 0", "3 -1 -1"]
+
+
+@pytest.mark.parametrize("sms", [152, 148, 76])
+def test_forms_follow_the_sms(policy, sms):
+    cases = {
+        f"heads {16 * sms} {sms}": "1", f"heads {16 * sms - 1} {sms}": "0", f"heads {2 ** 40} {sms}": "1",
+        f"halves {sms // 2} 64 5000 {sms}": "1", f"halves {sms // 2 + 1} 64 5000 {sms}": "0",
+        f"halves {sms // 2} 128 10 {sms}": "1", f"halves {sms // 2 + 1} 128 999 {sms}": "0",
+        f"halves {5 * sms // 2} 128 1000 {sms}": "1", f"halves {5 * sms // 2 + 1} 128 1000 {sms}": "0",
+    }
+    assert policy(list(cases)) == list(cases.values())
