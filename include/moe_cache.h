@@ -479,8 +479,10 @@ moe_status_t moe_kv_append(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
  * kv_heads). A row that sees no position is zero.
  *   q   : device bf16 rows [T] x q_heads x head_dim (rotated), q_stride apart
  *   out : device bf16 [T x q_heads x head_dim]
- * Made for one or a few new tokens per sequence; any number is right.
- * Asynchronous on `stream`. */
+ * Made for one or a few new tokens per sequence; any number is right. A call
+ * whose rows (8 at a time) times its block table's capacity (128 tokens at a
+ * time, and 6) times kv_heads could pass 2^30 is refused: the lengths are on
+ * the device. Asynchronous on `stream`. */
 moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_stride, int32_t T,
                            const moe_kv_batch_t* batch, float scale, void* out, void* stream);
 
@@ -496,7 +498,8 @@ moe_status_t moe_kv_read(moe_kv_t* h, int32_t layer, int32_t T, const moe_kv_bat
  * 0 .. lk - lq + i of its lk keys (rows cu_k[b] ..), so with cu_k = cu_q whole
  * prompts, and with more keys than queries a prompt's later chunk over its
  * context. Rows that see no key are zero; keys and values a row does not see
- * do not touch it, whatever they hold.
+ * do not touch it, whatever they hold. An infinity that a row sees makes its
+ * dimension infinite, or NaN where its weight is 0 in fp32.
  *   q, k, v : device bf16 rows [Tq], [Tk], [Tk]; strides and alignment as in
  *             moe_kv_append
  *   cu_q, cu_k : device int32 [num_seqs + 1], first entry 0, not decreasing,

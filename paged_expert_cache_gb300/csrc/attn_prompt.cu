@@ -32,9 +32,10 @@
 // and sums are fp32; a row's maximum is raised, and its output rescaled, only
 // when a score exceeds it by 2^8.
 //
-// Measured: 8192 tokens, 32 query heads over 4, head_dim 128: 335 us in a graph
-// (1640 TFLOP/s, 0.84 of cuBLAS's bf16 rate); 20 sequences of up to 1500 tokens at
-// head_dim 64 105 us. A key tile of a pair takes 2058 cycles of the tensor cores
+// Measured: 8192 tokens, 32 query heads over 4, head_dim 128: 351 us a call, where
+// the power limit lowers the clock, 333 us in a graph (1560 and 1650 TFLOP/s, 0.80
+// and 0.85 of cuBLAS's bf16 rate); 2451 tokens 51 us; 512 tokens over a context of
+// 4000 37 us; 20 sequences of up to 1500 tokens at head_dim 64 106 us. A key tile of a pair takes 2058 cycles of the tensor cores
 // at head_dim 128 and about 2770 here; at 64 it takes 1538 (N = 64 products run at
 // half rate) and 2240.
 #include <cuda.h>

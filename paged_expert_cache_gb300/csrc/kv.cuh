@@ -35,8 +35,9 @@ struct Cell {
     __device__ static int v_scale(int t, int b) { return (((t >> 3) * 4 + ((t & 7) >> 1)) * G + b) * 4 + (t & 1) * 2; }
 };
 
-// Division of 0 <= x < 2^31 by a divisor fixed on the host: with 2^(l - 1) < d
-// <= 2^l, x / d = (x + hi(x m)) / 2^l for m = 2^32 (2^l - d) / d + 1, rounded
+// Division of 0 <= x < 2^31 by a divisor fixed on the host (Granlund and
+// Montgomery, Division by Invariant Integers using Multiplication, 1994): with
+// 2^(l - 1) < d <= 2^l, x / d = (x + hi(x m)) / 2^l for m = 2^32 (2^l - d) / d + 1, rounded
 // down.
 struct FastDiv {
     uint32_t m, l;

@@ -52,7 +52,7 @@
 // Measured in a graph at head_dim 128: 64 sequences of 4000 to 12000 tokens, 64
 // query heads over 8, 120 us (4.9 TB/s, 0.73 of a copy's rate; the warps' issue slots
 // and latencies bound it, not the memory). 28 or 32 heads over 4: 32 sequences of up
-// to 4095 tokens 19.8 us, one of 100003 tokens 25.0, one of 513 tokens 8.5, where the
+// to 4095 tokens 19.3 us, one of 100003 tokens 24.0, one of 513 tokens 8.5, where the
 // two launches, an item's start and the join are most of it.
 #include <algorithm>
 #include <type_traits>
