@@ -36,15 +36,15 @@
 //    scores' layout by one 8 x 8 transposition, rounded to fp16 twice (p, then
 //    the product: 2^-11 each, an eighth of the output's own rounding each).
 //    fp16's range does not hold every product. What a row sees of a block of
-//    dimensions is `far` from the first product past kMost on, or from a warp's
+//    dimensions is `far` from the first product past it on, or from a warp's
 //    first step on where its scales there are below kQuiet: such products are
 //    formed in fp32 and taken as two bf16 operands (16 bits, fp32's range), in
 //    matrix products of their own to which the other rows give zeros. So neither
 //    other blocks, nor what other rows see, nor what no row sees touch a bit of it.
-//    (One power of two for all of a warp's scales is faster where values are large,
-//    157 us in place of 258 for the 64 sequences below with values 20 times as
-//    large, 236 with ones 1000 times as small; but a block 2^11 below the largest
-//    one met, hidden or not, loses bits by it.)
+//    (One power of two for all of a warp's scales is faster there, 157 us for the
+//    64 sequences below with values 20 times as large or 1000 times as small, in
+//    place of 169 and 250; but a block 2^11 below the largest one met, hidden or
+//    not, loses bits by it.)
 // Softmax statistics, sums and outputs are fp32. A row's running maximum is
 // raised only when a score exceeds it by 2^kLazy, the outputs being rescaled
 // then.
@@ -74,9 +74,11 @@ constexpr int kBegin = 6;
 // fp16's range for the product p * d. A row's largest weight is 2^kOffset when
 // its maximum is set and may grow by 2^kLazy, so with scales below 2 a product is
 // below 2^15, and with scales of kQuiet and more weights down to 2^-14 of the
-// largest keep all bits and down to 2^-24 count.
+// largest keep all bits and down to 2^-24 count. A row that has seen a scale of 2
+// or more raises its maximum at once: its products then hold scales up to 2^5
+// (with values 20 times as large as usual 169 us, 258 if it is as lazy as others).
 constexpr float kLazy = 4.0f, kOffset = 10.0f;
-constexpr uint32_t kMost = 0x7800, kQuiet = 0x1400;  // 2^15 and 2^-10 as fp16
+constexpr uint32_t kMost = 0x7bff, kQuiet = 0x1400;  // fp16's largest value, and 2^-10
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -515,6 +517,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
         unsigned far = 0;            // bit nt G + bl: row 8 nt + g's products in block bl are
+        unsigned loud = 0;           // bit nt: row 8 nt + g has seen a scale of 2 or more
 
         const int cells = warp_cells(p, warp), first = (p.u0 * kWarps + warp) * kCellTokens;
         auto words = [&](uint32_t (&r)[G], const uint8_t* src) {
@@ -560,6 +563,11 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         auto cells_step = [&](int k, auto count, auto wide) {
             constexpr int Z = decltype(count)::value;
             constexpr bool kWide = decltype(wide)::value;
+            // which of tokens 8h + 2i, + 1 of cell z row 8 nt + g sees
+            auto sees = [&](int z, int nt, int h) {
+                const int t = first + (k + z) * (kWarps * kCellTokens) + 8 * h + 2 * i;
+                return (t < lim_row[nt] ? 0xffffu : 0u) | (t + 1 < lim_row[nt] ? 0xffff0000u : 0u);
+            };
             float s[Z][NT][4];       // c0, c1: token g, rows 2i, 2i + 1; c2, c3: token g + 8
             uint32_t vs[Z][2][G];    // value scales
             uint32_t seen = 0;       // their bits
@@ -614,7 +622,27 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             // own scores and scales; only if one does not are the maxima shared.
             // (A scale of 2 or more, and NaN, have the top exponent bit.)
             bool raise = !kWide && (seen & 0x40004000u) != 0;
-            float mx[NT][2];
+            float mx[NT][2], lazy[NT][2];
+            if constexpr (kWide) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int z = 0; z < Z; ++z)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int bl = 0; bl < G; ++bl) any |= vs[z][h][bl];
+                            if (any & sees(z, nt, h) & 0x40004000u) loud |= 1u << nt;
+                        }
+                loud |= __shfl_xor_sync(0xffffffffu, loud, 1);
+                loud |= __shfl_xor_sync(0xffffffffu, loud, 2);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    lazy[nt][e] = kWide && (__shfl_sync(0xffffffffu, loud, 8 * i + 4 * e) >> nt & 1u) ? 0.f : kLazy;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -622,7 +650,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                     float v = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
                     if (Z == 2) v = fmaxf(v, fmaxf(s[Z - 1][nt][e], s[Z - 1][nt][e + 2]));
                     mx[nt][e] = rf[nt][e] * v;
-                    raise |= mx[nt][e] > m[nt][e] + kLazy;
+                    raise |= mx[nt][e] > m[nt][e] + lazy[nt][e];
                 }
             if (__any_sync(0xffffffffu, raise)) {
                 if (kWide && k == 0) far = small_blocks(vs, count, true);
@@ -637,7 +665,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
                         // raised where it is exceeded by enough, so that a row is raised by its own scores alone
-                        v = v > m[nt][e2] + kLazy ? v : m[nt][e2];
+                        v = v > m[nt][e2] + lazy[nt][e2] ? v : m[nt][e2];
                         f[e2] = v == m[nt][e2] ? 1.f : ex2(m[nt][e2] - v);
                         m[nt][e2] = v;
                         l[nt][e2] *= f[e2];
@@ -667,11 +695,6 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                         l[nt][1] += e1;
                         ph[nt][h] = transpose8(pack_h2(e0, e1));
                     }
-            };
-            // which of them row 8 nt + g sees
-            auto sees = [&](int z, int nt, int h) {
-                const int t = first + (k + z) * (kWarps * kCellTokens) + 8 * h + 2 * i;
-                return (t < lim_row[nt] ? 0xffffu : 0u) | (t + 1 < lim_row[nt] ? 0xffff0000u : 0u);
             };
             // values of cell z; `masked`: some row does not see all of it
             auto values = [&](int z, const uint32_t (&ph)[NT][2], auto masked) {
