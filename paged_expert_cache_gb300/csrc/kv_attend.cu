@@ -74,9 +74,11 @@ constexpr int kBegin = 6;
 // fp16's range for the product p * d. A row's largest weight is 2^kOffset when
 // its maximum is set and may grow by 2^kLazy, so with scales below 2 a product is
 // below 2^15, and with scales of kQuiet and more weights down to 2^-14 of the
-// largest keep all bits and down to 2^-24 count. A row that has seen a scale of 2
-// or more raises its maximum at once: its products then hold scales up to 2^5
-// (with values 20 times as large as usual 169 us, 258 if it is as lazy as others).
+// largest keep all bits and down to 2^-24 count (down to 2^-34 / d for a smaller
+// scale d that comes later in a block that is not far). A row that has seen a
+// scale of 2 or more raises its maximum at once: its products then hold scales up
+// to 2^5 (with values 20 times as large as usual 169 us, 258 if it is as lazy as
+// others).
 constexpr float kLazy = 4.0f, kOffset = 10.0f;
 constexpr uint32_t kMost = 0x7bff, kQuiet = 0x1400;  // fp16's largest value, and 2^-10
 constexpr float kLog2e = 1.4426950408889634f;
