@@ -526,6 +526,82 @@ moe_status_t moe_kv_status(moe_kv_t* h);
 /* Synchronises and frees everything the handle owns. NULL is accepted. */
 moe_status_t moe_kv_destroy(moe_kv_t* h);
 
+/* ---------------------------------------------------------------------------
+ * Between the halves, and behind the last layer (no counterpart on the pages, as
+ * above).
+ */
+
+/* Element types of tensors that may be either. */
+typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type_t;
+
+/* A block's output into the residual stream, and the sum, normed, for the next
+ * block:
+ *   s = x + scale * gate * (post_weight ? rms(y) * post_weight : y)   (x without y)
+ *   x_out = s, out = rms(s) * weight, rms(v) = v / sqrt(mean(v^2) + eps)
+ * in fp32, each output rounded once (out is made from s before it is rounded to
+ * x_out's type). All pointers device; a row's elements are contiguous and rows
+ * are *_stride elements apart. Aligned rows (addresses and strides multiples of
+ * 16 bytes, hidden of 8) are read 16 bytes at a time; any other is right. */
+typedef struct {
+    int32_t rows, hidden;        /* rows >= 0, hidden 1..32768 */
+    int32_t x_type;              /* moe_type_t of x and x_out */
+    int32_t y_type;              /* of y */
+    int32_t w_type;              /* of weight, post_weight and gate */
+    int32_t gate_wide;           /* 1: a gate row has hidden values; 0: one */
+    float scale, eps;            /* finite; eps not negative */
+    const void* x;               /* [rows x hidden] */
+    int64_t x_stride;
+    const void* y;               /* [rows x hidden], or NULL: s = x */
+    int64_t y_stride;
+    void* x_out;                 /* [rows x hidden], may be x itself; or NULL */
+    int64_t x_out_stride;
+    void* out;                   /* bf16 [rows x hidden], or NULL */
+    int64_t out_stride;
+    const void* weight;          /* [hidden], or NULL: ones */
+    const void* post_weight;     /* [hidden], or NULL: y is not normed */
+    const void* gate;            /* rows of hidden or of one value; or NULL: one */
+    int64_t gate_stride;         /* 0: the same gate row for all rows */
+} moe_norm_t;
+
+/* Runs on the current device, asynchronous on `stream`; allocates nothing.
+ * x_out may be x; no other output may overlap an input. MOE_ERR_INVALID for bad
+ * arguments (the message with moe_last_error(NULL)); rows = 0 does nothing. */
+moe_status_t moe_residual_norm(const moe_norm_t* args, void* stream);
+
+/* How each row's token is drawn; device arrays [rows], or NULL for the value
+ * named. A row's tokens are ranked by logit, the lower index first among equals,
+ * and those of logit -inf are left out. With weights w = exp((logit - largest) /
+ * temperature), each filter keeps the first tokens of that order:
+ *   top_k : the first k (k <= 0: all)
+ *   top_p : of what top_k kept, the fewest whose weights sum to at least top_p
+ *           times the sum of all of its weights (>= 1: all; never fewer than one)
+ *   min_p : those with w >= min_p (<= 0: all; never fewer than one)
+ * The token drawn is the first one, in that order, whose weight and those before
+ * it sum to more than uniform times the sum of all kept ones. */
+typedef struct {
+    const float* temperature;  /* finite, >= 0; 0 takes the first token (NULL: 1) */
+    const int32_t* top_k;      /* NULL: 0 */
+    const float* top_p;        /* NULL: 1 */
+    const float* min_p;        /* NULL: 0 */
+    const float* uniform;      /* in [0, 1), clamped to it (NULL: every row takes its first token) */
+} moe_sampling_t;
+
+/* The next token of each row of logits.
+ *   logits   : device [rows x vocab] of `type` (moe_type_t), rows row_stride
+ *              elements apart; vocab 1..2^20, rows up to 2^24
+ *   tokens   : device int32 [rows]
+ *   logprobs : device fp32 [rows], the logarithm of the token's share of the kept
+ *              weights (0 where the first token is taken); or NULL
+ * Weights are accurate to 2^-34 and sums of them are exact, so a token differs
+ * from the one that exact arithmetic draws only where a boundary lies that near;
+ * results do not depend on how the work is split. A row without a distribution (a
+ * NaN or +inf among its logits, nothing but -inf, a NaN or bad temperature, NaN
+ * settings) gives token -1 and a NaN. Runs on the current device, asynchronous on
+ * `stream`; allocates nothing. MOE_ERR_INVALID for bad arguments; rows = 0 does
+ * nothing. */
+moe_status_t moe_sample(const void* logits, int32_t type, int64_t row_stride, int32_t rows, int32_t vocab,
+                        const moe_sampling_t* settings, int32_t* tokens, float* logprobs, void* stream);
+
 /* Synchronises, empties every slot, restores the initial LRU order and clears
  * the counters and trace. Expert data stays loaded. */
 moe_status_t moe_cache_reset(moe_cache_t* h);
@@ -534,7 +610,8 @@ moe_status_t moe_cache_reset(moe_cache_t* h);
 moe_status_t moe_cache_destroy(moe_cache_t* h);
 
 /* Last error message of the handle (when h is NULL, of the calling thread's
- * last failed create, moe_kv_* or moe_attn_* call). Never NULL; valid until
+ * last failed create, moe_kv_*, moe_attn_*, moe_residual_norm or moe_sample
+ * call). Never NULL; valid until
  * the next call on h. */
 const char* moe_last_error(const moe_cache_t* h);
 

@@ -66,6 +66,17 @@ class KvInfo(ctypes.Structure):
     _fields_ = [("page_bytes", u64), ("pool_device_bytes", u64), ("scratch_device_bytes", u64)]
 
 
+class NormArgs(ctypes.Structure):
+    _fields_ = [("rows", i32), ("hidden", i32), ("x_type", i32), ("y_type", i32), ("w_type", i32), ("gate_wide", i32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("x", vp), ("x_stride", i64), ("y", vp),
+                ("y_stride", i64), ("x_out", vp), ("x_out_stride", i64), ("out", vp), ("out_stride", i64),
+                ("weight", vp), ("post_weight", vp), ("gate", vp), ("gate_stride", i64)]
+
+
+class SamplingArgs(ctypes.Structure):
+    _fields_ = [("temperature", vp), ("top_k", vp), ("top_p", vp), ("min_p", vp), ("uniform", vp)]
+
+
 NUM_STAGES = 7
 STAGES = ["route", "copy", "gateup", "down", "prefill_topk", "prefill_plan", "layer"]
 
@@ -119,6 +130,8 @@ def load():
         "moe_kv_destroy": (i32, [vp]),
         "moe_attn_prompt": (i32, [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, i32, i32, ctypes.c_float, vp,
                                   vp]),
+        "moe_residual_norm": (i32, [vp, vp]),
+        "moe_sample": (i32, [vp, i32, i64, i32, i32, vp, vp, vp, vp]),
         "moe_cache_reset": (i32, [vp]),
         "moe_cache_destroy": (i32, [vp]),
     }
@@ -632,3 +645,119 @@ def attention_prompt(q, k, v, out, cu_q, cu_k=None, scale=None, stream=None):
                                   cu_k.data_ptr(), hq, hkv, dim, dim ** -0.5 if scale is None else scale,
                                   out.data_ptr(), _stream(stream, dev)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Between the halves, and behind the last layer.
+# ---------------------------------------------------------------------------
+def _type_of(name, t):
+    """moe_type_t of a tensor."""
+    torch = _torch
+    if not isinstance(t, torch.Tensor):
+        _refuse(f"{name} must be a torch tensor")
+    if t.dtype is torch.bfloat16:
+        return 0
+    if t.dtype is torch.float32:
+        return 1
+    _refuse(f"{name} must be bfloat16 or float32")
+
+
+def _matrix(name, t, shape, dev):
+    """Checks t as rows of the given shape on CUDA device dev; returns (address, row stride)."""
+    if t.shape != shape:
+        _refuse(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, st = t.stride() if t.shape[0] > 1 else (shape[1], t.stride()[1])
+    if st != 1 and shape[1] > 1:
+        _refuse(f"the rows of {name} must be contiguous")
+    if t.get_device() != dev:
+        _refuse(f"{name} must be on the current CUDA device")
+    return t.data_ptr(), rows
+
+
+def residual_norm(x, y=None, out=None, weight=None, post_weight=None, gate=None, scale=1.0, eps=1e-6, x_out=None, stream=None):
+    """moe_residual_norm: s = x + scale * gate * (rms(y) * post_weight, or y
+    without post_weight), written to x_out (None: to x itself), and out = rms(s) *
+    weight, bf16. x, y bf16 or fp32 [T, H]; weight, post_weight [H] and gate ([H],
+    [T, H] or [T, 1]) of one type, bf16 or fp32. Without y only out is written;
+    without out only x_out. Returns out, or x_out without it."""
+    torch = _need_torch()
+    xt = _type_of("x", x)
+    if x.dim() != 2:
+        _refuse("x must be [T, H]")
+    shape = x.shape
+    T, H = shape
+    dev = x.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _refuse("x must be on the current CUDA device")
+    a = NormArgs(T, H, xt, xt, 0, 0, scale, eps)
+    a.x, a.x_stride = _matrix("x", x, shape, dev)
+    if y is not None:
+        a.y_type = _type_of("y", y)
+        a.y, a.y_stride = _matrix("y", y, shape, dev)
+        if x_out is None:
+            x_out = x
+        if _type_of("x_out", x_out) != xt:
+            _refuse("x_out must have x's type")
+        a.x_out, a.x_out_stride = _matrix("x_out", x_out, shape, dev)
+    elif x_out is not None or post_weight is not None or gate is not None:
+        _refuse("x_out, post_weight and gate need y")
+    if out is not None:
+        if _type_of("out", out) != 0:
+            _refuse("out must be bfloat16")
+        a.out, a.out_stride = _matrix("out", out, shape, dev)
+    wt = None
+    for name, t in (("weight", weight), ("post_weight", post_weight), ("gate", gate)):
+        if t is None:
+            continue
+        if _type_of(name, t) != (wt if wt is not None else _type_of(name, t)):
+            _refuse("weight, post_weight and gate must have one type")
+        wt = _type_of(name, t)
+        if name == "gate":
+            if t.dim() == 1 and t.shape[0] == H:
+                a.gate, _ = _matrix(name, t[None], (1, H), dev)
+                a.gate_wide = 1
+            elif t.dim() == 2 and t.shape == shape:
+                a.gate, a.gate_stride = _matrix(name, t, shape, dev)
+                a.gate_wide = 1
+            elif t.dim() == 2 and t.shape == (T, 1):
+                a.gate, a.gate_stride = _matrix(name, t, (T, 1), dev)
+            else:
+                _refuse(f"gate must be [{H}], [{T}, {H}] or [{T}, 1], got {tuple(t.shape)}")
+        else:
+            if t.dim() != 1:
+                _refuse(f"{name} must be [{H}]")
+            setattr(a, name, _matrix(name, t[None], (1, H), dev)[0])
+    a.w_type = wt or 0
+    _check(load().moe_residual_norm(ctypes.addressof(a), _stream(stream, dev)))
+    return x_out if out is None else out
+
+
+def sample(logits, tokens, uniform=None, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None, stream=None):
+    """moe_sample: the next token of each row of logits (bf16 or fp32 [T, V]) into
+    tokens (int32 [T]), and its log-probability into logprobs (fp32 [T]) if given.
+    uniform, temperature, top_p, min_p fp32 [T] and top_k int32 [T], or None: the
+    likeliest token (uniform), 1, no filter. Returns tokens."""
+    torch = _need_torch()
+    kind = _type_of("logits", logits)
+    if logits.dim() != 2:
+        _refuse("logits must be [T, V]")
+    T, V = logits.shape
+    dev = logits.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _refuse("logits must be on the current CUDA device")
+    at, rows = _matrix("logits", logits, logits.shape, dev)
+    out = []
+    for name, t, dtype in (("tokens", tokens, torch.int32), ("temperature", temperature, torch.float32),
+                           ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32),
+                           ("uniform", uniform, torch.float32), ("logprobs", logprobs, torch.float32)):
+        if t is None and name != "tokens":
+            out.append(None)
+            continue
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 1 and t.shape[0] == T and t.is_contiguous()):
+            _refuse(f"{name} must be a contiguous {str(dtype)[6:]} tensor of shape ({T},)")
+        if t.get_device() != dev:
+            _refuse(f"{name} must be on the current CUDA device")
+        out.append(t.data_ptr())
+    a = SamplingArgs(*out[1:6])
+    _check(load().moe_sample(at, kind, rows, T, V, ctypes.addressof(a), out[0], out[6], _stream(stream, dev)))
+    return tokens
