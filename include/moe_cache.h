@@ -486,6 +486,35 @@ moe_status_t moe_kv_append(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
 moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_stride, int32_t T,
                            const moe_kv_batch_t* batch, float scale, void* out, void* stream);
 
+/* Groups of neighbouring sequences of a batch whose first positions are the same:
+ * continuations of one prompt, requests behind one long instruction. Device arrays,
+ * read when the kernels run. */
+typedef struct {
+    int32_t num_groups;          /* >= 1 */
+    const int32_t* cu_seqs;      /* [num_groups + 1], not decreasing: group g is sequences cu_seqs[g] .. cu_seqs[g + 1] - 1 */
+    const int32_t* prefix_lens;  /* [num_groups]: positions that all of the group's sequences have in common */
+} moe_kv_groups_t;
+
+/* moe_kv_attend for such a batch, with each group's common positions read once for
+ * all of its rows (on the tensor cores, 128 or 256 rows at a time) instead of once
+ * for each sequence. Positions below prefix_lens[g] (rounded down to 16, and no
+ * more than the group's first sequence holds) are looked up in the first
+ * sequence's row of the block table, the others in each sequence's own; the
+ * sequences' rows name the same pages for them, or copies. Sequences in no group
+ * are attended over as moe_kv_attend does. A row sees the positions up to its own
+ * there too, if it lies among the common ones.
+ *   workspace : device, 256-byte aligned, at least moe_kv_shared_bytes for T; the
+ *               call's own until its work on `stream` is done (graphs that may run
+ *               at the same time need one each)
+ * The rest, and the limits, as in moe_kv_attend. Should a bounded wait inside the
+ * kernel give up (0.2 s), the rows concerned come out as NaN. */
+moe_status_t moe_kv_attend_shared(moe_kv_t* h, int32_t layer, const void* q, int64_t q_stride, int32_t T,
+                                  const moe_kv_batch_t* batch, const moe_kv_groups_t* groups, float scale, void* out,
+                                  void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Bytes of the workspace of a moe_kv_attend_shared call of T rows (or fewer). */
+moe_status_t moe_kv_shared_bytes(const moe_kv_t* h, int32_t T, uint64_t* bytes);
+
 /* Reads the keys and values of the batch's T rows back as bf16 (the held
  * values rounded once): k_out, v_out device bf16 [T x kv_heads x head_dim].
  * With cu_tokens the running sums of kv_lens that is every held token, packed

@@ -62,6 +62,10 @@ class KvBatchArgs(ctypes.Structure):
     _fields_ = [("num_seqs", i32), ("table_stride", i32), ("cu_tokens", vp), ("kv_lens", vp), ("block_table", vp)]
 
 
+class KvGroupArgs(ctypes.Structure):
+    _fields_ = [("num_groups", i32), ("cu_seqs", vp), ("prefix_lens", vp)]
+
+
 class KvInfo(ctypes.Structure):
     _fields_ = [("page_bytes", u64), ("pool_device_bytes", u64), ("scratch_device_bytes", u64)]
 
@@ -124,6 +128,8 @@ def load():
         "moe_kv_create": (i32, [P(KvConfig), P(vp)]),
         "moe_kv_append": (i32, [vp, i32, vp, i64, vp, i64, vp, i64, i32, vp, vp, i32, vp, vp, vp]),
         "moe_kv_attend": (i32, [vp, i32, vp, i64, i32, vp, ctypes.c_float, vp, vp]),
+        "moe_kv_attend_shared": (i32, [vp, i32, vp, i64, i32, vp, vp, ctypes.c_float, vp, vp, u64, vp]),
+        "moe_kv_shared_bytes": (i32, [vp, i32, ctypes.POINTER(u64)]),
         "moe_kv_read": (i32, [vp, i32, i32, vp, vp, vp, vp]),
         "moe_kv_info": (i32, [vp, P(KvInfo)]),
         "moe_kv_status": (i32, [vp]),
@@ -507,6 +513,23 @@ class KVBatch:
         self._ref, self._device = ctypes.addressof(self.args), kv_lens.get_device()
 
 
+class KVGroups:
+    """moe_kv_groups_t: groups of neighbouring sequences of a batch that have their
+    first positions in common. cu_seqs int32 [G + 1] (group g is the sequences
+    cu_seqs[g] .. cu_seqs[g + 1] - 1), prefix_lens int32 [G], on the device and kept
+    by the object; they may be rewritten between calls."""
+
+    def __init__(self, cu_seqs, prefix_lens):
+        _indexes("prefix_lens", prefix_lens)
+        G = prefix_lens.shape[0]
+        if G < 1:
+            _refuse("at least one group is needed")
+        _indexes("cu_seqs", cu_seqs, (G + 1,))
+        self.cu_seqs, self.prefix_lens = cu_seqs, prefix_lens
+        self.args = KvGroupArgs(G, cu_seqs.data_ptr(), prefix_lens.data_ptr())
+        self._ref, self._device = ctypes.addressof(self.args), prefix_lens.get_device()
+
+
 class KVCache:
     """One handle of the C library (moe_kv_t*): keys and values of every layer
     in pages of Q4_0 blocks. Calls run on torch's current stream unless one is
@@ -586,6 +609,38 @@ class KVCache:
         _check(_lib.moe_kv_attend(self.h, layer, q.data_ptr(), qs, T, _batch(batch, self._device),
                                   dim ** -0.5 if scale is None else scale, out.data_ptr(),
                                   _stream(stream, self._device)))
+        return out
+
+    def shared_workspace(self, T):
+        """A workspace for attend_shared calls of up to T rows (moe_kv_shared_bytes): a uint8 tensor."""
+        n = u64(0)
+        _check(_lib.moe_kv_shared_bytes(self.h, T, ctypes.byref(n)))
+        return _torch.empty(n.value, dtype=_torch.uint8, device=f"cuda:{self._device}")
+
+    def attend_shared(self, layer, q, batch, groups, out, workspace, scale=None, stream=None):
+        """moe_kv_attend_shared: attend for a batch whose sequences have their first
+        positions in common by groups (a KVGroups), each group's read once for all of
+        them. workspace: from shared_workspace, of at least q's rows, and not used by
+        another call until this one's work is done."""
+        hq, hkv, dim = self._dims
+        T = _torch.Tensor
+        if not isinstance(q, T) or not isinstance(out, T) or not isinstance(workspace, T):
+            _refuse("q, out and workspace must be torch tensors")
+        rows = q.shape[0]
+        qs = hq * dim
+        dev = self._device
+        if not _all_dense(_torch.bfloat16, dev, (q, (rows, hq, dim)), (out, (rows, hq, dim))):
+            qs = _rows("q", q, hq, dim)
+            _dense("out", out, hq, dim, rows)
+        if not isinstance(groups, KVGroups):
+            _refuse("groups must be a KVGroups")
+        if groups._device != dev or workspace.get_device() != dev:
+            _refuse(f"groups and workspace must be on the cache's CUDA device {dev}")
+        if not workspace.is_contiguous():
+            _refuse("workspace must be contiguous")
+        _check(_lib.moe_kv_attend_shared(self.h, layer, q.data_ptr(), qs, rows, _batch(batch, dev), groups._ref,
+                                         dim ** -0.5 if scale is None else scale, out.data_ptr(), workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), _stream(stream, dev)))
         return out
 
     def read(self, layer, batch, k_out, v_out, stream=None):

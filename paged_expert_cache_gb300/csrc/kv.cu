@@ -530,6 +530,41 @@ moe_status_t moe_kv_attend(moe_kv_t* h, int32_t layer, const void* q, int64_t q_
     return e == cudaSuccess ? MOE_OK : cuda_refuse(e);
 }
 
+moe_status_t moe_kv_shared_bytes(const moe_kv_t* h, int32_t T, uint64_t* bytes) {
+    if (!h || !bytes) return refuse("NULL argument");
+    if (T < 0) return refuse("T must be >= 0");
+    *bytes = moe::shared_bytes(h->cfg.device, T, h->cfg.q_heads, h->cfg.head_dim);
+    return MOE_OK;
+}
+
+moe_status_t moe_kv_attend_shared(moe_kv_t* h, int32_t layer, const void* q, int64_t q_stride, int32_t T,
+                                  const moe_kv_batch_t* batch, const moe_kv_groups_t* groups, float scale, void* out,
+                                  void* workspace, uint64_t workspace_bytes, void* stream) {
+    if (const char* p = call_problem(h, layer, T, batch)) return refuse(p);
+    const moe_kv_config_t& c = h->cfg;
+    if (!groups || !groups->cu_seqs || !groups->prefix_lens || groups->num_groups < 1)
+        return refuse("groups need at least one group, and neither array NULL");
+    if (T == 0) return MOE_OK;
+    if (!q || !out || !workspace) return refuse("NULL q, out or workspace");
+    const moe::KvDev d = dev_of(h, layer);
+    const moe::KvBatch b = batch_of(batch);
+    if (!moe::attend_fits(d, b, T) || !moe::shared_fits(d, b, groups->num_groups, T))
+        return refuse("the batch is too large: more than 2^30 units of 128 cache tokens and 8 rows are possible");
+    if (!(scale >= 0.f && scale <= 3.4028235e38f)) return refuse("scale must be finite and not negative");
+    if (!rows_ok(q, q_stride, c.q_heads, c.head_dim) || ((uintptr_t)out & 15u))
+        return refuse("q and out need 16-byte aligned rows: q_stride a multiple of 8 and not below q_heads * head_dim");
+    if ((uintptr_t)workspace & 255u) return refuse("the workspace must be 256-byte aligned");
+    if (workspace_bytes < moe::shared_bytes(c.device, T, c.q_heads, c.head_dim))
+        return refuse("the workspace is smaller than moe_kv_shared_bytes");
+    const moe::KvGroups g = {groups->cu_seqs, groups->prefix_lens, groups->num_groups};
+    const moe::SharedParts parts = moe::shared_parts(workspace, c.device, T, c.q_heads, c.head_dim);
+    cudaError_t e = moe::launch_shared(d, b, g, parts, c.head_dim, (const uint16_t*)q, q_stride, T, scale, (cudaStream_t)stream);
+    if (e == cudaSuccess)
+        e = moe::launch_attend_rest(d, b, g, parts, c.head_dim, (const uint16_t*)q, q_stride, T, scale, (uint16_t*)out,
+                                    h->scratch, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_refuse(e);
+}
+
 moe_status_t moe_kv_read(moe_kv_t* h, int32_t layer, int32_t T, const moe_kv_batch_t* batch, void* k_out,
                          void* v_out, void* stream) {
     if (const char* p = call_problem(h, layer, T, batch)) return refuse(p);

@@ -66,6 +66,43 @@ struct KvBatch {
     int B, table_stride;
 };
 
+// Groups of neighbouring sequences that have their first positions in common, and
+// what the kernel that attends over those leaves for the others: for each row a
+// sum that has begun (the unnormalised output and a head: the exponent that its
+// weights 2^(score - exponent) refer to, the sum of the weights, the first of the
+// slots that go on with it, and their number with, above 16 bits, its row there).
+struct KvGroups {
+    const int *cu, *prefix;
+    int n;
+};
+struct SharedParts {
+    float *o, *slot_o;          // [T x q_heads], [CTAs x kSlotRows] rows of head_dim
+    float4 *head, *slot_head;   // as many
+    int slots;
+};
+constexpr int kSlotRows = 256;
+
+// The positions that a group has in common, as far as they are read for it as a
+// whole: whole cells, held by its first sequence and in reach of its table.
+__device__ __forceinline__ int common_tokens(const KvDev& c, const KvBatch& b, const KvGroups& g, int group) {
+    const int first = g.cu[group];
+    if ((unsigned)first >= (unsigned)b.B) return 0;
+    const long long cap = (long long)b.table_stride * c.page_tokens;
+    const int p = (int)min((long long)min(g.prefix[group], b.kv_lens[first]), cap);
+    return max(p, 0) / kCellTokens * kCellTokens;
+}
+// The group of a sequence, or -1.
+__device__ __forceinline__ int group_of_seq(const KvGroups& g, int seq) {
+    if (seq < g.cu[0] || seq >= g.cu[g.n]) return -1;
+    int lo = 0, hi = g.n;  // cu[lo] <= seq < cu[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (g.cu[mid] <= seq) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 // Cell `n` of a sequence (positions 16 n ..) for head `head`, or null where the
 // table or the pool has no such page.
 template <int D>
@@ -100,5 +137,18 @@ uint64_t attend_scratch_bytes(int device);
 bool attend_fits(const KvDev& c, const KvBatch& b, int T);
 cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
                           uint16_t* out, void* scratch, cudaStream_t st);
+// The same behind launch_shared: over what the groups do not have in common, joined
+// with what it left.
+cudaError_t launch_attend_rest(const KvDev& c, const KvBatch& b, const KvGroups& g, const SharedParts& parts, int D,
+                               const uint16_t* q, int64_t q_stride, int T, float scale, uint16_t* out, void* scratch,
+                               cudaStream_t st);
+
+// Attention over what groups have in common (kv_shared.cu): the workspace of such a
+// call and its parts, whether its work can be numbered in 31 bits, and the launch.
+uint64_t shared_bytes(int device, int T, int hq, int D);
+SharedParts shared_parts(void* workspace, int device, int T, int hq, int D);
+bool shared_fits(const KvDev& c, const KvBatch& b, int groups, int T);
+cudaError_t launch_shared(const KvDev& c, const KvBatch& b, const KvGroups& g, const SharedParts& parts, int D,
+                          const uint16_t* q, int64_t q_stride, int T, float scale, cudaStream_t st);
 
 }  // namespace moe

@@ -90,6 +90,8 @@ struct AttendArgs {
     float scale;
     uint16_t* out;
     FastDiv group_div;
+    KvGroups groups;      // where they are given, with what launch_shared left of their rows
+    SharedParts parts;
     float* partial;       // [grid][2] records: first and last piece of each CTA
     struct Split* split;  // [grid] the item that starts in a CTA and ends in another
 };
@@ -102,6 +104,7 @@ struct alignas(16) Split {
     int pieces;            // 0: none
     int from, row, rows;   // rows `row` to rows - 1
     int t0, head, tile;
+    int common;            // the rows have a sum that has begun
 };
 constexpr int kJoinAhead = 5;  // pieces that a lane of k_join asks for at once
 // Whether a block takes a row instead of a warp. (pieces - 2 CTAs are in the item's
@@ -138,12 +141,14 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // What a sequence asks for. cells: of its context (one more than the table
 // has where the length is past it, so that the missing page is met). end: the row
 // after the sequence's last one, which sits at kv - 1, whether the call has all
-// of the rows (t0 to t0 + n - 1) or not.
+// of the rows (t0 to t0 + n - 1) or not. from: the first cell that is not its
+// group's in common (kShared); the others are counted from there.
 struct SeqWork {
-    int t0, n, end, kv, cells, units, tiles, work;
+    int t0, n, end, kv, cells, units, tiles, work, from;
 };
-template <int NT>
-__device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, int T, int group, int seq) {
+template <int NT, bool kShared>
+__device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, const AttendArgs& a, int group, int seq) {
+    const int T = a.T;
     SeqWork s;
     s.t0 = min(max(b.cu[seq], 0), T);
     s.end = b.cu[seq + 1];
@@ -151,6 +156,12 @@ __device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, in
     s.kv = b.kv_lens[seq];
     const long long cap = (long long)b.table_stride * c.page_tokens + 1;
     s.cells = (int)((unsigned)((int)min((long long)max(s.kv, 0), cap) + kCellTokens - 1) / kCellTokens);
+    s.from = 0;
+    if constexpr (kShared) {
+        const int g = group_of_seq(a.groups, seq);
+        if (g >= 0) s.from = common_tokens(c, b, a.groups, g) / kCellTokens;
+        s.cells = max(s.cells - s.from, 0);
+    }
     s.units = max(1, (s.cells + kWarps - 1) / kWarps);
     s.tiles = (s.n * group + 8 * NT - 1) / (8 * NT);
     s.work = (s.units + kBegin) * c.hkv * s.tiles;
@@ -178,9 +189,9 @@ __device__ __forceinline__ void piece_at(Piece& p, int x, int hi) {
     p.next = x - in + to;
 }
 // Steps to the next piece; false at `hi`. Whole warps.
-template <int NT>
-__device__ __forceinline__ bool next_piece(Piece& p, int hi, const KvDev& c, const KvBatch& b, int T, int group, int lane) {
-    const int x = p.next;
+template <int NT, bool kShared>
+__device__ __forceinline__ bool next_piece(Piece& p, int hi, const KvDev& c, const KvBatch& b, const AttendArgs& a, int group, int lane) {
+    const int x = p.next, T = a.T;
     if (x >= hi) return false;
     if (x >= p.prefix + p.s.work) {
         p.prefix += p.s.work;
@@ -193,7 +204,7 @@ __device__ __forceinline__ bool next_piece(Piece& p, int hi, const KvDev& c, con
             if (s + 32 >= b.B) return false;
         }
         p.seq = s;
-        p.s = seq_work<NT>(c, b, T, group, s);
+        p.s = seq_work<NT, kShared>(c, b, a, group, s);
     }
     piece_at(p, x, hi);
     return true;
@@ -251,7 +262,44 @@ __device__ __forceinline__ void put_row(const KvDev& c, const AttendArgs& a, int
         make_uint2(*reinterpret_cast<uint32_t*>(&y0), *reinterpret_cast<uint32_t*>(&y1));
 }
 
-template <int D, int NT>
+// Adds what launch_shared left of a row to four dims of its sum; m becomes an
+// exponent that the weights refer to (-inf: no weight but 0).
+template <int D>
+__device__ __forceinline__ void add_common(const KvDev& c, const AttendArgs& a, int t0, int head, int row, int d, float4& v, float& m, float& l) {
+    const int group = c.hq / c.hkv, tok = a.group_div.div(row);
+    const size_t at = (size_t)(t0 + tok) * c.hq + head * group + row - tok * group;
+    auto join = [&](const float4& h, const float4& x) {
+        const float high = fmaxf(m, h.x);
+        const float f0 = m == -INFINITY ? 0.f : ex2(m - high), f = h.x == -INFINITY ? 0.f : ex2(h.x - high);
+        m = high;
+        l = fmaf(f0, l, f * h.y);
+        v.x = fmaf(f0, v.x, f * x.x), v.y = fmaf(f0, v.y, f * x.y), v.z = fmaf(f0, v.z, f * x.z), v.w = fmaf(f0, v.w, f * x.w);
+    };
+    m -= kOffset;
+    const float4 h = __ldcg(a.parts.head + at);
+    join(h, __ldcg(reinterpret_cast<const float4*>(a.parts.o + at * D + d)));
+    const int more = __float_as_int(h.w) & 0xffff;
+    // a row that the groups do not cover (a batch whose arrays contradict each other) has a head of anything
+    if ((unsigned)__float_as_int(h.z) > (unsigned)a.parts.slots || more > a.parts.slots - __float_as_int(h.z)) {
+        l = __int_as_float(0x7fc00000);
+        return;
+    }
+    const size_t slot = (size_t)__float_as_int(h.z) * kSlotRows + (__float_as_int(h.w) >> 16 & (kSlotRows - 1));
+    for (int e = 0; e < more; e += 4) {
+        float4 hs[4], xs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const size_t s = slot + (size_t)min(e + k, more - 1) * kSlotRows;
+            hs[k] = __ldcg(a.parts.slot_head + s);
+            xs[k] = __ldcg(reinterpret_cast<const float4*>(a.parts.slot_o + s * D + d));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (e + k < more) join(hs[k], xs[k]);
+    }
+}
+
+template <int D, int NT, bool kShared>
 __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a) {
     constexpr int G = D / 32, kRows = 8 * NT;
     using C = Cell<D>;
@@ -285,7 +333,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         // every warp by itself: a lane takes a few neighbouring sequences
         const int per = (b.B + 31) / 32, s0 = min(lane * per, b.B), s1 = min(s0 + per, b.B);
         int mine = 0;
-        for (int s = s0; s < s1; ++s) mine += seq_work<NT>(c, b, a.T, group, s).work;
+        for (int s = s0; s < s1; ++s) mine += seq_work<NT, kShared>(c, b, a, group, s).work;
         int upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -300,7 +348,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         prefix = __shfl_sync(0xffffffffu, upto - mine, l);
         if (per > 1)
             for (;; ++seq) {
-                const int w = seq_work<NT>(c, b, a.T, group, seq).work;
+                const int w = seq_work<NT, kShared>(c, b, a, group, seq).work;
                 if (lo < prefix + w) break;
                 prefix += w;
             }
@@ -325,11 +373,11 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             __syncthreads();
         };
         int mine = 0, incl, sum, below = 0;
-        for (int s = tid; s < b.B; s += kAttThreads) mine += seq_work<NT>(c, b, a.T, group, s).work;
+        for (int s = tid; s < b.B; s += kAttThreads) mine += seq_work<NT, kShared>(c, b, a, group, s).work;
         block_scan(mine, incl, total);
         if (!share()) return;
         for (int s0 = 0; s0 < b.B; s0 += kAttThreads) {
-            const int s = s0 + tid, w = s < b.B ? seq_work<NT>(c, b, a.T, group, s).work : 0;
+            const int s = s0 + tid, w = s < b.B ? seq_work<NT, kShared>(c, b, a, group, s).work : 0;
             block_scan(w, incl, sum);
             incl += below;
             if (incl - w <= lo && lo < incl) {
@@ -353,7 +401,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
     // steps a kept piece on; false (and the piece as it was) at the end of the run, an item's idle units among it
     auto step = [&](Piece& at) {
         Piece p = at;
-        const bool there = next_piece<NT>(p, hi, c, b, a.T, group, lane) && p.u1 > p.u0;
+        const bool there = next_piece<NT, kShared>(p, hi, c, b, a, group, lane) && p.u1 > p.u0;
         if (there) keep_piece(at, p);
         return there;
     };
@@ -382,7 +430,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         Piece p;
         p.seq = seq;
         p.prefix = prefix;
-        p.s = seq_work<NT>(c, b, a.T, group, seq);
+        p.s = seq_work<NT, kShared>(c, b, a, group, seq);
         piece_at(p, lo, hi);
         if (p.u1 == p.u0) {  // a run of idle units only
             if (tid == 0) a.split[blockIdx.x].pieces = 0;
@@ -442,7 +490,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             if ((ask_k & 31) == 0) {  // the next 32 cells' places
                 const int k = ask_k + lane;
                 const Piece& q = sm.ask[warp];
-                addr = k < ask_n ? kv_cell<D>(c, b, q.seq, (q.u0 + k) * kWarps + warp, q.head) : nullptr;
+                addr = k < ask_n ? kv_cell<D>(c, b, q.seq, (kShared ? q.s.from : 0) + (q.u0 + k) * kWarps + warp, q.head) : nullptr;
             }
             copy_cell(ask_k & 31, issued % kStages);
             ++issued;
@@ -521,7 +569,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         unsigned far = 0;            // bit nt G + bl: row 8 nt + g's products in block bl are
         unsigned loud = 0;           // bit nt: row 8 nt + g has seen a scale of 2 or more
 
-        const int cells = warp_cells(p, warp), first = (p.u0 * kWarps + warp) * kCellTokens;
+        const int cells = warp_cells(p, warp), first = ((kShared ? p.s.from : 0) + p.u0 * kWarps + warp) * kCellTokens;
         auto words = [&](uint32_t (&r)[G], const uint8_t* src) {
             if constexpr (G == 4) {
                 const uint4 v = *reinterpret_cast<const uint4*>(src);
@@ -890,6 +938,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 v.x = fmaf(fu, x.x, v.x), v.y = fmaf(fu, x.y, v.y), v.z = fmaf(fu, x.z, v.z), v.w = fmaf(fu, x.w, v.w);
             }
             if (whole) {
+                if (kShared && p.s.from) add_common<D>(c, a, p.s.t0, p.head, p.tile * kRows + r, d, v, mm, ll);
                 put_row<D>(c, a, p.s.t0, p.head, p.tile * kRows + r, d, v, mm, ll);
             } else {
                 __stcg(reinterpret_cast<float4*>(rec + r * D + d), v);
@@ -902,7 +951,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             const int c0 = cta_of(p.first), c1 = cta_of(p.first + p.s.units - 1), row = (int)blockIdx.x - c0;
             const bool many = many_pieces<D>(c1 - c0 + 1, rows);
             if (row < (many ? rows : 1)) {
-                a.split[blockIdx.x] = {c1 - c0 + 1, c0, row, many ? row + 1 : rows, p.s.t0, p.head, p.tile};
+                a.split[blockIdx.x] = {c1 - c0 + 1, c0, row, many ? row + 1 : rows, p.s.t0, p.head, p.tile, kShared ? p.s.from : 0};
                 split_here = true;
             }
         }
@@ -918,7 +967,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 // one of 513 tokens 8.5 us (8.6, 8.9), one of 100003 25.0 (25.4, 24.5), 32 of up to
 // 4095 19.8 (20.2, 20.3). One wave of blocks: with four for each CTA, a quarter of
 // the rows each, the last two of these were 26.4 and 20.3 us.
-template <int D, int NT>
+template <int D, int NT, bool kShared>
 __global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
     constexpr int kLanes = D / 4, kSide = 32 / kLanes;  // lanes of a row's dims; pieces a warp takes side by side
     __shared__ float4 part[8][kSide][kLanes];
@@ -927,7 +976,7 @@ __global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
     griddep_wait();
     const int4* at = reinterpret_cast<const int4*>(a.split + blockIdx.x);
     const int4 s0 = __ldcg(at), s1 = __ldcg(at + 1);
-    const Split s = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z};
+    const Split s = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
     if (s.pieces == 0) return;
     const bool many = s.row + 1 == s.rows;  // one row: all warps take it (few pieces of a single row as well)
     const float* base = a.partial + (size_t)s.from * 2 * kPartFloats(D);
@@ -984,7 +1033,10 @@ __global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
                 m = high;
             }
         }
-        if (set == 0) put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
+        if (set == 0) {
+            if (kShared && s.common) add_common<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
+            put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
+        }
         if (many) break;
         __syncwarp();  // the sums are free again
     }
@@ -1013,29 +1065,31 @@ uint64_t attend_scratch_bytes(int device) {
     return (uint64_t)max_grid(device) * (2 * kPartFloats(128) * sizeof(float) + sizeof(Split));
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kShared>
 static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, int dev, int grid, cudaStream_t st) {
     static DeviceOnce once;
     const cudaError_t set = once.run(dev, [] {
-        cudaError_t e = cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT>));
+        cudaError_t e = cudaFuncSetAttribute(k_attend<D, NT, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT>));
         // the same division of L1 and shared memory for both: an SM is idle while it changes
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k_attend<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+            e = cudaFuncSetAttribute(k_attend<D, NT, kShared>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k_join<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+            e = cudaFuncSetAttribute(k_join<D, NT, kShared>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         return e;
     });
     if (set != cudaSuccess) return set;
-    const cudaError_t e = launch_ex(k_attend<D, NT>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
-    return e != cudaSuccess ? e : launch_ex(k_join<D, NT>, dim3(grid), dim3(256), 0, st, true, c, a);
+    const cudaError_t e = launch_ex(k_attend<D, NT, kShared>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
+    return e != cudaSuccess ? e : launch_ex(k_join<D, NT, kShared>, dim3(grid), dim3(256), 0, st, true, c, a);
 }
 
-cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
-                          uint16_t* out, void* scratch, cudaStream_t st) {
+template <bool kShared>
+static cudaError_t launch_form(const KvDev& c, const KvBatch& b, const KvGroups& g, const SharedParts& parts, int D,
+                               const uint16_t* q, int64_t q_stride, int T, float scale, uint16_t* out, void* scratch,
+                               cudaStream_t st) {
     int dev = 0;
     if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     const int n = max_grid(dev);
-    AttendArgs a = {q, q_stride, T, scale, out, fast_div((uint32_t)(c.hq / c.hkv)), (float*)scratch,
+    AttendArgs a = {q, q_stride, T, scale, out, fast_div((uint32_t)(c.hq / c.hkv)), g, parts, (float*)scratch,
                     (Split*)((uint8_t*)scratch + (size_t)n * 2 * kPartFloats(128) * sizeof(float))};
     // 16 rows at a time where a head has more than 8 in a step (its group times
     // the new tokens of an average sequence), although only half as many warps
@@ -1043,8 +1097,19 @@ cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_
     // rows at a time 26.4. Not at head_dim 64, where a row's part is smaller: 7
     // streams of 5000-54000 tokens 60.2 and 57.8 us.
     const bool wide = D == 128 && (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
-    if (wide) return launch<128, 2>(c, b, a, dev, (n + 1) / 2, st);
-    return D == 128 ? launch<128, 1>(c, b, a, dev, n, st) : launch<64, 1>(c, b, a, dev, n, st);
+    if (wide) return launch<128, 2, kShared>(c, b, a, dev, (n + 1) / 2, st);
+    return D == 128 ? launch<128, 1, kShared>(c, b, a, dev, n, st) : launch<64, 1, kShared>(c, b, a, dev, n, st);
 }
+
+cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
+                          uint16_t* out, void* scratch, cudaStream_t st) {
+    return launch_form<false>(c, b, KvGroups{}, SharedParts{}, D, q, q_stride, T, scale, out, scratch, st);
+}
+cudaError_t launch_attend_rest(const KvDev& c, const KvBatch& b, const KvGroups& g, const SharedParts& parts, int D,
+                               const uint16_t* q, int64_t q_stride, int T, float scale, uint16_t* out, void* scratch,
+                               cudaStream_t st) {
+    return launch_form<true>(c, b, g, parts, D, q, q_stride, T, scale, out, scratch, st);
+}
+
 
 }  // namespace moe
