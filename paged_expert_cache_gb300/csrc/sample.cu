@@ -7,16 +7,20 @@
 // out in that order, holds the point u.
 //
 // So all that is asked of a row are places in its order, by count or by mass, and
-// nothing is sorted: a place is found by a histogram over the keys (the logits'
-// bits, made to order as integers), then over the bin that holds it, until a bin
-// is a single key. 2048 bins at a time, so bf16 logits take two rounds, fp32 up to
-// three.
+// the row is never sorted. One histogram of 2048 bins, linear in the logit, says
+// which bin holds a place. Where no more than 512 tokens lie up to there, they are
+// listed, ranked and the row is done by one CTA; otherwise only the bin's own
+// tokens are listed, or, if these are too many, told apart by histograms over their
+// keys (the logits' bits, made to order as integers), 2048 bins a round: equal
+// tokens need no list.
 //
 // Which token holds a point is a comparison of sums over the whole vocabulary:
 // with 100000 tokens kept, an error of 1e-8 in the sums moves one draw in a
-// thousand. So weights are computed to about 2^-36 (weight_of) and summed as
+// thousand. So weights are computed to about 2^-36 (Weigher) and summed as
 // integers of 2^-43, exactly and in any order: results do not depend on how a row
-// is split, nor on the order of atomics.
+// is split, nor on the order of atomics. That costs about 45 instructions a token,
+// which bounds rows of wide nuclei; where top-k or min-p leave few tokens, only
+// theirs are computed, and the chain of steps over the cluster bounds the call.
 //
 // A row is a cluster's: its CTAs hold a slice of it each in shared memory, which
 // is read from HBM once, and put their histograms together over distributed
@@ -53,27 +57,21 @@ struct SampleArgs {
     float* logprobs;
 };
 
-struct alignas(16) Pow2Entry {  // 2^(r / 32)
-    float hi, lo;               // as a sum
-    unsigned long long fixed;   // in units of 2^-36
+struct Pow2Entry {  // 2^(r / 32), as a sum
+    float hi, lo;
 };
 __device__ const Pow2Entry kPow2[32] = {
-    {0x1.0000000000000p+0f, 0x0.0p+0f, 68719476736ull}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f, 70224237334ull},
-    {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f, 71761947898ull}, {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f, 73333329938ull},
-    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f, 74939120765ull}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f, 76580073833ull},
-    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f, 78256959093ull}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f, 79970563360ull},
-    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f, 81721690674ull}, {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f, 83511162683ull},
-    {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f, 85339819026ull}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f, 87208517730ull},
-    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f, 89118135606ull}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f, 91069568669ull},
-    {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f, 93063732552ull}, {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f, 95101562938ull},
-    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f, 97184015999ull}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f, 99312068844ull},
-    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f, 101486719979ull}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f, 103708989773ull},
-    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f, 105979920939ull}, {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f, 108300579022ull},
-    {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f, 110672052900ull}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f, 113095455294ull},
-    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f, 115571923291ull}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f, 118102618875ull},
-    {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f, 120688729477ull}, {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f, 123331468528ull},
-    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f, 126032076028ull}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f, 128791819132ull},
-    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f, 131611992741ull}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f, 134493920110ull},
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f},
+    {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}, {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f},
+    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}, {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f},
+    {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f},
+    {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}, {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f},
+    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}, {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f},
+    {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f},
+    {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}, {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f},
+    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f},
 };
 
 // What a CTA tells the others of its cluster, a line per sender.
@@ -81,16 +79,26 @@ struct SampleNote {
     uint64_t mass;
     uint32_t a, b, c, d;
 };
+constexpr int kList = kSampleThreads;  // tokens that a list takes
 struct alignas(16) SampleSmem {
-    uint32_t lo[kBins], hi[kBins];  // a histogram: counts in lo, or masses as two words
-    uint64_t sums[kBins];           // this CTA's chunk of the cluster's histogram
-    Pow2Entry pow2[32];
-    SampleNote note[2][kMaxCluster];             // a phase's and the next one's
-    SampleNote found;                            // the bin found, by its owner
-    uint64_t wmass[kSampleWarps];
+    union {
+        struct {
+            uint32_t lo[kBins], hi[kBins], cnt[kBins];  // a histogram: masses as two words, and counts
+        };
+        struct {
+            uint64_t mine[kList];                       // the tokens that this CTA lists: key, ~index
+            uint64_t list[kList], ranked[kList];        // the cluster's (rank 0)
+        };
+    };
+    uint64_t sums[kBins];                       // this CTA's chunk of the cluster's histogram
+    uint32_t cnts[kBins];
+    SampleNote note[2][kMaxCluster];            // a phase's and the next one's
+    SampleNote found;                           // a place, by who found it
+    uint64_t wmass[kSampleWarps], wsame[kSampleWarps];
     uint32_t wcnt[kSampleWarps], wa[kSampleWarps], wb[kSampleWarps], wc[kSampleWarps];
-    float c, cl;                                 // log2 e / temperature
-    double least;                                // temperature * log min_p
+    int listed;
+    float c, cl;                                // log2 e / temperature
+    double least;                               // temperature * log min_p
 };
 
 // Keys order as the values do; -0 is 0.
@@ -102,20 +110,21 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// 2^(c (v - top)) in units of 2^-kMassBits, c = log2 e / temperature.
+// 2^(c (v - top)) in units of 2^-kMassBits, c = log2 e / temperature. Whole warps.
 //
 // v - top is taken as a sum of two floats, and x = c (v - top) as x + xl. With k =
 // rint(32 x) and g = x - k / 32 (exact, at most 1/64), 2^x = 2^(k/32) (1 + z), z =
 // e^y - 1 for y = (g + xl) ln 2: the first term h = g ln 2 with its rounding, the
 // others by the series up to y^5 / 120 (the next term is below 2^-48). The power
-// of the table is held as hi + lo and in fixed point; hi * h keeps its rounding. The
+// 2^(r/32), r = k mod 32, is held by lane r as hi + lo (a shuffle has no bank
+// conflicts, as a table in shared memory has); hi * h keeps its rounding. The
 // largest error left is that of the last sums, about 2^-36.
 struct Weigher {
-    float top, c, cl;
-    __device__ uint64_t operator()(float v, const Pow2Entry* table) const {
+    float top, c, cl, hi, lo;  // hi, lo: this lane's power
+    __device__ __forceinline__ uint64_t operator()(float v) const {
         const float d = v - top, t = d - v, dl = (v - (d - t)) + (-top - t);
         const float x = d * c;
-        if (!(x > -44.f)) return 0;  // below half a unit, or -inf
+        const bool some = x > -44.f;  // not below half a unit, nor -inf
         const float xl = fmaf(dl, c, fmaf(d, cl, fmaf(d, c, -x)));
         const float j = fmaf(x, 32.f, 12582912.f), kf = j - 12582912.f;  // 1.5 2^23: rint in the last bits
         const int k = __float_as_int(j) - 0x4b400000;
@@ -126,12 +135,14 @@ struct Weigher {
         const float y = h + e;
         const float s = fmaf(y, fmaf(y, fmaf(y, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f);
         const float q = fmaf(y * y, s, e);
-        const Pow2Entry p = table[k & 31];
-        const float a = p.hi * h, b = fmaf(p.lo, h, fmaf(p.hi, q, fmaf(p.hi, h, -a)));
-        const uint64_t m = p.fixed + (uint64_t)(int64_t)(__float2int_rn(a * 0x1p36f) + __float2int_rn(b * 0x1p36f));
-        const int down = 36 - kMassBits - (k >> 5);
-        if (down <= 0) return m << -down;
-        return down > 62 ? 0 : (m + (1ull << (down - 1))) >> down;
+        const float p = __shfl_sync(0xffffffffu, hi, k & 31), pl = __shfl_sync(0xffffffffu, lo, k & 31);
+        const float a = p * h, b = fmaf(pl, h, fmaf(p, q, fmaf(p, h, -a))) + pl;
+        // in units of 2^-36: p is in [1, 2), its bits those of an integer
+        const uint64_t m = ((uint64_t)((__float_as_uint(p) & 0x7fffffu) | 0x800000u) << 13) +
+                           (uint64_t)(int64_t)(__float2int_rn(a * 0x1p36f) + __float2int_rn(b * 0x1p36f));
+        // 2^(k / 32) = 2^(k >> 5) 2^(r / 32)
+        const int down = 63 & -(k >> 5);
+        return some ? ((m << (kMassBits - 36)) + ((1ull << down) >> 1)) >> down : 0;
     }
 };
 
@@ -176,7 +187,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     const int first = min(rank * a.slice, a.vocab), n = min(a.slice, a.vocab - first);  // of this CTA's slice
 
     cluster_arrive();
-    if (tid < 32) sm.pow2[tid] = kPow2[tid];
+    if (tid == 0) sm.listed = 0;
+    const Pow2Entry pow2 = kPow2[lane];
     griddep_wait();
     griddep_launch();
     const T* src = (const T*)a.logits + row * a.stride + first;
@@ -200,35 +212,55 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         kmax = max(kmax, k);
         if (k > kKeyNegInf) kmin = min(kmin, k);
     };
-    auto as_float = [&](T v) {
-        if constexpr (sizeof(T) == 4) return v;
-        else return __uint_as_float((uint32_t)v << 16);
+    constexpr int kPer = 16 / sizeof(T);
+    auto unpack = [&](const uint4& w, float (&v)[kPer]) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (sizeof(T) == 4) {
+                v[e] = __uint_as_float(x[e]);
+            } else {
+                v[2 * e] = __uint_as_float(x[e] << 16);
+                v[2 * e + 1] = __uint_as_float(x[e] & 0xffff0000u);
+            }
+        }
     };
     {
-        constexpr int kPer = 16 / sizeof(T);
         const int whole = ((uintptr_t)src & 15u) == 0 ? n / kPer * kPer : 0;
 #pragma unroll 4
         for (int i = tid * kPer; i < whole; i += kSampleThreads * kPer) {
             const uint4 w = *reinterpret_cast<const uint4*>(src + i);
             if (i < value.held) *reinterpret_cast<uint4*>(values + i) = w;  // `held` is a multiple of 8, or all
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            float v[kPer];
+            unpack(w, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (sizeof(T) == 4) {
-                    look(__uint_as_float(x[e]));
-                } else {
-                    look(__uint_as_float(x[e] << 16));
-                    look(__uint_as_float(x[e] & 0xffff0000u));
-                }
-            }
+            for (int e = 0; e < kPer; ++e) look(v[e]);
         }
-#pragma unroll 4
+#pragma unroll 8
         for (int i = whole + tid; i < n; i += kSampleThreads) {
             const T v = src[i];
             if (i < value.held) values[i] = v;
-            look(as_float(v));
+            if constexpr (sizeof(T) == 4) look(v);
+            else look(__uint_as_float((uint32_t)v << 16));
         }
     }
+    // f(value, index) for all of the slice, by whole warps; -inf in the place of what is past it
+    auto each = [&](auto f) {
+        const int whole = value.held / kPer * kPer;
+        for (int i0 = warp * 32 * kPer; i0 < whole; i0 += kSampleThreads * kPer) {
+            const int i = i0 + lane * kPer;
+            float v[kPer];
+            if (i < whole) {
+                unpack(*reinterpret_cast<const uint4*>(values + i), v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) v[e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) f(v[e], i + e);
+        }
+        for (int i0 = whole + warp * 32; i0 < n; i0 += kSampleThreads) f(i0 + lane < n ? value(i0 + lane) : -INFINITY, i0 + lane);
+    };
     int phase = 0;
     // Every CTA's note to every CTA; all of them afterwards in sm.note[...], until the next but one.
     auto tell = [&](const SampleNote& note) -> const SampleNote* {
@@ -251,12 +283,16 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     bad |= kmax >= kKeyInf || kmax <= kKeyNegInf || !(temp >= 0.f && temp <= 3.4028235e38f) || top_p != top_p ||
            min_p != min_p || u != u;
 
+    auto logprob_of = [&](uint32_t key, uint64_t mass) {
+        return (float)(((double)value_of(key) - (double)value_of(kmax)) / (double)temp - log((double)mass * (1.0 / (1ull << kMassBits))));
+    };
     // The j-th token (from 0) of a key, in the order of the indexes: the CTA that has it writes it.
     auto pick = [&](uint32_t key, uint64_t j, uint64_t mass) {
         const int per = (n + kSampleThreads - 1) / kSampleThreads * 32;  // a warp's stretch of the slice
         const int from = min(warp * per, n), to = min(from + per, n);
+        auto hits = [&](int i) { return __ballot_sync(0xffffffffu, i + lane < to && key_of(value(min(i + lane, n - 1))) == key); };
         unsigned mine = 0;
-        for (int i = from; i < to; i += 32) mine += __popc(__ballot_sync(0xffffffffu, i + lane < to && key_of(value(min(i + lane, n - 1))) == key));
+        for (int i = from; i < to; i += 32) mine += __popc(hits(i));
         __syncthreads();
         if (lane == 0) sm.wcnt[warp] = mine;
         __syncthreads();
@@ -270,23 +306,19 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         for (int r = 0; r < rank; ++r) at += all[r].a;
         if (at > j || j >= at + mine) return;
         for (int i = from; i < to; i += 32) {
-            const unsigned hit = __ballot_sync(0xffffffffu, i + lane < to && key_of(value(min(i + lane, n - 1))) == key);
+            unsigned hit = hits(i);
             if (j < at + __popc(hit)) {
-                unsigned rest = hit;
-                for (uint64_t skip = j - at; skip; --skip) rest &= rest - 1;
+                for (int skip = (int)(j - at); skip; --skip) hit &= hit - 1;
                 if (lane == 0) {
-                    a.tokens[row] = first + i + __ffs(rest) - 1;
-                    if (a.logprobs)
-                        a.logprobs[row] = greedy ? 0.f
-                                                 : (float)(((double)value_of(key) - (double)value_of(kmax)) / (double)temp -
-                                                           log((double)mass * (1.0 / (1ull << kMassBits))));
+                    a.tokens[row] = first + i + __ffs(hit) - 1;
+                    if (a.logprobs) a.logprobs[row] = greedy ? 0.f : logprob_of(key, mass);
                 }
                 return;
             }
             at += __popc(hit);
         }
     };
-    auto finish = [&]() { cluster.sync(); };  // no CTA leaves while another may write to it
+    auto finish = [&]() { cluster.sync(); };  // no CTA leaves while another may read or write its memory
 
     if (bad) {
         if (rank == 0 && tid == 0) {
@@ -303,170 +335,330 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     }
 
     const float top = value_of(kmax);
-    const Weigher weigh = {top, sm.c, sm.cl};
-    auto weight_of = [&](uint32_t key) { return weigh(value_of(key), sm.pow2); };
+    const Weigher weigh = {top, sm.c, sm.cl, pow2.hi, pow2.lo};
+    auto weight_of = [&](uint32_t key) { return weigh(value_of(key)); };
 
-    struct Place {
-        uint32_t key;
-        uint64_t before, in;  // of the point: what lies before the key, and the rest
-    };
+    // Bins of the histogram over the row: linear in the logit down to where weights are nothing, or to the
+    // row's lowest; the last one has all that is lower.
+    const float reach = fminf(top - value_of(kmin), 44.5f / sm.c), grain = reach > 0.f ? (float)(kBins - 1) / reach : 0.f;
+    auto bin_of_value = [&](float v) { return (int)fminf((top - v) * grain, (float)(kBins - 1)); };
     const int chunk = kBins / C;  // bins that a CTA puts together
-    // The histogram of the keys klo .. khi, by (khi - key) >> shift, put together: this CTA's chunk in
-    // sm.sums.
-    auto histogram = [&](uint32_t klo, uint32_t khi, int shift, bool by_count) {
-        for (int b = tid; b < kBins; b += kSampleThreads) sm.lo[b] = sm.hi[b] = 0;
+
+    // The histogram of f(value, key) -> bin (below 0: none), put together: this CTA's chunk in sm.sums, sm.cnts.
+    // (It takes the lists' memory: behind a list comes a barrier of the cluster before the next one.)
+    auto histogram = [&](auto f, bool masses, bool counts) {
+        for (int b = tid; b < kBins; b += kSampleThreads) sm.lo[b] = sm.hi[b] = sm.cnt[b] = 0;
         __syncthreads();
-        for (int i = tid; i < n; i += kSampleThreads) {
-            const float v = value(i);
-            const uint32_t key = key_of(v);
-            if (key < klo || key > khi) continue;
-            const uint32_t bin = (khi - key) >> shift;
-            if (by_count) {
-                atomicAdd(&sm.lo[bin], 1u);
-            } else {
-                const uint64_t w = weigh(v, sm.pow2);
-                const uint32_t old = atomicAdd(&sm.lo[bin], (uint32_t)w), high = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
-                if (high) atomicAdd(&sm.hi[bin], high);
+        each([&](float v, int) {
+            const int bin = f(v, key_of(v));
+            if (!__any_sync(0xffffffffu, bin >= 0)) return;
+            if (masses) {
+                const uint64_t w = weigh(v);
+                if (bin >= 0 && w) {
+                    const uint32_t old = atomicAdd(&sm.lo[bin], (uint32_t)w);
+                    const uint32_t high = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
+                    if (high) atomicAdd(&sm.hi[bin], high);
+                }
             }
-        }
+            if (counts && bin >= 0) atomicAdd(&sm.cnt[bin], 1u);
+        });
         cluster.sync();
         for (int b = tid; b < chunk; b += kSampleThreads) {
             uint64_t sum = 0;
+            uint32_t cnt = 0;
             for (int r = 0; r < C; ++r) {
-                SampleSmem* s = cluster.map_shared_rank(&sm, r);
+                const SampleSmem* s = cluster.map_shared_rank(&sm, r);
                 const int at = rank * chunk + b;
-                sum += (uint64_t)s->hi[at] << 32 | s->lo[at];
+                if (masses) sum += (uint64_t)s->hi[at] << 32 | s->lo[at];
+                if (counts) cnt += s->cnt[at];
             }
             sm.sums[b] = sum;
+            sm.cnts[b] = cnt;
         }
         __syncthreads();
     };
-    // The bin of the histogram put together that holds the point (below the total): what lies before it, and its number.
-    auto bin_of = [&](uint64_t point, uint64_t& before, uint64_t& total) -> int {
+    // The bin of the histogram put together that holds the point (by count or by mass) that point_of gives for
+    // the total: its number (-1: the point is not below the total), what lies before it, and the tokens up to
+    // its end (where counted).
+    struct Bin {
+        int bin;
+        uint64_t before;
+        unsigned upto;
+    };
+    auto find_bin = [&](auto point_of, bool by_count) -> Bin {
         // each thread a stretch of the chunk
         const int per = (chunk + kSampleThreads - 1) / kSampleThreads, b0 = min(tid * per, chunk), b1 = min(b0 + per, chunk);
-        uint64_t mine = 0;
-        for (int b = b0; b < b1; ++b) mine += sm.sums[b];
-        uint64_t upto = mine;
+        uint64_t mass = 0;
+        uint32_t count = 0;
+        for (int b = b0; b < b1; ++b) mass += sm.sums[b], count += sm.cnts[b];
+        uint64_t mass_to = mass;
+        uint32_t count_to = count;
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint64_t v = __shfl_up_sync(0xffffffffu, mass_to, off);
+            const uint32_t w = __shfl_up_sync(0xffffffffu, count_to, off);
+            if (lane >= off) mass_to += v, count_to += w;
+        }
+        __syncthreads();
+        if (lane == 31) sm.wmass[warp] = mass_to, sm.wcnt[warp] = count_to;
+        __syncthreads();
+        uint64_t mass_here = 0, mass_at = mass_to - mass;
+        uint32_t count_here = 0, count_at = count_to - count;
+        for (int w = 0; w < kSampleWarps; ++w) {
+            if (w < warp) mass_at += sm.wmass[w], count_at += sm.wcnt[w];
+            mass_here += sm.wmass[w], count_here += sm.wcnt[w];
+        }
+        const SampleNote* all = tell({mass_here, count_here, 0, 0, 0});
+        uint64_t total = 0;
+        for (int r = 0; r < C; ++r) {
+            if (r < rank) mass_at += all[r].mass, count_at += all[r].a;
+            total += by_count ? all[r].a : all[r].mass;
+        }
+        const uint64_t at = by_count ? count_at : mass_at, size = by_count ? count : mass, point = point_of(total);
+        if (point < total && at <= point && point < at + size) {
+            uint64_t before = at;
+            int b = b0;
+            for (;; ++b) {
+                const uint64_t here = by_count ? sm.cnts[b] : sm.sums[b];
+                count_at += sm.cnts[b];
+                if (point < before + here) break;
+                before += here;
+            }
+            for (int r = 0; r < C; ++r) cluster.map_shared_rank(&sm, r)->found = {before, (uint32_t)(rank * chunk + b), count_at, 0, 0};
+        }
+        cluster.sync();
+        if (point >= total) return {-1, 0, 0};
+        return {(int)sm.found.a, sm.found.mass, sm.found.b};
+    };
+    // The tokens for which f(value, key) holds, in rank 0's list if there are at most kList; their number.
+    auto gather = [&](auto f) -> int {
+        each([&](float v, int i) {
+            const uint32_t key = key_of(v);
+            const bool in = key > kKeyNegInf && f(v, key);
+            const unsigned hit = __ballot_sync(0xffffffffu, in);
+            if (!hit) return;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&sm.listed, __popc(hit));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(hit & ((1u << lane) - 1u));
+            if (in && at < kList) sm.mine[at] = (uint64_t)key << 32 | (uint32_t)~(first + i);
+        });
+        __syncthreads();
+        const SampleNote* all = tell({0, (uint32_t)sm.listed, 0, 0, 0});
+        if (tid == 0) sm.listed = 0;
+        int sum = 0, from = -1, at = 0;
+        for (int r = 0; r < C; ++r) {
+            const int here = (int)all[r].a;
+            if (from < 0 && tid < sum + here) from = r, at = tid - sum;
+            sum += here;
+        }
+        if (rank == 0 && sum <= kList) {
+            if (from >= 0) sm.list[tid] = cluster.map_shared_rank(&sm, from)->mine[at];
+            __syncthreads();
+        }
+        return sum;
+    };
+    // Rank 0: the list in order. Thread r gets the r-th token (0 past the end), its weight, and what lies before it.
+    struct Ranked {
+        uint64_t token, weight, before;
+    };
+    auto rank_list = [&](int count, bool by_count) -> Ranked {
+        const uint64_t mine = tid < count ? sm.list[tid] : 0;
+        int above = 0;
+        if (warp * 32 < count)
+            for (int e = 0; e < count; ++e) above += sm.list[e] > mine;
+        if (tid < count) sm.ranked[above] = mine;
+        __syncthreads();
+        Ranked r;
+        r.token = tid < count ? sm.ranked[tid] : 0;
+        const uint64_t w = weigh(tid < count ? value_of((uint32_t)(r.token >> 32)) : -INFINITY);
+        r.weight = tid >= count ? 0 : by_count ? 1 : w;
+        uint64_t upto = r.weight;
         for (int off = 1; off < 32; off <<= 1) {
             const uint64_t v = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += v;
         }
         if (lane == 31) sm.wmass[warp] = upto;
         __syncthreads();
-        uint64_t here = 0, ahead = 0;
-        for (int w = 0; w < kSampleWarps; ++w) {
-            if (w == warp) ahead = here;
-            here += sm.wmass[w];
+        r.before = upto - r.weight;
+        for (int w2 = 0; w2 < warp; ++w2) r.before += sm.wmass[w2];
+        return r;
+    };
+
+    const bool some_p = top_p < 1.f, some_min = min_p > 0.f;
+    const uint32_t k_least = some_min ? (min_p > 1.f ? kmax : key_of(__double2float_ru((double)top + sm.least))) : 0;
+    // The row, where the list holds all tokens up to the last one kept (and maybe more): the first k of
+    // them, p of `mass` (0: of theirs), min-p, and the draw.
+    auto finish_list = [&](int count, int k, uint64_t mass) {
+        if (rank == 0) {
+            const Ranked r = rank_list(count, false);
+            const uint64_t upto = r.before + r.weight;
+            const int last = min(k, count) - 1;
+            if (tid == last) sm.wsame[0] = upto;
+            __syncthreads();
+            if (mass == 0) mass = sm.wsame[0];
+            const uint64_t want = !some_p ? ~0ull : top_p > 0.f ? max(part_of(mass, top_p, true), (uint64_t)1) : 1;
+            const bool keep = tid <= last && (tid == 0 || (r.before < want && !(min_p > 1.f) && (uint32_t)(r.token >> 32) >= k_least));
+            const int kept = __syncthreads_count(keep);  // a prefix
+            if (tid == kept - 1) sm.wsame[1] = upto;
+            __syncthreads();
+            const uint64_t left = sm.wsame[1], point = min(part_of(left, fminf(fmaxf(u, 0.f), 1.f), false), left - 1);
+            if (keep && r.before <= point && point < upto) {
+                a.tokens[row] = (int)~(uint32_t)r.token;
+                if (a.logprobs) a.logprobs[row] = logprob_of((uint32_t)(r.token >> 32), left);
+            }
         }
-        const SampleNote* all = tell({here, 0, 0, 0, 0});
-        total = 0;
-        uint64_t start = 0;
-        for (int r = 0; r < C; ++r) {
-            if (r == rank) start = total;
-            total += all[r].mass;
-        }
-        uint64_t at = start + ahead + upto - mine;
-        if (point < total && at <= point && point < at + mine) {
-            int b = b0;
-            while (point >= at + sm.sums[b]) at += sm.sums[b++];
-            for (int r = 0; r < C; ++r) cluster.map_shared_rank(&sm, r)->found = {at, (uint32_t)(rank * chunk + b), 0, 0, 0};
-        }
-        cluster.sync();
-        before = sm.found.mass;
-        return (int)sm.found.a;
+        finish();
+    };
+    // A point's place in a bin of the row's histogram: the key, what lies before it, and the number of the
+    // token among the key's.
+    struct Place {
+        uint32_t key;
+        uint64_t before, j;
     };
     auto shift_of = [](uint32_t klo, uint32_t khi) {
         int s = 0;
         while (((khi - klo) >> s) >= (uint32_t)kBins) ++s;
         return s;
     };
-    // The place of a point (by count or by mass) among the keys klo .. khi; total: of all of them.
-    auto locate = [&](uint32_t klo, uint32_t khi, uint64_t point, bool by_count, uint64_t& total) -> Place {
-        uint64_t before = 0;
-        for (bool outer = true;; outer = false) {
-            const int shift = shift_of(klo, khi);
-            histogram(klo, khi, shift, by_count);
-            uint64_t ahead, sum;
-            const int bin = bin_of(point - before, ahead, sum);
-            if (outer) {
-                total = sum;
-                if (point >= sum) return {klo, 0, 0};
+    bool fresh = true;  // the row's histogram is still there
+    auto place_in = [&](const Bin& bin, uint32_t from, uint64_t point, bool by_count) -> Place {
+        const int count = gather([&](float v, uint32_t key) { return key >= from && bin_of_value(v) == bin.bin; });
+        if (count <= kList) {
+            if (rank == 0) {
+                const Ranked r = rank_list(count, by_count);
+                const uint64_t rest = point - bin.before;
+                if (r.before <= rest && rest < r.before + r.weight) {
+                    int j = 0;  // tokens of its key before it
+                    while (j < tid && (sm.ranked[tid - 1 - j] >> 32) == (r.token >> 32)) ++j;
+                    const SampleNote note = {bin.before + r.before - j * r.weight, (uint32_t)(r.token >> 32), (uint32_t)j, 0, 0};
+                    for (int q = 0; q < C; ++q) cluster.map_shared_rank(&sm, q)->found = note;
+                }
             }
-            before += ahead;
-            khi -= (uint32_t)bin << shift;
-            if (shift == 0) return {khi, before, point - before};
+            cluster.sync();
+            return {sm.found.a, sm.found.mass, sm.found.b};
+        }
+        uint32_t klo = 0xffffffffu, khi = 0;
+        each([&](float v, int) {
+            const uint32_t key = key_of(v);
+            if (key >= from && key > kKeyNegInf && bin_of_value(v) == bin.bin) klo = min(klo, key), khi = max(khi, key);
+        });
+        klo = __reduce_min_sync(0xffffffffu, klo);
+        khi = __reduce_max_sync(0xffffffffu, khi);
+        __syncthreads();
+        if (lane == 0) sm.wa[warp] = khi, sm.wb[warp] = klo;
+        __syncthreads();
+        for (int w = 0; w < kSampleWarps; ++w) khi = max(khi, sm.wa[w]), klo = min(klo, sm.wb[w]);
+        const SampleNote* all = tell({0, khi, klo, 0, 0});
+        for (int r = 0; r < C; ++r) khi = max(khi, all[r].a), klo = min(klo, all[r].b);
+        uint64_t before = bin.before;
+        while (klo < khi) {
+            fresh = false;
+            const int shift = shift_of(klo, khi);
+            histogram([&](float, uint32_t key) { return key >= klo && key <= khi ? (int)((khi - key) >> shift) : -1; }, !by_count, by_count);
+            const Bin b = find_bin([&](uint64_t) { return point - before; }, by_count);
+            before += b.before;
+            khi -= (uint32_t)b.bin << shift;
             const uint32_t width = (1u << shift) - 1u;
             klo = khi - klo > width ? khi - width : klo;
         }
+        return {khi, before, (point - before) / (by_count ? 1 : weight_of(khi))};
     };
-
-    // --- top-k: the last key kept, and how many of its tokens
-    uint64_t total, j_keep = 0xffffffffull;
-    uint32_t k_keep = kmin;
-    if (top_k > 0 && top_k < a.vocab) {
-        const Place p = locate(kmin, kmax, (uint64_t)(top_k - 1), true, total);
-        if ((uint64_t)top_k <= total) k_keep = p.key, j_keep = p.in + 1;
-    }
-    // mass of the tokens of keys klo .. kmax, and of key klo alone
-    auto mass_from = [&](uint32_t klo, uint64_t& of_klo) {
+    // the mass of the tokens of keys above `from`, and of that key's first j
+    auto mass_from = [&](uint32_t from, uint64_t j) {
         uint64_t mine = 0, same = 0;
-        const uint64_t w_klo = weight_of(klo);
-        for (int i = tid; i < n; i += kSampleThreads) {
-            const float v = value(i);
+        each([&](float v, int) {
             const uint32_t key = key_of(v);
-            if (key > klo) mine += weigh(v, sm.pow2);
-            else if (key == klo) same += w_klo;
-        }
+            if (!__any_sync(0xffffffffu, key >= from && key > kKeyNegInf)) return;
+            const uint64_t w = weigh(v);
+            if (key > from) mine += w;
+            else if (key == from) ++same;
+        });
         for (int off = 16; off; off >>= 1) {
             mine += __shfl_xor_sync(0xffffffffu, mine, off);
             same += __shfl_xor_sync(0xffffffffu, same, off);
         }
         __syncthreads();
-        if (lane == 0) sm.wmass[warp] = mine, sm.sums[warp] = same;
+        if (lane == 0) sm.wmass[warp] = mine, sm.wsame[warp] = same;
         __syncthreads();
         mine = same = 0;
-        for (int w = 0; w < kSampleWarps; ++w) mine += sm.wmass[w], same += sm.sums[w];
-        const SampleNote* all = tell({mine, (uint32_t)same, (uint32_t)(same >> 32), 0, 0});
+        for (int w = 0; w < kSampleWarps; ++w) mine += sm.wmass[w], same += sm.wsame[w];
+        const SampleNote* all = tell({mine, (uint32_t)same, 0, 0, 0});
         mine = same = 0;
-        for (int r = 0; r < C; ++r) mine += all[r].mass, same += (uint64_t)all[r].b << 32 | all[r].a;
-        of_klo = same;
-        return mine;
+        for (int r = 0; r < C; ++r) mine += all[r].mass, same += all[r].a;
+        return mine + min(same, j) * weight_of(from);
     };
-    // the mass kept so far: that above k_keep, and of k_keep's tokens the first j_keep
-    auto kept_mass = [&]() {
-        uint64_t same;
-        const uint64_t above = mass_from(k_keep, same), w = weight_of(k_keep);
-        const uint64_t of_key = j_keep == 0xffffffffull ? same : min(same, w * j_keep);
-        return above + of_key;
-    };
-    uint64_t mass = kept_mass();
-    if (top_p < 1.f) {
-        // the tokens with less than p of the mass before them, the first one among them
-        const uint64_t want = top_p > 0.f ? max(part_of(mass, top_p, true), (uint64_t)1) : 1;
-        uint64_t all_mass;
-        const Place p = locate(k_keep, kmax, want - 1, false, all_mass);
-        k_keep = p.key;
-        j_keep = p.in / weight_of(p.key) + 1;
-        mass = p.before + j_keep * weight_of(p.key);
-    }
-    if (min_p > 0.f) {
-        const uint32_t k_least = key_of(__double2float_ru((double)top + sm.least));
-        if (min_p > 1.f) {  // no weight is above 1: the first token only
-            k_keep = kmax;
-            j_keep = 1;
-            mass = weight_of(kmax);
-        } else if (k_least > k_keep) {
-            k_keep = k_least;
-            j_keep = 0xffffffffull;
-            mass = kept_mass();
+
+    constexpr uint64_t kAll = 0xffffffffull;
+    constexpr int kNoCut = 0x7fffffff;
+    // --- top-k: the last key kept, and how many of its tokens
+    uint32_t k_keep = kmin;
+    uint64_t j_keep = kAll;
+    bool cut = false;
+    if (top_k > 0 && top_k < a.vocab) {
+        histogram([&](float v, uint32_t key) { return key > kKeyNegInf ? bin_of_value(v) : -1; }, false, true);
+        const Bin b = find_bin([&](uint64_t) { return (uint64_t)(top_k - 1); }, true);
+        if (b.bin >= 0 && b.upto <= kList) {
+            gather([&](float v, uint32_t) { return bin_of_value(v) <= b.bin; });
+            finish_list((int)b.upto, top_k, 0);
+            return;
+        }
+        if (b.bin >= 0) {
+            const Place p = place_in(b, 0, (uint64_t)(top_k - 1), true);
+            k_keep = p.key;
+            j_keep = p.j + 1;
+            cut = true;
         }
     }
+    if (!cut && !some_p && some_min && k_least > kmin) {
+        // min-p alone
+        const int count = gather([&](float, uint32_t key) { return key >= k_least; });
+        if (count <= kList) {
+            finish_list(count, kNoCut, 0);
+            return;
+        }
+        k_keep = k_least;
+    }
+    // --- the masses
+    const uint32_t from = k_keep;
+    auto masses = [&](bool counts) {
+        histogram([&](float v, uint32_t key) { return key >= from ? bin_of_value(v) : -1; }, true, counts);
+        fresh = true;
+    };
+    masses(some_p);
+    uint64_t mass = cut ? mass_from(k_keep, j_keep) : 0;  // 0: all of the histogram's
+    if (some_p) {
+        // the tokens with less than p of the mass before them, the first one among them
+        uint64_t last = 0;
+        const Bin b = find_bin([&](uint64_t total) {
+            if (!cut) mass = total;
+            return last = top_p > 0.f ? max(part_of(mass, top_p, true), (uint64_t)1) - 1 : 0;
+        }, false);
+        if (b.upto <= kList) {
+            gather([&](float v, uint32_t key) { return key >= from && bin_of_value(v) <= b.bin; });
+            finish_list((int)b.upto, cut ? top_k : kNoCut, mass);
+            return;
+        }
+        const Place p = place_in(b, from, last, false);
+        k_keep = p.key;
+        mass = p.before + (p.j + 1) * weight_of(p.key);
+    }
+    if (some_min && min_p > 1.f) {
+        pick(kmax, 0, weight_of(kmax));
+        finish();
+        return;
+    }
+    if (some_min && k_least > k_keep) {
+        k_keep = k_least;
+        mass = mass_from(k_keep, kAll);
+    }
     // --- the draw
-    const uint64_t point = min(part_of(mass, fminf(fmaxf(u, 0.f), 1.f), false), mass - 1);
-    uint64_t all_mass;
-    const Place p = locate(k_keep, kmax, point, false, all_mass);
-    pick(p.key, p.in / weight_of(p.key), mass);
+    if (!fresh) masses(false);
+    uint64_t point = 0;
+    const Bin b = find_bin([&](uint64_t total) {
+        if (mass == 0) mass = total;
+        return point = min(part_of(mass, fminf(fmaxf(u, 0.f), 1.f), false), mass - 1);
+    }, false);
+    const Place p = place_in(b, from, point, false);
+    pick(p.key, p.j, mass);
     finish();
 }
 
@@ -477,7 +669,7 @@ static cudaError_t launch_sample(SampleArgs a, int dev, cudaStream_t st) {
     const int sms = sm_count(dev);
     int C = 1;
     auto slice_of = [&](int c) { return ((a.vocab + c - 1) / c + 7) / 8 * 8; };
-    constexpr int kHeldBytes = 64 * 1024;
+    constexpr int kHeldBytes = 56 * 1024;
     while (C < kMaxCluster && ((size_t)slice_of(C) * sizeof(T) > kHeldBytes || ((int64_t)a.rows * C < 2 * sms && slice_of(C) > 2048))) C *= 2;
     a.slice = slice_of(C);
     a.held = (int)std::min<int64_t>(a.slice, kHeldBytes / sizeof(T));
