@@ -83,15 +83,13 @@ constexpr int kList = kSampleThreads;  // tokens that a list takes
 struct alignas(16) SampleSmem {
     union {
         struct {
-            uint32_t lo[kBins], hi[kBins], cnt[kBins];  // a histogram: masses as two words, and counts
+            uint32_t lo[kBins], hi[kBins];              // a histogram: counts in lo, or masses as two words
         };
         struct {
             uint64_t mine[kList];                       // the tokens that this CTA lists: key, ~index
             uint64_t list[kList], ranked[kList];        // the cluster's (rank 0)
         };
     };
-    uint64_t sums[kBins];                       // this CTA's chunk of the cluster's histogram
-    uint32_t cnts[kBins];
     SampleNote note[2][kMaxCluster];            // a phase's and the next one's
     SampleNote found;                           // a place, by who found it
     uint64_t wmass[kSampleWarps], wsame[kSampleWarps];
@@ -99,6 +97,7 @@ struct alignas(16) SampleSmem {
     int listed;
     float c, cl;                                // log2 e / temperature
     double least;                               // temperature * log min_p
+    // behind it: this CTA's chunk of the cluster's histogram (kBins / CTAs sums), then the values held
 };
 
 // Keys order as the values do; -0 is 0.
@@ -138,8 +137,9 @@ struct Weigher {
         const float p = __shfl_sync(0xffffffffu, hi, k & 31), pl = __shfl_sync(0xffffffffu, lo, k & 31);
         const float a = p * h, b = fmaf(pl, h, fmaf(p, q, fmaf(p, h, -a))) + pl;
         // in units of 2^-36: p is in [1, 2), its bits those of an integer
+        const int b2 = __float_as_int(fmaf(b, 0x1p35f, 12582912.f)) - 0x4b400000;  // b is below 2^-13
         const uint64_t m = ((uint64_t)((__float_as_uint(p) & 0x7fffffu) | 0x800000u) << 13) +
-                           (uint64_t)(int64_t)(__float2int_rn(a * 0x1p36f) + __float2int_rn(b * 0x1p36f));
+                           (uint64_t)(int64_t)(__float2int_rn(a * 0x1p36f) + 2 * b2);
         // 2^(k / 32) = 2^(k >> 5) 2^(r / 32)
         const int down = 63 & -(k >> 5);
         return some ? ((m << (kMassBits - 36)) + ((1ull << down) >> 1)) >> down : 0;
@@ -180,9 +180,11 @@ template <class T>
 __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     SampleSmem& sm = *reinterpret_cast<SampleSmem*>(raw);
-    T* values = reinterpret_cast<T*>(raw + sizeof(SampleSmem));
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int chunk = kBins / C;  // bins that a CTA puts together
+    uint64_t* sums = reinterpret_cast<uint64_t*>(raw + sizeof(SampleSmem));
+    T* values = reinterpret_cast<T*>(sums + chunk);
     const int row = (int)(blockIdx.x / (unsigned)C), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int first = min(rank * a.slice, a.vocab), n = min(a.slice, a.vocab - first);  // of this CTA's slice
 
@@ -205,12 +207,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     }
 
     // --- the slice into shared memory; its largest key, its smallest of a number, NaN
-    uint32_t kmax = 0, kmin = 0xffffffffu, bad = 0;
+    float most = -INFINITY, least = INFINITY;
+    uint32_t bad = 0;
     auto look = [&](float v) {
-        if (v != v) bad = 1;
-        const uint32_t k = key_of(v);
-        kmax = max(kmax, k);
-        if (k > kKeyNegInf) kmin = min(kmin, k);
+        bad |= v != v;
+        most = fmaxf(most, v);
+        least = fminf(least, v == -INFINITY ? INFINITY : v);
     };
     constexpr int kPer = 16 / sizeof(T);
     auto unpack = [&](const uint4& w, float (&v)[kPer]) {
@@ -269,8 +271,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         cluster.sync();
         return sm.note[phase];
     };
-    kmax = __reduce_max_sync(0xffffffffu, kmax);
-    kmin = __reduce_min_sync(0xffffffffu, kmin);
+    uint32_t kmax = __reduce_max_sync(0xffffffffu, key_of(most)), kmin = __reduce_min_sync(0xffffffffu, key_of(least));
     bad = __reduce_or_sync(0xffffffffu, bad);
     if (lane == 0) sm.wa[warp] = kmax, sm.wb[warp] = kmin, sm.wc[warp] = bad;
     __syncthreads();
@@ -341,105 +342,104 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     // Bins of the histogram over the row: linear in the logit down to where weights are nothing, or to the
     // row's lowest; the last one has all that is lower.
     const float reach = fminf(top - value_of(kmin), 44.5f / sm.c), grain = reach > 0.f ? (float)(kBins - 1) / reach : 0.f;
-    auto bin_of_value = [&](float v) { return (int)fminf((top - v) * grain, (float)(kBins - 1)); };
-    const int chunk = kBins / C;  // bins that a CTA puts together
+    auto bin_of_value = [&](float v) {  // 1.5 2^23: the nearest whole number in the last bits
+        return __float_as_int(fminf((v - top) * -grain, (float)(kBins - 1)) + 12582912.f) - 0x4b400000;
+    };
+    // The lowest key of bins up to b. (The bins order as the keys do.)
+    auto lowest_key = [&](int b) {
+        uint32_t lo = kmin, hi = kmax;  // the answer is among them, and hi is one of those bins'
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            if (bin_of_value(value_of(mid)) <= b) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    };
 
-    // The histogram of f(value, key) -> bin (below 0: none), put together: this CTA's chunk in sm.sums, sm.cnts.
-    // (It takes the lists' memory: behind a list comes a barrier of the cluster before the next one.)
-    auto histogram = [&](auto f, bool masses, bool counts) {
-        for (int b = tid; b < kBins; b += kSampleThreads) sm.lo[b] = sm.hi[b] = sm.cnt[b] = 0;
+    // The histogram by bin(value) (below 0: not in it), put together: this CTA's chunk in sums. few: where a
+    // warp often has none in it. (It takes the lists' memory: behind a list comes a barrier of the cluster
+    // before the next one.)
+    auto histogram = [&](auto bin_of, bool by_count, bool few) {
+        for (int b = tid; b < kBins; b += kSampleThreads) sm.lo[b] = sm.hi[b] = 0;
         __syncthreads();
         each([&](float v, int) {
-            const int bin = f(v, key_of(v));
-            if (!__any_sync(0xffffffffu, bin >= 0)) return;
-            if (masses) {
+            const int b = bin_of(v);
+            if (by_count) {
+                if (b >= 0) atomicAdd(&sm.lo[b], 1u);
+            } else {
+                if (few && !__any_sync(0xffffffffu, b >= 0)) return;
                 const uint64_t w = weigh(v);
-                if (bin >= 0 && w) {
-                    const uint32_t old = atomicAdd(&sm.lo[bin], (uint32_t)w);
+                if (b >= 0 && w) {
+                    const uint32_t old = atomicAdd(&sm.lo[b], (uint32_t)w);
                     const uint32_t high = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
-                    if (high) atomicAdd(&sm.hi[bin], high);
+                    if (high) atomicAdd(&sm.hi[b], high);
                 }
             }
-            if (counts && bin >= 0) atomicAdd(&sm.cnt[bin], 1u);
         });
         cluster.sync();
         for (int b = tid; b < chunk; b += kSampleThreads) {
             uint64_t sum = 0;
-            uint32_t cnt = 0;
             for (int r = 0; r < C; ++r) {
                 const SampleSmem* s = cluster.map_shared_rank(&sm, r);
                 const int at = rank * chunk + b;
-                if (masses) sum += (uint64_t)s->hi[at] << 32 | s->lo[at];
-                if (counts) cnt += s->cnt[at];
+                sum += (uint64_t)s->hi[at] << 32 | s->lo[at];
             }
-            sm.sums[b] = sum;
-            sm.cnts[b] = cnt;
+            sums[b] = sum;
         }
         __syncthreads();
     };
-    // The bin of the histogram put together that holds the point (by count or by mass) that point_of gives for
-    // the total: its number (-1: the point is not below the total), what lies before it, and the tokens up to
-    // its end (where counted).
+    // The bin of the histogram put together that holds the point that point_of gives for the total: its number
+    // (-1: the point is not below the total), what lies before it, and what up to its end.
     struct Bin {
         int bin;
-        uint64_t before;
-        unsigned upto;
+        uint64_t before, upto;
     };
-    auto find_bin = [&](auto point_of, bool by_count) -> Bin {
+    auto find_bin = [&](auto point_of) -> Bin {
         // each thread a stretch of the chunk
         const int per = (chunk + kSampleThreads - 1) / kSampleThreads, b0 = min(tid * per, chunk), b1 = min(b0 + per, chunk);
-        uint64_t mass = 0;
-        uint32_t count = 0;
-        for (int b = b0; b < b1; ++b) mass += sm.sums[b], count += sm.cnts[b];
-        uint64_t mass_to = mass;
-        uint32_t count_to = count;
+        uint64_t size = 0;
+        for (int b = b0; b < b1; ++b) size += sums[b];
+        uint64_t upto = size;
         for (int off = 1; off < 32; off <<= 1) {
-            const uint64_t v = __shfl_up_sync(0xffffffffu, mass_to, off);
-            const uint32_t w = __shfl_up_sync(0xffffffffu, count_to, off);
-            if (lane >= off) mass_to += v, count_to += w;
+            const uint64_t v = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += v;
         }
         __syncthreads();
-        if (lane == 31) sm.wmass[warp] = mass_to, sm.wcnt[warp] = count_to;
+        if (lane == 31) sm.wmass[warp] = upto;
         __syncthreads();
-        uint64_t mass_here = 0, mass_at = mass_to - mass;
-        uint32_t count_here = 0, count_at = count_to - count;
+        uint64_t here = 0, at = upto - size;
         for (int w = 0; w < kSampleWarps; ++w) {
-            if (w < warp) mass_at += sm.wmass[w], count_at += sm.wcnt[w];
-            mass_here += sm.wmass[w], count_here += sm.wcnt[w];
+            if (w < warp) at += sm.wmass[w];
+            here += sm.wmass[w];
         }
-        const SampleNote* all = tell({mass_here, count_here, 0, 0, 0});
+        const SampleNote* all = tell({here, 0, 0, 0, 0});
         uint64_t total = 0;
         for (int r = 0; r < C; ++r) {
-            if (r < rank) mass_at += all[r].mass, count_at += all[r].a;
-            total += by_count ? all[r].a : all[r].mass;
+            if (r < rank) at += all[r].mass;
+            total += all[r].mass;
         }
-        const uint64_t at = by_count ? count_at : mass_at, size = by_count ? count : mass, point = point_of(total);
+        const uint64_t point = point_of(total);
         if (point < total && at <= point && point < at + size) {
-            uint64_t before = at;
             int b = b0;
-            for (;; ++b) {
-                const uint64_t here = by_count ? sm.cnts[b] : sm.sums[b];
-                count_at += sm.cnts[b];
-                if (point < before + here) break;
-                before += here;
-            }
-            for (int r = 0; r < C; ++r) cluster.map_shared_rank(&sm, r)->found = {before, (uint32_t)(rank * chunk + b), count_at, 0, 0};
+            while (point >= at + sums[b]) at += sums[b++];
+            const uint64_t end = at + sums[b];
+            for (int r = 0; r < C; ++r)
+                cluster.map_shared_rank(&sm, r)->found = {at, (uint32_t)(rank * chunk + b), (uint32_t)end, (uint32_t)(end >> 32), 0};
         }
         cluster.sync();
         if (point >= total) return {-1, 0, 0};
-        return {(int)sm.found.a, sm.found.mass, sm.found.b};
+        return {(int)sm.found.a, sm.found.mass, (uint64_t)sm.found.c << 32 | sm.found.b};
     };
-    // The tokens for which f(value, key) holds, in rank 0's list if there are at most kList; their number.
-    auto gather = [&](auto f) -> int {
+    // The tokens of values lo .. hi, in rank 0's list if there are at most kList; their number.
+    auto gather = [&](float lo, float hi) -> int {
         each([&](float v, int i) {
-            const uint32_t key = key_of(v);
-            const bool in = key > kKeyNegInf && f(v, key);
+            const bool in = v >= lo && v <= hi;
             const unsigned hit = __ballot_sync(0xffffffffu, in);
             if (!hit) return;
             int at = 0;
             if (lane == 0) at = atomicAdd(&sm.listed, __popc(hit));
             at = __shfl_sync(0xffffffffu, at, 0) + __popc(hit & ((1u << lane) - 1u));
-            if (in && at < kList) sm.mine[at] = (uint64_t)key << 32 | (uint32_t)~(first + i);
+            if (in && at < kList) sm.mine[at] = (uint64_t)key_of(v) << 32 | (uint32_t)~(first + i);
         });
         __syncthreads();
         const SampleNote* all = tell({0, (uint32_t)sm.listed, 0, 0, 0});
@@ -520,29 +520,39 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         return s;
     };
     bool fresh = true;  // the row's histogram is still there
-    auto place_in = [&](const Bin& bin, uint32_t from, uint64_t point, bool by_count) -> Place {
-        const int count = gather([&](float v, uint32_t key) { return key >= from && bin_of_value(v) == bin.bin; });
+    // (Where `draw` and the list holds the token, it is written, and `done`.)
+    auto place_in = [&](const Bin& bin, uint32_t from, uint64_t point, bool by_count, uint64_t draw, bool& done) -> Place {
+        const uint32_t last = lowest_key(bin.bin);
+        uint32_t klo = max(from, last), khi = bin.bin ? lowest_key(bin.bin - 1) - 1 : kmax;
+        const int count = gather(value_of(klo), value_of(khi));
         if (count <= kList) {
             if (rank == 0) {
                 const Ranked r = rank_list(count, by_count);
                 const uint64_t rest = point - bin.before;
                 if (r.before <= rest && rest < r.before + r.weight) {
-                    int j = 0;  // tokens of its key before it
-                    while (j < tid && (sm.ranked[tid - 1 - j] >> 32) == (r.token >> 32)) ++j;
-                    const SampleNote note = {bin.before + r.before - j * r.weight, (uint32_t)(r.token >> 32), (uint32_t)j, 0, 0};
-                    for (int q = 0; q < C; ++q) cluster.map_shared_rank(&sm, q)->found = note;
+                    const uint32_t key = (uint32_t)(r.token >> 32);
+                    if (draw) {
+                        a.tokens[row] = (int)~(uint32_t)r.token;
+                        if (a.logprobs) a.logprobs[row] = logprob_of(key, draw);
+                    } else {
+                        int j = 0;  // tokens of its key before it
+                        while (j < tid && (uint32_t)(sm.ranked[tid - 1 - j] >> 32) == key) ++j;
+                        const SampleNote note = {bin.before + r.before - j * r.weight, key, (uint32_t)j, 0, 0};
+                        for (int q = 0; q < C; ++q) cluster.map_shared_rank(&sm, q)->found = note;
+                    }
                 }
             }
-            cluster.sync();
+            done = draw != 0;
+            if (!done) cluster.sync();
             return {sm.found.a, sm.found.mass, sm.found.b};
         }
-        uint32_t klo = 0xffffffffu, khi = 0;
+        const float vlo = value_of(klo), vhi = value_of(khi);
+        float least = INFINITY, most = -INFINITY;
         each([&](float v, int) {
-            const uint32_t key = key_of(v);
-            if (key >= from && key > kKeyNegInf && bin_of_value(v) == bin.bin) klo = min(klo, key), khi = max(khi, key);
+            if (v >= vlo && v <= vhi) least = fminf(least, v), most = fmaxf(most, v);
         });
-        klo = __reduce_min_sync(0xffffffffu, klo);
-        khi = __reduce_max_sync(0xffffffffu, khi);
+        klo = __reduce_min_sync(0xffffffffu, key_of(least));
+        khi = __reduce_max_sync(0xffffffffu, key_of(most));
         __syncthreads();
         if (lane == 0) sm.wa[warp] = khi, sm.wb[warp] = klo;
         __syncthreads();
@@ -553,8 +563,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         while (klo < khi) {
             fresh = false;
             const int shift = shift_of(klo, khi);
-            histogram([&](float, uint32_t key) { return key >= klo && key <= khi ? (int)((khi - key) >> shift) : -1; }, !by_count, by_count);
-            const Bin b = find_bin([&](uint64_t) { return point - before; }, by_count);
+            histogram([&](float v) {
+                const uint32_t key = key_of(v);
+                return key >= klo && key <= khi ? (int)((khi - key) >> shift) : -1;
+            }, by_count, true);
+            const Bin b = find_bin([&](uint64_t) { return point - before; });
             before += b.before;
             khi -= (uint32_t)b.bin << shift;
             const uint32_t width = (1u << shift) - 1u;
@@ -565,12 +578,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     // the mass of the tokens of keys above `from`, and of that key's first j
     auto mass_from = [&](uint32_t from, uint64_t j) {
         uint64_t mine = 0, same = 0;
+        const float bound = value_of(from);
         each([&](float v, int) {
-            const uint32_t key = key_of(v);
-            if (!__any_sync(0xffffffffu, key >= from && key > kKeyNegInf)) return;
+            if (!__any_sync(0xffffffffu, v >= bound)) return;
             const uint64_t w = weigh(v);
-            if (key > from) mine += w;
-            else if (key == from) ++same;
+            if (v > bound) mine += w;
+            else if (v == bound) ++same;
         });
         for (int off = 16; off; off >>= 1) {
             mine += __shfl_xor_sync(0xffffffffu, mine, off);
@@ -589,20 +602,20 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
 
     constexpr uint64_t kAll = 0xffffffffull;
     constexpr int kNoCut = 0x7fffffff;
+    bool done = false;
     // --- top-k: the last key kept, and how many of its tokens
     uint32_t k_keep = kmin;
     uint64_t j_keep = kAll;
     bool cut = false;
     if (top_k > 0 && top_k < a.vocab) {
-        histogram([&](float v, uint32_t key) { return key > kKeyNegInf ? bin_of_value(v) : -1; }, false, true);
-        const Bin b = find_bin([&](uint64_t) { return (uint64_t)(top_k - 1); }, true);
-        if (b.bin >= 0 && b.upto <= kList) {
-            gather([&](float v, uint32_t) { return bin_of_value(v) <= b.bin; });
-            finish_list((int)b.upto, top_k, 0);
+        histogram([&](float v) { return v > -INFINITY ? bin_of_value(v) : -1; }, true, false);
+        const Bin b = find_bin([&](uint64_t) { return (uint64_t)(top_k - 1); });
+        if (b.bin >= 0 && b.upto <= (uint64_t)kList) {
+            finish_list(gather(value_of(lowest_key(b.bin)), top), top_k, 0);
             return;
         }
         if (b.bin >= 0) {
-            const Place p = place_in(b, 0, (uint64_t)(top_k - 1), true);
+            const Place p = place_in(b, kmin, (uint64_t)(top_k - 1), true, 0, done);
             k_keep = p.key;
             j_keep = p.j + 1;
             cut = true;
@@ -610,7 +623,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     }
     if (!cut && !some_p && some_min && k_least > kmin) {
         // min-p alone
-        const int count = gather([&](float, uint32_t key) { return key >= k_least; });
+        const int count = gather(value_of(k_least), top);
         if (count <= kList) {
             finish_list(count, kNoCut, 0);
             return;
@@ -619,11 +632,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     }
     // --- the masses
     const uint32_t from = k_keep;
-    auto masses = [&](bool counts) {
-        histogram([&](float v, uint32_t key) { return key >= from ? bin_of_value(v) : -1; }, true, counts);
+    auto masses = [&]() {
+        const float bound = value_of(from);
+        histogram([&](float v) { return v >= bound ? bin_of_value(v) : -1; }, false, from > kmin);
         fresh = true;
     };
-    masses(some_p);
+    masses();
     uint64_t mass = cut ? mass_from(k_keep, j_keep) : 0;  // 0: all of the histogram's
     if (some_p) {
         // the tokens with less than p of the mass before them, the first one among them
@@ -631,13 +645,15 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         const Bin b = find_bin([&](uint64_t total) {
             if (!cut) mass = total;
             return last = top_p > 0.f ? max(part_of(mass, top_p, true), (uint64_t)1) - 1 : 0;
-        }, false);
-        if (b.upto <= kList) {
-            gather([&](float v, uint32_t key) { return key >= from && bin_of_value(v) <= b.bin; });
-            finish_list((int)b.upto, cut ? top_k : kNoCut, mass);
-            return;
+        });
+        if ((b.before >> kMassBits) < (uint64_t)kList) {  // at least so many tokens come before the bin
+            const int count = gather(value_of(max(from, lowest_key(b.bin))), top);
+            if (count <= kList) {
+                finish_list(count, cut ? top_k : kNoCut, mass);
+                return;
+            }
         }
-        const Place p = place_in(b, from, last, false);
+        const Place p = place_in(b, from, last, false, 0, done);
         k_keep = p.key;
         mass = p.before + (p.j + 1) * weight_of(p.key);
     }
@@ -651,32 +667,33 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         mass = mass_from(k_keep, kAll);
     }
     // --- the draw
-    if (!fresh) masses(false);
+    if (!fresh) masses();
     uint64_t point = 0;
     const Bin b = find_bin([&](uint64_t total) {
         if (mass == 0) mass = total;
         return point = min(part_of(mass, fminf(fmaxf(u, 0.f), 1.f), false), mass - 1);
-    }, false);
-    const Place p = place_in(b, from, point, false);
-    pick(p.key, p.j, mass);
+    });
+    const Place p = place_in(b, from, point, false, mass, done);
+    if (!done) pick(p.key, p.j, mass);
     finish();
 }
 
 template <class T>
 static cudaError_t launch_sample(SampleArgs a, int dev, cudaStream_t st) {
-    // A row's CTAs: enough that its slices fit in shared memory beside one another on an SM, more where
-    // there are few rows.
+    // A row's CTAs: enough that its slices fit in shared memory with two CTAs on an SM, more where there are
+    // few rows.
     const int sms = sm_count(dev);
     int C = 1;
     auto slice_of = [&](int c) { return ((a.vocab + c - 1) / c + 7) / 8 * 8; };
-    constexpr int kHeldBytes = 56 * 1024;
+    constexpr int kHeldBytes = 68 * 1024;
     while (C < kMaxCluster && ((size_t)slice_of(C) * sizeof(T) > kHeldBytes || ((int64_t)a.rows * C < 2 * sms && slice_of(C) > 2048))) C *= 2;
     a.slice = slice_of(C);
     a.held = (int)std::min<int64_t>(a.slice, kHeldBytes / sizeof(T));
-    const size_t bytes = sizeof(SampleSmem) + (size_t)a.held * sizeof(T);
+    const size_t bytes = sizeof(SampleSmem) + kBins / C * sizeof(uint64_t) + (size_t)a.held * sizeof(T);
     static DeviceOnce once;
     const cudaError_t set = once.run(dev, [] {
-        return cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleSmem) + kHeldBytes);
+        return cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)(sizeof(SampleSmem) + kBins * sizeof(uint64_t)) + kHeldBytes);
     });
     if (set != cudaSuccess) return set;
     cudaLaunchConfig_t cfg = {};
