@@ -9,6 +9,7 @@ fallback: if the library is missing or fails to load, using it raises.
 import ctypes
 import os
 import re
+import struct
 
 import numpy as np
 
@@ -707,12 +708,12 @@ def attention_prompt(q, k, v, out, cu_q, cu_k=None, scale=None, stream=None):
 # ---------------------------------------------------------------------------
 def _type_of(name, t):
     """moe_type_t of a tensor."""
-    torch = _torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch.Tensor):
         _refuse(f"{name} must be a torch tensor")
-    if t.dtype is torch.bfloat16:
+    dtype = t.dtype
+    if dtype is _torch.bfloat16:
         return 0
-    if t.dtype is torch.float32:
+    if dtype is _torch.float32:
         return 1
     _refuse(f"{name} must be bfloat16 or float32")
 
@@ -721,12 +722,33 @@ def _matrix(name, t, shape, dev):
     """Checks t as rows of the given shape on CUDA device dev; returns (address, row stride)."""
     if t.shape != shape:
         _refuse(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    rows, st = t.stride() if t.shape[0] > 1 else (shape[1], t.stride()[1])
-    if st != 1 and shape[1] > 1:
-        _refuse(f"the rows of {name} must be contiguous")
     if t.get_device() != dev:
         _refuse(f"{name} must be on the current CUDA device")
-    return t.data_ptr(), rows
+    if t.is_contiguous():  # the usual call (the strides of a single row or column mean nothing)
+        return t.data_ptr(), shape[1]
+    rows, st = t.stride()
+    if st != 1 and shape[1] > 1:
+        _refuse(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), rows if shape[0] > 1 else shape[1]
+
+
+def _vector(name, t, n, dev):
+    if t.shape != (n,) or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous tensor of shape ({n},)")
+    if t.get_device() != dev:
+        _refuse(f"{name} must be on the current CUDA device")
+    return t.data_ptr()
+
+
+def _same_type(name, t, kind):
+    own = _type_of(name, t)
+    if kind >= 0 and own != kind:
+        _refuse("weight, post_weight and gate must have one type")
+    return own
+
+
+_norm_args = struct.Struct("@6i2f" + "Pq" * 4 + "3Pq").pack  # moe_norm_t
+_sampling_args = struct.Struct("@5P").pack                   # moe_sampling_t
 
 
 def residual_norm(x, y=None, out=None, weight=None, post_weight=None, gate=None, scale=1.0, eps=1e-6, x_out=None, stream=None):
@@ -735,55 +757,58 @@ def residual_norm(x, y=None, out=None, weight=None, post_weight=None, gate=None,
     weight, bf16. x, y bf16 or fp32 [T, H]; weight, post_weight [H] and gate ([H],
     [T, H] or [T, 1]) of one type, bf16 or fp32. Without y only out is written;
     without out only x_out. Returns out, or x_out without it."""
-    torch = _need_torch()
+    _need_torch()
     xt = _type_of("x", x)
-    if x.dim() != 2:
-        _refuse("x must be [T, H]")
     shape = x.shape
+    if len(shape) != 2:
+        _refuse("x must be [T, H]")
     T, H = shape
     dev = x.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    if dev < 0 or dev != _torch._C._cuda_getDevice():
         _refuse("x must be on the current CUDA device")
-    a = NormArgs(T, H, xt, xt, 0, 0, scale, eps)
-    a.x, a.x_stride = _matrix("x", x, shape, dev)
+    xp, xs = _matrix("x", x, shape, dev)
+    yt, yp, ys, xop, xos, op, os_ = xt, 0, 0, 0, 0, 0, 0
     if y is not None:
-        a.y_type = _type_of("y", y)
-        a.y, a.y_stride = _matrix("y", y, shape, dev)
+        yt = _type_of("y", y)
+        yp, ys = _matrix("y", y, shape, dev)
         if x_out is None:
-            x_out = x
-        if _type_of("x_out", x_out) != xt:
-            _refuse("x_out must have x's type")
-        a.x_out, a.x_out_stride = _matrix("x_out", x_out, shape, dev)
+            x_out, xop, xos = x, xp, xs
+        else:
+            if _type_of("x_out", x_out) != xt:
+                _refuse("x_out must have x's type")
+            xop, xos = _matrix("x_out", x_out, shape, dev)
     elif x_out is not None or post_weight is not None or gate is not None:
         _refuse("x_out, post_weight and gate need y")
     if out is not None:
         if _type_of("out", out) != 0:
             _refuse("out must be bfloat16")
-        a.out, a.out_stride = _matrix("out", out, shape, dev)
-    wt = None
-    for name, t in (("weight", weight), ("post_weight", post_weight), ("gate", gate)):
-        if t is None:
-            continue
-        if _type_of(name, t) != (wt if wt is not None else _type_of(name, t)):
-            _refuse("weight, post_weight and gate must have one type")
-        wt = _type_of(name, t)
-        if name == "gate":
-            if t.dim() == 1 and t.shape[0] == H:
-                a.gate, _ = _matrix(name, t[None], (1, H), dev)
-                a.gate_wide = 1
-            elif t.dim() == 2 and t.shape == shape:
-                a.gate, a.gate_stride = _matrix(name, t, shape, dev)
-                a.gate_wide = 1
-            elif t.dim() == 2 and t.shape == (T, 1):
-                a.gate, a.gate_stride = _matrix(name, t, (T, 1), dev)
-            else:
-                _refuse(f"gate must be [{H}], [{T}, {H}] or [{T}, 1], got {tuple(t.shape)}")
+        op, os_ = _matrix("out", out, shape, dev)
+    wt = -1
+    wp = pp = gp = gs = wide = 0
+    if weight is not None:
+        wt = _type_of("weight", weight)
+        wp = _vector("weight", weight, H, dev)
+    if post_weight is not None:
+        wt = _same_type("post_weight", post_weight, wt)
+        pp = _vector("post_weight", post_weight, H, dev)
+    if gate is not None:
+        wt = _same_type("gate", gate, wt)
+        of = gate.shape
+        if of == shape:
+            gp, gs = _matrix("gate", gate, shape, dev)
+            wide = 1
+        elif of == (T, 1):
+            gp, gs = _matrix("gate", gate, of, dev)
+        elif of == (H,):
+            gp = _vector("gate", gate, H, dev)
+            wide = 1
         else:
-            if t.dim() != 1:
-                _refuse(f"{name} must be [{H}]")
-            setattr(a, name, _matrix(name, t[None], (1, H), dev)[0])
-    a.w_type = wt or 0
-    _check(load().moe_residual_norm(ctypes.addressof(a), _stream(stream, dev)))
+            _refuse(f"gate must be [{H}], [{T}, {H}] or [{T}, 1], got {tuple(of)}")
+    st = (_lib or load()).moe_residual_norm(
+        _norm_args(T, H, xt, yt, max(wt, 0), wide, scale, eps, xp, xs, yp, ys, xop, xos, op, os_, wp, pp, gp, gs),
+        _stream(stream, dev))
+    if st:
+        _check(st)
     return x_out if out is None else out
 
 
@@ -801,18 +826,23 @@ def sample(logits, tokens, uniform=None, temperature=None, top_k=None, top_p=Non
     if dev < 0 or dev != torch._C._cuda_getDevice():
         _refuse("logits must be on the current CUDA device")
     at, rows = _matrix("logits", logits, logits.shape, dev)
-    out = []
-    for name, t, dtype in (("tokens", tokens, torch.int32), ("temperature", temperature, torch.float32),
-                           ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32),
-                           ("uniform", uniform, torch.float32), ("logprobs", logprobs, torch.float32)):
-        if t is None and name != "tokens":
-            out.append(None)
-            continue
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 1 and t.shape[0] == T and t.is_contiguous()):
+    f32, i32t, shape = torch.float32, torch.int32, (T,)
+
+    def array(name, t, dtype):
+        if t is None:
+            return 0
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
             _refuse(f"{name} must be a contiguous {str(dtype)[6:]} tensor of shape ({T},)")
         if t.get_device() != dev:
             _refuse(f"{name} must be on the current CUDA device")
-        out.append(t.data_ptr())
-    a = SamplingArgs(*out[1:6])
-    _check(load().moe_sample(at, kind, rows, T, V, ctypes.addressof(a), out[0], out[6], _stream(stream, dev)))
+        return t.data_ptr()
+
+    if tokens is None:
+        _refuse("tokens must be an int32 tensor")
+    settings = _sampling_args(array("temperature", temperature, f32), array("top_k", top_k, i32t), array("top_p", top_p, f32),
+                              array("min_p", min_p, f32), array("uniform", uniform, f32))
+    st = (_lib or load()).moe_sample(at, kind, rows, T, V, settings, array("tokens", tokens, i32t),
+                                     array("logprobs", logprobs, f32), _stream(stream, dev))
+    if st:
+        _check(st)
     return tokens
