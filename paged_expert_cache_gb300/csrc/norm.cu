@@ -18,7 +18,7 @@
 #include <cmath>
 
 #include "common.cuh"
-#include "device_policy.h"
+#include "kv.cuh"
 #include "moe_cache.h"
 
 namespace moe {
@@ -74,6 +74,35 @@ __device__ __forceinline__ void store_values(T* p, const float (&v)[V]) {
             make_uint4(norm_pack(v[0], v[1]), norm_pack(v[2], v[3]), norm_pack(v[4], v[5]), norm_pack(v[6], v[7]));
     }
 }
+
+// V values as they are in memory, on their way.
+template <class T, int V>
+struct Raw {
+    uint32_t r[V == 1 ? 1 : V * sizeof(T) / 4];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (V == 1) {
+            if constexpr (sizeof(T) == 4) r[0] = *reinterpret_cast<const uint32_t*>(p);
+            else r[0] = *p;
+        } else {
+#pragma unroll
+            for (int e = 0; e < (int)(V * sizeof(T) / 16); ++e) {
+                const uint4 v = *(reinterpret_cast<const uint4*>(p) + e);
+                r[4 * e] = v.x, r[4 * e + 1] = v.y, r[4 * e + 2] = v.z, r[4 * e + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[V]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = __uint_as_float(r[e]);
+        } else if constexpr (V == 1) {
+            v[0] = __uint_as_float(r[0] << 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) v[2 * e] = __uint_as_float(r[e] << 16), v[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
+        }
+    }
+};
 
 // The sum over a row's threads: a warp (`group` 32), or the CTA. Each call of a
 // CTA has a line of `part` of its own, so that one barrier does.
@@ -168,11 +197,90 @@ __global__ void __launch_bounds__(1024) k_norm(NormArgs a, int group) {
     });
 }
 
+// The same for many rows: a CTA takes every gridDim-th one. Its threads keep their
+// columns' weights in registers (the post norm's times the gate's and the scale),
+// and a row's loads are on the way while the row before it is done.
+template <class X, class Y, class W, int V, int N>
+__global__ void __launch_bounds__(512, 2) k_norm_rows(NormArgs a, int group) {
+    constexpr int E = N * V;
+    __shared__ float part[2][4][32];
+    const int t = threadIdx.x;
+    griddep_wait();
+    griddep_launch();
+    auto at = [&](int n) { return (n * group + t) * V; };
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (at(n) < a.hidden) f(n);
+    };
+    float w[E], pw[E];  // of out; of y
+    float one = a.scale;
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] = 1.f, pw[e] = 1.f;
+    each([&](int n) {
+        if (a.weight) load_values<V>(*reinterpret_cast<float(*)[V]>(w + n * V), (const W*)a.weight + at(n));
+        if (a.post) load_values<V>(*reinterpret_cast<float(*)[V]>(pw + n * V), (const W*)a.post + at(n));
+        if (a.gate_wide) {
+            float g[V];
+            load_values<V>(g, (const W*)a.gate + at(n));
+#pragma unroll
+            for (int e = 0; e < V; ++e) pw[n * V + e] *= g[e];
+        }
+    });
+    Raw<X, V> xr[N];
+    Raw<Y, V> yr[N];
+    float gate = 1.f;
+    auto fetch = [&](int row) {
+        each([&](int n) {
+            xr[n].load((const X*)a.x + row * a.xs + at(n));
+            if (a.y) yr[n].load((const Y*)a.y + row * a.ys + at(n));
+        });
+        if (a.gate && !a.gate_wide) gate = to_float(*((const W*)a.gate + row * a.gs));
+    };
+    fetch(blockIdx.x);
+    int turn = 0;
+    for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        float x[E], y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = y[e] = 0.f;
+        each([&](int n) {
+            xr[n].get(*reinterpret_cast<float(*)[V]>(x + n * V));
+            if (a.y) yr[n].get(*reinterpret_cast<float(*)[V]>(y + n * V));
+        });
+        const float here = one * gate;
+        if (row + gridDim.x < (unsigned)a.rows) fetch(row + gridDim.x);
+        if (a.y) {
+            float2 r = make_float2(1.f, 1.f);
+            if (a.post) r = inverse_rms(y, a, group, part[turn]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = fmaf(here, y[e] * r.x * r.y * pw[e], x[e]);
+            if (a.x_out) {
+                X* dst = (X*)a.x_out + row * a.xos;
+                each([&](int n) { store_values<V>(dst + at(n), *reinterpret_cast<float(*)[V]>(x + n * V)); });
+            }
+        }
+        if (!a.out) continue;
+        const float2 r = inverse_rms(x, a, group, part[turn] + 2);
+        uint16_t* dst = (uint16_t*)a.out + row * a.os;
+        each([&](int n) {
+            float o[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = x[n * V + e] * r.x * r.y * w[n * V + e];
+            store_values<V>(dst + at(n), o);
+        });
+    }
+}
+
 template <class X, class Y, class W>
-static cudaError_t launch_norm(const NormArgs& a, bool aligned, cudaStream_t st) {
+static cudaError_t launch_norm(const NormArgs& a, bool aligned, int sms, cudaStream_t st) {
     const int per = 8, threads = std::min(1024, std::max(32, (a.hidden + per * 32 - 1) / (per * 32) * 32));
     const int n = (a.hidden + per * threads - 1) / (per * threads);  // eights a thread: 1, 2 or 4
     const int rows_a_cta = threads == 32 ? 4 : 1;
+    if (threads > 32 && threads <= 512 && n == 1 && !(a.gate_wide && a.gs) && a.rows >= 8 * sms) {
+        const int per_sm = 1024 / threads;
+        return launch_ex(aligned ? k_norm_rows<X, Y, W, 8, 1> : k_norm_rows<X, Y, W, 1, 8>, dim3((unsigned)(sms * per_sm)), dim3(threads),
+                         0, st, true, a, threads);
+    }
     const dim3 grid((unsigned)((a.rows + rows_a_cta - 1) / rows_a_cta)), block(threads * rows_a_cta);
     if (aligned)
         return launch_ex(n == 1 ? k_norm<X, Y, W, 8, 1> : n == 2 ? k_norm<X, Y, W, 8, 2> : k_norm<X, Y, W, 8, 4>, grid, block, 0,
@@ -243,7 +351,9 @@ extern "C" moe_status_t moe_residual_norm(const moe_norm_t* n, void* stream) {
     case 7: launch = moe::launch_norm<F, F, F>; break;
     default: break;
     }
-    const cudaError_t e = launch(a, aligned, (cudaStream_t)stream);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = launch(a, aligned, moe::sm_count(dev), (cudaStream_t)stream);
     if (e == cudaSuccess) return MOE_OK;
     moe::set_last_error(cudaGetErrorString(e));
     return MOE_ERR_CUDA;
