@@ -19,10 +19,14 @@
 //   8         the run's pieces
 //   9, 10     issue the MMAs of tile 0, 1: S = Q K^T, and O += P V with P in
 //             tensor memory
-//   12-15     codes into tiles: a warp takes two of a tile's eight cells, from the
-//             cache to registers one tile ahead, and writes d (q - 8) as fp16 to a
-//             ring K0 V0 K1 V1 ... of tiles in 128-byte swizzle. Keys lie [key][dim],
-//             values [dim][key], as the cells hold them; both K-major.
+//   11        copies a tile's cells, their keys and their values in turn, into a
+//             ring of three half tiles as they are (bulk copies)
+//   12-15     codes into tiles: a warp takes two of a tile's eight cells and writes
+//             d (q - 8) as fp16 to a ring K0 V0 K1 V1 ... of tiles in 128-byte
+//             swizzle. Keys lie [key][dim], values [dim][key], as the cells hold
+//             them; both K-major. The code is kept short: with the cells in
+//             registers and all written out, a tile took 6500 cycles, most of them
+//             waiting for instructions.
 // Where a group has no more than 128 rows, both tiles are the same rows and take
 // every other key tile (kSingle); their sums are joined at the end.
 //
@@ -74,14 +78,18 @@ template <int D>
 struct SharedSmem {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kRaw = 3;
     uint8_t q[2][kTileBytes];
     uint8_t kv[kStages][kTileBytes];
+    uint8_t raw[kRaw][kTile / kCellTokens][Cell<D>::kBytes / 2];  // the cells' keys, or values, with their scales
+    unsigned long long raw_full[kRaw], raw_empty[kRaw];
     unsigned long long q_full[2], full[kStages], empty[kStages], s_full[2], p_full[2][2], o_full[2];
     unsigned long long item_full[2], item_empty[2], half_done, half_read;
     float half[kTile][2];  // exponent and sum of a row's second half of key tiles
     SharedPiece item[2];
     int meta[kStages];     // of a tile of values: how often it is multiplied; + 256: another one of the same keys follows
-    unsigned large[8];     // of a key tile: the cells written 2^-4 times as large, a bit each
+    unsigned absent[kRaw]; // the cells that are not there, a bit each
+    unsigned long long large[8];  // of a key tile: the cells written 2^-4 times as large, a byte each
     int nan_from[2][4];    // of a piece, for each block of dims: the first position with a NaN scale
     int dead;
     uint32_t tmem;
@@ -125,11 +133,15 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
             bar_init_n(gsmem(&sm.p_full[x][1]), 128);
             bar_init_n(gsmem(&sm.o_full[x]), 1);
             bar_init_n(gsmem(&sm.item_full[x]), 1);
-            bar_init_n(gsmem(&sm.item_empty[x]), 14);  // the softmax, MMA and tile warps
+            bar_init_n(gsmem(&sm.item_empty[x]), 15);  // all warps but the pieces' own
         }
         for (int st = 0; st < kStages; ++st) {
-            bar_init_n(gsmem(&sm.full[st]), 128);
+            bar_init_n(gsmem(&sm.full[st]), 4);   // the warps that make tiles
             bar_init_n(gsmem(&sm.empty[st]), 2);  // both MMA warps
+        }
+        for (int r = 0; r < S::kRaw; ++r) {
+            bar_init_n(gsmem(&sm.raw_full[r]), 1);
+            bar_init_n(gsmem(&sm.raw_empty[r]), 4);  // the warps that make tiles
         }
         bar_init_n(gsmem(&sm.half_done), 128);
         bar_init_n(gsmem(&sm.half_read), 128);
@@ -163,188 +175,172 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
 
     // Registers: the launch gives 128 a thread (65536 in all).
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
         // --- codes into tiles. A warp has cells 2w and 2w + 1 of a tile. Keys: lane
-        // -> token lane % 8 (and + 8), quarter lane / 8 of each block, so that eight
-        // lanes write eight rows of the swizzle. Values: lane -> cell, half of its
-        // tokens, and dims g + 8 j of each block.
-        const int w = warp - 12, kt = lane & 7, ki = lane >> 3, vz = lane >> 4, vh = (lane >> 3) & 1, vg = lane & 7;
-        int st = 0, order = 0;  // tiles so far
-        uint32_t turn = 1;
-        uint32_t kr[4][G], ks[4][G / 2], vr[4][G], vs[4][G];
+        // -> token and quarter of each block, so that eight lanes read and write
+        // without conflicts. Values: lane -> cell, half of its tokens, and dims g +
+        // 8 j of each block.
+        const int w = warp - 12, ki = lane & 3, kp = lane >> 3, kt = lane & 4 ? kp ^ 5 : kp;
+        const int vz = lane >> 4, vh = (lane >> 3) & 1, vg = lane & 7;
+        int st = 0, raw_st = 0, order = 0;  // stage, half tile; tiles so far
+        uint32_t turn = 1, raw_turn = 0;
         auto step = [&]() { if (++st == kStages) st = 0, turn ^= 1; };
+        auto next_raw = [&]() {
+            bar_wait(gsmem(&sm.raw_full[raw_st]), raw_turn, dead);
+            __syncwarp();
+        };
+        auto free_raw = [&]() {
+            __syncwarp();
+            if (lane == 0) bar_arrive(gsmem(&sm.raw_empty[raw_st]));
+            if (++raw_st == S::kRaw) raw_st = 0, raw_turn ^= 1;
+        };
+        auto stage_full = [&]() {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(gsmem(&sm.full[st]));
+            step();
+        };
+        // The scales of the warp's two cells, a word a lane; none in cells that are not there.
+        constexpr bool kAll = C::kScales == 128;  // every lane has one
+        auto scale_word = [&](int z) { return reinterpret_cast<uint32_t*>(sm.raw[raw_st][2 * w + z] + C::kCodes) + lane; };
+        auto put_scales = [&](const uint32_t (&v)[2]) {
+            __syncwarp();
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+                if (kAll || lane < C::kScales / 4) *scale_word(z) = v[z];
+            __syncwarp();
+        };
+        auto get_scales = [&](uint32_t (&v)[2]) {
+            const unsigned absent = sm.absent[raw_st] >> (2 * w) & 3u;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) v[z] = kAll || lane < C::kScales / 4 ? *scale_word(z) : 0u;
+            if (absent) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                    if (absent >> z & 1u) v[z] = 0;
+                put_scales(v);
+            }
+        };
         for (int number = 0; take(number); ++number) {
-            const SharedPiece& p = sm.item[number & 1];
-            const int seq = p.seq, head = p.head, u1 = p.u1, cells = p.common / kCellTokens;
-            // the two cells of a tile; none past the common part, and none where the pool has no such page
-            auto place = [&](int tile, const uint8_t* (&at)[2]) {
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const int n = tile * (kTile / kCellTokens) + 2 * w + z;
-                    at[z] = n < cells ? kv_cell<D>(a.c, a.b, seq, n, head) : nullptr;
-                    if (n < cells && !at[z] && lane == 0) {
-                        atomicOr(a.c.err, 1u);
-                        for (int b = 0; b < G; ++b) atomicMin(&sm.nan_from[number & 1][b], n * kCellTokens);
-                    }
-                }
-            };
-            auto load_keys = [&](const uint8_t* const (&at)[2]) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint8_t* cell = at[u >> 1];
-                    const int t = kt + 8 * (u & 1);
-                    if (cell) {
-                        load_words<G>(kr[u], cell + C::k_word(t, ki, 0));
-                        load_words<G / 2>(ks[u], cell + C::kKs + C::k_scale(t, 0));
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < G; ++b) kr[u][b] = 0, ks[u][b / 2] = 0;
-                    }
-                }
-            };
-            auto load_values = [&](const uint8_t* const (&at)[2]) {
-                const uint8_t* cell = vz ? at[1] : at[0];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (cell) {
-                        load_words<G>(vr[i], cell + C::kV + ((vh * 32 + vg * 4 + i) * G) * 4);
-                        load_words<G>(vs[i], cell + C::kVs + ((vh * 4 + i) * G) * 4);
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < G; ++b) vr[i][b] = vs[i][b] = 0;
-                    }
-                }
-            };
-            // a tile of values from the codes and scales
-            auto put_values = [&](const uint32_t (&scale)[4][G], int meta) {
-                bar_wait(gsmem(&sm.empty[st]), turn, dead);
-                const int chunk = 2 * (2 * w + vz) + vh;  // 8 keys each
-                uint8_t* to = sm.kv[st] + (chunk >> 3) * (D * 128) + vg * 128 + (((chunk & 7) ^ vg) << 4);
-#pragma unroll
-                for (int b = 0; b < G; ++b) {
-                    uint32_t f[4][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) q4_to_frag(vr[i][b], f[i]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4*>(to + (32 * b + 8 * j) * 128) =
-                            make_uint4(times(f[0][j], scale[0][b]), times(f[1][j], scale[1][b]), times(f[2][j], scale[2][b]),
-                                       times(f[3][j], scale[3][b]));
-                }
-                if (tid == kSharedThreads - 128) sm.meta[st] = meta;
-                fence_async_smem();
-                bar_arrive(gsmem(&sm.full[st]));
-                step();
-            };
-            const uint8_t* at[2];
-            place(p.u0, at);
-            load_keys(at);
-            load_values(at);
-            for (int tile = p.u0; tile < u1; ++tile, ++order) {
-                const uint8_t* next[2] = {nullptr, nullptr};
-                if (tile + 1 < u1) place(tile + 1, next);
+            const int u1 = sm.item[number & 1].u1;
+#pragma unroll 1
+            for (int tile = sm.item[number & 1].u0; tile < u1; ++tile, ++order) {
+                uint32_t v[2];
                 // --- keys
+                next_raw();
+                get_scales(v);
+                {
+                    const bool l0 = __any_sync(0xffffffffu, larger_half(v[0]) >= kLargeScale);
+                    const bool l1 = __any_sync(0xffffffffu, larger_half(v[1]) >= kLargeScale);
+                    if (lane == 0) reinterpret_cast<uint16_t*>(&sm.large[order & 7])[w] = (uint16_t)((l0 ? 1 : 0) | (l1 ? 256 : 0));
+                    if (l0 || l1) {  // 2^-4 times as large
+                        if (l0) v[0] = times(v[0], 0x2c002c00u);
+                        if (l1) v[1] = times(v[1], 0x2c002c00u);
+                        put_scales(v);
+                    }
+                }
                 bar_wait(gsmem(&sm.empty[st]), turn, dead);
-#pragma unroll
+#pragma unroll 1
                 for (int z = 0; z < 2; ++z) {
-                    uint32_t big = 0;
+                    const uint8_t* cell = sm.raw[raw_st][2 * w + z];
+                    uint8_t* to = sm.kv[st] + ((2 * w + z) * kCellTokens + kt) * 128;
+                    uint32_t codes[2][G], ds[2][G / 2];
 #pragma unroll
-                    for (int u = 2 * z; u < 2 * z + 2; ++u)
-#pragma unroll
-                        for (int b = 0; b < G / 2; ++b) big = max(big, larger_half(ks[u][b]));
-                    const bool large = __any_sync(0xffffffffu, big >= kLargeScale);
-                    const unsigned bit = 1u << (2 * w + z);
-                    if (lane == 0) {
-                        if (large) atomicOr(&sm.large[order & 7], bit);
-                        else atomicAnd(&sm.large[order & 7], ~bit);
+                    for (int u = 0; u < 2; ++u) {
+                        load_words<G>(codes[u], cell + C::k_word(kt + 8 * u, ki, 0));
+                        load_words<G / 2>(ds[u], cell + C::kCodes + C::k_scale(kt + 8 * u, 0));
                     }
-                    if (large) {
 #pragma unroll
-                        for (int u = 2 * z; u < 2 * z + 2; ++u)
-#pragma unroll
-                            for (int b = 0; b < G / 2; ++b) ks[u][b] = times(ks[u][b], 0x2c002c00u);  // 2^-4
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int t = (2 * w + (u >> 1)) * kCellTokens + kt + 8 * (u & 1);
-#pragma unroll
-                    for (int b = 0; b < G; ++b) {
-                        const uint32_t d = __byte_perm(ks[u][b / 2], 0, b & 1 ? 0x3232 : 0x1010);
-                        uint32_t f[4];
-                        q4_to_frag(kr[u][b], f);
-                        *reinterpret_cast<uint4*>(sm.kv[st] + (b / 2) * kHalf + t * 128 + ((((b & 1) * 4 + ki) ^ (t & 7)) << 4)) =
-                            make_uint4(times(f[0], d), times(f[1], d), times(f[2], d), times(f[3], d));
-                    }
-                }
-                fence_async_smem();
-                bar_arrive(gsmem(&sm.full[st]));
-                step();
-                if (tile + 1 < u1) load_keys(next);
-                // --- values
-                uint32_t big = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int b = 0; b < G; ++b) big = max(big, larger_half(vs[i][b]));
-                uint32_t any;
-                asm volatile(
-                    "{\n.reg .pred p, r;\nsetp.ge.u32 p, %1, %2;\nbarrier.cta.red.or.pred.aligned r, 1, 128, p;\nselp.u32 %0, 1, 0, r;\n}\n"
-                    : "=r"(any)
-                    : "r"(big), "r"(kLargeScale)
-                    : "memory");
-                if (!any) {
-                    put_values(vs, 1);
-                } else {
-                    uint32_t rest[4][G];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int b = 0; b < G; ++b) {
-                            uint32_t small = vs[i][b], large = vs[i][b];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t bits = (vs[i][b] >> (16 * h)) & 0x7fffu, mask = 0xffffu << (16 * h);
-                                if (bits >= kNoNumber) {
-                                    atomicMin(&sm.nan_from[number & 1][b],
-                                              tile * kTile + (2 * w + vz) * kCellTokens + 8 * vh + 2 * i + h);
-                                    small &= ~mask, large &= ~mask;
-                                } else if (bits >= kLargeScale) {
-                                    small &= ~mask;
-                                } else {
-                                    large &= ~mask;
-                                }
-                            }
-                            vs[i][b] = small;
-                            rest[i][b] = times(large, 0x30003000u);  // an eighth
+                            const uint32_t d = __byte_perm(ds[u][b / 2], 0, b & 1 ? 0x3232 : 0x1010);
+                            uint32_t f[4];
+                            q4_to_frag(codes[u][b], f);
+                            *reinterpret_cast<uint4*>(to + u * 1024 + (b / 2) * kHalf + ((((b & 1) * 4 + ki) ^ kt) << 4)) =
+                                make_uint4(times(f[0], d), times(f[1], d), times(f[2], d), times(f[3], d));
                         }
-                    put_values(vs, 1 + 256);
-                    put_values(rest, 8);
                 }
-                if (tile + 1 < u1) load_values(next);
+                stage_full();
+                free_raw();
+                // --- values: once, and where some scales are large a second time
+                next_raw();
+                get_scales(v);
+                uint32_t any = max(larger_half(v[0]), larger_half(v[1])) >= kLargeScale;
+                asm volatile(
+                    "{\n.reg .pred p, r;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred.aligned r, 1, 128, p;\nselp.u32 %0, 1, 0, r;\n}\n"
+                    : "=r"(any)
+                    : "r"(any)
+                    : "memory");
+                uint32_t rest[2] = {0, 0};
+                if (any) {  // the small ones first, then an eighth of the large ones
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        rest[z] = times(v[z], 0x30003000u);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t bits = (v[z] >> (16 * h)) & 0x7fffu, other = ~(0xffffu << (16 * h));
+                            if (bits >= kNoNumber)
+                                atomicMin(&sm.nan_from[number & 1][lane % G],
+                                          tile * kTile + (2 * w + z) * kCellTokens + 8 * (lane / (4 * G)) + 2 * (lane / G % 4) + h);
+                            if (bits < kLargeScale || bits >= kNoNumber) rest[z] &= other;
+                            if (bits >= kLargeScale) v[z] &= other;
+                        }
+                    }
+                    put_scales(v);
+                }
+                const uint8_t* cell = sm.raw[raw_st][2 * w + vz];
+                const int chunk = 2 * (2 * w + vz) + vh;  // 8 keys each
+#pragma unroll 1
+                for (int pass = 0;; ++pass) {
+                    bar_wait(gsmem(&sm.empty[st]), turn, dead);
+                    uint8_t* to = sm.kv[st] + (chunk >> 3) * (D * 128) + vg * 128 + (((chunk & 7) ^ vg) << 4);
+                    uint32_t codes[4][G], scale[4][G];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        load_words<G>(codes[i], cell + ((vh * 32 + vg * 4 + i) * G) * 4);
+                        load_words<G>(scale[i], cell + C::kCodes + ((vh * 4 + i) * G) * 4);
+                    }
+#pragma unroll
+                    for (int b = 0; b < G; ++b) {
+                        uint32_t f[4][4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) q4_to_frag(codes[i][b], f[i]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(to + (32 * b + 8 * j) * 128) =
+                                make_uint4(times(f[0][j], scale[0][b]), times(f[1][j], scale[1][b]), times(f[2][j], scale[2][b]),
+                                           times(f[3][j], scale[3][b]));
+                    }
+                    if (tid == kSharedThreads - 128) sm.meta[st] = pass ? 8 : any ? 1 + 256 : 1;
+                    stage_full();
+                    if (pass == (int)any) break;
+                    put_scales(rest);
+                }
+                free_raw();
             }
             give_back(number);
         }
     } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
         if (warp == 8) {
             // --- the pieces of this CTA's run [lo, hi)
-            auto rows_of = [&](int g, int& seq, int& t0) {
+            int seq, t0, rows, common, work;  // of a lane's group
+            auto look = [&](int g) {
+                seq = t0 = rows = common = work = 0;
+                if (g >= a.g.n) return;
                 seq = a.g.cu[g];
                 const int last = min(max(a.g.cu[g + 1], 0), a.b.B);
-                if (seq < 0 || seq >= last) return 0;
+                if (seq < 0 || seq >= last) return;
                 t0 = min(max(a.b.cu[seq], 0), a.T);
-                return max(min(max(a.b.cu[last], 0), a.T) - t0, 0) * group;
-            };
-            auto units_of = [&](int g) { return (common_tokens(a.c, a.b, a.g, g) + kTile - 1) / kTile; };
-            auto work_of = [&](int units, int rows) {
-                return units ? (units + kPieceStart) * a.c.hkv * ((rows + kRows - 1) / kRows) : 0;
+                rows = max(min(max(a.b.cu[last], 0), a.T) - t0, 0) * group;
+                common = common_tokens(a.c, a.b, a.g, g);
+                if (rows && common) work = ((common + kTile - 1) / kTile + kPieceStart) * a.c.hkv * ((rows + kRows - 1) / kRows);
             };
             int total = 0;
-            for (int g = lane; g < a.g.n; g += 32) {
-                int seq, t0;
-                const int rows = rows_of(g, seq, t0);
-                if (rows) total += work_of(units_of(g), rows);
+            for (int g = lane; g - lane < a.g.n; g += 32) {
+                look(g);
+                total += work;
             }
             total = __reduce_add_sync(0xffffffffu, total);
             const int ctas = min(total, (int)gridDim.x), base = ctas ? total / ctas : 0, extra = total - base * ctas;
@@ -362,13 +358,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 __syncwarp();
             };
             for (int g0 = 0; g0 < a.g.n && x < hi; g0 += 32) {
-                const int g = g0 + lane;
-                int seq = 0, t0 = 0, rows = 0, common = 0, work = 0;
-                if (g < a.g.n) rows = rows_of(g, seq, t0);
-                if (rows) {
-                    common = common_tokens(a.c, a.b, a.g, g);
-                    work = work_of((common + kTile - 1) / kTile, rows);
-                }
+                if (a.g.n > 32) look(g0 + lane);
                 int upto = work;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -507,9 +497,53 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
             }
             // the last arrivals, so that none is under way when the CTA ends
             for (int e = 0; e < kStages; ++e) bar_wait(gsmem(&sm.empty[e]), e < st ? round : round ^ 1, dead);
+        } else {
+            // --- the cells' bytes: lane n has cell n of a tile
+            constexpr uint32_t kBytes = C::kBytes / 2;
+            int r = 0;
+            uint32_t turn = 1;
+            for (int number = 0; take(number); ++number) {
+                const SharedPiece& p = sm.item[number & 1];
+                const int seq = p.seq, head = p.head, u1 = p.u1, cells = p.common / kCellTokens;
+#pragma unroll 1
+                for (int tile = p.u0; tile < u1; ++tile) {
+                    const int n = tile * (kTile / kCellTokens) + lane;
+                    const bool inside = lane < kTile / kCellTokens && n < cells;
+                    const uint8_t* at = inside ? kv_cell<D>(a.c, a.b, seq, n, head) : nullptr;
+                    if (inside && !at) {  // no such page: its values are NaN
+                        atomicOr(a.c.err, 1u);
+                        for (int b = 0; b < G; ++b) atomicMin(&sm.nan_from[number & 1][b], n * kCellTokens);
+                    }
+                    const unsigned there = __ballot_sync(0xffffffffu, at != nullptr);
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        bar_wait(gsmem(&sm.raw_empty[r]), turn, dead);
+                        __syncwarp();
+                        const uint32_t bar = gsmem(&sm.raw_full[r]);
+                        if (!*(volatile int*)dead) {
+                            if (lane == 0) {
+                                sm.absent[r] = ~there;
+                                bar_expect(bar, kBytes * __popc(there));
+                            }
+                            __syncwarp();
+                            if (at)
+                                asm volatile(
+                                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                                        gsmem(sm.raw[r][lane & 7])),
+                                    "l"(at + half * kBytes), "r"(kBytes), "r"(bar)
+                                    : "memory");
+                        }
+                        if (++r == S::kRaw) r = 0, turn ^= 1;
+                    }
+                }
+                give_back(number);
+            }
+            // copies under way land before the CTA leaves, whatever else gave up
+            if (*(volatile int*)dead)
+                for (int e = 0; e < S::kRaw; ++e) gbar_wait(gsmem(&sm.raw_full[e]), e < r ? turn ^ 1 : turn);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n");
         // --- softmax of tile x, a thread per row
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -568,7 +602,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 const int tile = kSingle ? 2 * j + x : j, kt = u0 + tile;
                 __syncwarp();
                 tc_fence_after();
-                if (const unsigned large = *(volatile unsigned*)&sm.large[(order + tile) & 7]) {
+                if (const unsigned long long large = *(volatile unsigned long long*)&sm.large[(order + tile) & 7]) {
                     // scores of cells written 2^-4 times as large
 #pragma unroll 1
                     for (int h = 0; h < kTile / 32; ++h) {
@@ -577,7 +611,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                         tc_ld_wait32(v);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            v[e] = __float_as_uint(__uint_as_float(v[e]) * (large >> (2 * h + (e >> 4)) & 1u ? 16.f : 1.f));
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * (large >> (8 * (2 * h + (e >> 4))) & 1u ? 16.f : 1.f));
                         tc_st32(ts + 32 * h, v);
                     }
                     tc_st_wait();
