@@ -67,17 +67,18 @@ struct KvBatch {
 };
 
 // Groups of neighbouring sequences that have their first positions in common, and
-// what the kernel that attends over those leaves for the others: for each row a
-// sum that has begun (the unnormalised output and a head: the exponent that its
-// weights 2^(score - exponent) refer to, the sum of the weights, the first of the
-// slots that go on with it, and their number with, above 16 bits, its row there).
+// what the kernels leave of a row's sum for the one that joins it: unnormalised
+// outputs, each with a head: the exponent that its weights 2^(score - exponent) refer
+// to, the sum of the weights, and two words. Of the common positions: the first of
+// the slots that go on with the sum, and their number with, above 16 bits, its row
+// there. Of the rest: whether there is something to join.
 struct KvGroups {
     const int *cu, *prefix;
     int n;
 };
 struct SharedParts {
-    float *o, *slot_o;          // [T x q_heads], [CTAs x kSlotRows] rows of head_dim
-    float4 *head, *slot_head;   // as many
+    float *o, *slot_o, *rest_o;            // [T x q_heads], [CTAs x kSlotRows], [T x q_heads] rows of head_dim
+    float4 *head, *slot_head, *rest_head;  // as many
     int slots;
 };
 constexpr int kSlotRows = 256;
@@ -137,8 +138,8 @@ uint64_t attend_scratch_bytes(int device);
 bool attend_fits(const KvDev& c, const KvBatch& b, int T);
 cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
                           uint16_t* out, void* scratch, cudaStream_t st);
-// The same behind launch_shared: over what the groups do not have in common, joined
-// with what it left.
+// The same behind launch_shared: over what the groups do not have in common, and
+// both joined.
 cudaError_t launch_attend_rest(const KvDev& c, const KvBatch& b, const KvGroups& g, const SharedParts& parts, int D,
                                const uint16_t* q, int64_t q_stride, int T, float scale, uint16_t* out, void* scratch,
                                cudaStream_t st);

@@ -248,26 +248,32 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return h2_as_u32(__floats2half2_rn(lo, hi)); }
 
-// Four dims of a row's output: sums v of weights times values over the sum l of
-// weights (m their maximum).
-template <int D>
-__device__ __forceinline__ void put_row(const KvDev& c, const AttendArgs& a, int t0, int head, int row, int d, float4 v, float m, float l) {
+// A row's number among the call's.
+__device__ __forceinline__ size_t row_place(const KvDev& c, const AttendArgs& a, int t0, int head, int row) {
     const int group = c.hq / c.hkv, tok = a.group_div.div(row);
+    return (size_t)(t0 + tok) * c.hq + head * group + row - tok * group;
+}
+
+// Four dims of the output of row `at`: sums v of weights times values over the sum l
+// of weights (m their maximum).
+template <int D>
+__device__ __forceinline__ void put_at(const AttendArgs& a, size_t at, int d, float4 v, float m, float l) {
     const float inv = 1.0f / l;
     float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = m == -INFINITY && l == 0.f ? 0.f : x[e] * inv;
     __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0], x[1]), y1 = __floats2bfloat162_rn(x[2], x[3]);
-    *reinterpret_cast<uint2*>(a.out + ((size_t)(t0 + tok) * c.hq + head * group + row - tok * group) * D + d) =
-        make_uint2(*reinterpret_cast<uint32_t*>(&y0), *reinterpret_cast<uint32_t*>(&y1));
+    *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(*reinterpret_cast<uint32_t*>(&y0), *reinterpret_cast<uint32_t*>(&y1));
+}
+template <int D>
+__device__ __forceinline__ void put_row(const KvDev& c, const AttendArgs& a, int t0, int head, int row, int d, float4 v, float m, float l) {
+    put_at<D>(a, row_place(c, a, t0, head, row), d, v, m, l);
 }
 
-// Adds what launch_shared left of a row to four dims of its sum; m becomes an
-// exponent that the weights refer to (-inf: no weight but 0).
+// Adds what launch_shared left of a row to four dims of its sum, whose weights refer
+// to the exponent m (-inf: no weight but 0).
 template <int D>
-__device__ __forceinline__ void add_common(const KvDev& c, const AttendArgs& a, int t0, int head, int row, int d, float4& v, float& m, float& l) {
-    const int group = c.hq / c.hkv, tok = a.group_div.div(row);
-    const size_t at = (size_t)(t0 + tok) * c.hq + head * group + row - tok * group;
+__device__ __forceinline__ void add_common(const AttendArgs& a, size_t at, int d, float4& v, float& m, float& l) {
     auto join = [&](const float4& h, const float4& x) {
         const float high = fmaxf(m, h.x);
         const float f0 = m == -INFINITY ? 0.f : ex2(m - high), f = h.x == -INFINITY ? 0.f : ex2(h.x - high);
@@ -275,7 +281,6 @@ __device__ __forceinline__ void add_common(const KvDev& c, const AttendArgs& a, 
         l = fmaf(f0, l, f * h.y);
         v.x = fmaf(f0, v.x, f * x.x), v.y = fmaf(f0, v.y, f * x.y), v.z = fmaf(f0, v.z, f * x.z), v.w = fmaf(f0, v.w, f * x.w);
     };
-    m -= kOffset;
     const float4 h = __ldcg(a.parts.head + at);
     join(h, __ldcg(reinterpret_cast<const float4*>(a.parts.o + at * D + d)));
     const int more = __float_as_int(h.w) & 0xffff;
@@ -308,8 +313,12 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, i = lane & 3;
     const int group = c.hq / c.hkv;
 
-    griddep_wait();    // the batch's arrays, and the last call's records
+    // The batch's arrays, and the last call's records. (Behind launch_shared's kernel
+    // they are there from the start, since that one has waited for them before it let
+    // this one begin: its own records are waited for at the end.)
+    if (!kShared) griddep_wait();
     griddep_launch();  // k_join may be set up meanwhile
+    const auto leave = [&]() { if (kShared) griddep_wait(); };
     // --- this CTA's run of units [lo, hi), and the sequence that lo falls in.
     // CTA x takes base units, the first `extra` CTAs one more.
     int total = 0, ctas = 0, base = 0, extra = 0, lo = 0, hi = 0, seq = -1, prefix = 0;
@@ -341,7 +350,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             if (lane >= off) upto += v;
         }
         total = __shfl_sync(0xffffffffu, upto, 31);
-        if (!share()) return;
+        if (!share()) { leave(); return; }
         const unsigned hit = __ballot_sync(0xffffffffu, lo < upto);
         const int l = __ffs(hit) - 1;
         seq = l * per;
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         int mine = 0, incl, sum, below = 0;
         for (int s = tid; s < b.B; s += kAttThreads) mine += seq_work<NT, kShared>(c, b, a, group, s).work;
         block_scan(mine, incl, total);
-        if (!share()) return;
+        if (!share()) { leave(); return; }
         for (int s0 = 0; s0 < b.B; s0 += kAttThreads) {
             const int s = s0 + tid, w = s < b.B ? seq_work<NT, kShared>(c, b, a, group, s).work : 0;
             block_scan(w, incl, sum);
@@ -434,6 +443,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         piece_at(p, lo, hi);
         if (p.u1 == p.u0) {  // a run of idle units only
             if (tid == 0) a.split[blockIdx.x].pieces = 0;
+            leave();
             return;
         }
         load_q(p);
@@ -938,12 +948,19 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 v.x = fmaf(fu, x.x, v.x), v.y = fmaf(fu, x.y, v.y), v.z = fmaf(fu, x.z, v.z), v.w = fmaf(fu, x.w, v.w);
             }
             if (whole) {
-                if (kShared && p.s.from) add_common<D>(c, a, p.s.t0, p.head, p.tile * kRows + r, d, v, mm, ll);
-                put_row<D>(c, a, p.s.t0, p.head, p.tile * kRows + r, d, v, mm, ll);
+                const bool join = kShared && p.s.from;  // k_join does, with the common positions' sum
+                if (kShared) {
+                    const size_t at = row_place(c, a, p.s.t0, p.head, p.tile * kRows + r);
+                    if (join) __stcg(reinterpret_cast<float4*>(a.parts.rest_o + at * D + d), v);
+                    if (d == 0) __stcg(a.parts.rest_head + at, make_float4(mm - kOffset, ll, __int_as_float(join ? 1 : 0), 0.f));
+                }
+                if (!join) put_row<D>(c, a, p.s.t0, p.head, p.tile * kRows + r, d, v, mm, ll);
             } else {
                 __stcg(reinterpret_cast<float4*>(rec + r * D + d), v);
                 if (d == 0) {
                     __stcg(reinterpret_cast<float2*>(rec + 16 * D + 2 * r), make_float2(mm, ll));
+                    if (kShared && p.u0 == 0)  // its pieces are joined as they are
+                        __stcg(a.parts.rest_head + row_place(c, a, p.s.t0, p.head, p.tile * kRows + r), make_float4(0.f, 0.f, 0.f, 0.f));
                 }
             }
         }
@@ -958,6 +975,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         __syncthreads();  // o, m and l are free again
     }
     if (tid == 0 && !split_here) a.split[blockIdx.x].pieces = 0;
+    leave();
 }
 
 // Joins the pieces of split items, as k_attend's CTA of the same number says: a
@@ -968,12 +986,24 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 // 4095 19.8 (20.2, 20.3). One wave of blocks: with four for each CTA, a quarter of
 // the rows each, the last two of these were 26.4 and 20.3 us.
 template <int D, int NT, bool kShared>
-__global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
+__global__ void __launch_bounds__(256) k_join(KvDev c, KvBatch b, AttendArgs a, int splits) {
     constexpr int kLanes = D / 4, kSide = 32 / kLanes;  // lanes of a row's dims; pieces a warp takes side by side
     __shared__ float4 part[8][kSide][kLanes];
     __shared__ float mpart[8][kSide], lpart[8][kSide];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, side = lane / kLanes, d = 4 * (lane % kLanes);
     griddep_wait();
+    if (kShared && (int)blockIdx.x >= splits) {  // rows whose rest is whole
+        const size_t row = ((size_t)(blockIdx.x - splits) * 8 + warp) * kSide + side;
+        const long long t = quotient((long long)row, c.hq);
+        if (t >= a.T || t < b.cu[0] || t >= b.cu[b.B]) return;
+        const float4 h = __ldcg(a.parts.rest_head + row);
+        if (__float_as_int(h.z) != 1) return;
+        float4 v = __ldcg(reinterpret_cast<const float4*>(a.parts.rest_o + row * D + d));
+        float m = h.x, l = h.y;
+        add_common<D>(a, row, d, v, m, l);
+        put_at<D>(a, row, d, v, m, l);
+        return;
+    }
     const int4* at = reinterpret_cast<const int4*>(a.split + blockIdx.x);
     const int4 s0 = __ldcg(at), s1 = __ldcg(at + 1);
     const Split s = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
@@ -1034,7 +1064,10 @@ __global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
             }
         }
         if (set == 0) {
-            if (kShared && s.common) add_common<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
+            if (kShared && s.common) {
+                m -= kOffset;
+                add_common<D>(a, row_place(c, a, s.t0, s.head, s.tile * 8 * NT + r), d, v, m, l);
+            }
             put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
         }
         if (many) break;
@@ -1079,7 +1112,9 @@ static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a,
     });
     if (set != cudaSuccess) return set;
     const cudaError_t e = launch_ex(k_attend<D, NT, kShared>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
-    return e != cudaSuccess ? e : launch_ex(k_join<D, NT, kShared>, dim3(grid), dim3(256), 0, st, true, c, a);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = kShared ? (int64_t)a.T * c.hq : 0, per = 8 * (128 / D);  // rows a block
+    return launch_ex(k_join<D, NT, kShared>, dim3((unsigned)(grid + (rows + per - 1) / per)), dim3(256), 0, st, true, c, b, a, grid);
 }
 
 template <bool kShared>

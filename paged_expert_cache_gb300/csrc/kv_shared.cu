@@ -762,16 +762,18 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
 static uint64_t dense_rows(int T, int hq) { return (uint64_t)T * hq; }
 
 uint64_t shared_bytes(int device, int T, int hq, int D) {
-    return (dense_rows(T, hq) + (uint64_t)sm_count(device) * kSlotRows) * (D * sizeof(float) + sizeof(float4));
+    return (2 * dense_rows(T, hq) + (uint64_t)sm_count(device) * kSlotRows) * (D * sizeof(float) + sizeof(float4));
 }
 
 SharedParts shared_parts(void* workspace, int device, int T, int hq, int D) {
     const uint64_t rows = dense_rows(T, hq), slots = (uint64_t)sm_count(device) * kSlotRows;
     SharedParts p;
     p.o = (float*)workspace;
-    p.slot_o = p.o + rows * D;
+    p.rest_o = p.o + rows * D;
+    p.slot_o = p.rest_o + rows * D;
     p.head = (float4*)(p.slot_o + slots * D);
-    p.slot_head = p.head + rows;
+    p.rest_head = p.head + rows;
+    p.slot_head = p.rest_head + rows;
     p.slots = sm_count(device);
     return p;
 }
