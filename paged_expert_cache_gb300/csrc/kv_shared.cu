@@ -617,24 +617,26 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                     tc_st_wait();
                 }
                 if ((kt + 1) * kTile > lim_warp) hide_scores(ts, lim - kt * kTile);
-                uint32_t s[4][32];
+                // The row's scores are read twice, 32 at a time and the next ones on their
+                // way, in loops that stay short.
+                uint32_t s0[32], s1[32];
                 float mx4[4] = {m, m, m, m};
+                auto most = [&](const uint32_t (&v)[32]) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) tc_ld32(ts + 32 * h, s[h]);
-#pragma unroll
-                for (int b = 0; b < 4; b += 2) {
-#pragma unroll
-                    for (int h = b; h < b + 2; ++h) tc_ld_wait32(s[h]);
-                    if (b == 0) {
-#pragma unroll
-                        for (int h = 2; h < 4; ++h) tc_ld32(ts + 32 * h, s[h]);
-                    }
-#pragma unroll
-                    for (int h = b; h < b + 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
+                    for (int e = 0; e < 32; e += 2)
+                        mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                };
+                tc_ld32(ts, s0);
+#pragma unroll 1
+                for (int h = 0; h < 4; h += 2) {
+                    tc_ld_wait32(s0);
+                    tc_ld32(ts + 32 * h + 32, s1);
+                    most(s0);
+                    tc_ld_wait32(s1);
+                    tc_ld32(ts + (h ? 0 : 64), s0);  // the third quarter, then the first again
+                    most(s1);
                 }
+                tc_ld_wait32(s0);
                 const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
                 const bool raise = (mx - m) * c > kRaise;
                 if (__any_sync(0xffffffffu, raise)) {
@@ -656,23 +658,30 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 const float mc = m == -INFINITY ? 0.f : fmaf(m, c, -kBelow);
                 const unsigned long long c2 = pair2(c, c), mc2 = pair2(-mc, -mc);
                 unsigned long long sum[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                auto weights = [&](const uint32_t (&v)[32], int h) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const unsigned long long y =
-                            fma2(pair2(__uint_as_float(s[h][2 * e]), __uint_as_float(s[h][2 * e + 1])), c2, mc2);
+                            fma2(pair2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c2, mc2);
                         const float e0 = ex2f(lo2(y)), e1 = ex2f(hi2(y));
                         sum[e & 3] = add2(sum[e & 3], pair2(e0, e1));
                         w[e] = h2_as_u32(__floats2half2_rn(e0, e1));
                     }
                     tc_st16(ts + 16 * h, w);
-                    if (h & 1) {  // the products with the first 64 keys begin while the other weights are computed
-                        tc_st_wait();
-                        tc_fence_before();
-                        bar_arrive(gsmem(&sm.p_full[x][h >> 1]));
-                    }
+                };
+#pragma unroll 1
+                for (int h = 0; h < 4; h += 2) {
+                    if (h) tc_ld_wait32(s0);
+                    tc_ld32(ts + 32 * h + 32, s1);
+                    weights(s0, h);
+                    tc_ld_wait32(s1);
+                    if (h == 0) tc_ld32(ts + 64, s0);
+                    weights(s1, h + 1);
+                    // the products with the first 64 keys begin while the other weights are computed
+                    tc_st_wait();
+                    tc_fence_before();
+                    bar_arrive(gsmem(&sm.p_full[x][h >> 1]));
                 }
                 sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
                 l += lo2(sum[0]) + hi2(sum[0]);

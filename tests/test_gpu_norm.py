@@ -92,6 +92,33 @@ def test_a_norm_alone(T, H):
     check(None, out, reference(a["x"], None, None, None, None, 1.0, 1e-6), B)
 
 
+@pytest.mark.parametrize("xt,yt,wt", [(B, F, F), (F, B, B), (B, B, F), (F, F, B)])
+@pytest.mark.parametrize("post,gate", [(True, "channel"), (False, "token"), (True, None)])
+@pytest.mark.parametrize("H,offset,pad", [(264, 0, 0), (512, 8, 8), (261, 0, 0), (1000, 1, 2), (2047, 3, 0), (4095, 0, 1), (4096, 1, 7),
+                                          (4096, 0, 0)])
+def test_many_rows(xt, yt, wt, post, gate, H, offset, pad):
+    # CTAs that take several rows each, whole vectors or not, all tensors with their own offset
+    T = 1500
+    a = make(T, H, xt, yt, wt, post, gate, seed=H + offset)
+
+    def inside(t, shift):
+        w = torch.full((T, H + offset + pad), 77.0, dtype=t.dtype, device="cuda")
+        at = offset if shift else 0
+        w[:, at:at + H] = t
+        return w, w[:, at:at + H]
+
+    (xw, x), (yw, y) = inside(a["x"], True), inside(a["y"], False)
+    (ow, out), (xow, xo) = inside(torch.zeros(T, H, dtype=B, device="cuda"), True), inside(torch.zeros_like(a["x"]), False)
+    pec.residual_norm(x, y, out, weight=a["weight"], post_weight=a["post"], gate=a["gate"], scale=0.5, x_out=xo)
+    ref = reference(a["x"], a["y"], a["weight"], a["post"], a["gate"], 0.5, 1e-6)
+    check(xo, out, ref, xt)
+    assert (ow[:, :offset] == 77).all() and (ow[:, offset + H:] == 77).all() and (xow[:, H:] == 77).all()
+    pec.residual_norm(x, y, weight=a["weight"], post_weight=a["post"], gate=a["gate"], scale=0.5)  # in place, without out
+    assert torch.equal(x, xo) and (xw[:, :offset] == 77).all() and (xw[:, offset + H:] == 77).all()
+    pec.residual_norm(x, out=out, weight=a["weight"])
+    check(None, out, reference(x, None, a["weight"], None, None, 1.0, 1e-6), xt)
+
+
 @pytest.mark.parametrize("offset,pad", [(0, 0), (8, 16), (1, 3), (0, 1), (4, 4)])
 def test_rows_of_wider_tensors(offset, pad):
     T, H = 9, 264
