@@ -40,7 +40,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // 8 where the device has no place for 16
 constexpr int kMassBits = 43;                 // of weight 1: 2^20 tokens stay below 2^63
 constexpr int kMaxVocab = 1 << 20;
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // of -inf: the keys of numbers are above it
@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         }
         if (rank == 0 && sum <= kList) {
             if (from >= 0) sm.list[tid] = cluster.map_shared_rank(&sm, from)->mine[at];
+            else if (tid == sum) sm.list[tid] = 0;  // the list is read in pairs
             __syncthreads();
         }
         return sum;
@@ -464,7 +465,11 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         const uint64_t mine = tid < count ? sm.list[tid] : 0;
         int above = 0;
         if (warp * 32 < count)
-            for (int e = 0; e < count; ++e) above += sm.list[e] > mine;
+#pragma unroll 8
+            for (int e = 0; e < count; e += 2) {
+                const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(sm.list + e);
+                above += (two.x > mine) + (two.y > mine);
+            }
         if (tid < count) sm.ranked[above] = mine;
         __syncthreads();
         Ranked r;
@@ -513,6 +518,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     struct Place {
         uint32_t key;
         uint64_t before, j;
+        unsigned same;  // tokens of the key
     };
     auto shift_of = [](uint32_t klo, uint32_t khi) {
         int s = 0;
@@ -535,16 +541,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
                         a.tokens[row] = (int)~(uint32_t)r.token;
                         if (a.logprobs) a.logprobs[row] = logprob_of(key, draw);
                     } else {
-                        int j = 0;  // tokens of its key before it
+                        int j = 0, to = tid + 1;  // tokens of its key before it, and their end
                         while (j < tid && (uint32_t)(sm.ranked[tid - 1 - j] >> 32) == key) ++j;
-                        const SampleNote note = {bin.before + r.before - j * r.weight, key, (uint32_t)j, 0, 0};
+                        while (to < count && (uint32_t)(sm.ranked[to] >> 32) == key) ++to;
+                        const SampleNote note = {bin.before + r.before - j * r.weight, key, (uint32_t)j, (uint32_t)(to - tid + j), 0};
                         for (int q = 0; q < C; ++q) cluster.map_shared_rank(&sm, q)->found = note;
                     }
                 }
             }
             done = draw != 0;
             if (!done) cluster.sync();
-            return {sm.found.a, sm.found.mass, sm.found.b};
+            return {sm.found.a, sm.found.mass, sm.found.b, sm.found.c};
         }
         const float vlo = value_of(klo), vhi = value_of(khi);
         float least = INFINITY, most = -INFINITY;
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         for (int w = 0; w < kSampleWarps; ++w) khi = max(khi, sm.wa[w]), klo = min(klo, sm.wb[w]);
         const SampleNote* all = tell({0, khi, klo, 0, 0});
         for (int r = 0; r < C; ++r) khi = max(khi, all[r].a), klo = min(klo, all[r].b);
-        uint64_t before = bin.before;
+        uint64_t before = bin.before, upto = bin.upto;
         while (klo < khi) {
             fresh = false;
             const int shift = shift_of(klo, khi);
@@ -568,44 +575,41 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
                 return key >= klo && key <= khi ? (int)((khi - key) >> shift) : -1;
             }, by_count, true);
             const Bin b = find_bin([&](uint64_t) { return point - before; });
+            upto = before + b.upto;
             before += b.before;
             khi -= (uint32_t)b.bin << shift;
             const uint32_t width = (1u << shift) - 1u;
             klo = khi - klo > width ? khi - width : klo;
         }
-        return {khi, before, (point - before) / (by_count ? 1 : weight_of(khi))};
+        const uint64_t w = by_count ? 1 : weight_of(khi);
+        return {khi, before, (point - before) / w, (unsigned)((upto - before) / w)};
     };
-    // the mass of the tokens of keys above `from`, and of that key's first j
-    auto mass_from = [&](uint32_t from, uint64_t j) {
-        uint64_t mine = 0, same = 0;
+    // the mass of the tokens of keys from `from` on
+    auto mass_from = [&](uint32_t from) {
+        uint64_t mine = 0;
         const float bound = value_of(from);
         each([&](float v, int) {
             if (!__any_sync(0xffffffffu, v >= bound)) return;
             const uint64_t w = weigh(v);
-            if (v > bound) mine += w;
-            else if (v == bound) ++same;
+            if (v >= bound) mine += w;
         });
-        for (int off = 16; off; off >>= 1) {
-            mine += __shfl_xor_sync(0xffffffffu, mine, off);
-            same += __shfl_xor_sync(0xffffffffu, same, off);
-        }
+        for (int off = 16; off; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
         __syncthreads();
-        if (lane == 0) sm.wmass[warp] = mine, sm.wsame[warp] = same;
+        if (lane == 0) sm.wmass[warp] = mine;
         __syncthreads();
-        mine = same = 0;
-        for (int w = 0; w < kSampleWarps; ++w) mine += sm.wmass[w], same += sm.wsame[w];
-        const SampleNote* all = tell({mine, (uint32_t)same, 0, 0, 0});
-        mine = same = 0;
-        for (int r = 0; r < C; ++r) mine += all[r].mass, same += all[r].a;
-        return mine + min(same, j) * weight_of(from);
+        mine = 0;
+        for (int w = 0; w < kSampleWarps; ++w) mine += sm.wmass[w];
+        const SampleNote* all = tell({mine, 0, 0, 0, 0});
+        mine = 0;
+        for (int r = 0; r < C; ++r) mine += all[r].mass;
+        return mine;
     };
 
-    constexpr uint64_t kAll = 0xffffffffull;
     constexpr int kNoCut = 0x7fffffff;
     bool done = false;
     // --- top-k: the last key kept, and how many of its tokens
     uint32_t k_keep = kmin;
-    uint64_t j_keep = kAll;
+    uint64_t spare = 0;  // tokens of that key that are not
     bool cut = false;
     if (top_k > 0 && top_k < a.vocab) {
         histogram([&](float v) { return v > -INFINITY ? bin_of_value(v) : -1; }, true, false);
@@ -617,7 +621,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         if (b.bin >= 0) {
             const Place p = place_in(b, kmin, (uint64_t)(top_k - 1), true, 0, done);
             k_keep = p.key;
-            j_keep = p.j + 1;
+            spare = p.same - (p.j + 1);
             cut = true;
         }
     }
@@ -638,12 +642,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         fresh = true;
     };
     masses();
-    uint64_t mass = cut ? mass_from(k_keep, j_keep) : 0;  // 0: all of the histogram's
+    const uint64_t beyond = cut ? spare * weight_of(k_keep) : 0;  // the histogram's, not kept
+    uint64_t mass = 0;                                            // 0: all of the histogram's but that
     if (some_p) {
         // the tokens with less than p of the mass before them, the first one among them
         uint64_t last = 0;
         const Bin b = find_bin([&](uint64_t total) {
-            if (!cut) mass = total;
+            mass = total - beyond;
             return last = top_p > 0.f ? max(part_of(mass, top_p, true), (uint64_t)1) - 1 : 0;
         });
         if ((b.before >> kMassBits) < (uint64_t)kList) {  // at least so many tokens come before the bin
@@ -664,13 +669,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     }
     if (some_min && k_least > k_keep) {
         k_keep = k_least;
-        mass = mass_from(k_keep, kAll);
+        mass = mass_from(k_keep);
     }
     // --- the draw
     if (!fresh) masses();
     uint64_t point = 0;
     const Bin b = find_bin([&](uint64_t total) {
-        if (mass == 0) mass = total;
+        if (mass == 0) mass = total - beyond;
         return point = min(part_of(mass, fminf(fmaxf(u, 0.f), 1.f), false), mass - 1);
     });
     const Place p = place_in(b, from, point, false, mass, done);
@@ -680,35 +685,57 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
 
 template <class T>
 static cudaError_t launch_sample(SampleArgs a, int dev, cudaStream_t st) {
-    // A row's CTAs: enough that its slices fit in shared memory with two CTAs on an SM, more where there are
-    // few rows.
-    const int sms = sm_count(dev);
-    int C = 1;
-    auto slice_of = [&](int c) { return ((a.vocab + c - 1) / c + 7) / 8 * 8; };
     constexpr int kHeldBytes = 68 * 1024;
-    while (C < kMaxCluster && ((size_t)slice_of(C) * sizeof(T) > kHeldBytes || ((int64_t)a.rows * C < 2 * sms && slice_of(C) > 2048))) C *= 2;
-    a.slice = slice_of(C);
-    a.held = (int)std::min<int64_t>(a.slice, kHeldBytes / sizeof(T));
-    const size_t bytes = sizeof(SampleSmem) + kBins / C * sizeof(uint64_t) + (size_t)a.held * sizeof(T);
     static DeviceOnce once;
     const cudaError_t set = once.run(dev, [] {
+        const cudaError_t e = cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
         return cudaFuncSetAttribute(k_sample<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)(sizeof(SampleSmem) + kBins * sizeof(uint64_t)) + kHeldBytes);
     });
     if (set != cudaSuccess) return set;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.rows * C));
     cfg.blockDim = dim3(kSampleThreads);
-    cfg.dynamicSmemBytes = bytes;
     cfg.stream = st;
+    // A row's CTAs: enough that its slices fit in shared memory with two CTAs on an SM, and more as far as all
+    // rows' run at once (61 rows of 50021: 4 CTAs a row 61 us, 8 in two rounds 67). 16 for up to four rows (one
+    // of 131072: 14.8 us, 8 CTAs 15.6; without filters 18.5 and 22.4).
+    const int sms = sm_count(dev);
+    int C = 1;
+    auto slice_of = [&](int c) { return ((a.vocab + c - 1) / c + 7) / 8 * 8; };
+    while (C < 8 && (size_t)slice_of(C) * sizeof(T) > kHeldBytes) C *= 2;
+    while (C < 8 && (int64_t)a.rows * 2 * C <= 2 * sms && slice_of(C) > 2048) C *= 2;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)C;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    auto split = [&](int c) {
+        C = c;
+        a.slice = slice_of(C);
+        a.held = (int)std::min<int64_t>(a.slice, kHeldBytes / sizeof(T));
+        cfg.gridDim = dim3((unsigned)(a.rows * C));
+        cfg.dynamicSmemBytes = sizeof(SampleSmem) + kBins / C * sizeof(uint64_t) + (size_t)a.held * sizeof(T);
+        attr[1].val.clusterDim.x = (unsigned)C;
+    };
+    if (C == 8 && a.rows <= 4 && slice_of(C) > 2048) {
+        static std::atomic<int> most[kMaxDevices] = {};  // clusters of 16 that fit the device, + 1
+        int known = dev < kMaxDevices ? most[dev].load(std::memory_order_relaxed) : 0;
+        if (!known) {
+            split(16);
+            cfg.dynamicSmemBytes = sizeof(SampleSmem) + kBins / C * sizeof(uint64_t) + kHeldBytes;
+            if (cudaOccupancyMaxActiveClusters(&known, k_sample<T>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                known = 0;
+            }
+            ++known;
+            if (dev < kMaxDevices) most[dev].store(known, std::memory_order_relaxed);
+        }
+        C = known > 4 ? 16 : 8;
+    }
+    split(C);
     return cudaLaunchKernelEx(&cfg, k_sample<T>, a);
 }
 
