@@ -90,10 +90,19 @@ struct AttendArgs {
     float scale;
     uint16_t* out;
     FastDiv group_div;
-    KvGroups groups;      // where they are given, with what launch_shared left of their rows
-    SharedParts parts;
     float* partial;       // [grid][2] records: first and last piece of each CTA
     struct Split* split;  // [grid] the item that starts in a CTA and ends in another
+};
+
+// Where groups are given (kShared): them, what launch_shared leaves of their rows, and
+// the blocks of k_join that join split items.
+template <bool kShared>
+struct Rest {};
+template <>
+struct Rest<true> {
+    KvGroups groups;
+    SharedParts parts;
+    int splits;
 };
 
 // What a CTA leaves for the kernel that joins the pieces of an item: the last
@@ -143,23 +152,31 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // after the sequence's last one, which sits at kv - 1, whether the call has all
 // of the rows (t0 to t0 + n - 1) or not. from: the first cell that is not its
 // group's in common (kShared); the others are counted from there.
+template <bool kShared>
 struct SeqWork {
-    int t0, n, end, kv, cells, units, tiles, work, from;
+    int t0, n, end, kv, cells, units, tiles, work;
 };
+template <>
+struct SeqWork<true> : SeqWork<false> {
+    int from;
+};
+template <bool kShared>
+__device__ __forceinline__ int from_of(const SeqWork<kShared>& s) {
+    if constexpr (kShared) return s.from;
+    return 0;
+}
 template <int NT, bool kShared>
-__device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, const AttendArgs& a, int group, int seq) {
-    const int T = a.T;
-    SeqWork s;
+__device__ __forceinline__ SeqWork<kShared> seq_work(const KvDev& c, const KvBatch& b, const Rest<kShared>& rest, int T, int group, int seq) {
+    SeqWork<kShared> s;
     s.t0 = min(max(b.cu[seq], 0), T);
     s.end = b.cu[seq + 1];
     s.n = max(min(max(s.end, 0), T) - s.t0, 0);
     s.kv = b.kv_lens[seq];
     const long long cap = (long long)b.table_stride * c.page_tokens + 1;
     s.cells = (int)((unsigned)((int)min((long long)max(s.kv, 0), cap) + kCellTokens - 1) / kCellTokens);
-    s.from = 0;
     if constexpr (kShared) {
-        const int g = group_of_seq(a.groups, seq);
-        if (g >= 0) s.from = common_tokens(c, b, a.groups, g) / kCellTokens;
+        const int g = group_of_seq(rest.groups, seq);
+        s.from = g >= 0 ? common_tokens(c, b, rest.groups, g) / kCellTokens : 0;
         s.cells = max(s.cells - s.from, 0);
     }
     s.units = max(1, (s.cells + kWarps - 1) / kWarps);
@@ -170,14 +187,16 @@ __device__ __forceinline__ SeqWork seq_work(const KvDev& c, const KvBatch& b, co
 
 // A piece of an item: units [u0, u1) of (sequence, head, row tile); none (u0 ==
 // u1) where the run ends in the item's idle units.
+template <bool kShared>
 struct Piece {
     int seq, head, tile, u0, u1;
-    SeqWork s;
+    SeqWork<kShared> s;
     int first, next, prefix;  // numbers of the item's first unit, of the one after the piece, of the sequence's first
 };
 
 // The piece that starts at number x (x in seq's range), cut at `hi`.
-__device__ __forceinline__ void piece_at(Piece& p, int x, int hi) {
+template <bool kShared>
+__device__ __forceinline__ void piece_at(Piece<kShared>& p, int x, int hi) {
     const int len = p.s.units + kBegin;
     const unsigned off = x - p.prefix, item = off / (unsigned)len;
     const int in = (int)(off - item * len), to = min(len, in + (hi - x));
@@ -190,8 +209,9 @@ __device__ __forceinline__ void piece_at(Piece& p, int x, int hi) {
 }
 // Steps to the next piece; false at `hi`. Whole warps.
 template <int NT, bool kShared>
-__device__ __forceinline__ bool next_piece(Piece& p, int hi, const KvDev& c, const KvBatch& b, const AttendArgs& a, int group, int lane) {
-    const int x = p.next, T = a.T;
+__device__ __forceinline__ bool next_piece(Piece<kShared>& p, int hi, const KvDev& c, const KvBatch& b, const Rest<kShared>& rest, int T, int group,
+                                           int lane) {
+    const int x = p.next;
     if (x >= hi) return false;
     if (x >= p.prefix + p.s.work) {
         p.prefix += p.s.work;
@@ -204,26 +224,27 @@ __device__ __forceinline__ bool next_piece(Piece& p, int hi, const KvDev& c, con
             if (s + 32 >= b.B) return false;
         }
         p.seq = s;
-        p.s = seq_work<NT, kShared>(c, b, a, group, s);
+        p.s = seq_work<NT, kShared>(c, b, rest, T, group, s);
     }
     piece_at(p, x, hi);
     return true;
 }
 
 // Cells of the piece that fall to warp w: (u0 + k) * kWarps + w, k below this.
-__device__ __forceinline__ int warp_cells(const Piece& p, int w) {
+template <bool kShared>
+__device__ __forceinline__ int warp_cells(const Piece<kShared>& p, int w) {
     const int last = (p.s.cells - w + kWarps - 1) / kWarps;  // units in which the warp has a cell (cells >= 0)
     return max(0, min(p.u1, last) - p.u0);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kShared>
 struct AttSmem {
     static constexpr int kRows = 8 * NT, kPad = D + 4;
     alignas(128) uint8_t ring[kWarps][kStages][Cell<D>::kBytes];
     float o[kWarps][kRows][kPad];    // the warps' outputs
     float m[kWarps][kRows], l[kWarps][kRows];
     int wsum[kWarps];
-    Piece cur[kWarps], ask[kWarps];  // a warp's piece at work and the one it asks for: rarely read, so not in registers
+    Piece<kShared> cur[kWarps], ask[kWarps];  // a warp's piece at work and the one it asks for: rarely read, so not in registers
     int prefix, seq;
 };
 
@@ -270,10 +291,11 @@ __device__ __forceinline__ void put_row(const KvDev& c, const AttendArgs& a, int
     put_at<D>(a, row_place(c, a, t0, head, row), d, v, m, l);
 }
 
-// Adds what launch_shared left of a row to four dims of its sum, whose weights refer
-// to the exponent m (-inf: no weight but 0).
+// Adds what launch_shared left of a row (its head and four dims, and the slots that
+// they name) to four dims of its sum, whose weights refer to the exponent m (-inf: no
+// weight but 0).
 template <int D>
-__device__ __forceinline__ void add_common(const AttendArgs& a, size_t at, int d, float4& v, float& m, float& l) {
+__device__ __forceinline__ void add_common(const SharedParts& parts, const float4& h, const float4& x, int d, float4& v, float& m, float& l) {
     auto join = [&](const float4& h, const float4& x) {
         const float high = fmaxf(m, h.x);
         const float f0 = m == -INFINITY ? 0.f : ex2(m - high), f = h.x == -INFINITY ? 0.f : ex2(h.x - high);
@@ -281,35 +303,35 @@ __device__ __forceinline__ void add_common(const AttendArgs& a, size_t at, int d
         l = fmaf(f0, l, f * h.y);
         v.x = fmaf(f0, v.x, f * x.x), v.y = fmaf(f0, v.y, f * x.y), v.z = fmaf(f0, v.z, f * x.z), v.w = fmaf(f0, v.w, f * x.w);
     };
-    const float4 h = __ldcg(a.parts.head + at);
-    join(h, __ldcg(reinterpret_cast<const float4*>(a.parts.o + at * D + d)));
+    join(h, x);
     const int more = __float_as_int(h.w) & 0xffff;
     // a row that the groups do not cover (a batch whose arrays contradict each other) has a head of anything
-    if ((unsigned)__float_as_int(h.z) > (unsigned)a.parts.slots || more > a.parts.slots - __float_as_int(h.z)) {
+    if ((unsigned)__float_as_int(h.z) > (unsigned)parts.slots || more > parts.slots - __float_as_int(h.z)) {
         l = __int_as_float(0x7fc00000);
         return;
     }
     const size_t slot = (size_t)__float_as_int(h.z) * kSlotRows + (__float_as_int(h.w) >> 16 & (kSlotRows - 1));
-    for (int e = 0; e < more; e += 4) {
-        float4 hs[4], xs[4];
+    constexpr int kAhead = 4;
+    for (int e = 0; e < more; e += kAhead) {
+        float4 hs[kAhead], xs[kAhead];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kAhead; ++k) {
             const size_t s = slot + (size_t)min(e + k, more - 1) * kSlotRows;
-            hs[k] = __ldcg(a.parts.slot_head + s);
-            xs[k] = __ldcg(reinterpret_cast<const float4*>(a.parts.slot_o + s * D + d));
+            hs[k] = __ldcg(parts.slot_head + s);
+            xs[k] = __ldcg(reinterpret_cast<const float4*>(parts.slot_o + s * D + d));
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kAhead; ++k)
             if (e + k < more) join(hs[k], xs[k]);
     }
 }
 
 template <int D, int NT, bool kShared>
-__global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a) {
+__global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a, Rest<kShared> rest) {
     constexpr int G = D / 32, kRows = 8 * NT;
     using C = Cell<D>;
     extern __shared__ uint8_t raw[];
-    AttSmem<D, NT>& sm = *reinterpret_cast<AttSmem<D, NT>*>(raw);
+    AttSmem<D, NT, kShared>& sm = *reinterpret_cast<AttSmem<D, NT, kShared>*>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, i = lane & 3;
     const int group = c.hq / c.hkv;
 
@@ -342,7 +364,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         // every warp by itself: a lane takes a few neighbouring sequences
         const int per = (b.B + 31) / 32, s0 = min(lane * per, b.B), s1 = min(s0 + per, b.B);
         int mine = 0;
-        for (int s = s0; s < s1; ++s) mine += seq_work<NT, kShared>(c, b, a, group, s).work;
+        for (int s = s0; s < s1; ++s) mine += seq_work<NT, kShared>(c, b, rest, a.T, group, s).work;
         int upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -357,7 +379,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         prefix = __shfl_sync(0xffffffffu, upto - mine, l);
         if (per > 1)
             for (;; ++seq) {
-                const int w = seq_work<NT, kShared>(c, b, a, group, seq).work;
+                const int w = seq_work<NT, kShared>(c, b, rest, a.T, group, seq).work;
                 if (lo < prefix + w) break;
                 prefix += w;
             }
@@ -382,11 +404,11 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             __syncthreads();
         };
         int mine = 0, incl, sum, below = 0;
-        for (int s = tid; s < b.B; s += kAttThreads) mine += seq_work<NT, kShared>(c, b, a, group, s).work;
+        for (int s = tid; s < b.B; s += kAttThreads) mine += seq_work<NT, kShared>(c, b, rest, a.T, group, s).work;
         block_scan(mine, incl, total);
         if (!share()) { leave(); return; }
         for (int s0 = 0; s0 < b.B; s0 += kAttThreads) {
-            const int s = s0 + tid, w = s < b.B ? seq_work<NT, kShared>(c, b, a, group, s).work : 0;
+            const int s = s0 + tid, w = s < b.B ? seq_work<NT, kShared>(c, b, rest, a.T, group, s).work : 0;
             block_scan(w, incl, sum);
             incl += below;
             if (incl - w <= lo && lo < incl) {
@@ -402,27 +424,27 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
     }
 
     // --- the warp's ring: sm.ask is the piece being asked for, sm.cur the one at work
-    auto keep_piece = [&](Piece& to, const Piece& from) {
+    auto keep_piece = [&](Piece<kShared>& to, const Piece<kShared>& from) {
         __syncwarp();
         if (lane == 0) to = from;
         __syncwarp();
     };
     // steps a kept piece on; false (and the piece as it was) at the end of the run, an item's idle units among it
-    auto step = [&](Piece& at) {
+    auto step = [&](Piece<kShared>& at) {
         Piece p = at;
-        const bool there = next_piece<NT, kShared>(p, hi, c, b, a, group, lane) && p.u1 > p.u0;
+        const bool there = next_piece<NT, kShared>(p, hi, c, b, rest, a.T, group, lane) && p.u1 > p.u0;
         if (there) keep_piece(at, p);
         return there;
     };
     // row r of a piece's tile: new token and query head
-    auto token_head = [&](const Piece& p, int r, int& tok, int& head) {
+    auto token_head = [&](const Piece<kShared>& p, int r, int& tok, int& head) {
         const int row = p.tile * kRows + r;
         tok = a.group_div.div(row);
         head = p.head * group + row - tok * group;
     };
-    auto rows_of = [&](const Piece& p) { return min(kRows, p.s.n * group - p.tile * kRows); };
+    auto rows_of = [&](const Piece<kShared>& p) { return min(kRows, p.s.n * group - p.tile * kRows); };
     uint4 u[NT][G];  // this lane's part of q: row 8 nt + g, dims 32 bl + 8 i ..
-    auto load_q = [&](const Piece& p) {
+    auto load_q = [&](const Piece<kShared>& p) {
         const int rows = rows_of(p);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -436,10 +458,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
     };
     int ask_n, ask_k = 0;
     {
-        Piece p;
+        Piece<kShared> p;
         p.seq = seq;
         p.prefix = prefix;
-        p.s = seq_work<NT, kShared>(c, b, a, group, seq);
+        p.s = seq_work<NT, kShared>(c, b, rest, a.T, group, seq);
         piece_at(p, lo, hi);
         if (p.u1 == p.u0) {  // a run of idle units only
             if (tid == 0) a.split[blockIdx.x].pieces = 0;
@@ -486,7 +508,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 ask_n = more ? warp_cells(sm.ask[warp], warp) : 0;
                 ask_k = 0;
                 if (more && warp == 0) {  // the next piece's q on its way to L2
-                    const Piece& p = sm.ask[0];
+                    const Piece<kShared>& p = sm.ask[0];
                     const int r = lane / (D / 64);
                     if (r < rows_of(p)) {
                         int tok, head;
@@ -499,8 +521,8 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             if (!more) break;
             if ((ask_k & 31) == 0) {  // the next 32 cells' places
                 const int k = ask_k + lane;
-                const Piece& q = sm.ask[warp];
-                addr = k < ask_n ? kv_cell<D>(c, b, q.seq, (kShared ? q.s.from : 0) + (q.u0 + k) * kWarps + warp, q.head) : nullptr;
+                const Piece<kShared>& q = sm.ask[warp];
+                addr = k < ask_n ? kv_cell<D>(c, b, q.seq, from_of(q.s) + (q.u0 + k) * kWarps + warp, q.head) : nullptr;
             }
             copy_cell(ask_k & 31, issued % kStages);
             ++issued;
@@ -517,7 +539,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             if (!step(sm.cur[warp])) break;
             load_q(sm.cur[warp]);
         }
-        const Piece& p = sm.cur[warp];
+        const Piece<kShared>& p = sm.cur[warp];
         const int rows = rows_of(p);
         uint32_t qb[NT][G][2][2];        // B registers of the scores, row 8 nt + g: k-step, (b0, b1)
         float corr[NT][G][2];            // -8 sum(q) of rows 2i, 2i + 1, for codes of 2^-24
@@ -579,7 +601,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         unsigned far = 0;            // bit nt G + bl: row 8 nt + g's products in block bl are
         unsigned loud = 0;           // bit nt: row 8 nt + g has seen a scale of 2 or more
 
-        const int cells = warp_cells(p, warp), first = ((kShared ? p.s.from : 0) + p.u0 * kWarps + warp) * kCellTokens;
+        const int cells = warp_cells(p, warp), first = (from_of(p.s) + p.u0 * kWarps + warp) * kCellTokens;
         auto words = [&](uint32_t (&r)[G], const uint8_t* src) {
             if constexpr (G == 4) {
                 const uint4 v = *reinterpret_cast<const uint4*>(src);
@@ -948,19 +970,20 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 v.x = fmaf(fu, x.x, v.x), v.y = fmaf(fu, x.y, v.y), v.z = fmaf(fu, x.z, v.z), v.w = fmaf(fu, x.w, v.w);
             }
             if (whole) {
-                const bool join = kShared && p.s.from;  // k_join does, with the common positions' sum
-                if (kShared) {
+                const bool join = from_of(p.s) != 0;  // k_join does, with the common positions' sum
+                if constexpr (kShared) {
                     const size_t at = row_place(c, a, p.s.t0, p.head, p.tile * kRows + r);
-                    if (join) __stcg(reinterpret_cast<float4*>(a.parts.rest_o + at * D + d), v);
-                    if (d == 0) __stcg(a.parts.rest_head + at, make_float4(mm - kOffset, ll, __int_as_float(join ? 1 : 0), 0.f));
+                    if (join) __stcg(reinterpret_cast<float4*>(rest.parts.rest_o + at * D + d), v);
+                    if (d == 0) __stcg(rest.parts.rest_head + at, make_float4(mm - kOffset, ll, __int_as_float(join ? 1 : 0), 0.f));
                 }
                 if (!join) put_row<D>(c, a, p.s.t0, p.head, p.tile * kRows + r, d, v, mm, ll);
             } else {
                 __stcg(reinterpret_cast<float4*>(rec + r * D + d), v);
                 if (d == 0) {
                     __stcg(reinterpret_cast<float2*>(rec + 16 * D + 2 * r), make_float2(mm, ll));
-                    if (kShared && p.u0 == 0)  // its pieces are joined as they are
-                        __stcg(a.parts.rest_head + row_place(c, a, p.s.t0, p.head, p.tile * kRows + r), make_float4(0.f, 0.f, 0.f, 0.f));
+                    if constexpr (kShared)
+                        if (p.u0 == 0)  // its pieces are joined as they are
+                            __stcg(rest.parts.rest_head + row_place(c, a, p.s.t0, p.head, p.tile * kRows + r), make_float4(0.f, 0.f, 0.f, 0.f));
                 }
             }
         }
@@ -968,7 +991,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
             const int c0 = cta_of(p.first), c1 = cta_of(p.first + p.s.units - 1), row = (int)blockIdx.x - c0;
             const bool many = many_pieces<D>(c1 - c0 + 1, rows);
             if (row < (many ? rows : 1)) {
-                a.split[blockIdx.x] = {c1 - c0 + 1, c0, row, many ? row + 1 : rows, p.s.t0, p.head, p.tile, kShared ? p.s.from : 0};
+                a.split[blockIdx.x] = {c1 - c0 + 1, c0, row, many ? row + 1 : rows, p.s.t0, p.head, p.tile, from_of(p.s)};
                 split_here = true;
             }
         }
@@ -986,23 +1009,27 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 // 4095 19.8 (20.2, 20.3). One wave of blocks: with four for each CTA, a quarter of
 // the rows each, the last two of these were 26.4 and 20.3 us.
 template <int D, int NT, bool kShared>
-__global__ void __launch_bounds__(256) k_join(KvDev c, KvBatch b, AttendArgs a, int splits) {
+__global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a, Rest<kShared> rest, const int* cu, int B) {
     constexpr int kLanes = D / 4, kSide = 32 / kLanes;  // lanes of a row's dims; pieces a warp takes side by side
     __shared__ float4 part[8][kSide][kLanes];
     __shared__ float mpart[8][kSide], lpart[8][kSide];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, side = lane / kLanes, d = 4 * (lane % kLanes);
     griddep_wait();
-    if (kShared && (int)blockIdx.x >= splits) {  // rows whose rest is whole
-        const size_t row = ((size_t)(blockIdx.x - splits) * 8 + warp) * kSide + side;
-        const long long t = quotient((long long)row, c.hq);
-        if (t >= a.T || t < b.cu[0] || t >= b.cu[b.B]) return;
-        const float4 h = __ldcg(a.parts.rest_head + row);
-        if (__float_as_int(h.z) != 1) return;
-        float4 v = __ldcg(reinterpret_cast<const float4*>(a.parts.rest_o + row * D + d));
-        float m = h.x, l = h.y;
-        add_common<D>(a, row, d, v, m, l);
-        put_at<D>(a, row, d, v, m, l);
-        return;
+    if constexpr (kShared) {
+        if ((int)blockIdx.x >= rest.splits) {  // rows whose rest is whole
+            const SharedParts& p = rest.parts;
+            const size_t row = ((size_t)(blockIdx.x - rest.splits) * 8 + warp) * kSide + side;
+            const long long t = quotient((long long)row, c.hq);
+            if (t >= a.T || t < cu[0] || t >= cu[B]) return;
+            const float4 r = __ldcg(p.rest_head + row), h = __ldcg(p.head + row);
+            float4 v = __ldcg(reinterpret_cast<const float4*>(p.rest_o + row * D + d));
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(p.o + row * D + d));
+            if (__float_as_int(r.z) != 1) return;
+            float m = r.x, l = r.y;
+            add_common<D>(p, h, x, d, v, m, l);
+            put_at<D>(a, row, d, v, m, l);
+            return;
+        }
     }
     const int4* at = reinterpret_cast<const int4*>(a.split + blockIdx.x);
     const int4 s0 = __ldcg(at), s1 = __ldcg(at + 1);
@@ -1064,10 +1091,13 @@ __global__ void __launch_bounds__(256) k_join(KvDev c, KvBatch b, AttendArgs a, 
             }
         }
         if (set == 0) {
-            if (kShared && s.common) {
-                m -= kOffset;
-                add_common<D>(a, row_place(c, a, s.t0, s.head, s.tile * 8 * NT + r), d, v, m, l);
-            }
+            if constexpr (kShared)
+                if (s.common) {
+                    const SharedParts& p = rest.parts;
+                    const size_t place = row_place(c, a, s.t0, s.head, s.tile * 8 * NT + r);
+                    m -= kOffset;
+                    add_common<D>(p, __ldcg(p.head + place), __ldcg(reinterpret_cast<const float4*>(p.o + place * D + d)), d, v, m, l);
+                }
             put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
         }
         if (many) break;
@@ -1099,10 +1129,10 @@ uint64_t attend_scratch_bytes(int device) {
 }
 
 template <int D, int NT, bool kShared>
-static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, int dev, int grid, cudaStream_t st) {
+static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a, Rest<kShared> rest, int dev, int grid, cudaStream_t st) {
     static DeviceOnce once;
     const cudaError_t set = once.run(dev, [] {
-        cudaError_t e = cudaFuncSetAttribute(k_attend<D, NT, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT>));
+        cudaError_t e = cudaFuncSetAttribute(k_attend<D, NT, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(AttSmem<D, NT, kShared>));
         // the same division of L1 and shared memory for both: an SM is idle while it changes
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(k_attend<D, NT, kShared>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
@@ -1111,20 +1141,23 @@ static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a,
         return e;
     });
     if (set != cudaSuccess) return set;
-    const cudaError_t e = launch_ex(k_attend<D, NT, kShared>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT>), st, true, c, b, a);
-    if (e != cudaSuccess) return e;
-    const int64_t rows = kShared ? (int64_t)a.T * c.hq : 0, per = 8 * (128 / D);  // rows a block
-    return launch_ex(k_join<D, NT, kShared>, dim3((unsigned)(grid + (rows + per - 1) / per)), dim3(256), 0, st, true, c, b, a, grid);
+    unsigned blocks = grid;  // of k_join
+    if constexpr (kShared) {
+        const int64_t rows = (int64_t)a.T * c.hq, per = 8 * (128 / D);  // of a block
+        rest.splits = grid;
+        blocks += (unsigned)((rows + per - 1) / per);
+    }
+    const cudaError_t e = launch_ex(k_attend<D, NT, kShared>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT, kShared>), st, true, c, b, a, rest);
+    return e != cudaSuccess ? e : launch_ex(k_join<D, NT, kShared>, dim3(blocks), dim3(256), 0, st, true, c, a, rest, b.cu, b.B);
 }
 
 template <bool kShared>
-static cudaError_t launch_form(const KvDev& c, const KvBatch& b, const KvGroups& g, const SharedParts& parts, int D,
-                               const uint16_t* q, int64_t q_stride, int T, float scale, uint16_t* out, void* scratch,
-                               cudaStream_t st) {
+static cudaError_t launch_form(const KvDev& c, const KvBatch& b, const Rest<kShared>& rest, int D, const uint16_t* q,
+                               int64_t q_stride, int T, float scale, uint16_t* out, void* scratch, cudaStream_t st) {
     int dev = 0;
     if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     const int n = max_grid(dev);
-    AttendArgs a = {q, q_stride, T, scale, out, fast_div((uint32_t)(c.hq / c.hkv)), g, parts, (float*)scratch,
+    AttendArgs a = {q, q_stride, T, scale, out, fast_div((uint32_t)(c.hq / c.hkv)), (float*)scratch,
                     (Split*)((uint8_t*)scratch + (size_t)n * 2 * kPartFloats(128) * sizeof(float))};
     // 16 rows at a time where a head has more than 8 in a step (its group times
     // the new tokens of an average sequence), although only half as many warps
@@ -1132,18 +1165,18 @@ static cudaError_t launch_form(const KvDev& c, const KvBatch& b, const KvGroups&
     // rows at a time 26.4. Not at head_dim 64, where a row's part is smaller: 7
     // streams of 5000-54000 tokens 60.2 and 57.8 us.
     const bool wide = D == 128 && (int64_t)(c.hq / c.hkv) * T > 8 * (int64_t)b.B;
-    if (wide) return launch<128, 2, kShared>(c, b, a, dev, (n + 1) / 2, st);
-    return D == 128 ? launch<128, 1, kShared>(c, b, a, dev, n, st) : launch<64, 1, kShared>(c, b, a, dev, n, st);
+    if (wide) return launch<128, 2, kShared>(c, b, a, rest, dev, (n + 1) / 2, st);
+    return D == 128 ? launch<128, 1, kShared>(c, b, a, rest, dev, n, st) : launch<64, 1, kShared>(c, b, a, rest, dev, n, st);
 }
 
 cudaError_t launch_attend(const KvDev& c, const KvBatch& b, int D, const uint16_t* q, int64_t q_stride, int T, float scale,
                           uint16_t* out, void* scratch, cudaStream_t st) {
-    return launch_form<false>(c, b, KvGroups{}, SharedParts{}, D, q, q_stride, T, scale, out, scratch, st);
+    return launch_form<false>(c, b, {}, D, q, q_stride, T, scale, out, scratch, st);
 }
 cudaError_t launch_attend_rest(const KvDev& c, const KvBatch& b, const KvGroups& g, const SharedParts& parts, int D,
                                const uint16_t* q, int64_t q_stride, int T, float scale, uint16_t* out, void* scratch,
                                cudaStream_t st) {
-    return launch_form<true>(c, b, g, parts, D, q, q_stride, T, scale, out, scratch, st);
+    return launch_form<true>(c, b, {g, parts, 0}, D, q, q_stride, T, scale, out, scratch, st);
 }
 
 

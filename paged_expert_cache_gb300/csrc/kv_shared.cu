@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = a.c.hq / a.c.hkv;
 
-    if (warp == 8) {
+    if (warp == 10) {
         tc_alloc(gsmem(&sm.tmem), 512);
         tc_relinquish();
     } else if (warp == 9 && lane == 0) {
@@ -151,6 +151,26 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
     __syncwarp();
     griddep_wait();
     griddep_launch();
+    // the pieces' warp: what the groups ask for, while the others set up
+    int seq, t0, rows, common, work, total = 0;  // of a lane's group; of all
+    auto look = [&](int g) {
+        seq = t0 = rows = common = work = 0;
+        if (g >= a.g.n) return;
+        seq = a.g.cu[g];
+        const int last = min(max(a.g.cu[g + 1], 0), a.b.B);
+        if (seq < 0 || seq >= last) return;
+        t0 = min(max(a.b.cu[seq], 0), a.T);
+        rows = max(min(max(a.b.cu[last], 0), a.T) - t0, 0) * group;
+        common = common_tokens(a.c, a.b, a.g, g);
+        if (rows && common) work = ((common + kTile - 1) / kTile + kPieceStart) * a.c.hkv * ((rows + kRows - 1) / kRows);
+    };
+    if (warp == 8) {
+        for (int g = lane; g - lane < a.g.n; g += 32) {
+            look(g);
+            total += work;
+        }
+        total = __reduce_add_sync(0xffffffffu, total);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -325,24 +345,6 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
         if (warp == 8) {
             // --- the pieces of this CTA's run [lo, hi)
-            int seq, t0, rows, common, work;  // of a lane's group
-            auto look = [&](int g) {
-                seq = t0 = rows = common = work = 0;
-                if (g >= a.g.n) return;
-                seq = a.g.cu[g];
-                const int last = min(max(a.g.cu[g + 1], 0), a.b.B);
-                if (seq < 0 || seq >= last) return;
-                t0 = min(max(a.b.cu[seq], 0), a.T);
-                rows = max(min(max(a.b.cu[last], 0), a.T) - t0, 0) * group;
-                common = common_tokens(a.c, a.b, a.g, g);
-                if (rows && common) work = ((common + kTile - 1) / kTile + kPieceStart) * a.c.hkv * ((rows + kRows - 1) / kRows);
-            };
-            int total = 0;
-            for (int g = lane; g - lane < a.g.n; g += 32) {
-                look(g);
-                total += work;
-            }
-            total = __reduce_add_sync(0xffffffffu, total);
             const int ctas = min(total, (int)gridDim.x), base = ctas ? total / ctas : 0, extra = total - base * ctas;
             auto cta_of = [&](int x) {
                 const int wide = extra * (base + 1);
@@ -646,12 +648,13 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                     l *= f;
                     if (j > 0) {
 #pragma unroll 1
-                        for (int h = 0; h < D / 8; ++h) {
-                            uint32_t o[8];
-                            tc_ld8_wait(to + 8 * h, o);
+                        for (int h = 0; h < D / 32; ++h) {
+                            uint32_t o[32];
+                            tc_ld32(to + 32 * h, o);
+                            tc_ld_wait32(o);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc_st8(to + 8 * h, o);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc_st32(to + 32 * h, o);
                         }
                     }
                 }
@@ -762,7 +765,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 10) {
         tc_fence_after();
         tc_dealloc(tmem, 512);
     }
