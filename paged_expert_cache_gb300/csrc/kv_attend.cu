@@ -95,14 +95,14 @@ struct AttendArgs {
 };
 
 // Where groups are given (kShared): them, what launch_shared leaves of their rows, and
-// the blocks of k_join that join split items.
+// the CTAs of k_attend.
 template <bool kShared>
 struct Rest {};
 template <>
 struct Rest<true> {
     KvGroups groups;
     SharedParts parts;
-    int splits;
+    int ctas;
 };
 
 // What a CTA leaves for the kernel that joins the pieces of an item: the last
@@ -113,7 +113,6 @@ struct alignas(16) Split {
     int pieces;            // 0: none
     int from, row, rows;   // rows `row` to rows - 1
     int t0, head, tile;
-    int common;            // the rows have a sum that has begun
 };
 constexpr int kJoinAhead = 5;  // pieces that a lane of k_join asks for at once
 // Whether a block takes a row instead of a warp. (pieces - 2 CTAs are in the item's
@@ -291,40 +290,10 @@ __device__ __forceinline__ void put_row(const KvDev& c, const AttendArgs& a, int
     put_at<D>(a, row_place(c, a, t0, head, row), d, v, m, l);
 }
 
-// Adds what launch_shared left of a row (its head and four dims, and the slots that
-// they name) to four dims of its sum, whose weights refer to the exponent m (-inf: no
-// weight but 0).
-template <int D>
-__device__ __forceinline__ void add_common(const SharedParts& parts, const float4& h, const float4& x, int d, float4& v, float& m, float& l) {
-    auto join = [&](const float4& h, const float4& x) {
-        const float high = fmaxf(m, h.x);
-        const float f0 = m == -INFINITY ? 0.f : ex2(m - high), f = h.x == -INFINITY ? 0.f : ex2(h.x - high);
-        m = high;
-        l = fmaf(f0, l, f * h.y);
-        v.x = fmaf(f0, v.x, f * x.x), v.y = fmaf(f0, v.y, f * x.y), v.z = fmaf(f0, v.z, f * x.z), v.w = fmaf(f0, v.w, f * x.w);
-    };
-    join(h, x);
-    const int more = __float_as_int(h.w) & 0xffff;
-    // a row that the groups do not cover (a batch whose arrays contradict each other) has a head of anything
-    if ((unsigned)__float_as_int(h.z) > (unsigned)parts.slots || more > parts.slots - __float_as_int(h.z)) {
-        l = __int_as_float(0x7fc00000);
-        return;
-    }
-    const size_t slot = (size_t)__float_as_int(h.z) * kSlotRows + (__float_as_int(h.w) >> 16 & (kSlotRows - 1));
-    constexpr int kAhead = 4;
-    for (int e = 0; e < more; e += kAhead) {
-        float4 hs[kAhead], xs[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const size_t s = slot + (size_t)min(e + k, more - 1) * kSlotRows;
-            hs[k] = __ldcg(parts.slot_head + s);
-            xs[k] = __ldcg(reinterpret_cast<const float4*>(parts.slot_o + s * D + d));
-        }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (e + k < more) join(hs[k], xs[k]);
-    }
-}
+// How a row's rest is left for k_join_rows (bits of the third word of its head).
+constexpr int kWhole = 1;   // as a whole: its exponent and sum are the first two words
+constexpr int kPieces = 2;  // in pieces: the first one's CTA, their number, and (fourth word) its row there
+constexpr int kCommon = 4;  // and with what launch_shared left
 
 template <int D, int NT, bool kShared>
 __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c, KvBatch b, AttendArgs a, Rest<kShared> rest) {
@@ -347,7 +316,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
     auto share = [&]() {
         ctas = min(total, (int)gridDim.x);
         if ((int)blockIdx.x >= ctas) {
-            if (tid == 0) a.split[blockIdx.x].pieces = 0;
+            if (!kShared && tid == 0) a.split[blockIdx.x].pieces = 0;
             return false;
         }
         base = (unsigned)total / (unsigned)ctas;
@@ -464,7 +433,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
         p.s = seq_work<NT, kShared>(c, b, rest, a.T, group, seq);
         piece_at(p, lo, hi);
         if (p.u1 == p.u0) {  // a run of idle units only
-            if (tid == 0) a.split[blockIdx.x].pieces = 0;
+            if (!kShared && tid == 0) a.split[blockIdx.x].pieces = 0;
             leave();
             return;
         }
@@ -970,11 +939,11 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 v.x = fmaf(fu, x.x, v.x), v.y = fmaf(fu, x.y, v.y), v.z = fmaf(fu, x.z, v.z), v.w = fmaf(fu, x.w, v.w);
             }
             if (whole) {
-                const bool join = from_of(p.s) != 0;  // k_join does, with the common positions' sum
+                const bool join = from_of(p.s) != 0;  // with the common positions' sum
                 if constexpr (kShared) {
                     const size_t at = row_place(c, a, p.s.t0, p.head, p.tile * kRows + r);
                     if (join) __stcg(reinterpret_cast<float4*>(rest.parts.rest_o + at * D + d), v);
-                    if (d == 0) __stcg(rest.parts.rest_head + at, make_float4(mm - kOffset, ll, __int_as_float(join ? 1 : 0), 0.f));
+                    if (d == 0) __stcg(rest.parts.rest_head + at, make_float4(mm - kOffset, ll, __int_as_float(join ? kWhole | kCommon : 0), 0.f));
                 }
                 if (!join) put_row<D>(c, a, p.s.t0, p.head, p.tile * kRows + r, d, v, mm, ll);
             } else {
@@ -982,22 +951,26 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
                 if (d == 0) {
                     __stcg(reinterpret_cast<float2*>(rec + 16 * D + 2 * r), make_float2(mm, ll));
                     if constexpr (kShared)
-                        if (p.u0 == 0)  // its pieces are joined as they are
-                            __stcg(rest.parts.rest_head + row_place(c, a, p.s.t0, p.head, p.tile * kRows + r), make_float4(0.f, 0.f, 0.f, 0.f));
+                        if (p.u0 == 0) {
+                            const int c0 = cta_of(p.first), pieces = cta_of(p.first + p.s.units - 1) - c0 + 1;
+                            __stcg(rest.parts.rest_head + row_place(c, a, p.s.t0, p.head, p.tile * kRows + r),
+                                   make_float4(__int_as_float(c0), __int_as_float(pieces),
+                                               __int_as_float(from_of(p.s) ? kPieces | kCommon : kPieces), __int_as_float(r)));
+                        }
                 }
             }
         }
-        if (tid == 0 && p.u1 < p.s.units) {
+        if (!kShared && tid == 0 && p.u1 < p.s.units) {
             const int c0 = cta_of(p.first), c1 = cta_of(p.first + p.s.units - 1), row = (int)blockIdx.x - c0;
             const bool many = many_pieces<D>(c1 - c0 + 1, rows);
             if (row < (many ? rows : 1)) {
-                a.split[blockIdx.x] = {c1 - c0 + 1, c0, row, many ? row + 1 : rows, p.s.t0, p.head, p.tile, from_of(p.s)};
+                a.split[blockIdx.x] = {c1 - c0 + 1, c0, row, many ? row + 1 : rows, p.s.t0, p.head, p.tile};
                 split_here = true;
             }
         }
         __syncthreads();  // o, m and l are free again
     }
-    if (tid == 0 && !split_here) a.split[blockIdx.x].pieces = 0;
+    if (!kShared && tid == 0 && !split_here) a.split[blockIdx.x].pieces = 0;
     leave();
 }
 
@@ -1008,32 +981,16 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 2 : 1) k_attend(KvDev c
 // one of 513 tokens 8.5 us (8.6, 8.9), one of 100003 25.0 (25.4, 24.5), 32 of up to
 // 4095 19.8 (20.2, 20.3). One wave of blocks: with four for each CTA, a quarter of
 // the rows each, the last two of these were 26.4 and 20.3 us.
-template <int D, int NT, bool kShared>
-__global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a, Rest<kShared> rest, const int* cu, int B) {
+template <int D, int NT>
+__global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a) {
     constexpr int kLanes = D / 4, kSide = 32 / kLanes;  // lanes of a row's dims; pieces a warp takes side by side
     __shared__ float4 part[8][kSide][kLanes];
     __shared__ float mpart[8][kSide], lpart[8][kSide];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, side = lane / kLanes, d = 4 * (lane % kLanes);
     griddep_wait();
-    if constexpr (kShared) {
-        if ((int)blockIdx.x >= rest.splits) {  // rows whose rest is whole
-            const SharedParts& p = rest.parts;
-            const size_t row = ((size_t)(blockIdx.x - rest.splits) * 8 + warp) * kSide + side;
-            const long long t = quotient((long long)row, c.hq);
-            if (t >= a.T || t < cu[0] || t >= cu[B]) return;
-            const float4 r = __ldcg(p.rest_head + row), h = __ldcg(p.head + row);
-            float4 v = __ldcg(reinterpret_cast<const float4*>(p.rest_o + row * D + d));
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p.o + row * D + d));
-            if (__float_as_int(r.z) != 1) return;
-            float m = r.x, l = r.y;
-            add_common<D>(p, h, x, d, v, m, l);
-            put_at<D>(a, row, d, v, m, l);
-            return;
-        }
-    }
     const int4* at = reinterpret_cast<const int4*>(a.split + blockIdx.x);
     const int4 s0 = __ldcg(at), s1 = __ldcg(at + 1);
-    const Split s = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    const Split s = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z};
     if (s.pieces == 0) return;
     const bool many = s.row + 1 == s.rows;  // one row: all warps take it (few pieces of a single row as well)
     const float* base = a.partial + (size_t)s.from * 2 * kPartFloats(D);
@@ -1090,19 +1047,87 @@ __global__ void __launch_bounds__(256) k_join(KvDev c, AttendArgs a, Rest<kShare
                 m = high;
             }
         }
-        if (set == 0) {
-            if constexpr (kShared)
-                if (s.common) {
-                    const SharedParts& p = rest.parts;
-                    const size_t place = row_place(c, a, s.t0, s.head, s.tile * 8 * NT + r);
-                    m -= kOffset;
-                    add_common<D>(p, __ldcg(p.head + place), __ldcg(reinterpret_cast<const float4*>(p.o + place * D + d)), d, v, m, l);
-                }
-            put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
-        }
+        if (set == 0) put_row<D>(c, a, s.t0, s.head, s.tile * 8 * NT + r, d, v, m, l);
         if (many) break;
         __syncwarp();  // the sums are free again
     }
+}
+
+// Joins what k_attend and launch_shared left of every row: the rest, whole or in
+// pieces, the common positions' sum and the slots that go on with it. Four warps take
+// a row's parts in turn, four of them on the way at once, and add their sums up in
+// order. (One warp a row, and the pieces of split items by blocks of their own before
+// that: 6 us for 512 rows of 20 slots, 9 for 4096 of 10.)
+template <int D>
+__global__ void __launch_bounds__(256) k_join_rows(KvDev c, AttendArgs a, Rest<true> rest, const int* cu, int B) {
+    constexpr int kLanes = D / 4, kSide = 32 / kLanes;  // lanes of a row's dims; rows a warp takes side by side
+    __shared__ float4 part[8][32];
+    __shared__ float2 sums[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, side = lane / kLanes, d = 4 * (lane % kLanes), turn = warp & 3;
+    const SharedParts& p = rest.parts;
+    const size_t row = ((size_t)blockIdx.x * 2 + (warp >> 2)) * kSide + side;
+    griddep_wait();
+    const long long t = quotient((long long)row, c.hq);
+    const bool there = t < a.T && t >= cu[0] && t < cu[B];
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 r = there ? __ldcg(p.rest_head + row) : none, h = there ? __ldcg(p.head + row) : none;
+    const int kind = __float_as_int(r.z), slots = kind & kCommon ? __float_as_int(h.w) & 0xffff : 0, slot = __float_as_int(h.z);
+    const int pieces = kind & kWhole ? 1 : kind & kPieces ? __float_as_int(r.y) : 0, from = __float_as_int(r.x);
+    // a row that no sequence's work has covered (a batch whose arrays contradict each other) has heads of anything
+    const bool sound = (!(kind & kPieces) || kind & kWhole || ((unsigned)from < (unsigned)rest.ctas && pieces > 0 && pieces <= rest.ctas - from)) &&
+                       (slots == 0 || ((unsigned)slot <= (unsigned)p.slots && slots <= p.slots - slot));
+    const int parts = sound ? pieces + (kind & kCommon ? 1 + slots : 0) : 0;
+    float m = -INFINITY, l = sound ? 0.f : __int_as_float(0x7fc00000);
+    float4 v = none;
+    auto join = [&](float qm, float ql, const float4& x) {
+        const float high = fmaxf(m, qm);
+        const float f0 = m == -INFINITY ? 0.f : ex2(m - high), f = qm == -INFINITY ? 0.f : ex2(qm - high);
+        m = high;
+        l = fmaf(f0, l, f * ql);
+        v.x = fmaf(f0, v.x, f * x.x), v.y = fmaf(f0, v.y, f * x.y), v.z = fmaf(f0, v.z, f * x.z), v.w = fmaf(f0, v.w, f * x.w);
+    };
+    constexpr int kAhead = 4;
+    for (int e = turn; e < parts; e += 4 * kAhead) {
+        float qm[kAhead], ql[kAhead];
+        float4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int q = min(e + 4 * k, parts - 1), after = q - pieces;
+            const float* o;
+            if (q < pieces && !(kind & kWhole)) {
+                const float* rec = a.partial + ((size_t)(from + q) * 2 + (q == 0)) * kPartFloats(D);
+                const int at = __float_as_int(r.w) & 15;
+                const float2 s = __ldcg(reinterpret_cast<const float2*>(rec + 16 * D + 2 * at));
+                qm[k] = s.x - kOffset, ql[k] = s.y;
+                o = rec + at * D;
+            } else if (q < pieces) {
+                qm[k] = r.x, ql[k] = r.y;
+                o = p.rest_o + row * D;
+            } else if (after == 0) {
+                qm[k] = h.x, ql[k] = h.y;
+                o = p.o + row * D;
+            } else {
+                const size_t at = (size_t)(slot + after - 1) * kSlotRows + (__float_as_int(h.w) >> 16 & (kSlotRows - 1));
+                const float4 s = __ldcg(p.slot_head + at);
+                qm[k] = s.x, ql[k] = s.y;
+                o = p.slot_o + at * D;
+            }
+            x[k] = __ldcg(reinterpret_cast<const float4*>(o + d));
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (e + 4 * k < parts) join(qm[k], ql[k], x[k]);
+    }
+    part[warp][lane] = v;
+    sums[warp][lane] = make_float2(m, l);
+    __syncthreads();
+    if (turn != 0 || kind == 0) return;
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+        const float2 s = sums[warp + k][lane];
+        join(s.x, s.y, part[warp + k][lane]);
+    }
+    put_at<D>(a, row, d, v, m, l);
 }
 
 bool attend_fits(const KvDev& c, const KvBatch& b, int T) {
@@ -1136,19 +1161,24 @@ static cudaError_t launch(const KvDev& c, const KvBatch& b, const AttendArgs& a,
         // the same division of L1 and shared memory for both: an SM is idle while it changes
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(k_attend<D, NT, kShared>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k_join<D, NT, kShared>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        if (e == cudaSuccess) {
+            if constexpr (kShared)
+                e = cudaFuncSetAttribute(k_join_rows<D>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+            else
+                e = cudaFuncSetAttribute(k_join<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        }
         return e;
     });
     if (set != cudaSuccess) return set;
-    unsigned blocks = grid;  // of k_join
-    if constexpr (kShared) {
-        const int64_t rows = (int64_t)a.T * c.hq, per = 8 * (128 / D);  // of a block
-        rest.splits = grid;
-        blocks += (unsigned)((rows + per - 1) / per);
-    }
+    if constexpr (kShared) rest.ctas = grid;
     const cudaError_t e = launch_ex(k_attend<D, NT, kShared>, dim3(grid), dim3(kAttThreads), sizeof(AttSmem<D, NT, kShared>), st, true, c, b, a, rest);
-    return e != cudaSuccess ? e : launch_ex(k_join<D, NT, kShared>, dim3(blocks), dim3(256), 0, st, true, c, a, rest, b.cu, b.B);
+    if (e != cudaSuccess) return e;
+    if constexpr (kShared) {
+        const int64_t rows = (int64_t)a.T * c.hq, per = 2 * (128 / D);  // of a block
+        return launch_ex(k_join_rows<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, true, c, a, rest, b.cu, b.B);
+    } else {
+        return launch_ex(k_join<D, NT>, dim3(grid), dim3(256), 0, st, true, c, a);
+    }
 }
 
 template <bool kShared>
