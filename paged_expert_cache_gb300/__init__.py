@@ -804,9 +804,11 @@ def residual_norm(x, y=None, out=None, weight=None, post_weight=None, gate=None,
             wide = 1
         else:
             _refuse(f"gate must be [{H}], [{T}, {H}] or [{T}, 1], got {tuple(of)}")
-    st = (_lib or load()).moe_residual_norm(
-        _norm_args(T, H, xt, yt, max(wt, 0), wide, scale, eps, xp, xs, yp, ys, xop, xos, op, os_, wp, pp, gp, gs),
-        _stream(stream, dev))
+    try:
+        args = _norm_args(T, H, xt, yt, max(wt, 0), wide, scale, eps, xp, xs, yp, ys, xop, xos, op, os_, wp, pp, gp, gs)
+    except (struct.error, OverflowError, TypeError):
+        _refuse("scale and eps must be numbers that fp32 holds, T and H below 2^31")
+    st = (_lib or load()).moe_residual_norm(args, _stream(stream, dev))
     if st:
         _check(st)
     return x_out if out is None else out
@@ -822,6 +824,8 @@ def sample(logits, tokens, uniform=None, temperature=None, top_k=None, top_p=Non
     if logits.dim() != 2:
         _refuse("logits must be [T, V]")
     T, V = logits.shape
+    if T > 1 << 24 or V > 1 << 20:
+        _refuse("at most 2^24 rows of 2^20 logits")
     dev = logits.get_device()
     if dev < 0 or dev != torch._C._cuda_getDevice():
         _refuse("logits must be on the current CUDA device")

@@ -193,3 +193,20 @@ def test_no_rows_and_another_stream_and_a_graph():
         torch.cuda.synchronize()
         s1 = reference(xi, a["y"], None, None, None, 1.0, 1e-6)[0]
         check(xo, o2, reference(s1, a["y"], a["weight"], None, None, 1.0, 1e-6), F)
+
+
+def test_refusals_with_tensors_on_the_device():
+    x, y, w = torch.zeros(4, 64, device="cuda"), torch.zeros(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    out = torch.empty(4, 64, dtype=B, device="cuda")
+    calls = [((x,), dict()), ((x,), dict(out=out.float())), ((x,), dict(out=out[:3])), ((x,), dict(out=out.t())),
+             ((x,), dict(out=out, x_out=x)), ((x,), dict(out=out, gate=w)), ((x,), dict(out=out, post_weight=w)),
+             ((x, y[:, :32]), dict(out=out)), ((x, y.half()), dict(out=out)), ((x, y.cpu()), dict(out=out)),
+             ((x, y), dict(weight=w[:63], out=out)), ((x, y), dict(weight=w, post_weight=w.bfloat16(), out=out)),
+             ((x, y), dict(gate=w[:, None])), ((x, y), dict(gate=torch.ones(3, 1, device="cuda"))),
+             ((x, y), dict(x_out=torch.empty(4, 64, dtype=B, device="cuda"))), ((x, y), dict(x_out=torch.empty(4, 64))),
+             ((x, y), dict(scale=1e39)), ((x, y), dict(scale=float("nan"))), ((x, y), dict(eps=-1.0)), ((x, y), dict(scale="2")),
+             ((x[:, :1].expand(4, 64), y), dict()), ((x.t(), y.t()), dict()), ((torch.zeros(1, 40000, device="cuda"),), dict(out=torch.empty(1, 40000, dtype=B, device="cuda")))]
+    for args, kw in calls:
+        with pytest.raises(pec.MoeError) as e:
+            pec.residual_norm(*args, **kw)
+        assert e.value.status == pec.ERR_INVALID, (args, kw)

@@ -227,3 +227,15 @@ def test_streams_graphs_and_repeats_give_the_same():
 def test_no_rows():
     z = torch.empty(0, 100, device="cuda")
     assert pec.sample(z, torch.empty(0, dtype=torch.int32, device="cuda")).shape == (0,)
+
+
+def test_refusals_with_tensors_on_the_device():
+    z, t, f = torch.zeros(4, 64, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(4, device="cuda")
+    calls = [((z, t.long()), {}), ((z, t[:3]), {}), ((z, t.cpu()), {}), ((z, None), {}), ((z.half(), t), {}), ((z.cpu(), t), {}),
+             ((z.t(), t), {}), ((z[:, :1].expand(4, 64), t), {}), ((z, t, f.double()), {}), ((z, t, f.cpu()), {}), ((z, t, f[::2]), {}),
+             ((z, t), dict(top_k=f)), ((z, t), dict(temperature=t)), ((z, t), dict(top_p=0.9)), ((z, t), dict(min_p=f[:1])),
+             ((z, t), dict(logprobs=t)), ((torch.zeros(1, (1 << 20) + 1, device="cuda"), t[:1]), {})]
+    for args, kw in calls:
+        with pytest.raises(pec.MoeError) as e:
+            pec.sample(*args, **kw)
+        assert e.value.status == pec.ERR_INVALID, (args, kw)

@@ -87,3 +87,10 @@ def test_sample_wrapper_refuses_mismatched_tensors():
         with pytest.raises(pec.MoeError) as e:
             pec.sample(*args)
         assert e.value.status == pec.ERR_INVALID
+
+
+def test_packed_arguments_are_the_structures():
+    assert len(pec._norm_args(*([0] * 6), 0.0, 0.0, *([0] * 12))) == ctypes.sizeof(pec.NormArgs)
+    assert len(pec._sampling_args(*([0] * 5))) == ctypes.sizeof(pec.SamplingArgs)
+    n = pec.NormArgs.from_buffer_copy(pec._norm_args(1, 2, 3, 4, 5, 6, 0.5, 0.25, *range(11, 23)))
+    assert [getattr(n, f) for f, _ in pec.NormArgs._fields_] == [1, 2, 3, 4, 5, 6, 0.5, 0.25, *range(11, 23)]
