@@ -39,6 +39,15 @@
 // tile and follow in one of their own, divided by 8, which is multiplied eight times.
 // A NaN scale makes its block of the output NaN for the rows that see it and for no
 // others. Maxima, sums and outputs are fp32.
+//
+// Measured: 32768 common positions, 512 rows for each of 8 heads, head_dim 128: 74 us
+// of the call's 114 (930 TFLOP/s, 0.48 of cuBLAS's bf16 rate), about 4400 cycles a key
+// tile where the products take 2150 and shared memory's traffic for them and the
+// tiles 2500. The chain of a tile is what runs: softmax 2300, then the values'
+// products, the next scores and their waits 2100; the tile warps need 3500 beside
+// them. One key tile a CTA (2451 positions, 128 rows): 11 us, nearly all of it
+// latency (1.5 us to the first piece, cells, tiles, scores, weights, products, 2 us
+// for the sums' stores, much of it code fetched for the first time).
 #include <algorithm>
 
 #include "attn_tc.cuh"

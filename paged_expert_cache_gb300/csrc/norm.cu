@@ -9,7 +9,15 @@
 // every row. A row stays in its threads' registers between the two sums: eight
 // values a thread where rows are aligned (16-byte loads). A row of at most 256
 // values is a warp's (four rows a CTA, no barrier), a longer one a CTA's, up to
-// 1024 threads; so a call of one row has all its loads on the way at once.
+// 1024 threads; so a call of one row has all its loads on the way at once (k_norm).
+// From eight rows an SM on, and up to 4096 values, CTAs take several rows, the next
+// one's loads under the last one's sums (1300 rows of 2048, fp32 with a bf16 output
+// of the block: 5.8 us, a row a CTA 6.4): k_norm_rows where rows are aligned, and two
+// more for rows that are not.
+//
+// Measured in a graph: one row of 2048 1.9 us, 61 of 4096 with both norms 2.9, 2451
+// of 2048 8.9 (6.8 TB/s, part of it from L2), 15013 of 4000 with both norms 94 (6.4
+// TB/s, 0.95 of a copy), of 4001 147.
 //
 // Everything is fp32: the sums of squares too, which fp32 holds unless values
 // pass 2^63 or all are below 2^-50. A row whose sum left that range is summed
@@ -88,6 +96,19 @@ struct Raw {
             for (int e = 0; e < (int)(V * sizeof(T) / 16); ++e) {
                 const uint4 v = *(reinterpret_cast<const uint4*>(p) + e);
                 r[4 * e] = v.x, r[4 * e + 1] = v.y, r[4 * e + 2] = v.z, r[4 * e + 3] = v.w;
+            }
+        }
+    }
+    // elements lo .. hi - 1 only, 0 for the others
+    __device__ __forceinline__ void load_some(const T* p, int lo, int hi) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const bool in = e >= lo && e < hi;
+            if constexpr (sizeof(T) == 4) {
+                r[e] = in ? *reinterpret_cast<const uint32_t*>(p + e) : 0u;
+            } else {
+                const uint32_t v = in ? (uint32_t)p[e] << (16 * (e & 1)) : 0u;
+                r[e / 2] = e & 1 ? r[e / 2] | v : v;
             }
         }
     }
@@ -275,6 +296,95 @@ __global__ void __launch_bounds__(512, 2) k_norm_rows(NormArgs a, int group) {
     }
 }
 
+// The same for rows of any width whose tensors have one phase: element 0 of a row
+// lies as many elements behind a multiple of eight in each of them (dense tensors of
+// one odd width). A thread takes eight elements from a 16-byte boundary on, which
+// start at 8 t - phase and so move from row to row against the weights: these lie in
+// shared memory as [element mod 8][element / 8], where neighbouring threads read
+// neighbouring words whatever the phase is. 15013 rows of 4001, both norms: 147 us
+// (4.1 TB/s; element by element from memory 250, through k_norm_lines 182). What is
+// left over the aligned rows' 94 is the row's chain: its edges go element by element
+// in two of the warps, and the others wait for them at the sums.
+template <class X, class Y, class W>
+__global__ void __launch_bounds__(512, 2) k_norm_phase(NormArgs a, int group, int phase0) {
+    constexpr int V = 8;
+    extern __shared__ float columns[];
+    __shared__ float part[2][4][32];
+    const int t = threadIdx.x, H = a.hidden, wide = H / 8 + 3;  // words of a column: one before and one behind the row
+    float *ws = columns, *ps = columns + 8 * wide;              // of out; of y
+    griddep_wait();
+    griddep_launch();
+    for (int k = t; k < 8 * wide; k += group) {
+        const int i = 8 * (k % wide - 1) + k / wide;
+        const bool in = i >= 0 && i < H;
+        float p = !in ? 0.f : a.post ? to_float(((const W*)a.post)[i]) : 1.f;
+        if (a.gate_wide && in) p *= to_float(((const W*)a.gate)[i]);
+        ws[k] = !in ? 0.f : a.weight ? to_float(((const W*)a.weight)[i]) : 1.f;
+        ps[k] = p;
+    }
+    Raw<X, V> xr;
+    Raw<Y, V> yr;
+    float gate = 1.f;
+    auto phase_of = [&](int row) { return (phase0 + row * (int)(a.xs & 7)) & 7; };
+    auto fetch = [&](int row) {
+        const int i = 8 * t - phase_of(row);
+        const X* x = (const X*)a.x + row * a.xs + i;
+        const Y* y = (const Y*)a.y + row * a.ys + i;
+        if (i >= 0 && i + V <= H) {
+            xr.load(x);
+            if (a.y) yr.load(y);
+        } else {
+            xr.load_some(x, -i, H - i);
+            if (a.y) yr.load_some(y, -i, H - i);
+        }
+        if (a.gate && !a.gate_wide) gate = to_float(((const W*)a.gate)[row * a.gs]);
+    };
+    auto put = [&](auto* to, int i, const float (&v)[V]) {
+        if (i >= 0 && i + V <= H) {
+            store_values<V>(to, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (i + e >= 0 && i + e < H) {
+                    const float one[1] = {v[e]};
+                    store_values<1>(to + e, one);
+                }
+        }
+    };
+    fetch(blockIdx.x);
+    __syncthreads();
+    int turn = 0;
+    for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        const int phase = phase_of(row), i = 8 * t - phase;
+        float x[V], y[V];
+        xr.get(x);
+        if (a.y) yr.get(y);
+        const float here = a.scale * gate;
+        if (row + gridDim.x < (unsigned)a.rows) fetch(row + gridDim.x);
+        // f(e, weights of element i + e): one column on with each e, and to the first one's next word at the
+        // end of the eight
+        auto weights = [&](const float* from, auto f) {
+            const float* at = from + (phase ? (8 - phase) * wide : 1) + min(t, wide - 2);
+#pragma unroll
+            for (int e = 0; e < V; ++e, at += wide) {
+                if (e == phase && e) at -= 8 * wide - 1;
+                f(e, *at);
+            }
+        };
+        if (a.y) {
+            float r = 1.f;
+            if (a.post) r = inverse_rms(y, a, group, part[turn]);
+            weights(ps, [&](int e, float w) { x[e] = fmaf(here, y[e] * r * w, x[e]); });
+            if (a.x_out) put((X*)a.x_out + row * a.xos + i, i, x);
+        }
+        if (!a.out) continue;
+        const float r = inverse_rms(x, a, group, part[turn] + 2);
+        float o[V];
+        weights(ws, [&](int e, float w) { o[e] = x[e] * r * w; });
+        put((uint16_t*)a.out + row * a.os + i, i, o);
+    }
+}
+
 // A row that need not start on a 16-byte boundary, between memory and shared
 // memory: there its bytes lie from the row's own phase on, so that aligned 16-byte
 // pieces go over as they are. The pieces that the row shares with its neighbours are
@@ -328,8 +438,8 @@ struct Line {
     static __host__ __device__ constexpr int bytes(int group) { return 8 * group * (int)sizeof(T) + 32; }
 };
 
-// k_norm_rows for rows that are not aligned. (Element by element from memory 250 us
-// for 15013 rows of 4001, 98 for the aligned 4000: the instructions bound it.)
+// k_norm_rows for rows of any width, each tensor with a phase of its own. Its
+// instructions bound it (3.1 TB/s).
 template <class X, class Y, class W>
 __global__ void __launch_bounds__(512, 2) k_norm_lines(NormArgs a, int group) {
     constexpr int E = 8;
@@ -416,6 +526,16 @@ static cudaError_t launch_norm(const NormArgs& a, bool aligned, int dev, cudaStr
     if (threads > 32 && threads <= 512 && n == 1 && !(a.gate_wide && a.gs) && a.rows >= 8 * sms) {
         const dim3 grid((unsigned)(sms * (1024 / threads)));
         if (aligned) return launch_ex(k_norm_rows<X, Y, W>, grid, dim3(threads), 0, st, true, a, threads);
+        // the phase that all rows of all tensors have, if there is one
+        const int sx = sizeof(X), sy = sizeof(Y), phase = (int)((uintptr_t)a.x / sx & 7u);
+        const bool one = (!a.y || ((int)((uintptr_t)a.y / sy & 7u) == phase && ((a.ys - a.xs) & 7) == 0)) &&
+                         (!a.x_out || ((int)((uintptr_t)a.x_out / sx & 7u) == phase && ((a.xos - a.xs) & 7) == 0)) &&
+                         (!a.out || ((int)((uintptr_t)a.out / 2 & 7u) == phase && ((a.os - a.xs) & 7) == 0));
+        if (one && a.hidden + 7 <= 8 * 512) {
+            const int wider = std::max(64, (a.hidden + 7 + 255) / 256 * 32);  // 8 threads' elements, and the phase
+            return launch_ex(k_norm_phase<X, Y, W>, dim3((unsigned)(sms * (1024 / wider))), dim3(wider),
+                             2 * 8 * (a.hidden / 8 + 3) * sizeof(float), st, true, a, wider, phase);
+        }
         const int bytes = 2 * Line<X>::bytes(threads) + Line<Y>::bytes(threads) + Line<uint16_t>::bytes(threads);
         static DeviceOnce once;
         const cudaError_t set = once.run(dev, [] {
