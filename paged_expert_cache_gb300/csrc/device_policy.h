@@ -46,6 +46,18 @@ inline bool prompt_in_halves(int64_t pairs, int head_dim, int64_t keys_per_seque
     return 2 * pairs <= (long_ones ? 5 : 1) * (int64_t)sms;
 }
 
+// Whether attention over common positions takes rows a tile at a time, its key tiles
+// in turn between the two halves of a CTA, in place of pairs of tiles. A single tile
+// costs two thirds of a pair, so it is taken where groups fill one tile or three (32
+// rows, head_dim 64: 25.4 us, in pairs 27.1; 320 rows behind 2451 positions 29.3 and
+// 33.3, behind 20000 45.2 and 46.8), not for two, four or more (160 rows 26.5 and 24.9;
+// 512 rows behind 32768 139 and 114). The groups are on the device: their average
+// stands for them.
+inline bool shared_in_single_tiles(int64_t rows, int groups, int tile) {
+    const int64_t tiles = (rows + (int64_t)groups * tile - 1) / ((int64_t)groups * tile);
+    return tiles <= 1 || tiles == 3;
+}
+
 // Makes a device current while it lives, and then the caller's again. Runtime
 // has get(int*) and set(int), with statuses whose zero is success.
 template <class Runtime>

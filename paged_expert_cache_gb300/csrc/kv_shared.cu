@@ -27,7 +27,7 @@
 //             them; both K-major. The code is kept short: with the cells in
 //             registers and all written out, a tile took 6500 cycles, most of them
 //             waiting for instructions.
-// Where a group has no more than 128 rows, both tiles are the same rows and take
+// Where groups fill one tile of rows, or three, both tiles are the same rows and take
 // every other key tile (kSingle); their sums are joined at the end.
 //
 // Arithmetic. d (q - 8) is rounded to fp16 once, by at most 2^-11 of itself (an eighth
@@ -822,8 +822,7 @@ cudaError_t launch_shared(const KvDev& c, const KvBatch& b, const KvGroups& g, c
     if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
     const int group = c.hq / c.hkv;
     const SharedArgs a = {c, b, g, parts, q, q_stride, T, scale * 1.4426950408889634f, fast_div((uint32_t)group)};
-    // one tile of rows where an average group fills no more
-    const bool single = (int64_t)T * group <= (int64_t)kTile * g.n;
+    const bool single = shared_in_single_tiles((int64_t)T * group, g.n, kTile);
     if (D == 128) return single ? launch_k<128, true>(a, dev, st) : launch_k<128, false>(a, dev, st);
     return single ? launch_k<64, true>(a, dev, st) : launch_k<64, false>(a, dev, st);
 }

@@ -10,10 +10,11 @@
 // values a thread where rows are aligned (16-byte loads). A row of at most 256
 // values is a warp's (four rows a CTA, no barrier), a longer one a CTA's, up to
 // 1024 threads; so a call of one row has all its loads on the way at once (k_norm).
-// From eight rows an SM on, and up to 4096 values, CTAs take several rows, the next
-// one's loads under the last one's sums (1300 rows of 2048, fp32 with a bf16 output
-// of the block: 5.8 us, a row a CTA 6.4): k_norm_rows where rows are aligned, and two
-// more for rows that are not.
+// From two rows an SM on, and up to 4096 values, CTAs take several rows, the next
+// one's loads under the last one's sums: k_norm_rows where rows are aligned, and two
+// more kernels for rows that are not. (Rows of 4096 bf16 with both norms, of 4001, of
+// 2048 fp32 with one: 320 rows 4.6, 7.1 and 2.9 us, a row a CTA 5.1, 10.9 and 2.8; 2451
+// rows 18.1, 25.8 and 8.9, 21.2, 39.8 and 9.4.)
 //
 // Measured in a graph: one row of 2048 1.9 us, 61 of 4096 with both norms 2.9, 2451
 // of 2048 8.9 (6.8 TB/s, part of it from L2), 15013 of 4000 with both norms 94 (6.4
@@ -523,7 +524,7 @@ static cudaError_t launch_norm(const NormArgs& a, bool aligned, int dev, cudaStr
     const int per = 8, threads = std::min(1024, std::max(32, (a.hidden + per * 32 - 1) / (per * 32) * 32));
     const int n = (a.hidden + per * threads - 1) / (per * threads);  // eights a thread: 1, 2 or 4
     const int rows_a_cta = threads == 32 ? 4 : 1;
-    if (threads > 32 && threads <= 512 && n == 1 && !(a.gate_wide && a.gs) && a.rows >= 8 * sms) {
+    if (threads > 32 && threads <= 512 && n == 1 && !(a.gate_wide && a.gs) && a.rows >= 2 * sms) {
         const dim3 grid((unsigned)(sms * (1024 / threads)));
         if (aligned) return launch_ex(k_norm_rows<X, Y, W>, grid, dim3(threads), 0, st, true, a, threads);
         // the phase that all rows of all tensors have, if there is one
