@@ -504,10 +504,12 @@ typedef struct {
  * are attended over as moe_kv_attend does. A row sees the positions up to its own
  * there too, if it lies among the common ones.
  *   workspace : device, 256-byte aligned, at least moe_kv_shared_bytes for T; the
- *               call's own until its work on `stream` is done (graphs that may run
- *               at the same time need one each)
- * The rest, and the limits, as in moe_kv_attend. Should a bounded wait inside the
- * kernel give up (0.2 s), the rows concerned come out as NaN. */
+ *               call's own until its work on `stream` is done
+ *   out       : must not overlap q
+ * The rest, and the limits, as in moe_kv_attend (keys, values and weights of the
+ * common positions are rounded to fp16 on the way). Should a bounded wait inside
+ * the kernel give up (0.2 s, and 20 us for each 128 positions of a piece of work),
+ * the rows concerned come out as NaN. */
 moe_status_t moe_kv_attend_shared(moe_kv_t* h, int32_t layer, const void* q, int64_t q_stride, int32_t T,
                                   const moe_kv_batch_t* batch, const moe_kv_groups_t* groups, float scale, void* out,
                                   void* workspace, uint64_t workspace_bytes, void* stream);

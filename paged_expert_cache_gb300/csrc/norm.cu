@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(512, 2) k_norm_rows(NormArgs a, int group) {
         });
         if (a.gate && !a.gate_wide) gate = to_float(*((const W*)a.gate + row * a.gs));
     };
+    if ((int)blockIdx.x >= a.rows) return;  // the whole CTA
     fetch(blockIdx.x);
     int turn = 0;
     for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
@@ -352,6 +353,7 @@ __global__ void __launch_bounds__(512, 2) k_norm_phase(NormArgs a, int group, in
                 }
         }
     };
+    if ((int)blockIdx.x >= a.rows) return;  // the whole CTA
     fetch(blockIdx.x);
     __syncthreads();
     int turn = 0;
@@ -469,6 +471,7 @@ __global__ void __launch_bounds__(512, 2) k_norm_lines(NormArgs a, int group) {
         if (a.y) yl.fetch(y_row(row), H, inner, t, group);
         if (a.gate && !a.gate_wide) gate = to_float(((const W*)a.gate)[row * a.gs]);
     };
+    if ((int)blockIdx.x >= a.rows) return;  // the whole CTA
     fetch(blockIdx.x);
     const int last = H - 1 - t;  // element e * group + t is the row's where e * group <= last
     int turn = 0;
@@ -525,7 +528,8 @@ static cudaError_t launch_norm(const NormArgs& a, bool aligned, int dev, cudaStr
     const int n = (a.hidden + per * threads - 1) / (per * threads);  // eights a thread: 1, 2 or 4
     const int rows_a_cta = threads == 32 ? 4 : 1;
     if (threads > 32 && threads <= 512 && n == 1 && !(a.gate_wide && a.gs) && a.rows >= 2 * sms) {
-        const dim3 grid((unsigned)(sms * (1024 / threads)));
+        auto ctas = [&](int per) { return dim3((unsigned)std::min(a.rows, sms * (1024 / per))); };  // 1024 threads an SM
+        const dim3 grid = ctas(threads);
         if (aligned) return launch_ex(k_norm_rows<X, Y, W>, grid, dim3(threads), 0, st, true, a, threads);
         // the phase that all rows of all tensors have, if there is one
         const int sx = sizeof(X), sy = sizeof(Y), phase = (int)((uintptr_t)a.x / sx & 7u);
@@ -534,7 +538,7 @@ static cudaError_t launch_norm(const NormArgs& a, bool aligned, int dev, cudaStr
                          (!a.out || ((int)((uintptr_t)a.out / 2 & 7u) == phase && ((a.os - a.xs) & 7) == 0));
         if (one && a.hidden + 7 <= 8 * 512) {
             const int wider = std::max(64, (a.hidden + 7 + 255) / 256 * 32);  // 8 threads' elements, and the phase
-            return launch_ex(k_norm_phase<X, Y, W>, dim3((unsigned)(sms * (1024 / wider))), dim3(wider),
+            return launch_ex(k_norm_phase<X, Y, W>, ctas(wider), dim3(wider),
                              2 * 8 * (a.hidden / 8 + 3) * sizeof(float), st, true, a, wider, phase);
         }
         const int bytes = 2 * Line<X>::bytes(threads) + Line<Y>::bytes(threads) + Line<uint16_t>::bytes(threads);

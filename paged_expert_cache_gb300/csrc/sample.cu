@@ -438,22 +438,32 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         if (point >= total) return {-1, 0, 0};
         return {(int)sm.found.a, sm.found.mass, (uint64_t)sm.found.c << 32 | sm.found.b};
     };
-    // The tokens of values lo .. hi, in rank 0's list if there are at most kList; their number.
+    // The tokens of values lo .. hi, in rank 0's list if there are at most kList; their number, and their
+    // lowest and highest key.
+    uint32_t listed_lo, listed_hi;
     auto gather = [&](float lo, float hi) -> int {
+        float least = INFINITY, most = -INFINITY;
         each([&](float v, int i) {
             const bool in = v >= lo && v <= hi;
             const unsigned hit = __ballot_sync(0xffffffffu, in);
             if (!hit) return;
+            if (in) least = fminf(least, v), most = fmaxf(most, v);
             int at = 0;
             if (lane == 0) at = atomicAdd(&sm.listed, __popc(hit));
             at = __shfl_sync(0xffffffffu, at, 0) + __popc(hit & ((1u << lane) - 1u));
             if (in && at < kList) sm.mine[at] = (uint64_t)key_of(v) << 32 | (uint32_t)~(first + i);
         });
+        listed_lo = __reduce_min_sync(0xffffffffu, key_of(least));
+        listed_hi = __reduce_max_sync(0xffffffffu, key_of(most));
+        if (lane == 0) sm.wa[warp] = listed_hi, sm.wb[warp] = listed_lo;
         __syncthreads();
-        const SampleNote* all = tell({0, (uint32_t)sm.listed, 0, 0, 0});
+        for (int w = 0; w < kSampleWarps; ++w) listed_hi = max(listed_hi, sm.wa[w]), listed_lo = min(listed_lo, sm.wb[w]);
+        const SampleNote* all = tell({0, (uint32_t)sm.listed, listed_lo, listed_hi, 0});
         if (tid == 0) sm.listed = 0;
         int sum = 0, from = -1, at = 0;
         for (int r = 0; r < C; ++r) {
+            listed_lo = min(listed_lo, all[r].b);
+            listed_hi = max(listed_hi, all[r].c);
             const int here = (int)all[r].a;
             if (from < 0 && tid < sum + here) from = r, at = tid - sum;
             sum += here;
@@ -561,19 +571,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
             if (!done) cluster.sync();
             return {sm.found.a, sm.found.mass, sm.found.b, sm.found.c};
         }
-        const float vlo = value_of(klo), vhi = value_of(khi);
-        float least = INFINITY, most = -INFINITY;
-        each([&](float v, int) {
-            if (v >= vlo && v <= vhi) least = fminf(least, v), most = fmaxf(most, v);
-        });
-        klo = __reduce_min_sync(0xffffffffu, key_of(least));
-        khi = __reduce_max_sync(0xffffffffu, key_of(most));
-        __syncthreads();
-        if (lane == 0) sm.wa[warp] = khi, sm.wb[warp] = klo;
-        __syncthreads();
-        for (int w = 0; w < kSampleWarps; ++w) khi = max(khi, sm.wa[w]), klo = min(klo, sm.wb[w]);
-        const SampleNote* all = tell({0, khi, klo, 0, 0});
-        for (int r = 0; r < C; ++r) khi = max(khi, all[r].a), klo = min(klo, all[r].b);
+        klo = listed_lo;
+        khi = listed_hi;
         uint64_t before = bin.before, upto = bin.upto;
         while (klo < khi) {
             fresh = false;

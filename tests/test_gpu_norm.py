@@ -210,3 +210,15 @@ def test_refusals_with_tensors_on_the_device():
         with pytest.raises(pec.MoeError) as e:
             pec.residual_norm(*args, **kw)
         assert e.value.status == pec.ERR_INVALID, (args, kw)
+
+
+@pytest.mark.parametrize("H,odd", [(264, False), (512, False), (261, True), (520, True)])
+def test_fewer_rows_than_ctas_fit(H, odd):
+    # between two rows an SM and as many CTAs as run at once: every CTA has a row of its own, and no CTA one past the last
+    for T in (310, 608, 1500):
+        wide = torch.full((T, H + (1 if odd else 0)), 1.0, device="cuda")
+        x, y = wide[:, :H], torch.randn(T, H, device="cuda").bfloat16()
+        out = torch.empty(T, H, dtype=B, device="cuda")
+        ref = reference(x, y, None, None, None, 1.0, 1e-6)
+        pec.residual_norm(x, y, out)
+        check(x, out, ref, F)
