@@ -30,15 +30,16 @@
 // Where groups fill one tile of rows, or three, both tiles are the same rows and take
 // every other key tile (kSingle); their sums are joined at the end.
 //
-// Arithmetic. d (q - 8) is rounded to fp16 once, by at most 2^-11 of itself (an eighth
-// of what a bf16 key or value may be off by), and so are the weights. A row's weights refer to an exponent 6 below its maximum when that was raised, which
-// happens when a score exceeds it by 2^kRaise: they reach 2^14, keep all bits down to
-// 2^-20 of the largest and count down to 2^-30. fp16 does not hold values from 65504
-// on: keys of a cell with a scale of 4096 or more are written 2^-4 times as large,
-// and its scores raised again; value blocks with such a scale are left out of their
-// tile and follow in one of their own, divided by 8, which is multiplied eight times.
-// A NaN scale makes its block of the output NaN for the rows that see it and for no
-// others. Maxima, sums and outputs are fp32.
+// Arithmetic. d (q - 8) is rounded to fp16 once, by at most 2^-11 of itself (an eighth of
+// what a bf16 key or value may be off by), and so are the weights. A row's weights refer
+// to an exponent 6 below its maximum when that was raised, which happens when a score
+// exceeds it by 2^kRaise: they reach 2^14, keep all bits down to 2^-20 of the largest and
+// count down to 2^-30. fp16 does not hold values from 65504 on: keys of a cell with a
+// scale of 4096 or more are written 2^-4 times as large, and its scores raised again;
+// value blocks with such a scale are left out of their tile and follow in one of their
+// own, divided by 8, which is multiplied eight times. A NaN scale makes its block of the
+// output NaN for the rows that see it and for no others. Maxima, sums and outputs are
+// fp32.
 //
 // Measured: 32768 common positions, 512 rows for each of 8 heads, head_dim 128: 74 us
 // of the call's 114 (930 TFLOP/s, 0.48 of cuBLAS's bf16 rate), about 4400 cycles a key

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(512, 2) k_norm_phase(NormArgs a, int group, in
     Raw<X, V> xr;
     Raw<Y, V> yr;
     float gate = 1.f;
-    auto phase_of = [&](int row) { return (phase0 + row * (int)(a.xs & 7)) & 7; };
+    auto phase_of = [&](int row) { return (int)((unsigned)phase0 + (unsigned)row * (unsigned)(a.xs & 7)) & 7; };
     auto fetch = [&](int row) {
         const int i = 8 * t - phase_of(row);
         const X* x = (const X*)a.x + row * a.xs + i;
@@ -550,7 +550,7 @@ static cudaError_t launch_norm(const NormArgs& a, bool aligned, int dev, cudaStr
         if (set != cudaSuccess) return set;
         return launch_ex(k_norm_lines<X, Y, W>, grid, dim3(threads), bytes, st, true, a, threads);
     }
-    const dim3 grid((unsigned)((a.rows + rows_a_cta - 1) / rows_a_cta)), block(threads * rows_a_cta);
+    const dim3 grid((unsigned)((a.rows - 1) / rows_a_cta + 1)), block(threads * rows_a_cta);
     if (aligned)
         return launch_ex(n == 1 ? k_norm<X, Y, W, 8, 1> : n == 2 ? k_norm<X, Y, W, 8, 2> : k_norm<X, Y, W, 8, 4>, grid, block, 0,
                          st, true, a, threads);

@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     auto weight_of = [&](uint32_t key) { return weigh(value_of(key)); };
 
     // Bins of the histogram over the row: linear in the logit down to where weights are nothing, or to the
-    // row's lowest; the last one has all that is lower.
-    const float reach = fminf(top - value_of(kmin), 44.5f / sm.c), grain = reach > 0.f ? (float)(kBins - 1) / reach : 0.f;
+    // row's lowest; the last one has all that is lower. The grain stays finite, so that the top is bin 0's.
+    const float reach = fminf(top - value_of(kmin), 44.5f / sm.c), grain = (float)(kBins - 1) / fmaxf(reach, 0x1p-110f);
     auto bin_of_value = [&](float v) {  // 1.5 2^23: the nearest whole number in the last bits
         return __float_as_int(fminf((v - top) * -grain, (float)(kBins - 1)) + 12582912.f) - 0x4b400000;
     };
@@ -471,8 +471,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
         if (rank == 0 && sum <= kList) {
             if (from >= 0) sm.list[tid] = cluster.map_shared_rank(&sm, from)->mine[at];
             else if (tid == sum) sm.list[tid] = 0;  // the list is read in pairs
-            __syncthreads();
         }
+        __syncthreads();  // and `listed` is 0 again before the next list
         return sum;
     };
     // Rank 0: the list in order. Thread r gets the r-th token (0 past the end), its weight, and what lies before it.

@@ -112,6 +112,18 @@ def test_flat_rows_are_drawn_in_the_order_of_their_indexes(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("V", [300, 9000])
+@pytest.mark.parametrize("spread", [1e-30, 1e-37, 1e-39])
+def test_rows_that_are_nearly_flat(dtype, V, spread):
+    T = 12
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = (torch.randn(T, V, generator=g, device="cuda") * 8).round().mul(spread).to(dtype)
+    u = (torch.arange(T) + 0.3) / T
+    for k, p, m in [(1, 1.0, 0.0), (3, 1.0, 0.0), (250, 0.7, 0.0), (0, 0.9, 0.0), (0, 1.0, 1.0), (0, 1.0, 0.0)]:
+        check(z, 1.0, k, p, m, u)
+
+
+@pytest.mark.parametrize("dtype", [B, F])
 def test_a_cut_inside_a_run_of_equals(dtype):
     V = 9000
     z = torch.zeros(40, V, device="cuda")
