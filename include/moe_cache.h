@@ -502,7 +502,10 @@ typedef struct {
  * sequence's row of the block table, the others in each sequence's own; the
  * sequences' rows name the same pages for them, or copies. Sequences in no group
  * are attended over as moe_kv_attend does. A row sees the positions up to its own
- * there too, if it lies among the common ones.
+ * there too, if it lies among the common ones. A call that is too small for this to
+ * pay, by T, the number of sequences and the room of the block table, is
+ * moe_kv_attend, every position looked up in its sequence's own row; much more room
+ * than the sequences need makes a small call count as large (8 us).
  *   workspace : device, 256-byte aligned, at least moe_kv_shared_bytes for T; the
  *               call's own until its work on `stream` is done
  *   out       : must not overlap q

@@ -621,7 +621,8 @@ class KVCache:
     def attend_shared(self, layer, q, batch, groups, out, workspace, scale=None, stream=None):
         """moe_kv_attend_shared: attend for a batch whose sequences have their first
         positions in common by groups (a KVGroups), each group's read once for all of
-        them. workspace: from shared_workspace, of at least q's rows, and not used by
+        them (small calls, by the rows and the room of the block table, are attend's).
+        workspace: from shared_workspace, of at least q's rows, and not used by
         another call until this one's work is done."""
         hq, hkv, dim = self._dims
         T = _torch.Tensor

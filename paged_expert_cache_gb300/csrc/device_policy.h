@@ -3,6 +3,7 @@
 // (the CPU tests do).
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 
@@ -44,6 +45,23 @@ inline bool append_takes_32_heads(int64_t tasks, int sms) { return tasks >= (int
 inline bool prompt_in_halves(int64_t pairs, int head_dim, int64_t keys_per_sequence, int sms) {
     const bool long_ones = head_dim == 128 && keys_per_sequence >= 1000;
     return 2 * pairs <= (long_ones ? 5 : 1) * (int64_t)sms;
+}
+
+// Whether reading what groups have in common once pays for its own kernels, against
+// attention over each sequence by itself: by the most work that the call can hold, in
+// cells of 16 positions and 64 dims for 8 rows (rows: of queries a key/value head;
+// positions: what a row of the block table has room for). The common positions cost as
+// much as 3 such row tiles whatever their rows are, and 8 us (32 query heads over 4,
+// head_dim 128: 16 sequences behind 2451 positions 23.4 us, each by itself 15.2; behind
+// 10000 27.1 and 27.0, 20000 30.8 and 42.2; 8 behind 10000 23.1 and 19.5; 48 behind
+// 2451 30.7 and 25.9, 5000 32.9 and 37.2. 16 heads of their own, head_dim 64: 4 behind
+// 20000 33.6 and 26.5, 8 behind 10000 25.9 and 27.5, 16 behind 5000 21.9 and 29.0.)
+// Lengths and groups are on the device, so the room stands for them: in a table with
+// much more of it than is held, short prefixes are read once for their group as well.
+constexpr int64_t kSharedWork = 1 << 16;
+inline bool sharing_pays(int64_t rows, int64_t sequences, int64_t positions, int kv_heads, int head_dim) {
+    const int64_t tiles = std::max((rows + 7) / 8, std::min(sequences, rows));
+    return tiles * (positions / 16) * kv_heads * (head_dim / 64) >= kSharedWork + 3 * kSharedWork / std::max<int64_t>(tiles, 1);
 }
 
 // Whether attention over common positions takes rows a tile at a time, its key tiles

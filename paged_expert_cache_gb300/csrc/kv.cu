@@ -556,6 +556,11 @@ moe_status_t moe_kv_attend_shared(moe_kv_t* h, int32_t layer, const void* q, int
     if ((uintptr_t)workspace & 255u) return refuse("the workspace must be 256-byte aligned");
     if (workspace_bytes < moe::shared_bytes(c.device, T, c.q_heads, c.head_dim))
         return refuse("the workspace is smaller than moe_kv_shared_bytes");
+    if (!moe::sharing_pays((int64_t)T * (c.q_heads / c.kv_heads), b.B, (int64_t)b.table_stride * c.page_tokens, c.kv_heads, c.head_dim)) {
+        const cudaError_t e = moe::launch_attend(d, b, c.head_dim, (const uint16_t*)q, q_stride, T, scale, (uint16_t*)out, h->scratch,
+                                                 (cudaStream_t)stream);
+        return e == cudaSuccess ? MOE_OK : cuda_refuse(e);
+    }
     const moe::KvGroups g = {groups->cu_seqs, groups->prefix_lens, groups->num_groups};
     const moe::SharedParts parts = moe::shared_parts(workspace, c.device, T, c.q_heads, c.head_dim);
     cudaError_t e = moe::launch_shared(d, b, g, parts, c.head_dim, (const uint16_t*)q, q_stride, T, scale, (cudaStream_t)stream);

@@ -26,12 +26,12 @@
 // is read from HBM once, and put their histograms together over distributed
 // shared memory.
 //
-// Measured in a graph. One row of 131072 bf16 logits: top-k 50 and top-p 0.95 14.6
+// Measured in a graph. One row of 131072 bf16 logits: top-k 50 and top-p 0.95 15.0
 // us, no filter 18.5: a chain of about eight steps over the cluster, 1 to 2 us each.
-// 61 rows of 50021 fp32, settings mixed: 60. 128 rows of 131072: greedy 38, top-k 50
-// 50, no filter 127, top-p 0.98 of flat logits 165, where 114 million warp
-// instructions at 0.65 an SM quarter's cycle are what it takes (the weights of all
-// tokens once, 50 instructions each, two atomics, and four or five passes that
+// 61 rows of 50021 fp32, settings mixed: 61. 128 rows of 131072: greedy 38, top-k 50
+// 50, no filter 127, top-p 0.98 of flat logits 154, where 109 million warp
+// instructions at 0.66 an SM quarter's cycle are what it takes (the weights of all
+// tokens once, 50 instructions each, two atomics, and three or four passes that
 // compare).
 #include <cooperative_groups.h>
 

@@ -71,7 +71,8 @@ def test_a_step_as_a_graph_follows_lengths_and_draws():
     qr, o, room = torch.empty_like(q), torch.empty_like(q), layer.kv.shared_workspace(n)
     h, tokens = torch.empty(n, layer.hidden, dtype=torch.bfloat16, device="cuda"), torch.empty(n, dtype=torch.int32, device="cuda")
     back, logits = torch.empty_like(h), torch.empty(n, 1000, dtype=torch.bfloat16, device="cuda")
-    batch = pec.KVBatch(more.step_cu, more.kv_lens, more.table)
+    table = torch.nn.functional.pad(more.table, (0, 1 << 16), value=-1)  # wide: groups are read once though they are small
+    batch = pec.KVBatch(more.step_cu, more.kv_lens, table)
 
     def step():
         layer.kv.append(0, q, k, v, batch, rope=layer.rope, q_out=qr)
@@ -116,7 +117,7 @@ import torch, paged_expert_cache_gb300 as pec
 B, n = torch.bfloat16, 2
 kv = pec.KVCache(pec.make_kv_config(1, 16, 8, 2, 128, page_tokens=16))
 i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
-table = i32([[0, 1, 2], [0, 1, 3]])
+table = torch.nn.functional.pad(i32([[0, 1, 2], [0, 1, 3]]), (0, 1 << 16))
 k = torch.randn(80, 2, 128, device="cuda").to(B)
 kv.append(0, None, k, k, pec.KVBatch(i32([0, 40, 80]), i32([40, 40]), table))
 batch, groups = pec.KVBatch(i32([0, 1, 2]), i32([40, 40]), table), pec.KVGroups(i32([0, 2]), i32([32]))

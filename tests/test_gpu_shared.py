@@ -36,9 +36,10 @@ def cumulative(n):
 
 class Shared:
     """groups: (positions in common, [each sequence's own positions]); whole pages of the common part are the same pages, in
-    random order, the page that it ends in is each sequence's own."""
+    random order, the page that it ends in is each sequence's own. room: the table is so wide that common positions are read
+    once for their group even in these small batches."""
 
-    def __init__(self, groups, hq, hkv, dim, page=64, seed=0, k_scale=1.0, v_scale=1.0, change=None):
+    def __init__(self, groups, hq, hkv, dim, page=64, seed=0, k_scale=1.0, v_scale=1.0, change=None, room=True):
         g = self.g = torch.Generator(device="cuda").manual_seed(seed)
         self.hq, self.hkv, self.dim, self.page = hq, hkv, dim, page
 
@@ -61,6 +62,8 @@ class Shared:
         ids = torch.randperm(pages + 2, generator=torch.Generator().manual_seed(seed)).tolist()
         self.pages = pages + 2
         width = max(-(-n // page) for n in self.kv) + 1
+        if room:
+            width = max(width, -(-4 * (1 << 16) * 16 * 64 // (hkv * dim * page)) + 1)
         self.table = torch.full((len(self.kv), width), -1, dtype=torch.int32)
         b = 0
         for P, own in groups:
@@ -161,6 +164,17 @@ def test_matches_the_definition(groups, new, hq, hkv, dim, page):
     # moe_kv_attend differs by its own bound and this one's
     plain = S.plain(q, news)
     assert float((got.double() - plain.double()).norm() / plain.double().norm().clamp_min(1e-30)) <= 2 * L2_TOL
+
+
+@pytest.mark.parametrize("groups,new,hq,hkv,dim,page", CASES[:9])
+def test_small_batches_are_attended_over_each_sequence_by_itself(groups, new, hq, hkv, dim, page):
+    S = Shared(groups, hq, hkv, dim, page, seed=len(groups) + hq, room=False)
+    news = [min(new, n) for n in S.kv]
+    q, got = S.check(news)
+    assert torch.equal(got, S.plain(q, news))
+    more = torch.cat([q, q[:1]])  # a row past the batch
+    got = S.attend(more, news)
+    assert torch.equal(got, S.plain(more, news)) and (got[len(q):] == 7).all()
 
 
 def test_some_sequences_without_new_tokens_and_rows_of_none():
