@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(512, 2) k_norm_phase(NormArgs a, int group, in
         const int i = 8 * t - phase_of(row);
         const X* x = (const X*)a.x + row * a.xs + i;
         const Y* y = (const Y*)a.y + row * a.ys + i;
-        if (i >= 0 && i + V <= H) {
+        const bool inner = row > 0 && row + 1 < a.rows;  // what lies beside the row is the tensor's as well
+        if (inner ? i < H : i >= 0 && i + V <= H) {
             xr.load(x);
             if (a.y) yr.load(y);
         } else {
@@ -362,6 +363,11 @@ __global__ void __launch_bounds__(512, 2) k_norm_phase(NormArgs a, int group, in
         float x[V], y[V];
         xr.get(x);
         if (a.y) yr.get(y);
+        if (i < 0 || i + V > H) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (i + e < 0 || i + e >= H) x[e] = y[e] = 0.f;
+        }
         const float here = a.scale * gate;
         if (row + gridDim.x < (unsigned)a.rows) fetch(row + gridDim.x);
         // f(e, weights of element i + e): one column on with each e, and to the first one's next word at the
