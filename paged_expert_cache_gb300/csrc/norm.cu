@@ -13,12 +13,12 @@
 // From two rows an SM on, and up to 4096 values, CTAs take several rows, the next
 // one's loads under the last one's sums: k_norm_rows where rows are aligned, and two
 // more kernels for rows that are not. (Rows of 4096 bf16 with both norms, of 4001, of
-// 2048 fp32 with one: 320 rows 4.6, 7.1 and 2.9 us, a row a CTA 5.1, 10.9 and 2.8; 2451
-// rows 18.1, 25.8 and 8.9, 21.2, 39.8 and 9.4.)
+// 2048 fp32 with one: 320 rows 4.6, 7.6 and 2.9 us, a row a CTA 5.1, 10.9 and 2.8; 2451
+// rows 18.1, 21.4 and 8.9, 21.2, 39.8 and 9.4.)
 //
 // Measured in a graph: one row of 2048 1.9 us, 61 of 4096 with both norms 2.9, 2451
 // of 2048 8.9 (6.8 TB/s, part of it from L2), 15013 of 4000 with both norms 94 (6.4
-// TB/s, 0.95 of a copy), of 4001 147.
+// TB/s, 0.95 of a copy), of 4001 103.
 //
 // Everything is fp32: the sums of squares too, which fp32 holds unless values
 // pass 2^63 or all are below 2^-50. A row whose sum left that range is summed
@@ -301,54 +301,54 @@ __global__ void __launch_bounds__(512, 2) k_norm_rows(NormArgs a, int group) {
 // The same for rows of any width whose tensors have one phase: element 0 of a row
 // lies as many elements behind a multiple of eight in each of them (dense tensors of
 // one odd width). A thread takes eight elements from a 16-byte boundary on, which
-// start at 8 t - phase and so move from row to row against the weights: these lie in
-// shared memory as [element mod 8][element / 8], where neighbouring threads read
-// neighbouring words whatever the phase is. 15013 rows of 4001, both norms: 147 us
-// (4.1 TB/s; element by element from memory 250, through k_norm_lines 182). What is
-// left over the aligned rows' 94 is the row's chain: its edges go element by element
-// in two of the warps, and the others wait for them at the sums.
+// start at 8 t - phase. The phase changes from row to row, but over eight rows it
+// comes back, and the grid is a multiple of eight: a CTA's rows have one, and its
+// threads' columns stay as they are. The pieces at a row's edges are read whole, but
+// for the tensor's first and last row, and written element by element.
+// 15013 rows of 4001, both norms: 103 us (5.8 TB/s, 0.87 of a copy; weights in shared
+// memory and edges read element by element, whose packing waits for them, 147; through
+// k_norm_lines 182). What is left over the aligned rows' 94 is mostly the edges' stores.
 template <class X, class Y, class W>
 __global__ void __launch_bounds__(512, 2) k_norm_phase(NormArgs a, int group, int phase0) {
     constexpr int V = 8;
-    extern __shared__ float columns[];
     __shared__ float part[2][4][32];
-    const int t = threadIdx.x, H = a.hidden, wide = H / 8 + 3;  // words of a column: one before and one behind the row
-    float *ws = columns, *ps = columns + 8 * wide;              // of out; of y
+    const int H = a.hidden, i = 8 * (int)threadIdx.x - (int)(((unsigned)phase0 + blockIdx.x * (unsigned)(a.xs & 7)) & 7u);
+    const bool edge = i < 0 || i + V > H;
+    auto in = [&](int e) { return i + e >= 0 && i + e < H; };
     griddep_wait();
     griddep_launch();
-    for (int k = t; k < 8 * wide; k += group) {
-        const int i = 8 * (k % wide - 1) + k / wide;
-        const bool in = i >= 0 && i < H;
-        float p = !in ? 0.f : a.post ? to_float(((const W*)a.post)[i]) : 1.f;
-        if (a.gate_wide && in) p *= to_float(((const W*)a.gate)[i]);
-        ws[k] = !in ? 0.f : a.weight ? to_float(((const W*)a.weight)[i]) : 1.f;
-        ps[k] = p;
+    float w[V], pw[V];  // of out; of y. Past the row's ends they are 0, and so are the values there made
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        w[e] = !in(e) ? 0.f : a.weight ? to_float(((const W*)a.weight)[i + e]) : 1.f;
+        pw[e] = !in(e) ? 0.f : a.post ? to_float(((const W*)a.post)[i + e]) : 1.f;
+        if (a.gate_wide && in(e)) pw[e] *= to_float(((const W*)a.gate)[i + e]);
     }
     Raw<X, V> xr;
     Raw<Y, V> yr;
     float gate = 1.f;
-    auto phase_of = [&](int row) { return (int)((unsigned)phase0 + (unsigned)row * (unsigned)(a.xs & 7)) & 7; };
     auto fetch = [&](int row) {
-        const int i = 8 * t - phase_of(row);
         const X* x = (const X*)a.x + row * a.xs + i;
         const Y* y = (const Y*)a.y + row * a.ys + i;
         const bool inner = row > 0 && row + 1 < a.rows;  // what lies beside the row is the tensor's as well
-        if (inner ? i < H : i >= 0 && i + V <= H) {
-            xr.load(x);
-            if (a.y) yr.load(y);
+        if (inner || !edge) {
+            if (i < H) {
+                xr.load(x);
+                if (a.y) yr.load(y);
+            }
         } else {
             xr.load_some(x, -i, H - i);
             if (a.y) yr.load_some(y, -i, H - i);
         }
         if (a.gate && !a.gate_wide) gate = to_float(((const W*)a.gate)[row * a.gs]);
     };
-    auto put = [&](auto* to, int i, const float (&v)[V]) {
-        if (i >= 0 && i + V <= H) {
+    auto put = [&](auto* to, const float (&v)[V]) {
+        if (!edge) {
             store_values<V>(to, v);
-        } else {
+        } else if (i < H) {
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (i + e >= 0 && i + e < H) {
+                if (in(e)) {
                     const float one[1] = {v[e]};
                     store_values<1>(to + e, one);
                 }
@@ -356,41 +356,31 @@ __global__ void __launch_bounds__(512, 2) k_norm_phase(NormArgs a, int group, in
     };
     if ((int)blockIdx.x >= a.rows) return;  // the whole CTA
     fetch(blockIdx.x);
-    __syncthreads();
     int turn = 0;
     for (int row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        const int phase = phase_of(row), i = 8 * t - phase;
         float x[V], y[V];
         xr.get(x);
         if (a.y) yr.get(y);
-        if (i < 0 || i + V > H) {
+        if (edge) {
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (i + e < 0 || i + e >= H) x[e] = y[e] = 0.f;
+                if (!in(e)) x[e] = y[e] = 0.f;
         }
         const float here = a.scale * gate;
         if (row + gridDim.x < (unsigned)a.rows) fetch(row + gridDim.x);
-        // f(e, weights of element i + e): one column on with each e, and to the first one's next word at the
-        // end of the eight
-        auto weights = [&](const float* from, auto f) {
-            const float* at = from + (phase ? (8 - phase) * wide : 1) + min(t, wide - 2);
-#pragma unroll
-            for (int e = 0; e < V; ++e, at += wide) {
-                if (e == phase && e) at -= 8 * wide - 1;
-                f(e, *at);
-            }
-        };
         if (a.y) {
             float r = 1.f;
             if (a.post) r = inverse_rms(y, a, group, part[turn]);
-            weights(ps, [&](int e, float w) { x[e] = fmaf(here, y[e] * r * w, x[e]); });
-            if (a.x_out) put((X*)a.x_out + row * a.xos + i, i, x);
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[e] = fmaf(here, y[e] * r * pw[e], x[e]);
+            if (a.x_out) put((X*)a.x_out + row * a.xos + i, x);
         }
         if (!a.out) continue;
         const float r = inverse_rms(x, a, group, part[turn] + 2);
         float o[V];
-        weights(ws, [&](int e, float w) { o[e] = x[e] * r * w; });
-        put((uint16_t*)a.out + row * a.os + i, i, o);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = x[e] * r * w[e];
+        put((uint16_t*)a.out + row * a.os + i, o);
     }
 }
 
@@ -544,8 +534,9 @@ static cudaError_t launch_norm(const NormArgs& a, bool aligned, int dev, cudaStr
                          (!a.out || ((int)((uintptr_t)a.out / 2 & 7u) == phase && ((a.os - a.xs) & 7) == 0));
         if (one && a.hidden + 7 <= 8 * 512) {
             const int wider = std::max(64, (a.hidden + 7 + 255) / 256 * 32);  // 8 threads' elements, and the phase
-            return launch_ex(k_norm_phase<X, Y, W>, ctas(wider), dim3(wider),
-                             2 * 8 * (a.hidden / 8 + 3) * sizeof(float), st, true, a, wider, phase);
+            dim3 eights = ctas(wider);
+            eights.x = std::max(8u, eights.x & ~7u);  // rows 8 n apart have one phase
+            return launch_ex(k_norm_phase<X, Y, W>, eights, dim3(wider), 0, st, true, a, wider, phase);
         }
         const int bytes = 2 * Line<X>::bytes(threads) + Line<Y>::bytes(threads) + Line<uint16_t>::bytes(threads);
         static DeviceOnce once;

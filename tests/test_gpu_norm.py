@@ -222,3 +222,28 @@ def test_fewer_rows_than_ctas_fit(H, odd):
         ref = reference(x, y, None, None, None, 1.0, 1e-6)
         pec.residual_norm(x, y, out)
         check(x, out, ref, F)
+
+
+@pytest.mark.parametrize("xt,yt", [(B, F), (F, B)])
+@pytest.mark.parametrize("H,offset,pad", [(257, 0, 0), (4001, 0, 0), (4089, 3, 1), (2048, 5, 6), (1001, 7, 8), (264, 1, 7)])
+def test_rows_of_one_phase_and_what_lies_between_them(xt, yt, H, offset, pad):
+    # tensors of one offset and distance, whose rows' edges lie in the same 16 bytes as NaN that are no one's
+    T = 1203
+    a = make(T, H, xt, yt, F, True, "token", seed=H)
+
+    def inside(t, fill):
+        w = torch.full((T, offset + H + pad), fill, dtype=t.dtype, device="cuda")
+        w[:, offset:offset + H] = t
+        return w, w[:, offset:offset + H]
+
+    (xw, x), (_, y) = inside(a["x"], float("nan")), inside(a["y"], float("nan"))
+    (ow, out), (xow, xo) = inside(torch.zeros(T, H, dtype=B, device="cuda"), 77.0), inside(torch.zeros_like(a["x"]), 77.0)
+    args = dict(weight=a["weight"], post_weight=a["post"], gate=a["gate"], scale=0.5)
+    pec.residual_norm(x, y, out, x_out=xo, **args)
+    check(xo, out, reference(a["x"], a["y"], a["weight"], a["post"], a["gate"], 0.5, 1e-6), xt)
+    for w in (ow, xow):
+        assert (w[:, :offset] == 77).all() and (w[:, offset + H:] == 77).all()
+    first = out.clone()
+    pec.residual_norm(x, y, out, **args)  # in place
+    assert torch.equal(x, xo) and torch.equal(out, first)
+    assert xw[:, :offset].isnan().all() and xw[:, offset + H:].isnan().all()
