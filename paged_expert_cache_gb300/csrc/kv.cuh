@@ -79,7 +79,8 @@ struct KvGroups {
 struct SharedParts {
     float *o, *slot_o, *rest_o;            // [T x q_heads], [CTAs x kSlotRows], [T x q_heads] rows of head_dim
     float4 *head, *slot_head, *rest_head;  // as many
-    int slots;
+    int* failed;                           // [CTAs] of launch_shared's kernel: whether a wait there gave up
+    int slots;                             // CTAs
 };
 constexpr int kSlotRows = 256;
 

@@ -1067,6 +1067,9 @@ __global__ void __launch_bounds__(256) k_join_rows(KvDev c, AttendArgs a, Rest<t
     const SharedParts& p = rest.parts;
     const size_t row = ((size_t)blockIdx.x * 2 + (warp >> 2)) * kSide + side;
     griddep_wait();
+    // A CTA of launch_shared's whose wait gave up may have left rows as they were, and their heads do not say which.
+    bool lost = false;
+    for (int e = threadIdx.x; e < p.slots; e += 256) lost |= __ldcg(p.failed + e) != 0;
     const long long t = quotient((long long)row, c.hq);
     const bool there = t < a.T && t >= cu[0] && t < cu[B];
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1120,14 +1123,14 @@ __global__ void __launch_bounds__(256) k_join_rows(KvDev c, AttendArgs a, Rest<t
     }
     part[warp][lane] = v;
     sums[warp][lane] = make_float2(m, l);
-    __syncthreads();
+    lost = __syncthreads_or(lost) && kind & kCommon;
     if (turn != 0 || kind == 0) return;
 #pragma unroll
     for (int k = 1; k < 4; ++k) {
         const float2 s = sums[warp + k][lane];
         join(s.x, s.y, part[warp + k][lane]);
     }
-    put_at<D>(a, row, d, v, m, l);
+    put_at<D>(a, row, d, v, m, lost ? __int_as_float(0x7fc00000) : l);
 }
 
 bool attend_fits(const KvDev& c, const KvBatch& b, int T) {

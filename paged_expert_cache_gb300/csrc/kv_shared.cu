@@ -53,6 +53,7 @@
 
 #include "attn_tc.cuh"
 #include "kv.cuh"
+#include "piece_ring.h"
 
 namespace moe {
 
@@ -94,14 +95,16 @@ struct SharedSmem {
     uint8_t raw[kRaw][kTile / kCellTokens][Cell<D>::kBytes / 2];  // the cells' keys, or values, with their scales
     unsigned long long raw_full[kRaw], raw_empty[kRaw];
     unsigned long long q_full[2], full[kStages], empty[kStages], s_full[2], p_full[2][2], o_full[2];
-    unsigned long long item_full[2], item_empty[2], half_done, half_read;
+    unsigned long long item_full[2], item_empty[2], half_done, half_read, voted, drained[2];
     float half[kTile][2];  // exponent and sum of a row's second half of key tiles
     SharedPiece item[2];
     int meta[kStages];     // of a tile of values: how often it is multiplied; + 256: another one of the same keys follows
     unsigned absent[kRaw]; // the cells that are not there, a bit each
     unsigned long long large[8];  // of a key tile: the cells written 2^-4 times as large, a byte each
     int nan_from[2][4];    // of a piece, for each block of dims: the first position with a NaN scale
-    int dead;
+    Votes votes;           // on whether a tile of values has large scales
+    int longest;           // key tiles of the longest piece put so far
+    int dead;              // a wait has given up
     uint32_t tmem;
 };
 
@@ -155,6 +158,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
         }
         bar_init_n(gsmem(&sm.half_done), 128);
         bar_init_n(gsmem(&sm.half_read), 128);
+        bar_init_n(gsmem(&sm.voted), 4);  // the warps that make tiles
+        bar_init_n(gsmem(&sm.drained[0]), 1);
+        bar_init_n(gsmem(&sm.drained[1]), 1);
+        sm.longest = 0;
         sm.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -187,11 +194,14 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
     const uint32_t tmem = sm.tmem;
     int* dead = &sm.dead;
 
-    // The next piece; false at the end. `number` counts the pieces taken.
+    // What a wait for a piece has, to be put or to be given back: 20 us for each key tile
+    // of the longest one, which may be at work meanwhile.
+    auto limit = [&]() { return kGWaitNs + 20000ull * (unsigned)*(volatile int*)&sm.longest; };
+    // The next piece, for whole warps; false at the end. `number` counts the pieces taken.
     auto take = [&](int number) {
-        bar_wait(gsmem(&sm.item_full[number & 1]), (number >> 1) & 1, dead, true);
-        __syncwarp();
-        return !sm.item[number & 1].end;
+        return take_piece(
+            number, [&](int place, uint32_t parity) { return warp_wait(gsmem(&sm.item_full[place]), parity, dead, true, limit()); },
+            [&](int place) { return sm.item[place].end != 0; });
     };
     auto give_back = [&](int number) {
         __syncwarp();
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
             __syncwarp();
         };
         auto get_scales = [&](uint32_t (&v)[2]) {
-            const unsigned absent = sm.absent[raw_st] >> (2 * w) & 3u;
+            const unsigned absent = __shfl_sync(0xffffffffu, sm.absent[raw_st] >> (2 * w) & 3u, 0);
 #pragma unroll
             for (int z = 0; z < 2; ++z) v[z] = kAll || lane < C::kScales / 4 ? *scale_word(z) : 0u;
             if (absent) {
@@ -296,12 +306,17 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 // --- values: once, and where some scales are large a second time
                 next_raw();
                 get_scales(v);
-                uint32_t any = max(larger_half(v[0]), larger_half(v[1])) >= kLargeScale;
-                asm volatile(
-                    "{\n.reg .pred p, r;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.or.pred.aligned r, 1, 128, p;\nselp.u32 %0, 1, 0, r;\n}\n"
-                    : "=r"(any)
-                    : "r"(any)
-                    : "memory");
+                const bool any = __any_sync(
+                    0xffffffffu,
+                    any_of_four(
+                        sm.votes, order, w, __any_sync(0xffffffffu, max(larger_half(v[0]), larger_half(v[1])) >= kLargeScale),
+                        [&](auto vote) {
+                            if (lane == 0) {
+                                vote();
+                                bar_arrive(gsmem(&sm.voted));
+                            }
+                        },
+                        [&](uint32_t parity) { warp_wait(gsmem(&sm.voted), parity, dead); }));
                 uint32_t rest[2] = {0, 0};
                 if (any) {  // the small ones first, then an eighth of the large ones
 #pragma unroll
@@ -364,12 +379,26 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
             const int lo = has ? blockIdx.x * base + min((int)blockIdx.x, extra) : 0;
             const int hi = has ? lo + base + ((int)blockIdx.x < extra) : 0;
             int number = 0, before = 0, x = lo;
-            int long_one = 0;  // key tiles of the longest piece so far: the wait for a piece to end has 20 us for each
-            auto wait_empty = [&]() {
-                bar_wait(gsmem(&sm.item_empty[number & 1]), ((number >> 1) & 1) ^ 1, dead, true, kGWaitNs + 20000ull * long_one);
-                __syncwarp();
+            bool open = true;  // false once a wait for a place has given up: no more pieces
+            auto put = [&](const SharedPiece& p) {
+                open = open && put_piece(
+                                   number,
+                                   [&](int place, uint32_t parity) {
+                                       return warp_wait(gsmem(&sm.item_empty[place]), parity, dead, true, limit());
+                                   },
+                                   [&](int place) {
+                                       if (lane < 4) sm.nan_from[place][lane] = 0x7fffffff;
+                                       __syncwarp();
+                                       if (lane == 0) {
+                                           sm.longest = max(sm.longest, p.u1 - p.u0);
+                                           sm.item[place] = p;
+                                           bar_arrive(gsmem(&sm.item_full[place]));
+                                       }
+                                       __syncwarp();
+                                   });
+                ++number;
             };
-            for (int g0 = 0; g0 < a.g.n && x < hi; g0 += 32) {
+            for (int g0 = 0; g0 < a.g.n && x < hi && open; g0 += 32) {
                 if (a.g.n > 32) look(g0 + lane);
                 int upto = work;
 #pragma unroll
@@ -379,7 +408,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 }
                 upto += before;
                 before = __shfl_sync(0xffffffffu, upto, 31);
-                while (x < hi && x < before) {
+                while (x < hi && x < before && open) {
                     const int l = __ffs(__ballot_sync(0xffffffffu, x < upto)) - 1;  // the group of number x
                     SharedPiece p;
                     p.seq = __shfl_sync(0xffffffffu, seq, l);
@@ -398,24 +427,12 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                     p.slot = c0 + 1;
                     p.more = cta_of(first + units - 1) - c0;
                     x += to - in;
-                    if (p.u1 > p.u0) {
-                        wait_empty();
-                        long_one = max(long_one, p.u1 - p.u0);
-                        if (lane < 4) sm.nan_from[number & 1][lane] = 0x7fffffff;
-                        __syncwarp();
-                        if (lane == 0) {
-                            sm.item[number & 1] = p;
-                            bar_arrive(gsmem(&sm.item_full[number & 1]));
-                        }
-                        ++number;
-                    }
+                    if (p.u1 > p.u0) put(p);
                 }
             }
-            wait_empty();
-            if (lane == 0) {
-                sm.item[number & 1].end = 1;
-                bar_arrive(gsmem(&sm.item_full[number & 1]));
-            }
+            SharedPiece none = {};
+            none.end = 1;
+            put(none);
         } else if (warp < 11) {
             // --- the MMAs of tile x. The whole warp walks the loop and one lane
             // issues. Both warps pass every stage of the ring, needed or not: no
@@ -447,6 +464,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 if (used) tc_commit(gsmem(&sm.empty[st]));
                 else bar_arrive(gsmem(&sm.empty[st]));
             };
+            auto meta_of = [&](int st) { return __shfl_sync(0xffffffffu, *(volatile int*)&sm.meta[st], 0); };
             int st = 0;
             uint32_t round = 0, p_turn = 0, q_turn = 0;
             auto next_stage = [&]() {  // waits for the stage, and steps on
@@ -461,7 +479,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 const int n = sm.item[number & 1].u1 - sm.item[number & 1].u0, nx = tiles_of(sm.item[number & 1], x);
                 give_back(number);
                 int done = 0;
-                for (int i = 0; i < n; ++i) {
+                for (int i = 0; i < n; ++i) {  // (the whole warp alike, whatever the waits have seen)
                     const bool mine = kSingle ? (i & 1) == x : nx > 0;
                     const int sk = next_stage();
                     if (mine) {
@@ -476,7 +494,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                     free_stage(sk, mine);
                     __syncwarp();
                     int sv = next_stage();
-                    int meta = *(volatile int*)&sm.meta[sv];
+                    int meta = meta_of(sv);
                     if (mine) {
                         for (int half = 0; half < 2; ++half) {
                             bar_wait(gsmem(&sm.p_full[x][half]), p_turn, dead);
@@ -493,7 +511,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                     __syncwarp();
                     while (meta >= 256) {  // the keys' large values
                         sv = next_stage();
-                        meta = *(volatile int*)&sm.meta[sv];
+                        meta = meta_of(sv);
                         if (mine && leader) {
                             for (int e = 0; e < (meta & 255); ++e) {
                                 values(0, sv, false);
@@ -503,12 +521,17 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                         }
                         free_stage(sv, mine);
                         __syncwarp();
-                        if (*(volatile int*)dead) break;
+                        if (warp_dead(dead)) break;
                     }
                 }
             }
-            // the last arrivals, so that none is under way when the CTA ends
+            // the last arrivals and products, so that none is under way when the CTA ends,
+            // whatever else gave up
             for (int e = 0; e < kStages; ++e) bar_wait(gsmem(&sm.empty[e]), e < st ? round : round ^ 1, dead);
+            __syncwarp();
+            if (leader) tc_commit(gsmem(&sm.drained[x]));
+            __syncwarp();
+            bar_wait(gsmem(&sm.drained[x]), 0, dead, true);
         } else {
             // --- the cells' bytes: lane n has cell n of a tile
             constexpr uint32_t kBytes = C::kBytes / 2;
@@ -530,29 +553,26 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         bar_wait(gsmem(&sm.raw_empty[r]), turn, dead);
-                        __syncwarp();
+                        if (warp_dead(dead)) break;  // no more copies: r is the stage after the last one
                         const uint32_t bar = gsmem(&sm.raw_full[r]);
-                        if (!*(volatile int*)dead) {
-                            if (lane == 0) {
-                                sm.absent[r] = ~there;
-                                bar_expect(bar, kBytes * __popc(there));
-                            }
-                            __syncwarp();
-                            if (at)
-                                asm volatile(
-                                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                                        gsmem(sm.raw[r][lane & 7])),
-                                    "l"(at + half * kBytes), "r"(kBytes), "r"(bar)
-                                    : "memory");
+                        if (lane == 0) {
+                            sm.absent[r] = ~there;
+                            bar_expect(bar, kBytes * __popc(there));
                         }
+                        __syncwarp();
+                        if (at)
+                            asm volatile(
+                                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                                    gsmem(sm.raw[r][lane & 7])),
+                                "l"(at + half * kBytes), "r"(kBytes), "r"(bar)
+                                : "memory");
                         if (++r == S::kRaw) r = 0, turn ^= 1;
                     }
                 }
                 give_back(number);
             }
             // copies under way land before the CTA leaves, whatever else gave up
-            if (*(volatile int*)dead)
-                for (int e = 0; e < S::kRaw; ++e) gbar_wait(gsmem(&sm.raw_full[e]), e < r ? turn ^ 1 : turn);
+            for (int e = 0; e < S::kRaw; ++e) gbar_wait(gsmem(&sm.raw_full[e]), e < r ? turn ^ 1 : turn);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n");
@@ -614,7 +634,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 const int tile = kSingle ? 2 * j + x : j, kt = u0 + tile;
                 __syncwarp();
                 tc_fence_after();
-                if (const unsigned long long large = *(volatile unsigned long long*)&sm.large[(order + tile) & 7]) {
+                const unsigned long long large = *(volatile unsigned long long*)&sm.large[(order + tile) & 7];
+                if (__any_sync(0xffffffffu, large != 0)) {
                     // scores of cells written 2^-4 times as large
 #pragma unroll 1
                     for (int h = 0; h < kTile / 32; ++h) {
@@ -775,6 +796,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
     }
     tc_fence_before();
     __syncthreads();
+    if (tid == 0) a.parts.failed[blockIdx.x] = *(volatile int*)dead;
     if (warp == 10) {
         tc_fence_after();
         tc_dealloc(tmem, 512);
@@ -784,7 +806,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
 static uint64_t dense_rows(int T, int hq) { return (uint64_t)T * hq; }
 
 uint64_t shared_bytes(int device, int T, int hq, int D) {
-    return (2 * dense_rows(T, hq) + (uint64_t)sm_count(device) * kSlotRows) * (D * sizeof(float) + sizeof(float4));
+    const uint64_t ctas = sm_count(device);
+    return (2 * dense_rows(T, hq) + ctas * kSlotRows) * (D * sizeof(float) + sizeof(float4)) + ctas * sizeof(int);
 }
 
 SharedParts shared_parts(void* workspace, int device, int T, int hq, int D) {
@@ -796,6 +819,7 @@ SharedParts shared_parts(void* workspace, int device, int T, int hq, int D) {
     p.head = (float4*)(p.slot_o + slots * D);
     p.rest_head = p.head + rows;
     p.slot_head = p.rest_head + rows;
+    p.failed = (int*)(p.slot_head + slots);
     p.slots = sm_count(device);
     return p;
 }
