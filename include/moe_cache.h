@@ -543,7 +543,8 @@ moe_status_t moe_kv_read(moe_kv_t* h, int32_t layer, int32_t T, const moe_kv_bat
  *   out     : device bf16 [Tq x q_heads x head_dim]
  * Runs on the current device, asynchronous on `stream`. MOE_ERR_INVALID for
  * bad arguments. Allocates nothing. Should a bounded wait inside the kernel
- * give up (0.2 s), the rows concerned come out as NaN. */
+ * give up (0.2 s, and 20 us for each 128 keys of an item of work), the rows
+ * concerned come out as NaN. */
 moe_status_t moe_attn_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, int32_t Tq, int32_t Tk, int32_t num_seqs, const int32_t* cu_q,
                              const int32_t* cu_k, int32_t q_heads, int32_t kv_heads, int32_t head_dim, float scale,

@@ -45,6 +45,7 @@
 #include "attn_tc.cuh"
 #include "kv.cuh"
 #include "moe_cache.h"
+#include "piece_ring.h"
 
 namespace moe {
 
@@ -88,13 +89,14 @@ struct PromptSmem {
     // keys have one a slot, in the first two: there the slot's own MMA warp alone
     // waits, and its next scores come after.
     unsigned long long clean[kStages];
-    unsigned long long item_full[2], item_empty[2], asked, half_done, half_read;
+    unsigned long long item_full[2], item_empty[2], asked, half_done, half_read, drained[2];
     float half[kTile][2];  // maximum and sum of a row's second half of keys
     Item item[2];
     int flag[2];        // number of the last item (of each parity) with infinities or NaN among its cleaned values, + 1
     int prefix[kTable], total;
     int wsum[kTable / 32];
-    int dead;
+    int longest;        // key tiles of the longest item put so far
+    int dead;           // a wait has given up
     uint32_t tmem;
 };
 
@@ -213,6 +215,17 @@ __device__ __noinline__ void add_nonfinite(const PromptArgs& a, uint16_t* row, c
     }
 }
 
+// The outputs of rows `row` .. `end` - 1 and a key/value head that no warp works on,
+// since a wait gave up: NaN. A warp; out of line: it hardly runs.
+template <int D>
+__device__ __noinline__ void lose_rows(uint16_t* out, int hq, int group, int head, int row, int end, int lane) {
+    const uint4 nan = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+    for (; row < end; ++row) {
+        uint4* at = reinterpret_cast<uint4*>(out + ((size_t)row * hq + (size_t)head * group) * D);
+        for (int e = lane; e < group * D / 8; e += 32) at[e] = nan;
+    }
+}
+
 // kSingle: items are one tile, its keys in two halves, in place of two tiles.
 template <int D, bool kSingle>
 __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_constant__ PromptArgs a,
@@ -269,6 +282,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
             bar_init_n(gsmem(&sm.half_done), 128);
             bar_init_n(gsmem(&sm.half_read), 128);
             bar_init_n(gsmem(&sm.asked), 1);
+            bar_init_n(gsmem(&sm.drained[0]), 1);
+            bar_init_n(gsmem(&sm.drained[1]), 1);
+            sm.longest = 0;
             sm.dead = 0;
             asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         }
@@ -318,11 +334,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
         p.first_masked = p.seen_by_all / kTile;
         return p;
     };
-    // The next item, for a warp that uses them; false at the end. `number` counts the items taken.
+    // What the longest item may take, beyond a wait's 0.2 s: 20 us for each key tile.
+    auto at_work = [&]() { return 20000ull * (unsigned)*(volatile int*)&sm.longest; };
+    // The next item, for a warp that uses them; false at the end. `number` counts the
+    // items taken. The limit is above all that warp 8 may wait for between two items
+    // (three waits, two of them of twice the time, and the loads of an item), so that
+    // an item that was put is taken, and what is not put is lost to warp 8 alone.
     auto take = [&](int number) {
-        bar_wait(gsmem(&sm.item_full[number & 1]), (number >> 1) & 1, dead, true);
-        __syncwarp();
-        return !sm.item[number & 1].end;
+        return take_piece(
+            number,
+            [&](int place, uint32_t parity) {
+                return warp_wait(gsmem(&sm.item_full[place]), parity, dead, [&] { return 8 * kGWaitNs + 2 * at_work(); });
+            },
+            [&](int place) { return sm.item[place].end != 0; });
     };
     auto give_back = [&](int number) {
         __syncwarp();
@@ -340,8 +364,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
             int which = blockIdx.x, number = 0, st = 0;
             uint32_t turn = 1, asks = 0;   // the ring's parity of `empty`; parity of `asked`
             uint32_t q_turn[2] = {1, 1};
+            bool open = true;  // false once the wait for a place has given up: no more items
+            auto put = [&](const Item& it) {
+                open = open && put_piece(
+                                   number,
+                                   [&](int place, uint32_t parity) {
+                                       return warp_wait(gsmem(&sm.item_empty[place]), parity, dead, [&] { return kGWaitNs + at_work(); });
+                                   },
+                                   [&](int place) {
+                                       if (lane == 0) {
+                                           sm.item[place] = it;
+                                           bar_arrive(gsmem(&sm.item_full[place]));
+                                       }
+                                       __syncwarp();
+                                   });
+                ++number;
+                return open;
+            };
             while (which >= 0) {
-                const bool ask = !*(volatile int*)dead;
+                const bool ask = !warp_dead(dead);
                 if (ask && lane == 0) {
                     bar_expect(gsmem(&sm.asked), 16);
                     ask_next_cta(gsmem(&sm.answer), gsmem(&sm.asked));
@@ -385,56 +426,53 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
                     it.i0 = (at - base) * reach;
                     it.head = head;
                     it.end = 0;
-                    bar_wait(gsmem(&sm.item_empty[number & 1]), ((number >> 1) & 1) ^ 1, dead, true);
-                    if (lane == 0) {
-                        sm.item[number & 1] = it;
-                        bar_arrive(gsmem(&sm.item_full[number & 1]));
-                    }
-                    ++number;
-                    const Span p = span_of(it);
-                    for (int x = 0; x < 2; ++x) {
-                        if ((x ? p.n1 : p.n0) == 0) continue;
-                        const uint32_t bar = gsmem(&sm.q_full[x]);
-                        bar_wait(gsmem(&sm.q_empty[x]), q_turn[x], dead);
-                        q_turn[x] ^= 1;
-                        if (lane == 0 && !*(volatile int*)dead) {
-                            bar_expect(bar, (uint32_t)(kHalves * 128 * group * tokens));
-                            for (int h = 0; h < kHalves; ++h)
-                                tma_4d(gsmem(sm.q[x]) + h * kHalf, &mq, bar, 64 * h, 0, it.head, it.q0 + it.i0 + (kSingle ? 0 : x * tokens));
+                    if (put(it)) {
+                        const Span p = span_of(it);
+                        if (lane == 0) *(volatile int*)&sm.longest = max(sm.longest, p.n);
+                        for (int x = 0; x < 2; ++x) {
+                            if ((x ? p.n1 : p.n0) == 0) continue;
+                            const uint32_t bar = gsmem(&sm.q_full[x]);
+                            bar_wait(gsmem(&sm.q_empty[x]), q_turn[x], dead);
+                            if (warp_dead(dead)) break;
+                            q_turn[x] ^= 1;
+                            if (lane == 0) {
+                                bar_expect(bar, (uint32_t)(kHalves * 128 * group * tokens));
+                                for (int h = 0; h < kHalves; ++h)
+                                    tma_4d(gsmem(sm.q[x]) + h * kHalf, &mq, bar, 64 * h, 0, it.head, it.q0 + it.i0 + (kSingle ? 0 : x * tokens));
+                            }
                         }
-                    }
-                    for (int e = 0; e < 2 * p.n; ++e) {  // K0 V0 K1 V1 ...; the two halves' in turn
-                        const int tile = !kSingle ? e >> 1 : (e & 2) ? p.n0 + (e >> 2) : e >> 2;
-                        const uint32_t bar = gsmem(&sm.full[st]);
-                        bar_wait(gsmem(&sm.empty[st]), turn, dead);
-                        if (*(volatile int*)dead) break;
-                        if (lane == 0) {
-                            bar_expect(bar, S::kTileBytes);
-                            for (int h = 0; h < kHalves; ++h)
-                                tma_3d(gsmem(sm.kv[st]) + h * kHalf, (e & 1) ? &mv : &mk, bar, 64 * h, it.head, it.k0 + tile * kTile);
+                        for (int e = 0; e < 2 * p.n; ++e) {  // K0 V0 K1 V1 ...; the two halves' in turn
+                            const int tile = !kSingle ? e >> 1 : (e & 2) ? p.n0 + (e >> 2) : e >> 2;
+                            const uint32_t bar = gsmem(&sm.full[st]);
+                            bar_wait(gsmem(&sm.empty[st]), turn, dead);
+                            if (warp_dead(dead)) break;
+                            if (lane == 0) {
+                                bar_expect(bar, S::kTileBytes);
+                                for (int h = 0; h < kHalves; ++h)
+                                    tma_3d(gsmem(sm.kv[st]) + h * kHalf, (e & 1) ? &mv : &mk, bar, 64 * h, it.head, it.k0 + tile * kTile);
+                            }
+                            if (++st == kStages) st = 0, turn ^= 1;
                         }
-                        if (++st == kStages) st = 0, turn ^= 1;
+                    } else {
+                        lose_rows<D>(a.out, a.hq, group, it.head, it.q0 + it.i0, it.q0 + min(it.i0 + reach, it.lq), lane);
                     }
                     __syncwarp();
                 }
                 which = -1;
                 if (ask) {
-                    bar_wait(gsmem(&sm.asked), asks, dead, true);
+                    const bool answered = warp_wait(gsmem(&sm.asked), asks, dead, [] { return 2 * kGWaitNs; });
                     asks ^= 1;
-                    __syncwarp();
-                    if (!*(volatile int*)dead || bar_try(gsmem(&sm.asked), asks ^ 1)) which = next_cta(gsmem(&sm.answer));
+                    if (answered) which = next_cta(gsmem(&sm.answer));
                     fence_async_smem();  // the answer is read before the next one is asked for
                     __syncwarp();
                 }
             }
-            bar_wait(gsmem(&sm.item_empty[number & 1]), ((number >> 1) & 1) ^ 1, dead, true);
-            if (lane == 0) {
-                sm.item[number & 1].end = 1;
-                bar_arrive(gsmem(&sm.item_full[number & 1]));
-            }
-            if (*(volatile int*)dead && lane == 0) {  // copies under way land before the CTA leaves
-                for (int e = 0; e < kStages; ++e) gbar_wait(gsmem(&sm.full[e]), e < st ? turn ^ 1 : turn);
-            }
+            Item none = {};
+            none.end = 1;
+            put(none);
+            // copies under way land before the CTA leaves, whatever else gave up
+            for (int e = 0; e < kStages; ++e) bar_wait(gsmem(&sm.full[e]), e < st ? turn ^ 1 : turn, dead, true);
+            for (int x = 0; x < 2; ++x) bar_wait(gsmem(&sm.q_full[x]), q_turn[x], dead, true);
         } else if (warp < 11) {
             // --- the MMAs of tile x. A warp each, so that the tensor cores have
             // the other tile's products while this one waits for its weights. The
@@ -494,7 +532,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
                             sv = st;
                             bar_wait(gsmem(&sm.full[sv]), round, dead);
                             step();
-                            if (*(volatile int*)dead) break;
+                            if (warp_dead(dead)) break;
                             if ((x ? p.n0 : 0) + j - 1 >= p.first_masked) {
                                 bar_wait(gsmem(&sm.clean[x]), c_turn, dead);
                                 c_turn ^= 1;
@@ -530,7 +568,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
                         }
                         __syncwarp();
                     }
-                    if (*(volatile int*)dead) break;
+                    if (warp_dead(dead)) break;
                     continue;
                 }
                 sk = st;
@@ -564,7 +602,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
                     bar_wait(gsmem(&sm.full[sv]), round, dead);
                     step();
                     if (!kLate) next_keys();
-                    if (*(volatile int*)dead) break;
+                    if (warp_dead(dead)) break;
                     if (j >= p.first_masked) {
                         bar_wait(gsmem(&sm.clean[sv]), (c_turn >> sv) & 1, dead);
                         c_turn ^= 1u << sv;
@@ -596,11 +634,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_prompt(const __grid_const
                     if (leader && j + 1 < p.n) free_stage(sk, j < nx);
                     __syncwarp();
                 }
-                if (*(volatile int*)dead) break;
+                if (warp_dead(dead)) break;
             }
-            // the last arrivals, so that none is under way when the CTA ends:
-            // a stage's `empty` completes once for each time it was filled
-            for (int e = 0; e < kStages; ++e) bar_wait(gsmem(&sm.empty[e]), e < st ? round : round ^ 1, dead);
+            // the last arrivals, so that none is under way when the CTA ends: a stage's `empty`
+            // completes once for each time it was filled. Where one does not come, the products.
+            bool over = true;
+            for (int e = 0; e < kStages; ++e) over &= bar_wait(gsmem(&sm.empty[e]), e < st ? round : round ^ 1, dead);
+            if (!__all_sync(0xffffffffu, over)) {
+                if (leader) tc_commit(gsmem(&sm.drained[x]));
+                __syncwarp();
+                bar_wait(gsmem(&sm.drained[x]), 0, dead, true);
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");

@@ -31,24 +31,27 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // Waits for the phase; whether it has completed. A wait that gives up marks the CTA,
 // whose rows come out as NaN and whose other waits give up at once, but for those on
 // the items themselves (`always`), which keep their own limit. Lanes may differ in
-// what they see.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int* dead, bool always = false,
-                                         unsigned long long limit = kGWaitNs) {
+// what they see. limit(): in ns, asked for while it waits.
+template <class Limit>
+__device__ __forceinline__ bool bar_wait_for(uint32_t bar, uint32_t parity, int* dead, bool always, Limit limit) {
     if (bar_try(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     while (!bar_try(bar, parity)) {
         if (!always && *(volatile int*)dead) return false;
-        if (globaltimer_ns() - t0 > limit) {
+        if (globaltimer_ns() - t0 > limit()) {
             *(volatile int*)dead = 1;
             return false;
         }
     }
     return true;
 }
-// The same for a whole warp: lanes that disagreed would part ways for good.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* dead, bool always = false,
-                                          unsigned long long limit = kGWaitNs) {
-    return __all_sync(0xffffffffu, bar_wait(bar, parity, dead, always, limit));
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int* dead, bool always = false) {
+    return bar_wait_for(bar, parity, dead, always, [] { return kGWaitNs; });
+}
+// `always`, for a whole warp: lanes that disagreed would part ways for good.
+template <class Limit>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* dead, Limit limit) {
+    return __all_sync(0xffffffffu, bar_wait_for(bar, parity, dead, true, limit));
 }
 // Whether a wait of the CTA has given up, the same to a warp's lanes.
 __device__ __forceinline__ bool warp_dead(const int* dead) { return __any_sync(0xffffffffu, *(const volatile int*)dead); }

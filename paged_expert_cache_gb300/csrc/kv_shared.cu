@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
     // The next piece, for whole warps; false at the end. `number` counts the pieces taken.
     auto take = [&](int number) {
         return take_piece(
-            number, [&](int place, uint32_t parity) { return warp_wait(gsmem(&sm.item_full[place]), parity, dead, true, limit()); },
+            number, [&](int place, uint32_t parity) { return warp_wait(gsmem(&sm.item_full[place]), parity, dead, limit); },
             [&](int place) { return sm.item[place].end != 0; });
     };
     auto give_back = [&](int number) {
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                                 bar_arrive(gsmem(&sm.voted));
                             }
                         },
-                        [&](uint32_t parity) { warp_wait(gsmem(&sm.voted), parity, dead); }));
+                        [&](uint32_t parity) { bar_wait(gsmem(&sm.voted), parity, dead); }));
                 uint32_t rest[2] = {0, 0};
                 if (any) {  // the small ones first, then an eighth of the large ones
 #pragma unroll
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 open = open && put_piece(
                                    number,
                                    [&](int place, uint32_t parity) {
-                                       return warp_wait(gsmem(&sm.item_empty[place]), parity, dead, true, limit());
+                                       return warp_wait(gsmem(&sm.item_empty[place]), parity, dead, limit);
                                    },
                                    [&](int place) {
                                        if (lane < 4) sm.nan_from[place][lane] = 0x7fffffff;
@@ -525,13 +525,15 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                     }
                 }
             }
-            // the last arrivals and products, so that none is under way when the CTA ends,
-            // whatever else gave up
-            for (int e = 0; e < kStages; ++e) bar_wait(gsmem(&sm.empty[e]), e < st ? round : round ^ 1, dead);
-            __syncwarp();
-            if (leader) tc_commit(gsmem(&sm.drained[x]));
-            __syncwarp();
-            bar_wait(gsmem(&sm.drained[x]), 0, dead, true);
+            // the last arrivals, so that none is under way when the CTA ends; where one does not
+            // come, the products
+            bool over = true;
+            for (int e = 0; e < kStages; ++e) over &= bar_wait(gsmem(&sm.empty[e]), e < st ? round : round ^ 1, dead);
+            if (!__all_sync(0xffffffffu, over)) {
+                if (leader) tc_commit(gsmem(&sm.drained[x]));
+                __syncwarp();
+                bar_wait(gsmem(&sm.drained[x]), 0, dead, true);
+            }
         } else {
             // --- the cells' bytes: lane n has cell n of a tile
             constexpr uint32_t kBytes = C::kBytes / 2;
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
                 give_back(number);
             }
             // copies under way land before the CTA leaves, whatever else gave up
-            for (int e = 0; e < S::kRaw; ++e) gbar_wait(gsmem(&sm.raw_full[e]), e < r ? turn ^ 1 : turn);
+            for (int e = 0; e < S::kRaw; ++e) bar_wait(gsmem(&sm.raw_full[e]), e < r ? turn ^ 1 : turn, dead, true);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n");
