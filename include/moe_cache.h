@@ -627,9 +627,12 @@ typedef struct {
  *   tokens   : device int32 [rows]
  *   logprobs : device fp32 [rows], the logarithm of the token's share of the kept
  *              weights (0 where the first token is taken); or NULL
- * Weights are accurate to 2^-34 and sums of them are exact, so a token differs
- * from the one that exact arithmetic draws only where a boundary lies that near;
- * results do not depend on how the work is split. A row without a distribution (a
+ * A weight is off by at most 2^-34 of itself and 2^-44 of the row's largest, and
+ * sums of weights are exact. So a token differs from the one that exact arithmetic
+ * draws only where a boundary lies within about 2^-34 of the sum and 2^-44 of the
+ * largest weight for each of the row's tokens (2^-24 for 2^20 of them, which matters
+ * where nearly all lie some 30 temperatures below the largest). Results do not
+ * depend on how the work is split. A row without a distribution (a
  * NaN or +inf among its logits, nothing but -inf, a NaN or bad temperature, NaN
  * settings) gives token -1 and a NaN. Runs on the current device, asynchronous on
  * `stream`; allocates nothing. MOE_ERR_INVALID for bad arguments; rows = 0 does

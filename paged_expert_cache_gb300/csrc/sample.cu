@@ -18,7 +18,10 @@
 // with 100000 tokens kept, an error of 1e-8 in the sums moves one draw in a
 // thousand. So weights are computed to about 2^-36 (Weigher) and summed as
 // integers of 2^-43, exactly and in any order: results do not depend on how a row
-// is split, nor on the order of atomics. That costs about 45 instructions a token,
+// is split, nor on the order of atomics. (The unit is what 64 bits leave for the sum
+// of 2^20 tokens. Weights are rounded to it, to nothing below half of it: 2^-44 a
+// token, 2^-24 of the largest weight where 2^20 tokens lie 30.5 temperatures below
+// the top and are left out.) That costs about 45 instructions a token,
 // which bounds rows of wide nuclei; where top-k or min-p leave few tokens, only
 // theirs are computed, and the chain of steps over the cluster bounds the call.
 //
