@@ -29,6 +29,7 @@
 #include "common.cuh"
 #include "kv.cuh"
 #include "moe_cache.h"
+#include "row_piece.h"
 
 namespace moe {
 
@@ -403,13 +404,9 @@ struct Line {
             if (whole || (k > 0 && 16 * k + 16 <= bytes)) {
                 piece[i] = from[k];
             } else {  // only what is the row's
-                T v[16 / sizeof(T)];
-#pragma unroll
-                for (int e = 0; e < (int)(16 / sizeof(T)); ++e) {
-                    const int at = (16 * k - phase) / (int)sizeof(T) + e;
-                    v[e] = at >= 0 && at < n ? row[at] : T(0);
-                }
-                piece[i] = *reinterpret_cast<const uint4*>(v);
+                uint32_t w[4];
+                row_piece(w, row, (16 * k - phase) / (int)sizeof(T), n);
+                piece[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
     }
