@@ -614,7 +614,9 @@ moe_status_t moe_residual_norm(const moe_norm_t* args, void* stream);
  * The token drawn is the first one, in that order, whose weight and those before
  * it sum to more than uniform times the sum of all kept ones. */
 typedef struct {
-    const float* temperature;  /* finite, >= 0; 0 takes the first token (NULL: 1) */
+    const float* temperature;  /* finite, >= 0; 0 takes the first token, anything between is
+                                * at least 2^-99; above 2^99 for logits less than 2^114
+                                * apart (NULL: 1) */
     const int32_t* top_k;      /* NULL: 0 */
     const float* top_p;        /* NULL: 1 */
     const float* min_p;        /* NULL: 0 */

@@ -128,7 +128,8 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 // others by the series up to y^5 / 120 (the next term is below 2^-48). The power
 // 2^(r/32), r = k mod 32, is held by lane r as hi + lo (a shuffle has no bank
 // conflicts, as a table in shared memory has); hi * h keeps its rounding. The
-// largest error left is that of the last sums, about 2^-36.
+// largest error left is that of the last sums, about 2^-36. (A c below 2^-100 has not all
+// of its bits in two floats: off by 2^-150, which v - top from 2^114 on shows.)
 struct Weigher {
     float top, c, cl, hi, lo;  // hi, lo: this lane's power
     __device__ __forceinline__ uint64_t operator()(float v) const {
@@ -206,12 +207,14 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(SampleArgs a) {
     griddep_launch();
     const T* src = (const T*)a.logits + row * a.stride + first;
     const Slice<T> value = {values, src, min(a.held, n)};
-    const float temp = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
+    float temp = a.temperature ? a.temperature[row] : 1.f;
+    if (temp > 0.f) temp = fmaxf(temp, 0x1p-99f);  // log2 e / temp stays far below fp32's largest
+    const float top_p = a.top_p ? a.top_p[row] : 1.f;
     const float min_p = a.min_p ? a.min_p[row] : 0.f, u = a.uniform ? a.uniform[row] : 0.f;
     const int top_k = a.top_k ? a.top_k[row] : 0;
     const bool greedy = !a.uniform || temp == 0.f;
     if (tid == 0) {  // fp64 is slow: one thread's work
-        const double c = fmin(1.4426950408889634 / (double)temp, 0x1p100);
+        const double c = 1.4426950408889634 / (double)temp;
         sm.c = (float)c;
         sm.cl = (float)(c - (double)sm.c);
         if (min_p > 0.f) sm.least = (double)temp * log((double)min_p);
