@@ -69,9 +69,11 @@ struct KvBatch {
 // Groups of neighbouring sequences that have their first positions in common, and
 // what the kernels leave of a row's sum for the one that joins it: unnormalised
 // outputs, each with a head: the exponent that its weights 2^(score - exponent) refer
-// to, the sum of the weights, and two words. Of the common positions: the first of
-// the slots that go on with the sum, and their number with, above 16 bits, its row
-// there. Of the rest: whether there is something to join.
+// to, the sum of the weights, and two words. Of the common positions they are the first
+// of the slots that go on with the sum, and their number with, above 16 bits, its row
+// there. Of the rest the third word has the flags kWhole, kPieces and kCommon of
+// kv_attend.cu; where the rest is in pieces there is no sum yet, and the first two words
+// are the CTA of the first piece and their number, the fourth the row's place there.
 struct KvGroups {
     const int *cu, *prefix;
     int n;
