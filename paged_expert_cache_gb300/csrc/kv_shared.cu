@@ -21,7 +21,8 @@
 //             tensor memory
 //   11        copies a tile's cells, their keys and their values in turn, into a
 //             ring of three half tiles as they are (bulk copies)
-//   12-15     codes into tiles: a warp takes two of a tile's eight cells and writes
+//   12-15     codes into tiles (they vote on rare cases over a barrier of their own): a
+//             warp takes two of a tile's eight cells and writes
 //             d (q - 8) as fp16 to a ring K0 V0 K1 V1 ... of tiles in 128-byte
 //             swizzle. Keys lie [key][dim], values [dim][key], as the cells hold
 //             them; both K-major. The code is kept short: with the cells in
@@ -41,8 +42,11 @@
 // output NaN for the rows that see it and for no others. Maxima, sums and outputs are
 // fp32.
 //
-// Measured: 32768 common positions, 512 rows for each of 8 heads, head_dim 128: 74 us
-// of the call's 114 (930 TFLOP/s, 0.48 of cuBLAS's bf16 rate), about 4400 cycles a key
+// All waits are bounded. Where one gives up, its warp takes no more pieces (piece_ring.h)
+// and the CTA says so in parts.failed, for the join to write NaN.
+//
+// Measured: 32768 common positions, 512 rows for each of 8 heads, head_dim 128: 75 us
+// of the call's 116 (916 TFLOP/s, 0.47 of cuBLAS's bf16 rate), about 4400 cycles a key
 // tile where the products take 2150 and shared memory's traffic for them and the
 // tiles 2500. The chain of a tile is what runs: softmax 2300, then the values'
 // products, the next scores and their waits 2100; the tile warps need 3500 beside

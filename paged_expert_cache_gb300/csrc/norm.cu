@@ -10,15 +10,20 @@
 // values a thread where rows are aligned (16-byte loads). A row of at most 256
 // values is a warp's (four rows a CTA, no barrier), a longer one a CTA's, up to
 // 1024 threads; so a call of one row has all its loads on the way at once (k_norm).
+// From 8193 values on a thread has 16 or 32 of x and as many of y, more than its
+// registers hold: part of them go through local memory, most of them where rows past
+// 16384 are not aligned.
 // From two rows an SM on, and up to 4096 values, CTAs take several rows, the next
 // one's loads under the last one's sums: k_norm_rows where rows are aligned, and two
-// more kernels for rows that are not. (Rows of 4096 bf16 with both norms, of 4001, of
-// 2048 fp32 with one: 320 rows 4.6, 7.6 and 2.9 us, a row a CTA 5.1, 10.9 and 2.8; 2451
-// rows 18.1, 21.4 and 8.9, 21.2, 39.8 and 9.4.)
+// more kernels for rows that are not. (Rows of 4096 bf16 with both norms, of 4001, and of
+// 2048 fp32 with one norm and y bf16, two sets of inputs in turn: 320 rows 4.0, 5.4 and 2.9
+// us, a row a CTA 4.7, 8.3 and 2.7; 2451 rows 17.0, 18.9 and 10.6, a row a CTA 27.7, 44.8
+// and 11.2, their bytes 12.0, 11.7 and 9.0.)
 //
 // Measured in a graph: one row of 2048 1.9 us, 61 of 4096 with both norms 2.9, 2451
 // of 2048 8.9 (6.8 TB/s, part of it from L2), 15013 of 4000 with both norms 94 (6.4
-// TB/s, 0.95 of a copy), of 4001 103.
+// TB/s, 0.95 of a copy), of 4001 103. Past 4096 values, a row a CTA: 7500 rows of 5120 bf16
+// with both norms 86, of 8192 174, of 16384 252, of 16391 3520 (bytes 46, 74, 147 and 147).
 //
 // Everything is fp32: the sums of squares too, which fp32 holds unless values
 // pass 2^63 or all are below 2^-50. A row whose sum left that range is summed
