@@ -511,8 +511,8 @@ typedef struct {
  *   out       : must not overlap q
  * The rest, and the limits, as in moe_kv_attend (keys, values and weights of the
  * common positions are rounded to fp16 on the way). Should a bounded wait inside
- * the kernel give up (0.2 s, and 20 us for each 128 positions of a piece of work),
- * all rows with common positions come out as NaN. */
+ * the kernel give up (0.2 s, and 20 us for each 128 positions of a piece of work and
+ * 0.1 us for each group), all rows with common positions come out as NaN. */
 moe_status_t moe_kv_attend_shared(moe_kv_t* h, int32_t layer, const void* q, int64_t q_stride, int32_t T,
                                   const moe_kv_batch_t* batch, const moe_kv_groups_t* groups, float scale, void* out,
                                   void* workspace, uint64_t workspace_bytes, void* stream);

@@ -199,8 +199,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1) k_shared(const __grid_const
     int* dead = &sm.dead;
 
     // What a wait for a piece has, to be put or to be given back: 20 us for each key tile
-    // of the longest one, which may be at work meanwhile.
-    auto limit = [&]() { return kGWaitNs + 20000ull * (unsigned)*(volatile int*)&sm.longest; };
+    // of the longest one, which may be at work meanwhile, and 0.1 us for each group, which
+    // are looked through for the next one (32 at a time, in 0.5 us).
+    auto limit = [&]() { return kGWaitNs + 20000ull * (unsigned)*(volatile int*)&sm.longest + 100ull * (unsigned)a.g.n; };
     // The next piece, for whole warps; false at the end. `number` counts the pieces taken.
     auto take = [&](int number) {
         return take_piece(
